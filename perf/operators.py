@@ -182,8 +182,7 @@ def _balance_own(st):
     from moe_expert_layer_histogram_gb300 import router_balance, router_balance_backward
     K = st["case"]["K"]
     r = router_balance(st["logits"], K, st["coef"], mask=st["mask"])
-    d = router_balance_backward(st["logits"], r, d_loss=st["d_loss"], d_weights=st["d_weights"],
-                                mask=st["mask"])
+    d = router_balance_backward(st["logits"], r, d_loss=st["d_loss"], d_weights=st["d_weights"])
     return dict(ids=r.ids, weights=r.weights, counts=r.counts, loss=r.loss, d_logits=d)
 
 
