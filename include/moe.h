@@ -331,6 +331,117 @@ moe_status moe_route_permute_static(const float *router_logits, int T, int E,
                                     int32_t *offsets, int32_t *perm,
                                     void *stream);
 
+/* ---- the router in training ------------------------------------------------
+ * Element type of the router logits and of their gradient.                 */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype;
+
+/* Workspace bytes of moe_balance_forward (0 for sizes it refuses).  The
+ * contents need no initialisation and mean nothing after the call.        */
+size_t moe_balance_workspace(int T, int E);
+
+/* Top-k routing with the load-balance loss.  logits: device [T, E] of
+ * `dtype` with a row stride of ld >= E elements; mask: device uint8 [T] (0 =
+ * padding) or NULL.  A token is live when its mask is not 0 and at least one
+ * of its logits is above -inf; n is the number of live tokens.  Outputs,
+ * device: ids int32 [T, K] and weights f32 [T, K] as moe_forward routes
+ * (value descending, lower index first on ties, softmax over the K; -1 and 0
+ * for tokens that are not live), counts int32 [E] (live slots per expert),
+ * mean_probs f32 [E] or NULL (P_e, the mean over live tokens of the softmax
+ * over all E experts) and loss f32 [1] = coef * sum_e f_e P_e with
+ * f_e = counts_e * E / (K * n), the loss whose minimum is an even load; 0
+ * when no token is live.  Sums are in fp32 in a fixed order: the same inputs
+ * give the same bits.  A NaN logit makes its token's weights and the loss
+ * NaN.  T == 0 writes zero counts and loss.  1 <= E <= 512, K <= min(E, 16)
+ * and T * K < 2^31, else MOE_ERR_UNSUPPORTED.  Asynchronous on `stream`;
+ * the workspace must stay until the work is done.  Errors:
+ * MOE_ERR_INVALID_ARG (sizes, a NULL or misaligned pointer: logits to their
+ * element, the workspace to 16 bytes, the others to 4; workspace_bytes below
+ * moe_balance_workspace), MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.  The build's
+ * own call, as the other moe_balance_* and moe_blockscale_* ones.         */
+moe_status moe_balance_forward(const void *logits, int dtype, int64_t ld,
+                               const uint8_t *mask, int T, int E, int K,
+                               float coef, int32_t *ids, float *weights,
+                               int32_t *counts, float *mean_probs, float *loss,
+                               void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* Gradient of the logits.  ids, weights and counts as moe_balance_forward
+ * wrote them for the same logits, K and coef; d_loss: device f32 [1], the
+ * gradient of the loss, or NULL (no part from the loss); d_weights: device
+ * f32 [T, K], the gradient of the weights, or NULL.  d_logits: device [T, E]
+ * of `dtype`, row stride ld_d >= E, rounded once from fp32; zero for tokens
+ * that are not live.  With p the softmax over the E experts and
+ * g_e = d_loss * coef * f_e / n:
+ *   d_logits_e = p_e (g_e - sum_j p_j g_j)
+ *              + [e = ids_k] w_k (d_w_k - sum_j w_j d_w_j).
+ * (The counts are piecewise constant: no gradient passes through them.)
+ * T == 0 is a no-op.  Limits, alignment and errors as the forward.        */
+moe_status moe_balance_backward(const void *logits, int dtype, int64_t ld,
+                                int T, int E, int K, float coef,
+                                const int32_t *ids, const float *weights,
+                                const int32_t *counts, const float *d_loss,
+                                const float *d_weights, void *d_logits,
+                                int64_t ld_d, void *stream);
+
+/* ---- FP8 products with a scale per block of 128 ------------------------------
+ * Activations: e4m3 codes [rows, cols] (row stride ld_codes) with one fp32
+ * scale per row and 128 columns, stored block-major: scales[b * ld_scales +
+ * row], b = column / 128.  Weights: e4m3 codes with one fp32 scale per 128 x
+ * 128 block, scales [ceil(rows/128), ceil(cols/128)] per expert.  Last
+ * blocks may be short.
+ *
+ * Quantise bf16 rows: per row and block, s = amax / 448 and codes
+ * e4m3(x / s), both quotients rounded to nearest in fp32; an all-zero block
+ * gets s = 0 and zero codes, one with an infinity or NaN s = NaN and NaN
+ * codes.  x: device bf16 [x_rows, cols], row stride ldx, any alignment of
+ * whole elements.  slots: device int32 [rows] or NULL; row r reads row
+ * slots[r] / top_k of x (the permuted slots of moe_route_permute_static
+ * gather each expert's rows), or row r; a slot outside x gives a zero row.
+ * cols >= 1 of any size, ld_codes >= cols, ld_scales >= rows.  rows == 0 is
+ * a no-op.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (more than
+ * 2^31 blocks), MOE_ERR_CUDA.                                             */
+moe_status moe_blockscale_quantize(const void *x, int64_t ldx, int x_rows,
+                                   const int32_t *slots, int top_k, int rows,
+                                   int cols, void *codes, int64_t ld_codes,
+                                   float *scales, int64_t ld_scales,
+                                   void *stream);
+
+/* out[m, n] = sum_k a[m, k] w_e[n, k] for the rows m of each expert e, both
+ * operands with their scales, fp32 sums, one rounding to bf16.  a: M rows
+ * of K codes; offsets: device int32 [E + 1], rows offsets[e] ..
+ * offsets[e+1] - 1 belong to expert e, or NULL for one expert of all M rows
+ * (E = 1: a plain product).  w: [E, N, K], rows of ldw codes (transpose_w:
+ * [E, K, N], the same product with the weights' transpose, i.e. the input
+ * gradient from the weights as they are stored; w_scales keeps the stored
+ * orientation).  out: bf16 [M, N], row stride ldo.  Rows of no expert are
+ * not written; offsets outside [0, M] or falling are clamped into range.
+ * N, K, M of any size; a and w 16-byte aligned with row strides that are
+ * multiples of 16 (ld >= the row), E <= 512.  M == 0 is a no-op.
+ * Asynchronous on `stream`, allocates nothing, no workspace.  Errors:
+ * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.                 */
+moe_status moe_blockscale_matmul(const void *a, int64_t lda,
+                                 const float *a_scales, int64_t ld_as,
+                                 const void *w, int64_t ldw,
+                                 const float *w_scales, const int32_t *offsets,
+                                 int E, int M, int N, int K, int transpose_w,
+                                 void *out, int64_t ldo, void *stream);
+
+/* The gate/up product with SwiGLU and re-quantisation: w13 [E, 2I, K], rows
+ * 0..I-1 of an expert the gate and I..2I-1 the up projection (as
+ * moe_prepare_weights takes them); h = silu(gate) * up in fp32, gate and up
+ * clamped to [-clamp_limit, clamp_limit] first when that is > 0 and finite;
+ * h quantised as moe_blockscale_quantize does, without an intermediate
+ * rounding, into codes h [M, I] (16-byte aligned, ldh a multiple of 16) and
+ * h_scales [I / 128, ld_hs].  I a multiple of 128 (else
+ * MOE_ERR_UNSUPPORTED); the rest as moe_blockscale_matmul.                */
+moe_status moe_blockscale_swiglu(const void *a, int64_t lda,
+                                 const float *a_scales, int64_t ld_as,
+                                 const void *w13, int64_t ldw,
+                                 const float *w13_scales,
+                                 const int32_t *offsets, int E, int M, int I,
+                                 int K, float clamp_limit, void *h, int64_t ldh,
+                                 float *h_scales, int64_t ld_hs, void *stream);
+
 /* Tensor-pipe rate of one MMA kind on this GPU (measurement, not part of the
  * layer): one CTA per SM issues `iters` groups of four back-to-back
  * tcgen05.mma (M = 128, N = n_cols in {128, 256}) on zero operands resident

@@ -46,7 +46,9 @@ EXPORTS = ("moe_create", "moe_prepare_weights", "moe_forward", "moe_forward_batc
            "moe_debug_weight_tiles",
            "moe_get_status", "moe_timing_start", "moe_timing_stop", "moe_last_launch_count",
            "moe_gemm_ctas",
-           "moe_route_permute_static", "moe_measure_mma_rate", "moe_status_string",
+           "moe_route_permute_static", "moe_balance_workspace", "moe_balance_forward",
+           "moe_balance_backward", "moe_blockscale_quantize", "moe_blockscale_matmul",
+           "moe_blockscale_swiglu", "moe_measure_mma_rate", "moe_status_string",
            "moe_destroy")
 
 _lib = None
@@ -77,6 +79,17 @@ def lib():
     L.moe_last_launch_count.argtypes = [vp]
     L.moe_gemm_ctas.argtypes = [vp, ci]
     L.moe_route_permute_static.argtypes = [vp, ci, ci, ci, vp, vp, vp, vp, vp]
+    i64, cf = ctypes.c_int64, ctypes.c_float
+    L.moe_balance_workspace.argtypes = [ci, ci]
+    L.moe_balance_forward.argtypes = [vp, ci, i64, vp, ci, ci, ci, cf, vp, vp, vp, vp, vp, vp,
+                                      ctypes.c_size_t, vp]
+    L.moe_balance_backward.argtypes = [vp, ci, i64, ci, ci, ci, cf, vp, vp, vp, vp, vp, vp, i64,
+                                       vp]
+    L.moe_blockscale_quantize.argtypes = [vp, i64, ci, vp, ci, ci, ci, vp, i64, vp, i64, vp]
+    L.moe_blockscale_matmul.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp,
+                                        i64, vp]
+    L.moe_blockscale_swiglu.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, cf, vp,
+                                        i64, vp, i64, vp]
     L.moe_measure_mma_rate.argtypes = [ci, ci, ci, ci, ctypes.POINTER(ctypes.c_double), vp]
     L.moe_status_string.argtypes = [ci]
     L.moe_status_string.restype = ctypes.c_char_p
@@ -85,6 +98,7 @@ def lib():
     for name in EXPORTS:
         if name not in ("moe_status_string", "moe_destroy"):
             getattr(L, name).restype = ci
+    L.moe_balance_workspace.restype = ctypes.c_size_t
     _lib = L
     return L
 
@@ -208,6 +222,50 @@ def moe_route_permute_static(router_logits, T, E, K, topk_ids, topk_w, offsets, 
                                           _ptr(perm), stream), "moe_route_permute_static")
 
 
+MOE_DTYPE = {"f32": 0, "bf16": 1}
+
+
+def moe_balance_workspace(T, E):
+    return lib().moe_balance_workspace(int(T), int(E))
+
+
+def moe_balance_forward(logits, dtype, ld, mask, T, E, K, coef, ids, weights, counts, mean_probs,
+                        loss, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_balance_forward(_ptr(logits), dtype, ld, _ptr(mask), T, E, K, coef, _ptr(ids),
+                                     _ptr(weights), _ptr(counts), _ptr(mean_probs), _ptr(loss),
+                                     _ptr(workspace), workspace_bytes, stream),
+           "moe_balance_forward")
+
+
+def moe_balance_backward(logits, dtype, ld, T, E, K, coef, ids, weights, counts, d_loss, d_weights,
+                         d_logits, ld_d, stream=None):
+    _check(lib().moe_balance_backward(_ptr(logits), dtype, ld, T, E, K, coef, _ptr(ids),
+                                      _ptr(weights), _ptr(counts), _ptr(d_loss), _ptr(d_weights),
+                                      _ptr(d_logits), ld_d, stream), "moe_balance_backward")
+
+
+def moe_blockscale_quantize(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,
+                            ld_scales, stream=None):
+    _check(lib().moe_blockscale_quantize(_ptr(x), ldx, x_rows, _ptr(slots), top_k, rows, cols,
+                                         _ptr(codes), ld_codes, _ptr(scales), ld_scales, stream),
+           "moe_blockscale_quantize")
+
+
+def moe_blockscale_matmul(a, lda, a_scales, ld_as, w, ldw, w_scales, offsets, E, M, N, K,
+                          transpose_w, out, ldo, stream=None):
+    _check(lib().moe_blockscale_matmul(_ptr(a), lda, _ptr(a_scales), ld_as, _ptr(w), ldw,
+                                       _ptr(w_scales), _ptr(offsets), E, M, N, K, transpose_w,
+                                       _ptr(out), ldo, stream), "moe_blockscale_matmul")
+
+
+def moe_blockscale_swiglu(a, lda, a_scales, ld_as, w13, ldw, w13_scales, offsets, E, M, I, K,
+                          clamp_limit, h, ldh, h_scales, ld_hs, stream=None):
+    _check(lib().moe_blockscale_swiglu(_ptr(a), lda, _ptr(a_scales), ld_as, _ptr(w13), ldw,
+                                       _ptr(w13_scales), _ptr(offsets), E, M, I, K, clamp_limit,
+                                       _ptr(h), ldh, _ptr(h_scales), ld_hs, stream),
+           "moe_blockscale_swiglu")
+
+
 def moe_measure_mma_rate(fmt, n_cols=128, copy_scales=False, iters=20000, stream=None):
     """Dense TFLOP/s of the layer's MMA kind for `fmt` on the current GPU
     (tcgen05.mma on shared-memory-resident operands, one CTA per SM)."""
@@ -313,3 +371,8 @@ class MoELayer:
             self.close()
         except Exception:
             pass
+
+
+from .balance import RouterBalance, router_balance, router_balance_backward  # noqa: E402,F401
+from .blockscale import (blockscale_experts, blockscale_linear,  # noqa: E402,F401
+                         blockscale_linear_dx, blockscale_matmul, blockscale_quantize)
