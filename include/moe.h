@@ -418,7 +418,9 @@ moe_status moe_blockscale_quantize(const void *x, int64_t ldx, int x_rows,
  * N, K, M of any size; a and w 16-byte aligned with row strides that are
  * multiples of 16 (ld >= the row), E <= 512.  M == 0 is a no-op.
  * Asynchronous on `stream`, allocates nothing, no workspace.  Errors:
- * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.                 */
+ * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_NO_DEVICE,
+ * MOE_ERR_CUDA.  A kernel that gives up a bounded wait leaves its output
+ * incomplete and records it for moe_blockscale_status.                    */
 moe_status moe_blockscale_matmul(const void *a, int64_t lda,
                                  const float *a_scales, int64_t ld_as,
                                  const void *w, int64_t ldw,
@@ -441,6 +443,45 @@ moe_status moe_blockscale_swiglu(const void *a, int64_t lda,
                                  const int32_t *offsets, int E, int M, int I,
                                  int K, float clamp_limit, void *h, int64_t ldh,
                                  float *h_scales, int64_t ld_hs, void *stream);
+
+/* Workspace bytes for `rows` quantised rows of `cols` columns (inter > 0: and
+ * as many of `inter` columns); 0 for sizes out of range.  The contents need
+ * no initialisation and mean nothing after the call.                      */
+size_t moe_blockscale_workspace(int rows, int cols, int inter);
+
+/* moe_blockscale_quantize of the bf16 rows x [M, K] and the product with one
+ * matrix w [N, K] (transpose_w: [K, N]) in one call, for which the product's
+ * set-up and first weight loads overlap the quantisation.  workspace: device,
+ * 16-byte aligned, moe_blockscale_workspace(M, K, 0) bytes, in use until the
+ * work is done.  The rest as moe_blockscale_matmul.                        */
+moe_status moe_blockscale_linear(const void *x, int64_t ldx, const void *w,
+                                 int64_t ldw, const float *w_scales, int M,
+                                 int N, int K, int transpose_w, void *out,
+                                 int64_t ldo, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* The experts' products of one layer on routed rows, in one call: row r of
+ * out (bf16 [rows, H], row stride ldo) is expert e's MLP of row
+ * slots[r] / top_k of x (bf16 [T, H]) for offsets[e] <= r < offsets[e+1]:
+ * quantised, through w13 [E, 2I, H] and SwiGLU (moe_blockscale_swiglu), and
+ * through w2 [E, H, I]; both contiguous.  slots int32 [rows] and offsets
+ * int32 [E+1] as moe_route_permute_static writes perm and offsets.  H a
+ * multiple of 16 and I of 128 (else MOE_ERR_UNSUPPORTED).  workspace: device,
+ * 16-byte aligned, moe_blockscale_workspace(rows, H, I) bytes.  rows == 0 is
+ * a no-op.  The rest as moe_blockscale_swiglu and moe_blockscale_matmul.   */
+moe_status moe_blockscale_experts(const void *x, int64_t ldx, int T,
+                                  const int32_t *slots, int top_k, int rows,
+                                  const int32_t *offsets, int E,
+                                  const void *w13, const float *w13_scales,
+                                  const void *w2, const float *w2_scales,
+                                  int H, int I, float clamp_limit, void *out,
+                                  int64_t ldo, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Synchronises the device and returns (and clears) what the moe_blockscale_*
+ * kernels recorded on it since the last call: MOE_ERR_DEVICE_TIMEOUT if one
+ * gave up a bounded wait, else MOE_OK; MOE_ERR_CUDA on a CUDA error.      */
+moe_status moe_blockscale_status(void);
 
 /* Tensor-pipe rate of one MMA kind on this GPU (measurement, not part of the
  * layer): one CTA per SM issues `iters` groups of four back-to-back

@@ -48,7 +48,8 @@ EXPORTS = ("moe_create", "moe_prepare_weights", "moe_forward", "moe_forward_batc
            "moe_gemm_ctas",
            "moe_route_permute_static", "moe_balance_workspace", "moe_balance_forward",
            "moe_balance_backward", "moe_blockscale_quantize", "moe_blockscale_matmul",
-           "moe_blockscale_swiglu", "moe_measure_mma_rate", "moe_status_string",
+           "moe_blockscale_swiglu", "moe_blockscale_workspace", "moe_blockscale_linear",
+           "moe_blockscale_experts", "moe_blockscale_status", "moe_measure_mma_rate", "moe_status_string",
            "moe_destroy")
 
 _lib = None
@@ -90,6 +91,12 @@ def lib():
                                         i64, vp]
     L.moe_blockscale_swiglu.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, cf, vp,
                                         i64, vp, i64, vp]
+    L.moe_blockscale_workspace.argtypes = [ci, ci, ci]
+    L.moe_blockscale_linear.argtypes = [vp, i64, vp, i64, vp, ci, ci, ci, ci, vp, i64, vp,
+                                        ctypes.c_size_t, vp]
+    L.moe_blockscale_experts.argtypes = [vp, i64, ci, vp, ci, ci, vp, ci, vp, vp, vp, vp, ci, ci,
+                                         cf, vp, i64, vp, ctypes.c_size_t, vp]
+    L.moe_blockscale_status.argtypes = []
     L.moe_measure_mma_rate.argtypes = [ci, ci, ci, ci, ctypes.POINTER(ctypes.c_double), vp]
     L.moe_status_string.argtypes = [ci]
     L.moe_status_string.restype = ctypes.c_char_p
@@ -98,7 +105,7 @@ def lib():
     for name in EXPORTS:
         if name not in ("moe_status_string", "moe_destroy"):
             getattr(L, name).restype = ci
-    L.moe_balance_workspace.restype = ctypes.c_size_t
+    L.moe_balance_workspace.restype = L.moe_blockscale_workspace.restype = ctypes.c_size_t
     _lib = L
     return L
 
@@ -264,6 +271,30 @@ def moe_blockscale_swiglu(a, lda, a_scales, ld_as, w13, ldw, w13_scales, offsets
                                        _ptr(w13_scales), _ptr(offsets), E, M, I, K, clamp_limit,
                                        _ptr(h), ldh, _ptr(h_scales), ld_hs, stream),
            "moe_blockscale_swiglu")
+
+
+def moe_blockscale_workspace(rows, cols, inter=0):
+    return lib().moe_blockscale_workspace(rows, cols, inter)
+
+
+def moe_blockscale_linear(x, ldx, w, ldw, w_scales, M, N, K, transpose_w, out, ldo, workspace,
+                          workspace_bytes, stream=None):
+    _check(lib().moe_blockscale_linear(_ptr(x), ldx, _ptr(w), ldw, _ptr(w_scales), M, N, K,
+                                       transpose_w, _ptr(out), ldo, _ptr(workspace),
+                                       workspace_bytes, stream), "moe_blockscale_linear")
+
+
+def moe_blockscale_experts(x, ldx, T, slots, top_k, rows, offsets, E, w13, w13_scales, w2,
+                           w2_scales, H, I, clamp_limit, out, ldo, workspace, workspace_bytes,
+                           stream=None):
+    _check(lib().moe_blockscale_experts(_ptr(x), ldx, T, _ptr(slots), top_k, rows, _ptr(offsets),
+                                        E, _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales),
+                                        H, I, clamp_limit, _ptr(out), ldo, _ptr(workspace),
+                                        workspace_bytes, stream), "moe_blockscale_experts")
+
+
+def moe_blockscale_status():
+    return lib().moe_blockscale_status()
 
 
 def moe_measure_mma_rate(fmt, n_cols=128, copy_scales=False, iters=20000, stream=None):

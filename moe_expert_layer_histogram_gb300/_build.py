@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_gb300.so")
 SOURCES = ["gemm.cu", "gemm_pair.cu", "decode.cu", "route.cu", "prep.cu", "api.cu",
-           "route_static.cu", "peak.cu", "balance.cu", "blockscale.cu"]
+           "route_static.cu", "peak.cu", "balance.cu", "blockscale.cu",
+           "blockscale_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

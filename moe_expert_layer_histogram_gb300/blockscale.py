@@ -97,43 +97,75 @@ def blockscale_matmul(codes, scales, w, w_scales, offsets=None, transpose_w=Fals
     return out
 
 
+def _linear(x, w, w_scales, transpose_w, out):
+    import torch
+
+    from . import lib, moe_blockscale_linear
+    ldx = _rows(x, torch.bfloat16, "x")
+    E, wr, wc, ldw = _weights(torch, w, w_scales)
+    N, K = (wc, wr) if transpose_w else (wr, wc)
+    M, dev = x.shape[0], w.device
+    if w.dim() != 2 or x.shape[1] != K or x.device != dev:
+        raise ValueError("x [M, %d] and one weight matrix, both on %s" % (K, dev))
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    ldo = _rows(out, torch.bfloat16, "out")
+    if tuple(out.shape) != (M, N) or out.device != dev:
+        raise ValueError("out: [%d, %d] on %s" % (M, N, dev))
+    nbytes = lib().moe_blockscale_workspace(M, K, 0)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    moe_blockscale_linear(x, ldx, w, ldw, w_scales, M, N, K, int(transpose_w), out, ldo, ws,
+                          nbytes, torch.cuda.current_stream(dev).cuda_stream)
+    return out
+
+
 def blockscale_linear(x, w, w_scales, out=None):
     """y = x w^T for bf16 x [M, K] and weights [N, K] -> bf16 [M, N]."""
-    codes, scales = blockscale_quantize(x)
-    return blockscale_matmul(codes, scales, w, w_scales, out=out)
+    return _linear(x, w, w_scales, False, out)
 
 
 def blockscale_linear_dx(dy, w, w_scales, out=None):
     """Input gradient of blockscale_linear: dx = dy w for bf16 dy [M, N], from
     the same stored weights [N, K] -> bf16 [M, K]."""
-    codes, scales = blockscale_quantize(dy)
-    return blockscale_matmul(codes, scales, w, w_scales, transpose_w=True, out=out)
+    return _linear(dy, w, w_scales, True, out)
 
 
 def blockscale_experts(x, slots, offsets, top_k, w13, w13_scales, w2, w2_scales, clamp=0.0,
                        out=None):
     """The experts' products on routed rows: row r of the result is expert
     e's MLP of x's row slots[r] // top_k, for offsets[e] <= r < offsets[e+1]
-    (slots and offsets as moe_route_permute_static writes them).  w13
-    [E, 2I, H] (gate rows, then up rows), w2 [E, H, I] -> bf16
-    [len(slots), H], in permuted row order."""
+    (slots and offsets as moe_route_permute_static writes perm and offsets).
+    w13 [E, 2I, H] (gate rows, then up rows), w2 [E, H, I], contiguous -> bf16
+    [len(slots), H], in permuted row order; rows of no expert are left as
+    they are."""
     import torch
 
-    from . import moe_blockscale_swiglu
-    E, I2, H, ldw = _weights(torch, w13, w13_scales)
+    from . import lib, moe_blockscale_experts
+    ldx = _rows(x, torch.bfloat16, "x")
+    E, I2, H, _ = _weights(torch, w13, w13_scales)
     I = I2 // 2
-    if w13.dim() != 3 or w2.dim() != 3 or tuple(w2.shape) != (E, H, I) or I2 % 256:
-        raise ValueError("w13 [E, 2I, H] and w2 [E, H, I] with I a multiple of 128")
-    if x.shape[-1] != H or x.device != w13.device:
-        raise ValueError("x: [T, %d] on %s" % (H, w13.device))
-    codes, scales = blockscale_quantize(x, slots, top_k)
-    _offsets(torch, offsets, E, x.device)
+    _weights(torch, w2, w2_scales)
+    if (w13.dim() != 3 or tuple(w2.shape) != (E, H, I) or I2 % 256 or not w13.is_contiguous()
+            or not w2.is_contiguous()):
+        raise ValueError("contiguous w13 [E, 2I, H] and w2 [E, H, I] with I a multiple of 128")
+    dev = w13.device
+    if x.shape[1] != H or x.device != dev or w2.device != dev:
+        raise ValueError("x: [T, %d], all on %s" % (H, dev))
+    if (slots.dim() != 1 or slots.dtype != torch.int32 or slots.device != dev
+            or not slots.is_contiguous()):
+        raise ValueError("slots: contiguous int32 [R] on %s" % dev)
     if offsets is None:
         raise ValueError("offsets: int32 [%d]" % (E + 1))
+    _offsets(torch, offsets, E, dev)
     R = slots.shape[0]
-    h = torch.empty(R, I, dtype=torch.float8_e4m3fn, device=x.device)
-    hs = torch.empty(I // 128, R, dtype=torch.float32, device=x.device)
-    moe_blockscale_swiglu(codes, _ceil(H, 16) * 16, scales, R, w13, ldw, w13_scales, offsets, E,
-                          R, I, H, clamp, h, I, hs, R,
-                          torch.cuda.current_stream(x.device).cuda_stream)
-    return blockscale_matmul(h, hs, w2, w2_scales, offsets, out=out)
+    if out is None:
+        out = torch.empty(R, H, dtype=torch.bfloat16, device=dev)
+    ldo = _rows(out, torch.bfloat16, "out")
+    if tuple(out.shape) != (R, H) or out.device != dev:
+        raise ValueError("out: [%d, %d] on %s" % (R, H, dev))
+    nbytes = lib().moe_blockscale_workspace(R, H, I)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    moe_blockscale_experts(x, ldx, x.shape[0], slots, top_k, R, offsets, E, w13, w13_scales, w2,
+                           w2_scales, H, I, clamp, out, ldo, ws, nbytes,
+                           torch.cuda.current_stream(dev).cuda_stream)
+    return out

@@ -26,6 +26,19 @@ using namespace moe;
 thread_local bool moe::g_pdl_small = true;
 thread_local bool moe::g_pdl_gemm = true;
 
+PFN_cuTensorMapEncodeTiled_v12000 moe::tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
 struct moe_layer {
   moe_config cfg;
   int device = 0, num_sms = 0;
@@ -82,25 +95,12 @@ struct moe_layer {
 
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 // 2-D byte tensor [rows, row_bytes], box of 128 bytes x box_rows, 128-byte
 // swizzle (the layout the MMA descriptors expect) or none (data stored
 // pre-swizzled).
 bool make_map(CUtensorMap* m, void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows,
               bool swizzle = true) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {row_bytes, rows};
   cuuint64_t strides[1] = {row_bytes};
@@ -115,7 +115,7 @@ bool make_map(CUtensorMap* m, void* base, uint64_t row_bytes, uint64_t rows, uin
 // Prepared weight tiles viewed as rows of 2 KiB (256 x 64-bit elements), box
 // of 8 rows (16 KiB), no swizzle: the codes are stored pre-swizzled.
 bool make_tile_map(CUtensorMap* m, void* base, uint64_t rows) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {256, rows};
   cuuint64_t strides[1] = {2048};
@@ -386,7 +386,7 @@ moe_status moe_create(const moe_config* cfg, moe_layer** out) {
     cudaGetLastError();
     return MOE_ERR_NO_DEVICE;
   }
-  if (!encode_fn()) return MOE_ERR_NO_DEVICE;
+  if (!tensor_map_encoder()) return MOE_ERR_NO_DEVICE;
   const char* pv = std::getenv("MOE_PAIR_SCALE_COPIES");
 
   moe_layer* L = new moe_layer;

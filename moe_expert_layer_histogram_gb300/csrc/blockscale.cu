@@ -1,23 +1,16 @@
 // blockscale.cu -- products of e4m3 matrices with one fp32 scale per block of
-// 128: activations carry a scale per row and 128 columns, weights one per
-// 128 x 128 block.
-//
-//   quantise:  s = amax / 448 and codes e4m3(x / s) of each row's 128-column
-//              blocks, both quotients rounded to fp32; an all-zero block has
-//              s = 0 and zero codes, a block with an infinity or NaN s = NaN
-//              and NaN codes (so every product with it is NaN).
-//   product:   y[m][n] = sum_b sa[m][b] sw[n/128][b] sum_{k in b} a[m][k] w[n][k]
-//              over the rows of each expert, fp32 sums, one rounding to bf16.
-//   SwiGLU:    the same for gate and up rows, h = silu(gate) up in fp32,
-//              quantised as above.
+// 128 (activations: per row and 128 columns, weights: per 128 x 128): the
+// quantiser of the activations, and the entry points with their checks.  The
+// products run in blockscale_gemm.cu.
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
 
+#include "blockscale_quant.cuh"
 #include "internal.h"
 #include "moe.h"
-#include "quant.cuh"
 
 namespace moe {
 
@@ -28,133 +21,219 @@ constexpr int kBlk = 128;
 __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
 
 // ---------------------------------------------------------------- quantise
-// One warp per (row, block); lane l holds columns 4l .. 4l+3.
+// Eight lanes per (row, block), 16 columns each: with aligned rows two
+// 16-byte loads and one 16-byte store per thread.
+template <bool VEC>
 __global__ void __launch_bounds__(256)
     blockscale_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t ldx, int x_rows,
                                const int32_t* __restrict__ slots, int top_k, int rows, int cols,
                                uint8_t* __restrict__ codes, int64_t ld_codes,
                                float* __restrict__ scales, int64_t ld_scales) {
+  // a product that follows may set itself up and load weights meanwhile
+  pdl_launch_dependents();
   const int kb = blocks_of(cols);
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (unit >= static_cast<int64_t>(rows) * kb) return;
-  const int r = static_cast<int>(unit / kb), b = static_cast<int>(unit % kb);
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 3);
+  const bool real = unit < static_cast<int64_t>(rows) * kb;
+  const int r = real ? static_cast<int>(unit / kb) : 0;
+  const int b = real ? static_cast<int>(unit - static_cast<int64_t>(r) * kb) : 0;
+  const int c0 = b * kBlk + (threadIdx.x & 7) * 16;
   const int src = slots ? slots[r] / top_k : r;
-  const bool in = src >= 0 && src < x_rows;
-  float v[4], amax = 0.0f;
-  bool bad = false;
+  const bool in = real && src >= 0 && src < x_rows;
+  const __nv_bfloat16* p = x + src * ldx + c0;
+  uint32_t v[8];  // pairs of bf16
+  if (VEC && in && c0 + 16 <= cols) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 8);
+    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = b * kBlk + lane * 4 + i;
-    v[i] = in && c < cols ? __bfloat162float(x[src * ldx + c]) : 0.0f;
-    amax = fmaxf(amax, fabsf(v[i]));
-    bad |= !(fabsf(v[i]) < INFINITY);
-  }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-  bad = __any_sync(0xFFFFFFFFu, bad);
-  const float s = bad ? NAN : __fdiv_rn(amax, 448.0f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = b * kBlk + lane * 4 + i;
-    if (c < cols)
-      codes[r * ld_codes + c] = bad ? 0x7Fu : s == 0.0f ? 0u : float_to_e4m3(__fdiv_rn(v[i], s));
-  }
-  if (lane == 0) scales[b * ld_scales + r] = s;
-}
-
-// ---------------------------------------------------------------- product
-struct ProductArgs {
-  const uint8_t* a;        // [M, lda]
-  int64_t lda;
-  const float* a_scales;   // [ceil(K/128), ld_as]
-  int64_t ld_as;
-  const uint8_t* w;
-  int64_t ldw;
-  const float* w_scales;
-  const int32_t* offsets;  // [E+1] or null (one expert, all rows)
-  int E, M, N, K;
-  int transpose_w;
-  void* out;
-  int64_t ldo;
-};
-
-__device__ __forceinline__ void expert_rows(const ProductArgs& p, int e, int& r0, int& r1) {
-  r0 = p.offsets ? min(max(p.offsets[e], 0), p.M) : 0;
-  r1 = p.offsets ? min(max(p.offsets[e + 1], r0), p.M) : p.M;
-}
-
-// One thread per output element.
-__device__ __forceinline__ float product_dot(const ProductArgs& p, int e, int m, int n) {
-  const int wr = p.transpose_w ? p.K : p.N, wc = p.transpose_w ? p.N : p.K;
-  const uint8_t* w = p.w + static_cast<int64_t>(e) * wr * p.ldw;
-  const float* ws = p.w_scales + static_cast<int64_t>(e) * blocks_of(wr) * blocks_of(wc);
-  float acc = 0.0f;
-  for (int b = 0; b < blocks_of(p.K); ++b) {
-    float s = 0.0f;
-    for (int k = b * kBlk; k < min(p.K, (b + 1) * kBlk); ++k) {
-      const float av = e4m3_to_float(p.a[m * p.lda + k]);
-      const float wv = e4m3_to_float(p.transpose_w ? w[k * p.ldw + n] : w[n * p.ldw + k]);
-      s = fmaf(av, wv, s);
+    for (int i = 0; i < 8; ++i) {
+      uint32_t lo = 0u, hi = 0u;
+      if (in && c0 + 2 * i < cols) lo = reinterpret_cast<const uint16_t*>(p)[2 * i];
+      if (in && c0 + 2 * i + 1 < cols) hi = reinterpret_cast<const uint16_t*>(p)[2 * i + 1];
+      v[i] = lo | (hi << 16);
     }
-    const float sw = p.transpose_w ? ws[b * blocks_of(wc) + n / kBlk]
-                                   : ws[(n / kBlk) * blocks_of(wc) + b];
-    acc = fmaf(p.a_scales[b * p.ld_as + m] * sw, s, acc);
   }
-  return acc;
-}
-
-__global__ void __launch_bounds__(128) blockscale_matmul_kernel(const ProductArgs p) {
-  int r0, r1;
-  expert_rows(p, blockIdx.z, r0, r1);
-  const int n = blockIdx.x * 128 + threadIdx.x;
-  if (n >= p.N) return;
-  for (int m = r0 + blockIdx.y; m < r1; m += gridDim.y)
-    static_cast<__nv_bfloat16*>(p.out)[m * p.ldo + n] =
-        __float2bfloat16_rn(product_dot(p, blockIdx.z, m, n));
-}
-
-// p.N = 2 I; one block per 128 columns of h.
-__global__ void __launch_bounds__(128)
-    blockscale_swiglu_kernel(const ProductArgs p, float clamp, float* h_scales, int64_t ld_hs) {
-  __shared__ float s_max[4];
-  int r0, r1;
-  expert_rows(p, blockIdx.z, r0, r1);
-  const int I = p.N / 2, n = blockIdx.x * 128 + threadIdx.x;
-  for (int m = r0 + blockIdx.y; m < r1; m += gridDim.y) {
-    const float g = fminf(fmaxf(product_dot(p, blockIdx.z, m, n), -clamp), clamp);
-    const float u = fminf(fmaxf(product_dot(p, blockIdx.z, m, I + n), -clamp), clamp);
-    const float h = g / (1.0f + expf(-g)) * u;
-    float amax = fabsf(h);
-    for (int off = 16; off; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-    const bool bad = __syncthreads_or(!(fabsf(h) < INFINITY));
-    amax = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    const float s = bad ? NAN : __fdiv_rn(amax, 448.0f);
-    static_cast<uint8_t*>(p.out)[m * p.ldo + n] =
-        bad ? 0x7Fu : s == 0.0f ? 0u : float_to_e4m3(__fdiv_rn(h, s));
-    if (threadIdx.x == 0) h_scales[blockIdx.x * ld_hs + m] = s;
-    __syncthreads();
+  float f[16];
+  uint32_t amax = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    amax = max(amax, max(abs_bits(f[2 * i]), abs_bits(f[2 * i + 1])));
   }
+#pragma unroll
+  for (int off = 4; off; off >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+  if (!real) return;
+  const BlockQuant bq(amax);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = bq.code4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  uint8_t* d = codes + r * ld_codes + c0;
+  if (VEC && c0 + 16 <= cols) {
+    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c0 + i < cols) d[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+  }
+  if ((threadIdx.x & 7) == 0) scales[b * ld_scales + r] = bq.scale;
 }
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// The operands of both products.  TMA wants 16-byte aligned bases and row
-// strides; the scales and offsets are read as 32-bit words.
-moe_status check_product(const ProductArgs& p) {
+// ---------------------------------------------------------------- arguments
+struct Product {
+  const void* a;
+  int64_t lda;
+  const float* a_scales;
+  int64_t ld_as;
+  const void* w;
+  int64_t ldw;
+  const float* w_scales;
+  const int32_t* offsets;
+  int E, M, N, K;
+  bool transpose;
+};
+
+// TMA wants 16-byte aligned bases and row strides; scales and offsets are
+// read as 32-bit words.
+moe_status check_weights(const Product& p) {
   if (p.M < 0 || p.N < 1 || p.K < 1 || p.E < 1 || (!p.offsets && p.E != 1))
     return MOE_ERR_INVALID_ARG;
   if (p.E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
-  if (p.lda < p.K || p.ld_as < p.M || p.ldw < (p.transpose_w ? p.N : p.K))
-    return MOE_ERR_INVALID_ARG;
+  if (p.ldw < (p.transpose ? p.N : p.K)) return MOE_ERR_INVALID_ARG;
   if (p.M == 0) return MOE_OK;
-  if (!p.a || !p.a_scales || !p.w || !p.w_scales || !p.out) return MOE_ERR_INVALID_ARG;
-  if (!aligned_to(p.a, 16) || p.lda % 16 || !aligned_to(p.w, 16) || p.ldw % 16 ||
-      !aligned_to(p.a_scales, 4) || !aligned_to(p.w_scales, 4) || !aligned_to(p.offsets, 4))
+  if (!p.w || !p.w_scales || !aligned_to(p.w, 16) || p.ldw % 16 || !aligned_to(p.w_scales, 4) ||
+      !aligned_to(p.offsets, 4))
     return MOE_ERR_INVALID_ARG;
+  // strides of the tensor maps and the item count stay in range
+  const int64_t rows = p.transpose ? p.K : p.N;
+  if (p.ldw >= (int64_t{1} << 39) / rows ||
+      (static_cast<int64_t>(p.E) + p.M / kBlk + 1) * blocks_of(p.N) > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
+
+moe_status check_product(const Product& p) {
+  if (p.lda < p.K || p.ld_as < p.M) return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_weights(p);
+  if (st != MOE_OK || p.M == 0) return st;
+  if (!p.a || !p.a_scales || !aligned_to(p.a, 16) || p.lda % 16 || !aligned_to(p.a_scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  return p.lda >= (int64_t{1} << 39) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base),
+                              dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SM count of the current device, 0 unless it is an sm_103 one (looked up
+// once per device).
+int device_sms() {
+  constexpr int kMaxDevices = 64;
+  static int cached[kMaxDevices] = {};  // 0: not looked up, -1: not usable
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (cached[dev] == 0) {
+    int major = 0, minor = 0, sms = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cached[dev] = major == 10 && minor == 3 && tensor_map_encoder() ? sms : -1;
+  }
+  return std::max(cached[dev], 0);
+}
+
+// early: the product follows the library's own kernel on the stream and may
+// start while it runs (programmatic dependent launch).
+moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, float clamp,
+                       float* h_scales, int64_t ld_hs, bool early, cudaStream_t s) {
+  const int sms = device_sms();
+  if (!sms) return MOE_ERR_NO_DEVICE;
+  BlockscaleMaps maps;
+  const int boxes = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 3 : 4;
+  const cuuint64_t adims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M)};
+  const cuuint64_t astr[1] = {static_cast<cuuint64_t>(p.lda)};
+  for (int i = 0; i < boxes; ++i) {
+    const cuuint32_t box[2] = {128, 16u << i};
+    if (!encode(&maps.a[i], p.a, 2, adims, astr, box)) return MOE_ERR_CUDA;
+  }
+  const int wrows = p.transpose ? p.K : p.N, wcols = p.transpose ? p.N : p.K;
+  const cuuint64_t wdims[3] = {static_cast<cuuint64_t>(wcols), static_cast<cuuint64_t>(wrows),
+                               static_cast<cuuint64_t>(p.E)};
+  const cuuint64_t wstr[2] = {static_cast<cuuint64_t>(p.ldw),
+                              static_cast<cuuint64_t>(p.ldw) * wrows};
+  const cuuint32_t wbox[3] = {128, 128, 1};
+  if (!encode(&maps.w, p.w, 3, wdims, wstr, wbox)) return MOE_ERR_CUDA;
+  BlockscaleArgs a{};
+  a.a_scales = p.a_scales;
+  a.ld_as = p.ld_as;
+  a.w_scales = p.w_scales;
+  a.w_blocks = static_cast<int64_t>(blocks_of(p.N)) * blocks_of(p.K);
+  a.w_stride_n = p.transpose ? 1 : blocks_of(p.K);
+  a.w_stride_k = p.transpose ? blocks_of(p.N) : 1;
+  a.offsets = p.offsets;
+  a.E = p.E;
+  a.M = p.M;
+  a.N = p.N;
+  a.K = p.K;
+  a.out = out;
+  a.ldo = ldo;
+  a.out_vec = aligned_to(out, 16) && ldo % 8 == 0;
+  a.clamp = clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY;
+  a.h_scales = h_scales;
+  a.ld_hs = ld_hs;
+  a.early = early;
+  return launch_blockscale(maps, a, swiglu, p.transpose, early, sms, s) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* slots, int top_k,
+                        int rows, int cols, void* codes, int64_t ld_codes, float* scales,
+                        int64_t ld_scales, cudaStream_t s) {
+  if (rows < 0 || cols < 1 || x_rows < 0 || ldx < cols || ld_codes < cols || ld_scales < rows)
+    return MOE_ERR_INVALID_ARG;
+  if (slots ? top_k < 1 : x_rows < rows) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if ((!x && x_rows > 0) || !codes || !scales || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
+      !aligned_to(scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t grid = (static_cast<int64_t>(rows) * blocks_of(cols) + 31) / 32;
+  if (grid > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const bool vec = aligned_to(x, 16) && ldx % 8 == 0 && aligned_to(codes, 16) && ld_codes % 16 == 0;
+  const cudaError_t e = launch_pdl(
+      false, vec ? blockscale_quantize_kernel<true> : blockscale_quantize_kernel<false>,
+      dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(x),
+      ldx, x_rows, slots, top_k, rows, cols, static_cast<uint8_t*>(codes), ld_codes, scales,
+      ld_scales);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Quantised activations in a workspace: codes in rows of a multiple of 16
+// bytes, then the scales.
+int64_t padded(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+int64_t quantized_bytes(int64_t rows, int64_t cols) {
+  return padded(rows * padded(cols, 16), 256) + padded(rows * ((cols + 127) / 128) * 4, 256);
+}
+struct Quantized {
+  uint8_t* codes;
+  int64_t ld;
+  float* scales;
+  int64_t ld_scales;
+  Quantized(void* ws, int64_t rows, int64_t cols)
+      : codes(static_cast<uint8_t*>(ws)), ld(padded(cols, 16)),
+        scales(reinterpret_cast<float*>(codes + padded(rows * ld, 256))), ld_scales(rows) {}
+};
 
 }  // namespace
 
@@ -167,37 +246,22 @@ extern "C" {
 moe_status moe_blockscale_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* slots,
                                    int top_k, int rows, int cols, void* codes, int64_t ld_codes,
                                    float* scales, int64_t ld_scales, void* stream) {
-  if (rows < 0 || cols < 1 || x_rows < 0 || ldx < cols || ld_codes < cols || ld_scales < rows)
-    return MOE_ERR_INVALID_ARG;
-  if (slots ? top_k < 1 : x_rows < rows) return MOE_ERR_INVALID_ARG;
-  if (rows == 0) return MOE_OK;
-  if ((!x && x_rows > 0) || !codes || !scales || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
-      !aligned_to(scales, 4))
-    return MOE_ERR_INVALID_ARG;
-  const int64_t grid = (static_cast<int64_t>(rows) * blocks_of(cols) + 7) / 8;
-  if (grid > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  const cudaError_t e = launch_pdl(
-      false, blockscale_quantize_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
-      static_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(x), ldx, x_rows, slots,
-      top_k, rows, cols, static_cast<uint8_t*>(codes), ld_codes, scales, ld_scales);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return run_quantize(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales, ld_scales,
+                      static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_blockscale_matmul(const void* a, int64_t lda, const float* a_scales, int64_t ld_as,
                                  const void* w, int64_t ldw, const float* w_scales,
                                  const int32_t* offsets, int E, int M, int N, int K,
                                  int transpose_w, void* out, int64_t ldo, void* stream) {
-  const ProductArgs p{static_cast<const uint8_t*>(a), lda, a_scales, ld_as,
-                      static_cast<const uint8_t*>(w), ldw, w_scales, offsets, E, M, N, K,
-                      transpose_w != 0, out, ldo};
+  const Product p{a, lda, a_scales, ld_as, w, ldw, w_scales, offsets, E, M, N, K, transpose_w != 0};
   const moe_status st = check_product(p);
   if (st != MOE_OK) return st;
-  if (ldo < N || !aligned_to(out, 2)) return MOE_ERR_INVALID_ARG;
+  if (ldo < N) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  const cudaError_t e =
-      launch_pdl(false, blockscale_matmul_kernel, dim3((N + 127) / 128, std::min(M, 256), E),
-                 dim3(128), 0, static_cast<cudaStream_t>(stream), p);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (!out || !aligned_to(out, 2)) return MOE_ERR_INVALID_ARG;
+  return run_product(p, false, out, ldo, 0.0f, nullptr, 0, false,
+                     static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_blockscale_swiglu(const void* a, int64_t lda, const float* a_scales, int64_t ld_as,
@@ -207,21 +271,87 @@ moe_status moe_blockscale_swiglu(const void* a, int64_t lda, const float* a_scal
                                  int64_t ld_hs, void* stream) {
   if (I < 1 || I > (1 << 29)) return MOE_ERR_INVALID_ARG;
   if (I % kBlk) return MOE_ERR_UNSUPPORTED;
-  const ProductArgs p{static_cast<const uint8_t*>(a), lda, a_scales, ld_as,
-                      static_cast<const uint8_t*>(w13), ldw, w13_scales, offsets, E, M, 2 * I, K,
-                      0, h, ldh};
+  const Product p{a, lda, a_scales, ld_as, w13, ldw, w13_scales, offsets, E, M, 2 * I, K, false};
   const moe_status st = check_product(p);
   if (st != MOE_OK) return st;
   if (ldh < I || ld_hs < M) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  if (!h_scales || !aligned_to(h_scales, 4) || !aligned_to(h, 16) || ldh % 16)
+  if (!h || !h_scales || !aligned_to(h_scales, 4) || !aligned_to(h, 16) || ldh % 16)
     return MOE_ERR_INVALID_ARG;
-  const float clamp =
-      clamp_limit > 0.0f && std::isfinite(clamp_limit) ? clamp_limit : INFINITY;
-  const cudaError_t e =
-      launch_pdl(false, blockscale_swiglu_kernel, dim3(I / 128, std::min(M, 256), E), dim3(128), 0,
-                 static_cast<cudaStream_t>(stream), p, clamp, h_scales, ld_hs);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return run_product(p, true, h, ldh, clamp_limit, h_scales, ld_hs, false,
+                     static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_blockscale_workspace(int rows, int cols, int inter) {
+  if (rows < 0 || cols < 1 || inter < 0) return 0;
+  return static_cast<size_t>(quantized_bytes(rows, cols) +
+                             (inter ? quantized_bytes(rows, inter) : 0));
+}
+
+moe_status moe_blockscale_linear(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                 const float* w_scales, int M, int N, int K, int transpose_w,
+                                 void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  Product p{nullptr, 0, nullptr, 0, w, ldw, w_scales, nullptr, 1, M, N, K, transpose_w != 0};
+  const moe_status st = check_weights(p);
+  if (st != MOE_OK) return st;
+  if (ldx < K || ldo < N) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x || !out || !workspace || !aligned_to(x, 2) || !aligned_to(out, 2) ||
+      !aligned_to(workspace, 16) || workspace_bytes < moe_blockscale_workspace(M, K, 0))
+    return MOE_ERR_INVALID_ARG;
+  if (!device_sms()) return MOE_ERR_NO_DEVICE;
+  const Quantized q(workspace, M, K);
+  p.a = q.codes;
+  p.lda = q.ld;
+  p.a_scales = q.scales;
+  p.ld_as = q.ld_scales;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const moe_status sq =
+      run_quantize(x, ldx, M, nullptr, 1, M, K, q.codes, q.ld, q.scales, q.ld_scales, s);
+  if (sq != MOE_OK) return sq;
+  return run_product(p, false, out, ldo, 0.0f, nullptr, 0, true, s);
+}
+
+moe_status moe_blockscale_experts(const void* x, int64_t ldx, int T, const int32_t* slots,
+                                  int top_k, int rows, const int32_t* offsets, int E,
+                                  const void* w13, const float* w13_scales, const void* w2,
+                                  const float* w2_scales, int H, int I, float clamp_limit,
+                                  void* out, int64_t ldo, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (I < 1 || I > (1 << 29) || T < 0 || top_k < 1 || !offsets) return MOE_ERR_INVALID_ARG;
+  if (I % kBlk || H % 16) return MOE_ERR_UNSUPPORTED;
+  Product p1{nullptr, 0, nullptr, 0, w13, H, w13_scales, offsets, E, rows, 2 * I, H, false};
+  Product p2{nullptr, 0, nullptr, 0, w2, I, w2_scales, offsets, E, rows, H, I, false};
+  moe_status st = check_weights(p1);
+  if (st == MOE_OK) st = check_weights(p2);
+  if (st != MOE_OK) return st;
+  if (ldx < H || ldo < H) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if ((!x && T > 0) || !slots || !out || !workspace || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
+      !aligned_to(out, 2) || !aligned_to(workspace, 16) ||
+      workspace_bytes < moe_blockscale_workspace(rows, H, I))
+    return MOE_ERR_INVALID_ARG;
+  if (!device_sms()) return MOE_ERR_NO_DEVICE;
+  const Quantized q(workspace, rows, H);
+  const Quantized h(static_cast<uint8_t*>(workspace) + quantized_bytes(rows, H), rows, I);
+  p1.a = q.codes, p1.lda = q.ld, p1.a_scales = q.scales, p1.ld_as = q.ld_scales;
+  p2.a = h.codes, p2.lda = h.ld, p2.a_scales = h.scales, p2.ld_as = h.ld_scales;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = run_quantize(x, ldx, T, slots, top_k, rows, H, q.codes, q.ld, q.scales, q.ld_scales, s);
+  if (st == MOE_OK)
+    st = run_product(p1, true, h.codes, h.ld, clamp_limit, h.scales, h.ld_scales, true, s);
+  if (st == MOE_OK) st = run_product(p2, false, out, ldo, 0.0f, nullptr, 0, true, s);
+  return st;
+}
+
+moe_status moe_blockscale_status(void) {
+  int v = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess || blockscale_status(&v) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return v ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
 
 }  // extern "C"

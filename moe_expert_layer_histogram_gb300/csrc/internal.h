@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 namespace moe {
 
@@ -125,6 +126,9 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 #endif
 
+// The driver's tensor-map encoder (null if there is none), looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 cudaError_t gemm_prepare(int fmt);  // raise the dynamic shared-memory limit
 // max_rows: upper bound on the rows of any expert in this launch (<= T);
 // selects the activation-tile height of the shared-memory stages.
@@ -181,6 +185,40 @@ cudaError_t decode_prepare(int fmt);
 cudaError_t launch_decode(int fmt, int epi1, const GemmMaps& maps1, const GemmArgs& args1,
                           const GemmMaps& maps2, const GemmArgs& args2, const DecodeArgs& d,
                           int grid, cudaStream_t s);
+
+// Block-scaled FP8 products (blockscale_gemm.cu).
+struct BlockscaleMaps {
+  CUtensorMap a[4];  // codes [M, K], boxes of 16/32/64/128 rows x 128 columns
+  CUtensorMap w;     // codes [E, N, K] (transposed: [E, K, N]), boxes of 128 x 128
+};
+
+struct BlockscaleArgs {
+  const float* a_scales;   // [ceil(K/128), ld_as]
+  int64_t ld_as;
+  const float* w_scales;   // expert e, 128-block nb of N, block kb of K at
+  int64_t w_blocks;        // e * w_blocks + nb * w_stride_n + kb * w_stride_k
+  int64_t w_stride_n, w_stride_k;
+  const int32_t* offsets;  // [E+1] or null (one expert of all M rows)
+  int E, M, N, K;
+  void* out;               // bf16 [M, ldo], or (SwiGLU) codes [M, ldo]
+  int64_t ldo;
+  int out_vec;             // bf16 rows start on 16-byte boundaries
+  float clamp;             // SwiGLU (+inf: none)
+  float* h_scales;         // SwiGLU [N/256, ld_hs]
+  int64_t ld_hs;
+  int early;               // the kernel before this one is the library's own and writes
+                           // neither weights nor offsets
+  // set by launch_blockscale
+  int a_rows, tiles, stages, split;
+};
+
+// swiglu: N = 2 I, gate and up rows; transpose: weights stored [E, K, N].
+// pdl: programmatic dependent launch.
+cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs args, bool swiglu,
+                              bool transpose, bool pdl, int sms, cudaStream_t s);
+// The first status code its kernels recorded on the current device since the
+// last call (0: none).
+cudaError_t blockscale_status(int* code);
 
 // Routing, permutation + activation quantisation, combine.
 cudaError_t launch_route(const float* logits, int T, int E, int K, int32_t* ids, float* w,
