@@ -17,9 +17,11 @@
 // chunk, so that CTAs running together share a weight tile in L2.  Warp 0
 // (one thread) fills a ring of stages by TMA: 128 columns of the chunk's
 // rows (box height 16 / 32 / 64 / 128, so short chunks pull no padding) and
-// of the NT weight rows.  Warp 1 (one thread) issues the MMAs.  Warps 4-11
-// are the epilogue: warp w reads TMEM lanes 32 (w % 4).. and half of the
-// tile's columns, so a thread owns one row and NT / 2 columns.
+// of the NT weight rows.  Warp 1 (one thread) issues the MMAs.  Warp 2 runs
+// ahead through the same blocks and leaves every row's scale product in a
+// ring in shared memory.  Warps 4-11 are the epilogue: warp w reads TMEM
+// lanes 32 (w % 4).. and half of the tile's columns, so a thread owns one row
+// and NT / 2 columns.
 //
 // With the weights transposed (input gradient) the reduction runs along the
 // stored rows: the tile is 128 rows of 128 bytes of output columns, an
@@ -43,13 +45,14 @@ namespace {
 
 constexpr int kBsThreads = 384;
 constexpr int kBsEpiWarp0 = 4;
-constexpr int kBsLeanRegs = 80;
-constexpr int kBsEpiRegs = 208;
-// registers per thread at launch: the lean warpgroup gives up 88 of 168, the
-// two epilogue warpgroups claim 40 each
+constexpr int kBsLeanRegs = 72;
+constexpr int kBsEpiRegs = 216;
+// registers per thread at launch: the lean warpgroup gives up 96 of 168, the
+// two epilogue warpgroups claim 48 each
 constexpr int kBsLaunchRegs = 168;
 static_assert(kBsLeanRegs + 2 * kBsEpiRegs <= 3 * kBsLaunchRegs, "register split");
 constexpr int kBsMaxStages = 8;
+constexpr int kBsScaleSlots = 8;  // blocks the scale warp may run ahead
 constexpr int kBsSmemLimit = 232448;
 constexpr int kBsSplitRows = 32;  // largest chunk whose reduction is split
 
@@ -244,12 +247,15 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   const int stages = p.stages;
   float* s_part = reinterpret_cast<float*>(smem + stages * stage_bytes);  // SPLIT: [32][NT + 4]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_part);                 // SWIGLU: [2][128]
-  uint64_t* full = reinterpret_cast<uint64_t*>(
-      s_part + (SPLIT ? kBsSplitRows * (NT + 4) : SWIGLU ? 256 : 0));
+  constexpr int kSets = NT / 128;  // weight blocks of the tile: scale sets of a slot
+  float* s_scale = s_part + (SPLIT ? kBsSplitRows * (NT + 4) : SWIGLU ? 256 : 0);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + kBsScaleSlots * kSets * 128);
   uint64_t* empty = full + kBsMaxStages;
   uint64_t* tfull = empty + kBsMaxStages;
   uint64_t* tempty = tfull + 4;
-  uint64_t* drained = tempty + 4;
+  uint64_t* sfull = tempty + 4;
+  uint64_t* sempty = sfull + kBsScaleSlots;
+  uint64_t* drained = sempty + kBsScaleSlots;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_tab = reinterpret_cast<int*>(tmem_holder + 2);
@@ -265,6 +271,10 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 8);
+    }
+    for (int i = 0; i < kBsScaleSlots; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sempty[i], 8);
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
@@ -387,6 +397,63 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       tc_commit(drained);
       mbar_wait(drained, 0, nullptr);
       if (!ok) report_status(&g_blockscale_status, kStatusTimeout);
+    } else if (warp == 2) {
+      // ------------------------------------------------ scales
+      // Lane l takes rows l, l + 32, ..; four blocks' loads are in flight at
+      // a time, and the ring lets them run ahead of the tensor pipe.
+      constexpr int kAhead = 4;
+      if (p.early) pdl_wait();
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int item = first; item < total && ok; item += step) {
+        const BsItem it = map_bs_item(tab, p.E, p.tiles, item);
+        const float* sa = p.a_scales + it.row0 + lane;
+        // SWIGLU: the gate's block and the up half's; else the tile's blocks
+        // (one past N has no scale of its own and is not stored)
+        const float* sw[kSets];
+#pragma unroll
+        for (int h = 0; h < kSets; ++h) {
+          const int nb = SWIGLU ? it.tile + h * (p.N / 256)
+                                : min(it.tile * kSets + h, (p.N + 127) / 128 - 1);
+          sw[h] = p.w_scales + it.e * p.w_blocks + nb * p.w_stride_n;
+        }
+        for (int kb = kb0; kb < kb1 && ok; kb += kAhead) {
+          float a[kAhead][4], w[kAhead][kSets];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              a[i][j] = kb + i < kb1 && lane + 32 * j < it.rows
+                            ? __ldg(sa + (kb + i) * p.ld_as + 32 * j)
+                            : 0.0f;
+#pragma unroll
+            for (int h = 0; h < kSets; ++h)
+              w[i][h] = kb + i < kb1 ? __ldg(sw[h] + (kb + i) * p.w_stride_k) : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            if (kb + i >= kb1) break;
+            const bool free = mbar_wait(&sempty[slot], phase ^ 1u, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, free)) {
+              ok = false;
+              break;
+            }
+            float* d = s_scale + slot * kSets * 128 + lane;
+#pragma unroll
+            for (int h = 0; h < kSets; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) d[h * 128 + 32 * j] = a[i][j] * w[i][h];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfull[slot]);
+            if (++slot == kBsScaleSlots) {
+              slot = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+      }
+      if (!ok && lane == 0) report_status(&g_blockscale_status, kStatusTimeout);
     }
     if constexpr (SPLIT) {
       // the epilogue warps' two barriers take every thread of the cluster;
@@ -397,65 +464,63 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     }
   } else {
     regs_claim<kBsEpiRegs>();
-    if (p.early) pdl_wait();
     // ------------------------------------------------ epilogue warps
     const int q = warp & 3, g = (warp - kBsEpiWarp0) >> 2;
-    int buf = 0;
-    uint32_t bphase = 0;
+    int buf = 0, slot = 0;
+    uint32_t bphase = 0, sphase = 0;
     bool ok = true;
     for (int item = first; item < total && ok; item += step) {
       const BsItem it = map_bs_item(tab, p.E, p.tiles, item);
       const int r = q * 32 + lane;
       const bool active = q * 32 < it.rows, live = r < it.rows;
       const int64_t row = it.row0 + (live ? r : 0);
-      // scales of block kb: the row's, and those of the thread's column
-      // groups (SWIGLU: 64 gate and 64 up columns, else kCols columns that lie
-      // in one 128-column block)
-      const float* sa = p.a_scales + row;
-      // (a half tile past N has no block of its own and is not stored)
-      const int nb = SWIGLU ? it.tile
-                            : min((it.tile * NT + g * kCols) / 128, (p.N + 127) / 128 - 1);
-      const float* sw = p.w_scales + static_cast<int64_t>(it.e) * p.w_blocks +
-                        static_cast<int64_t>(nb) * p.w_stride_n;
-      const int64_t sw_up = SWIGLU ? static_cast<int64_t>(p.N / 256) * p.w_stride_n : 0;
       uint64_t acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
       for (int kb = kb0; kb < kb1; ++kb) {
-        float s0 = 0.0f, s1 = 0.0f;
-        if (active) {
-          const float a = __ldg(sa + kb * p.ld_as);
-          s0 = a * __ldg(sw + kb * p.w_stride_k);
-          if (SWIGLU) s1 = a * __ldg(sw + sw_up + kb * p.w_stride_k);
-        }
-        const bool landed = mbar_wait(&tfull[buf], bphase, abort_flag);
+        const bool landed = mbar_wait(&sfull[slot], sphase, abort_flag) &&
+                            mbar_wait(&tfull[buf], bphase, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, landed)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (active) {
-          const uint64_t p0 = pack2(s0), p1 = SWIGLU ? pack2(s1) : p0;
+          const float* ss = s_scale + slot * kSets * 128 + r;
+          const uint64_t p0 = pack2(ss[SWIGLU || kSets == 1 ? 0 : g * 128]),
+                         p1 = SWIGLU ? pack2(ss[128]) : p0;
           const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT;
+          // SWIGLU: columns 64 g.. of the gate, then of the up half
+          auto col = [&](int c) {
+            return SWIGLU ? (c < 2 ? 0 : 128) + g * 64 + (c & 1) * 32 : g * kCols + c * 32;
+          };
+          // the next 32 columns are read while these are added
+          uint32_t v[2][32];
+          tmem_ld32(t0 + col(0), v[0]);
 #pragma unroll
           for (int c = 0; c < kCols / 32; ++c) {
-            // SWIGLU: columns 64 g.. of the gate, then of the up half
-            const int col = SWIGLU ? (c < 2 ? 0 : 128) + g * 64 + (c & 1) * 32 : g * kCols + c * 32;
-            uint32_t v[32];
-            tmem_ld32(t0 + col, v);
             tmem_ld_wait();
-            reg_fence32(v);
+            reg_fence32(v[c & 1]);
+            if (c + 1 < kCols / 32) tmem_ld32(t0 + col(c + 1), v[(c + 1) & 1]);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              fma2(acc[c * 16 + i], v[2 * i], v[2 * i + 1], SWIGLU && c >= 2 ? p1 : p0);
+              fma2(acc[c * 16 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1],
+                   SWIGLU && c >= 2 ? p1 : p0);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (lane == 0) {
+          mbar_arrive(&tempty[buf]);
+          mbar_arrive(&sempty[slot]);
+        }
         if (++buf == kBufs) {
           buf = 0;
           bphase ^= 1u;
+        }
+        if (++slot == kBsScaleSlots) {
+          slot = 0;
+          sphase ^= 1u;
         }
       }
       if (!ok) break;
@@ -572,8 +637,8 @@ using Kernel = void (*)(BlockscaleMaps, BlockscaleArgs);
 
 template <int NT, bool SWIGLU, bool TRANS, bool SPLIT>
 constexpr int extra_smem() {
-  return (SPLIT ? kBsSplitRows * (NT + 4) * 4 : SWIGLU ? 1024 : 0) +
-         (2 * kBsMaxStages + 9) * 8 + 8;
+  return (SPLIT ? kBsSplitRows * (NT + 4) * 4 : SWIGLU ? 1024 : 0) + kBsScaleSlots * NT * 4 +
+         (2 * kBsMaxStages + 2 * kBsScaleSlots + 9) * 8 + 8;
 }
 
 template <int NT, bool SWIGLU, bool TRANS, bool SPLIT>
