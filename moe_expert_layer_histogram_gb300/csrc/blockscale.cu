@@ -172,7 +172,7 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
                                static_cast<cuuint64_t>(p.E)};
   const cuuint64_t wstr[2] = {static_cast<cuuint64_t>(p.ldw),
                               static_cast<cuuint64_t>(p.ldw) * wrows};
-  const cuuint32_t wbox[3] = {128, 128, 1};
+  const cuuint32_t wbox[3] = {128, swiglu ? 64u : 128u, 1};
   if (!encode(&maps.w, p.w, 3, wdims, wstr, wbox)) return MOE_ERR_CUDA;
   BlockscaleArgs a{};
   a.a_scales = p.a_scales;

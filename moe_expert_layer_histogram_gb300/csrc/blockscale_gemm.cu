@@ -8,20 +8,33 @@
 // e4m3 product therefore goes into a TMEM buffer of its own (four MMAs of
 // K = 32, the first one overwriting), and the epilogue warps add it, times
 // sa sw, to fp32 accumulators that stay in registers for the whole item: one
-// scaled fused multiply-add per output and block, two at a time
-// (fma.f32x2).  The buffers are double (256 columns) or fourfold (128), so
-// the tensor pipe works on the next block meanwhile.
+// fused multiply-add per output and block.  (Plain ones: the packed pair
+// instruction took 333 cycles per 128 x 256 block where these take 263.)
+//
+// A buffer's turn is an MMA, the hand-off to the epilogue, its reads and the
+// hand-off back.  TMEM holds two buffers of 256 columns (or four of 128), and
+// the epilogue hands a buffer back as soon as it has read it.  The issuing
+// warp stays whole and elects a thread for each group of MMAs: the same code
+// under `lane == 0` spent 631 cycles on a block (two waits, four MMAs, two
+// commits), longer than the tensor pipe's 512.
 //
 // Structure: one persistent CTA per SM walks the items (expert, tile of NT
 // weight rows, chunk of at most 128 rows), expert-major, then tile, then
 // chunk, so that CTAs running together share a weight tile in L2.  Warp 0
 // (one thread) fills a ring of stages by TMA: 128 columns of the chunk's
 // rows (box height 16 / 32 / 64 / 128, so short chunks pull no padding) and
-// of the NT weight rows.  Warp 1 (one thread) issues the MMAs.  Warp 2 runs
-// ahead through the same blocks and leaves every row's scale product in a
-// ring in shared memory.  Warps 4-11 are the epilogue: warp w reads TMEM
-// lanes 32 (w % 4).. and half of the tile's columns, so a thread owns one row
-// and NT / 2 columns.
+// of the NT weight rows.  Warp 1 issues the MMAs.  Warp 2 runs ahead through
+// the same blocks and leaves every row's scale product in a ring in shared
+// memory.  Warps 4-11 are the epilogue: warp w reads TMEM lanes
+// 32 (w % 4).. and half of the tile's columns, so a thread owns one row and
+// NT / 2 columns.
+//
+// Chunks of full experts come in pairs (PAIR): a cluster of two CTAs shares
+// one MMA of 256 rows x 256 columns (cta_group::2), each CTA loading its own
+// 128 rows and half of the weight tile.  A single CTA's 128 x 256 block moves
+// 48 KB into shared memory and reads 48 KB of operands back out, 768 cycles
+// at 128 bytes a cycle against 512 cycles of MMA; in a pair it is 32 KB each
+// way, and both take 512.
 //
 // With the weights transposed (input gradient) the reduction runs along the
 // stored rows: the tile is 128 rows of 128 bytes of output columns, an
@@ -52,7 +65,8 @@ constexpr int kBsEpiRegs = 216;
 constexpr int kBsLaunchRegs = 168;
 static_assert(kBsLeanRegs + 2 * kBsEpiRegs <= 3 * kBsLaunchRegs, "register split");
 constexpr int kBsMaxStages = 8;
-constexpr int kBsScaleSlots = 8;  // blocks the scale warp may run ahead
+constexpr int kBsAhead = 4;       // blocks whose scales are passed on together
+constexpr int kBsGroups = 2;      // such groups in the scale ring
 constexpr int kBsSmemLimit = 232448;
 constexpr int kBsSplitRows = 32;  // largest chunk whose reduction is split
 
@@ -64,22 +78,84 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool transpose_b
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// PAIR: issued by rank 0 for both CTAs of the cluster (A rows and B rows half
+// from each), else for this CTA alone.
+template <bool PAIR>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
 }
 
-// MN-major operand staged by TMA with the 128-byte swizzle: rows of 128
-// bytes along M/N, one per reduction index, 8-row atoms of 1024 bytes
-// stacked along the reduction (stride 1024); the next 128 columns of M/N
-// follow `chunk` bytes later.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t chunk) {
-  return desc_sw128(saddr) | (static_cast<uint64_t>((chunk >> 4) & 0x3FFFu) << 16);
+// (An MN-major operand tile, staged by TMA with the 128-byte swizzle, has one
+// row of 128 bytes per reduction index and 8-row atoms of 1024 bytes stacked
+// along the reduction: desc_sw128 describes it too, with the transpose bit of
+// the instruction descriptor set.)
+
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait by a whole warp, with its branches on votes: the lanes stay
+// together without the compiler's reconvergence points, which made a wait on
+// a phase that had completed cost 62 cycles instead of 36 in eight warps (and
+// 176 when one lane waited for the others).
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort) {
+  uint32_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 127u) == 0) {
+      // (the low half of the timer: its differences are good for 4 s)
+      uint32_t now;
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+      if (i == 0) t0 = now;
+      if (__any_sync(0xFFFFFFFFu, *abort != 0 || now - t0 > static_cast<uint32_t>(kWaitTimeoutNs))) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// One thread of a whole warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int32_t x, int32_t y,
+                                                 int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -116,23 +192,15 @@ __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
                    "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
-// acc += {lo, hi} * {s, s}, two fp32 fused multiply-adds.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
-  uint64_t p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(p), "l"(s2));
-}
-
-__device__ __forceinline__ uint64_t pack2(float s) {
-  uint64_t p;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(p) : "f"(s));
-  return p;
-}
-
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
+// Arrive, where `on`, on a barrier at a shared::cluster address (an address
+// of this CTA's own shared memory is one; see also mbar_arrive_cluster): a
+// predicated instruction, no branch.
+__device__ __forceinline__ void mbar_arrive_if(bool on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(static_cast<uint32_t>(on))
+      : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
@@ -148,15 +216,19 @@ struct BsItem {
   int e, tile, row0, rows;
 };
 
-// Chunk table in shared memory: off[0..E] exclusive chunk counts, start[e]
-// and the row end of every expert, clamped into [0, M].
+// Chunk table in shared memory: exclusive counts of the items' chunk groups
+// (`group` chunks of 128 rows each), and the first and last row of every
+// expert, clamped into [0, M].
 struct BsTable {
   int* chunk_off;  // [E + 1]
   int* start;      // [E]
   int* end;        // [E]
 };
 
-__device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int E, int tiles, int item) {
+// group: chunks per item (a pair's two; the second may have no rows), rank:
+// the chunk of the item that is wanted.
+__device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int E, int tiles, int item,
+                                              int group, int rank) {
   int lo = 0, hi = E;  // chunk_off[lo] * tiles <= item < chunk_off[hi] * tiles
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -168,13 +240,15 @@ __device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int E, int tiles
   BsItem it;
   it.e = lo;
   it.tile = local / chunks;
-  it.row0 = t.start[lo] + (local % chunks) * 128;
+  it.row0 = t.start[lo] + (local % chunks * group + rank) * 128;
   it.rows = min(128, t.end[lo] - it.row0);
   return it;
 }
 
 // One warp fills the table: lane l takes kMaxExperts / 32 consecutive experts.
-__device__ __forceinline__ void fill_bs_table(const BlockscaleArgs& p, const BsTable& t, int lane) {
+__device__ __forceinline__ void fill_bs_table(const BlockscaleArgs& p, const BsTable& t, int group,
+                                              int lane) {
+  const int per_item = 128 * group;
   constexpr int kPer = kMaxExperts / 32;
   int chunks = 0;
   for (int i = 0; i < kPer; ++i) {
@@ -184,7 +258,7 @@ __device__ __forceinline__ void fill_bs_table(const BlockscaleArgs& p, const BsT
     const int r1 = p.offsets ? min(max(p.offsets[e + 1], r0), p.M) : p.M;
     t.start[e] = r0;
     t.end[e] = r1;
-    chunks += (r1 - r0 + 127) / 128;
+    chunks += (r1 - r0 + per_item - 1) / per_item;
   }
   int inc = chunks;
 #pragma unroll
@@ -197,20 +271,30 @@ __device__ __forceinline__ void fill_bs_table(const BlockscaleArgs& p, const BsT
     const int e = lane * kPer + i;
     if (e >= p.E) break;
     t.chunk_off[e] = run;
-    run += (t.end[e] - t.start[e] + 127) / 128;
+    run += (t.end[e] - t.start[e] + per_item - 1) / per_item;
     if (e == p.E - 1) t.chunk_off[p.E] = run;
+  }
+}
+
+// acc += s v for 32 columns.
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float s) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 t = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+                                make_float2(s, s), make_float2(acc[i], acc[i + 1]));
+    acc[i] = t.x;
+    acc[i + 1] = t.y;
   }
 }
 
 // bf16 of 32 consecutive fp32 columns n0 .. n0 + 31 of one row (n0 + 32 may
 // pass N).
 __device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row, int n0, int N, bool vec,
-                                              const uint64_t* acc) {
+                                              const float* acc) {
   uint32_t v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float2 f = unpack2(acc[i]);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
     v[i] = reinterpret_cast<const uint32_t&>(b);
   }
   if (vec && n0 + 32 <= N) {
@@ -234,28 +318,33 @@ __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
 // NT: weight rows per item.  SWIGLU: the tile is 128 gate rows and the 128
 // up rows of the same columns (NT = 256).  SPLIT: the grid is clusters of
 // args.split CTAs, one item each (one expert, at most kBsSplitRows rows).
-template <int NT, bool SWIGLU, bool TRANS, bool SPLIT>
+// PAIR: the grid is clusters of two CTAs that share each item (NT = 256).
+template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR>
 __global__ void __launch_bounds__(kBsThreads, 1)
     blockscale_gemm_kernel(const __grid_constant__ BlockscaleMaps maps,
                            const __grid_constant__ BlockscaleArgs p) {
-  constexpr int kBufs = 512 / NT;  // TMEM accumulators of one block each
-  constexpr int kCols = NT / 2;    // columns per epilogue thread
+  constexpr int kHalves = NT / 128;  // 128-column halves of the tile
+  constexpr int kBufs = 4;           // TMEM buffers of 128 columns, used in turn
+  constexpr int kSets = kHalves;     // weight blocks of the tile: its scale sets
+  constexpr int kCols = NT / 2;      // columns per epilogue thread
+  constexpr int kGroup = PAIR ? 2 : 1;
+  constexpr int kBBytes = NT / kGroup * 128;  // this CTA's part of the weight tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int a_bytes = p.a_rows * 128;
-  const int stage_bytes = a_bytes + NT * 128;
+  const int stage_bytes = a_bytes + kBBytes;
   const int stages = p.stages;
   float* s_part = reinterpret_cast<float*>(smem + stages * stage_bytes);  // SPLIT: [32][NT + 4]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_part);                 // SWIGLU: [2][128]
-  constexpr int kSets = NT / 128;  // weight blocks of the tile: scale sets of a slot
+  // [group][block][weight block of the tile][row]
   float* s_scale = s_part + (SPLIT ? kBsSplitRows * (NT + 4) : SWIGLU ? 256 : 0);
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + kBsScaleSlots * kSets * 128);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + kBsGroups * kBsAhead * kSets * 128);
   uint64_t* empty = full + kBsMaxStages;
   uint64_t* tfull = empty + kBsMaxStages;
   uint64_t* tempty = tfull + 4;
   uint64_t* sfull = tempty + 4;
-  uint64_t* sempty = sfull + kBsScaleSlots;
-  uint64_t* drained = sempty + kBsScaleSlots;
+  uint64_t* sempty = sfull + kBsGroups;
+  uint64_t* drained = sempty + kBsGroups;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_tab = reinterpret_cast<int*>(tmem_holder + 2);
@@ -266,40 +355,51 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], kHalves);
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);
+      // the epilogue warps that read it (of both CTAs)
+      mbar_init(&tempty[b], 8 / kHalves * kGroup);
     }
-    for (int i = 0; i < kBsScaleSlots; ++i) {
+    for (int i = 0; i < kBsGroups; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&sempty[i], 8);
     }
-    mbar_init(drained, 1);
+    mbar_init(drained, kHalves);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_holder, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, 512);
+      tmem_relinquish();
+    }
   }
   // (early: the only kernel this one may overlap is the library's own before
   // it, which writes the activations and their scales but no offsets or
   // weights)
   if (!p.early) pdl_wait();
-  if (warp == 2) fill_bs_table(p, tab, lane);
+  if (warp == 2) fill_bs_table(p, tab, kGroup, lane);
   tc_fence_before();
   __syncthreads();
+  // both CTAs' barriers are initialised before either arrives on the other's
+  if constexpr (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int kb_all = (p.K + 127) / 128;
-  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int rank = SPLIT || PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int kb0 = SPLIT ? kb_all * rank / p.split : 0;
   const int kb1 = SPLIT ? kb_all * (rank + 1) / p.split : kb_all;
-  const int first = SPLIT ? blockIdx.x / p.split : blockIdx.x;
-  const int step = SPLIT ? gridDim.x / p.split : gridDim.x;
+  const int first = blockIdx.x / (SPLIT ? p.split : kGroup);
+  const int step = gridDim.x / (SPLIT ? p.split : kGroup);
   const int total = tab.chunk_off[p.E] * p.tiles;
+  auto map_item = [&](int item) {
+    return map_bs_item(tab, p.E, p.tiles, item, kGroup, PAIR ? rank : 0);
+  };
 
   if (warp < kBsEpiWarp0) {
     regs_release<kBsLeanRegs>();
@@ -310,32 +410,53 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
-      // announce a stage's bytes and load its weight tile
+      auto a_size = [&](int rows) { return rows > 0 ? (16u << box_of(rows)) * 128u : 0u; };
+      const uint32_t full_lead = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
+      // announce a stage's bytes (a pair's on rank 0) and load its weight tile
       auto load_w = [&](const BsItem& it, int st, int kb) {
         // weights of an expert with one chunk are read once
         const uint64_t policy =
             tab.chunk_off[it.e + 1] - tab.chunk_off[it.e] > 1 ? reused : once;
         uint8_t* sb = smem + st * stage_bytes + a_bytes;
-        mbar_arrive_expect_tx(&full[st], (16u << box_of(it.rows)) * 128u + NT * 128u);
+        if constexpr (PAIR) {
+          if (rank == 0)
+            mbar_arrive_expect_tx(&full[st],
+                                  a_size(it.rows) + a_size(min(128, tab.end[it.e] - it.row0 - 128)) +
+                                      NT * 128u);
+        } else {
+          mbar_arrive_expect_tx(&full[st], a_size(it.rows) + NT * 128u);
+        }
+        // A single CTA's half h is tile columns 128 h..; a pair's CTA `rank`
+        // supplies tile columns 128 rank.., 64 of them to each half.  SWIGLU:
+        // a half is 64 gate columns, then the up columns that go with them
+        // (of a pair, rank 0 has the gate rows and rank 1 the up rows).
+        constexpr int kBoxRows = SWIGLU ? 64 : 128;
 #pragma unroll
-        for (int h = 0; h < NT / 128; ++h) {
-          const int n0 = SWIGLU ? it.tile * 128 + h * (p.N / 2) : it.tile * NT + h * 128;
-          if constexpr (TRANS)
-            tma_load_3d_hint(sb + h * 16384, &maps.w, &full[st], n0, kb * 128, it.e, policy);
+        for (int i = 0; i < kBBytes / 128 / kBoxRows; ++i) {
+          int n0;
+          if constexpr (SWIGLU)
+            n0 = it.tile * 128 + (PAIR ? i * 64 + rank * (p.N / 2)
+                                       : (i >> 1) * 64 + (i & 1) * (p.N / 2));
           else
-            tma_load_3d_hint(sb + h * 16384, &maps.w, &full[st], kb * 128, n0, it.e, policy);
+            n0 = it.tile * NT + (PAIR ? rank : i) * 128;
+          const int x = TRANS ? n0 : kb * 128, y = TRANS ? kb * 128 : n0;
+          uint8_t* d = sb + i * kBoxRows * 128;
+          if constexpr (PAIR)
+            tma_load_3d_pair(d, &maps.w, full_lead + st * 8, x, y, it.e, policy);
+          else
+            tma_load_3d_hint(d, &maps.w, &full[st], x, y, it.e, policy);
         }
       };
       int ahead = 0;  // stages of the first item whose weights are on their way
       if (p.early) {
         if (first < total) {
-          const BsItem it = map_bs_item(tab, p.E, p.tiles, first);
+          const BsItem it = map_item(first);
           for (; ahead < min(stages, kb1 - kb0); ++ahead) load_w(it, ahead, kb0 + ahead);
         }
         pdl_wait();
       }
       for (int item = first; item < total && ok; item += step) {
-        const BsItem it = map_bs_item(tab, p.E, p.tiles, item);
+        const BsItem it = map_item(item);
         const int box = box_of(it.rows);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
@@ -343,7 +464,13 @@ __global__ void __launch_bounds__(kBsThreads, 1)
             break;
           }
           if (slots >= ahead) load_w(it, stage, kb);
-          tma_load_2d(smem + stage * stage_bytes, &maps.a[box], &full[stage], kb * 128, it.row0);
+          uint8_t* sa = smem + stage * stage_bytes;
+          if constexpr (PAIR) {
+            if (it.rows > 0)
+              tma_load_2d_pair(sa, &maps.a[box], full_lead + stage * 8, kb * 128, it.row0, reused);
+          } else {
+            tma_load_2d(sa, &maps.a[box], &full[stage], kb * 128, it.row0);
+          }
           ++slots;
           if (++stage == stages) {
             stage = 0;
@@ -351,107 +478,130 @@ __global__ void __launch_bounds__(kBsThreads, 1)
           }
         }
       }
-      // no copy of this thread is in flight when it leaves
-      for (int back = 1; back <= stages && back <= slots; ++back) {
+      // no copy of this thread is in flight when it leaves (a pair's complete
+      // on rank 0's barriers, and neither CTA leaves before the other)
+      for (int back = 1; back <= stages && back <= slots && (!PAIR || rank == 0); ++back) {
         const int idx = slots - back;
         mbar_wait(&full[idx % stages], static_cast<uint32_t>((idx / stages) & 1), nullptr);
       }
       if (!ok) report_status(&g_blockscale_status, kStatusTimeout);
-    } else if (warp == 1 && lane == 0) {
-      // ------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = idesc_e4m3(128, NT, TRANS);
-      int stage = 0, buf = 0;
+    } else if ((warp == 1 || (kHalves == 2 && warp == 3)) && (!PAIR || rank == 0)) {
+      // ------------------------------------------------ MMA issuers
+      constexpr uint32_t idesc = idesc_e4m3(128 * kGroup, 128, TRANS);
+      // 32 reduction columns are 32 bytes along a K-major row, 32 rows (4096
+      // bytes) of an MN-major tile.  The second half is 128 / kGroup weight
+      // rows on; of an MN-major tile as many bytes along its rows, or the
+      // next 16 KB box.
+      constexpr uint64_t kStepB = TRANS ? 256 : 2;
+      constexpr int kHalfB = TRANS && PAIR ? 64 : 16384 / kGroup;
+      const int half = warp >> 1;
+      const uint64_t da0 = desc_sw128(smem_u32(smem));
+      const uint64_t db0 = desc_sw128(smem_u32(smem) + a_bytes + half * kHalfB);
+      int stage = 0, buf = half;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag) ||
-              !mbar_wait(&full[stage], phase, abort_flag)) {
+          if (!mbar_wait_warp(&full[stage], phase, abort_flag) ||
+              !mbar_wait_warp(&tempty[buf], bphase ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * stage_bytes);
-          const uint64_t da = desc_sw128(sa);
-          const uint64_t db = TRANS ? desc_mn_sw128(sa + a_bytes, 16384) : desc_sw128(sa + a_bytes);
-          const uint32_t d = tmem + buf * NT;
-          // 32 reduction columns are 32 bytes along a K-major row, 32 rows
-          // (4096 bytes) of an MN-major tile
-          constexpr uint64_t kStepB = TRANS ? 256 : 2;
-          mma_e4m3(d, da, db, idesc, 0u);
-          mma_e4m3(d, da + 2, db + kStepB, idesc, 1u);
-          mma_e4m3(d, da + 4, db + 2 * kStepB, idesc, 1u);
-          mma_e4m3(d, da + 6, db + 3 * kStepB, idesc, 1u);
-          tc_commit(&empty[stage]);
-          tc_commit(&tfull[buf]);
+          const uint64_t off = static_cast<uint64_t>(stage * (stage_bytes >> 4));
+          const uint64_t da = da0 + off, db = db0 + off;
+          const uint32_t d = tmem + buf * 128;
+          if (elect_one()) {
+            mma_e4m3<PAIR>(d, da, db, idesc, 0u);
+            mma_e4m3<PAIR>(d, da + 2, db + kStepB, idesc, 1u);
+            mma_e4m3<PAIR>(d, da + 4, db + 2 * kStepB, idesc, 1u);
+            mma_e4m3<PAIR>(d, da + 6, db + 3 * kStepB, idesc, 1u);
+            if constexpr (PAIR) {
+              tc_commit_pair(&tfull[buf], 3);
+              tc_commit_pair(&empty[stage], 3);
+            } else {
+              tc_commit(&tfull[buf]);
+              tc_commit(&empty[stage]);
+            }
+          }
+          __syncwarp();
           if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++buf == kBufs) {
-            buf = 0;
+          if ((buf += kHalves) >= kBufs) {
+            buf = half;
             bphase ^= 1u;
           }
         }
       }
-      tc_commit(drained);
-      mbar_wait(drained, 0, nullptr);
-      if (!ok) report_status(&g_blockscale_status, kStatusTimeout);
+      // (the same lane is elected every time: its commit covers what it issued)
+      if (elect_one()) {
+        if constexpr (PAIR) tc_commit_pair(drained, 3);
+        else tc_commit(drained);
+      }
+      __syncwarp();
+      if constexpr (!PAIR) mbar_wait_warp(drained, 0, abort_flag);
+      if (!ok && lane == 0) report_status(&g_blockscale_status, kStatusTimeout);
     } else if (warp == 2) {
       // ------------------------------------------------ scales
-      // Lane l takes rows l, l + 32, ..; four blocks' loads are in flight at
-      // a time, and the ring lets them run ahead of the tensor pipe.
-      constexpr int kAhead = 4;
+      // Lane l takes rows l, l + 32, ..; four blocks' loads are in flight at a
+      // time, and the ring lets the warp run ahead of the tensor pipe.
       if (p.early) pdl_wait();
-      int slot = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int item = first; item < total && ok; item += step) {
-        const BsItem it = map_bs_item(tab, p.E, p.tiles, item);
-        const float* sa = p.a_scales + it.row0 + lane;
+      int item = first, kb = kb0;  // the block the loads have come to
+      BsItem it{};
+      float a[kBsAhead][4], w[kBsAhead][kSets];
+      auto load = [&]() {
+        // up to four blocks of one item
+        if (kb == kb0) it = map_item(item);
+        const int n = min(kBsAhead, kb1 - kb);
+        const float* sa = p.a_scales + it.row0 + lane + kb * p.ld_as;
+#pragma unroll
+        for (int i = 0; i < kBsAhead; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            a[i][j] = i < n && lane + 32 * j < it.rows ? __ldg(sa + i * p.ld_as + 32 * j) : 0.0f;
         // SWIGLU: the gate's block and the up half's; else the tile's blocks
         // (one past N has no scale of its own and is not stored)
-        const float* sw[kSets];
 #pragma unroll
         for (int h = 0; h < kSets; ++h) {
           const int nb = SWIGLU ? it.tile + h * (p.N / 256)
                                 : min(it.tile * kSets + h, (p.N + 127) / 128 - 1);
-          sw[h] = p.w_scales + it.e * p.w_blocks + nb * p.w_stride_n;
+          const float* sw = p.w_scales + it.e * p.w_blocks + nb * p.w_stride_n + kb * p.w_stride_k;
+#pragma unroll
+          for (int i = 0; i < kBsAhead; ++i) w[i][h] = i < n ? __ldg(sw + i * p.w_stride_k) : 0.0f;
         }
-        for (int kb = kb0; kb < kb1 && ok; kb += kAhead) {
-          float a[kAhead][4], w[kAhead][kSets];
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              a[i][j] = kb + i < kb1 && lane + 32 * j < it.rows
-                            ? __ldg(sa + (kb + i) * p.ld_as + 32 * j)
-                            : 0.0f;
-#pragma unroll
-            for (int h = 0; h < kSets; ++h)
-              w[i][h] = kb + i < kb1 ? __ldg(sw[h] + (kb + i) * p.w_stride_k) : 0.0f;
-          }
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            if (kb + i >= kb1) break;
-            const bool free = mbar_wait(&sempty[slot], phase ^ 1u, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, free)) {
-              ok = false;
-              break;
-            }
-            float* d = s_scale + slot * kSets * 128 + lane;
-#pragma unroll
-            for (int h = 0; h < kSets; ++h)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) d[h * 128 + 32 * j] = a[i][j] * w[i][h];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sfull[slot]);
-            if (++slot == kBsScaleSlots) {
-              slot = 0;
-              phase ^= 1u;
-            }
-          }
+        kb += n;
+        if (kb == kb1) {
+          kb = kb0;
+          item += step;
         }
+      };
+      int group = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto write = [&]() {
+        if (!mbar_wait_warp(&sempty[group], phase ^ 1u, abort_flag)) {
+          ok = false;
+          return;
+        }
+        float* d = s_scale + group * kBsAhead * kSets * 128 + lane;
+#pragma unroll
+        for (int i = 0; i < kBsAhead; ++i)
+#pragma unroll
+          for (int h = 0; h < kSets; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[(i * kSets + h) * 128 + 32 * j] = a[i][j] * w[i][h];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[group]);
+        if (++group == kBsGroups) {
+          group = 0;
+          phase ^= 1u;
+        }
+      };
+      while (item < total && kb0 < kb1 && ok) {
+        load();
+        write();
       }
       if (!ok && lane == 0) report_status(&g_blockscale_status, kStatusTimeout);
     }
@@ -464,90 +614,123 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     }
   } else {
     regs_claim<kBsEpiRegs>();
+    // Where warpgroup g's c-th 32 columns lie in the tile (SWIGLU: in its 128
+    // gate columns, then its 128 up columns).  NT = 256: the half of its own,
+    // two times 64 columns of the halves that a pair's CTAs supplied or that
+    // are gate and up; NT = 128: 64 columns of the one half.
+    auto tile_col = [](int c, int g) {
+      return SWIGLU || PAIR ? (c >> 1) * 128 + g * 64 + (c & 1) * 32 : g * kCols + c * 32;
+    };
     // ------------------------------------------------ epilogue warps
-    const int q = warp & 3, g = (warp - kBsEpiWarp0) >> 2;
-    int buf = 0, slot = 0;
-    uint32_t bphase = 0, sphase = 0;
+    const int q = warp & 3, g = (warp - kBsEpiWarp0) >> 2, r = q * 32 + lane;
+    const uint32_t tempty_lead = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
+    int buf = kHalves == 2 ? g : 0, group = 0;
+    uint32_t bphase = 0, gphase = 0;
     bool ok = true;
     for (int item = first; item < total && ok; item += step) {
-      const BsItem it = map_bs_item(tab, p.E, p.tiles, item);
-      const int r = q * 32 + lane;
-      const bool active = q * 32 < it.rows, live = r < it.rows;
-      const int64_t row = it.row0 + (live ? r : 0);
-      uint64_t acc[kCols / 2];
-#pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const bool landed = mbar_wait(&sfull[slot], sphase, abort_flag) &&
-                            mbar_wait(&tfull[buf], bphase, abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, landed)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (active) {
-          const float* ss = s_scale + slot * kSets * 128 + r;
-          const uint64_t p0 = pack2(ss[SWIGLU || kSets == 1 ? 0 : g * 128]),
-                         p1 = SWIGLU ? pack2(ss[128]) : p0;
-          const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT;
-          // SWIGLU: columns 64 g.. of the gate, then of the up half
-          auto col = [&](int c) {
-            return SWIGLU ? (c < 2 ? 0 : 128) + g * 64 + (c & 1) * 32 : g * kCols + c * 32;
-          };
-          // the next 32 columns are read while these are added
-          uint32_t v[2][32];
-          tmem_ld32(t0 + col(0), v[0]);
-#pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) {
-            tmem_ld_wait();
-            reg_fence32(v[c & 1]);
-            if (c + 1 < kCols / 32) tmem_ld32(t0 + col(c + 1), v[(c + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              fma2(acc[c * 16 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1],
-                   SWIGLU && c >= 2 ? p1 : p0);
-          }
-        }
+      // (a vote: the compiler then knows that the warp goes one way)
+      const bool active = __any_sync(0xFFFFFFFFu, q * 32 < map_item(item).rows);
+      // a warp whose rows are all past the chunk's only hands the buffers back
+      auto hand_back = [&](int b, bool group_done) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&tempty[buf]);
-          mbar_arrive(&sempty[slot]);
+        mbar_arrive_if(lane == 0, tempty_lead + b * 8);
+        mbar_arrive_if(lane == 0 && group_done, smem_u32(&sempty[group]));
+        if (group_done && ++group == kBsGroups) {
+          group = 0;
+          gphase ^= 1u;
         }
-        if (++buf == kBufs) {
-          buf = 0;
-          bphase ^= 1u;
+      };
+      auto last_of_group = [&](int kb) {
+        return ((kb + 1 - kb0) & (kBsAhead - 1)) == 0 || kb + 1 == kb1;
+      };
+      float acc[kCols];
+      if (active && kb0 < kb1) {
+        // The warp's reads and sums run on across the blocks: while 32 columns
+        // are added the next 32 are read, the first of the next block before
+        // the last of this one are added.
+        constexpr int kParts = kCols / 32;
+        constexpr bool kTwoSets = SWIGLU || PAIR;  // the second 64 columns have other scales
+        const uint32_t t_lane =
+            tmem + (static_cast<uint32_t>(q * 32) << 16) + (kHalves == 1 ? g * kCols : 0);
+        uint32_t v[2][32];
+        float s0 = 0.0f, s1 = 0.0f;
+        // wait for a block's buffer and scales, and read its first columns
+        auto open = [&](int in_group, int b, uint32_t ph, bool known) {
+          if (in_group == 0) ok &= mbar_wait_warp(&sfull[group], gphase, abort_flag);
+          if (!known) ok &= mbar_wait_warp(&tfull[b], ph, abort_flag);
+          tc_fence_after();
+          const float* ss = s_scale + (group * kBsAhead + in_group) * kSets * 128 + r;
+          s0 = ss[kTwoSets || kSets == 1 ? 0 : g * 128];
+          if (kTwoSets) s1 = ss[128];
+          tmem_ld32(t_lane + b * 128, v[0]);
+        };
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+        open(0, buf, bphase, false);
+        // (a wait that gave up is followed by nothing but quick ones, so the
+        // loop just runs to its end)
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const int nbuf = (buf + kHalves) & (kBufs - 1);
+          const uint32_t nphase = bphase ^ (nbuf < kHalves ? 1u : 0u);
+          bool next = false;
+#pragma unroll
+          for (int c = 0; c < kParts; ++c) {
+            const float sc = kTwoSets && c >= 2 ? s1 : s0;
+            tmem_ld_wait();
+            reg_fence32(v[c & 1]);
+            if (c + 1 < kParts) {
+              tmem_ld32(t_lane + buf * 128 + (c + 1) * 32, v[(c + 1) & 1]);
+              if (c + 2 == kParts) next = mbar_test(&tfull[nbuf], nphase);
+            } else {
+              hand_back(buf, last_of_group(kb));
+              if (kb + 1 < kb1)
+                open((kb + 1 - kb0) & (kBsAhead - 1), nbuf, nphase, __all_sync(0xFFFFFFFFu, next));
+            }
+            add_scaled(acc + c * 32, v[c & 1], sc);
+          }
+          buf = nbuf;
+          bphase = nphase;
         }
-        if (++slot == kBsScaleSlots) {
-          slot = 0;
-          sphase ^= 1u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+        for (int kb = kb0; kb < kb1 && ok; ++kb) {
+          if (((kb - kb0) & (kBsAhead - 1)) == 0)
+            ok = mbar_wait_warp(&sfull[group], gphase, abort_flag);
+          ok = ok && mbar_wait_warp(&tfull[buf], bphase, abort_flag);
+          if (!ok) break;
+          hand_back(buf, last_of_group(kb));
+          buf = (buf + kHalves) & (kBufs - 1);
+          if (buf < kHalves) bphase ^= 1u;
         }
       }
       if (!ok) break;
+      // (mapped again: nothing of it stays in registers during the sums)
+      const BsItem it = map_item(item);
+      const bool live = r < it.rows;
+      const int64_t row = it.row0 + (live ? r : 0);
       if constexpr (SPLIT) {
         // this rank's partial sums; joined below
         if (live) {
 #pragma unroll
           for (int c = 0; c < kCols / 32; ++c) {
-            const int col = SWIGLU ? (c < 2 ? 0 : 128) + g * 64 + (c & 1) * 32 : g * kCols + c * 32;
+            const int col = tile_col(c, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 lo = unpack2(acc[c * 16 + 2 * i]), hi = unpack2(acc[c * 16 + 2 * i + 1]);
+            for (int i = 0; i < 8; ++i)
               *reinterpret_cast<float4*>(s_part + r * (NT + 4) + col + 4 * i) =
-                  make_float4(lo.x, lo.y, hi.x, hi.y);
-            }
+                  make_float4(acc[c * 32 + 4 * i], acc[c * 32 + 4 * i + 1], acc[c * 32 + 4 * i + 2],
+                              acc[c * 32 + 4 * i + 3]);
           }
         }
       } else if constexpr (SWIGLU) {
-        // h of 64 columns; the block's maximum is over both warpgroups
-        float h[64];
+        // h of 64 columns, in place of the gate; the block's maximum is over
+        // both warpgroups
         uint32_t amax = 0u;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 gg = unpack2(acc[i]), uu = unpack2(acc[32 + i]);
-          h[2 * i] = swiglu(gg.x, uu.x, p.clamp);
-          h[2 * i + 1] = swiglu(gg.y, uu.y, p.clamp);
-          amax = max(amax, max(abs_bits(h[2 * i]), abs_bits(h[2 * i + 1])));
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = swiglu(acc[i], acc[64 + i], p.clamp);
+          amax = max(amax, abs_bits(acc[i]));
         }
         s_amax[g * 128 + r] = amax;
         asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -557,7 +740,8 @@ __global__ void __launch_bounds__(kBsThreads, 1)
           const BlockQuant bq(amax);
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = bq.code4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+          for (int i = 0; i < 16; ++i)
+            w[i] = bq.code4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
           uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + row * p.ldo +
                                               it.tile * 128 + g * 64);
 #pragma unroll
@@ -569,7 +753,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c)
-          store_bf16_32(d, it.tile * NT + g * kCols + c * 32, p.N, p.out_vec, acc + c * 16);
+          store_bf16_32(d, it.tile * NT + tile_col(c, g), p.N, p.out_vec, acc + c * 32);
       }
     }
     if (!ok && lane == 0) report_status(&g_blockscale_status, kStatusTimeout);
@@ -579,7 +763,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       __syncwarp();
       cluster_sync();
       if (first < total) {
-        const BsItem it = map_bs_item(tab, p.E, p.tiles, first);
+        const BsItem it = map_item(first);
         constexpr int kGroups = SWIGLU ? 1 : NT / 128;  // 128-column groups of a row
         for (int u = rank * 8 + warp - kBsEpiWarp0; u < it.rows * kGroups; u += 8 * p.split) {
           const int r = u / kGroups, c = (u % kGroups) * 128 + lane * 4;
@@ -628,23 +812,33 @@ __global__ void __launch_bounds__(kBsThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if constexpr (PAIR) {
+    // every MMA of the pair has completed, and neither CTA leaves while the
+    // other may still arrive on its barriers
+    if (warp == 1 && lane == 0) mbar_wait(drained, 0, nullptr);
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  } else {
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+  }
 }
 
 // ---------------------------------------------------------------- host
 using Kernel = void (*)(BlockscaleMaps, BlockscaleArgs);
 
-template <int NT, bool SWIGLU, bool TRANS, bool SPLIT>
+template <int NT, bool SWIGLU, bool SPLIT>
 constexpr int extra_smem() {
-  return (SPLIT ? kBsSplitRows * (NT + 4) * 4 : SWIGLU ? 1024 : 0) + kBsScaleSlots * NT * 4 +
-         (2 * kBsMaxStages + 2 * kBsScaleSlots + 9) * 8 + 8;
+  return (SPLIT ? kBsSplitRows * (NT + 4) * 4 : SWIGLU ? 1024 : 0) + kBsGroups * kBsAhead * NT * 4 +
+         (2 * kBsMaxStages + 2 * kBsGroups + 9) * 8 + 8;
 }
 
-template <int NT, bool SWIGLU, bool TRANS, bool SPLIT>
+template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR = false>
 cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bool pdl,
                       cudaStream_t s) {
-  auto k = blockscale_gemm_kernel<NT, SWIGLU, TRANS, SPLIT>;
+  auto k = blockscale_gemm_kernel<NT, SWIGLU, TRANS, SPLIT, PAIR>;
   // Once per instance: the shared-memory limit, and that the launch
   // allocation covers the register split (setmaxnreg would wait forever).
   static const cudaError_t ready = [&] {
@@ -656,8 +850,8 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
     return e;
   }();
   if (ready != cudaSuccess) return ready;
-  const int stage = p.a_rows * 128 + NT * 128;
-  const int fixed = 1024 + extra_smem<NT, SWIGLU, TRANS, SPLIT>() + (3 * p.E + 1) * 4;
+  const int stage = p.a_rows * 128 + NT / (PAIR ? 2 : 1) * 128;
+  const int fixed = 1024 + extra_smem<NT, SWIGLU, SPLIT>() + (3 * p.E + 1) * 4;
   p.stages = std::min(kBsMaxStages, (kBsSmemLimit - fixed) / stage);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
@@ -670,9 +864,9 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
   }
-  if (SPLIT) {
+  if (SPLIT || PAIR) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = p.split;
+    attr[cfg.numAttrs].val.clusterDim.x = PAIR ? 2 : p.split;
     attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
@@ -703,6 +897,12 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
                      : launch_bs<128, false, false, true>(maps, p, grid, pdl, s);
   }
   const int grid = static_cast<int>(std::min<int64_t>(sms, items));
+  if (wide && p.M / 256 >= p.E) {
+    const int pairs = static_cast<int>(std::min<int64_t>(sms / 2, (items + 1) / 2));
+    if (swiglu) return launch_bs<256, true, false, false, true>(maps, p, 2 * pairs, pdl, s);
+    return transpose ? launch_bs<256, false, true, false, true>(maps, p, 2 * pairs, pdl, s)
+                     : launch_bs<256, false, false, false, true>(maps, p, 2 * pairs, pdl, s);
+  }
   if (swiglu) return launch_bs<256, true, false, false>(maps, p, grid, pdl, s);
   if (wide)
     return transpose ? launch_bs<256, false, true, false>(maps, p, grid, pdl, s)

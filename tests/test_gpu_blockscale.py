@@ -184,6 +184,24 @@ def test_linear_dx_matches_64_bits(M, N, K):
     assert_product(out, a @ b, a.abs() @ b.abs(), N)
 
 
+# enough 256-column items for every SM: the wide kernels, in CTA pairs and alone
+LARGE = [(2570, 2000, 272), (4900, 1030, 130), (2561, 4100, 400), (130, 39000, 144)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_products_match_64_bits(M, N, K):
+    from moe_expert_layer_histogram_gb300 import (blockscale_linear, blockscale_linear_dx,
+                                                  blockscale_quantize)
+    x = draw_x(M, K, M + N + K)
+    w, s = draw_w(1, N, K, N)
+    codes, scales = blockscale_quantize(x)
+    assert_product(blockscale_linear(x, w[0], s[0]), *product_ref(codes, scales, w[0], s[0]), K)
+    w, s = draw_w(1, K, N, N)                  # the reduction along the stored rows
+    out = blockscale_linear_dx(x, w[0], s[0])
+    a, b = dequant_rows(codes, scales).cpu(), dequant_weight(w[0], s[0]).cpu()
+    assert_product(out, a @ b, a.abs() @ b.abs(), K)
+
+
 def test_gradient_against_differences():
     # Rows whose blocks quantise exactly (multiples of 2^-3 up to 14 with 14
     # in every block: s = 2^-5, codes are e4m3 values), so y is linear in x:
@@ -246,7 +264,7 @@ def offsets_of(counts, first=0):
     return (off + first).cuda()
 
 
-GROUPS = [[0, 5, 1, 0, 130, 17, 0], [1, 1, 1, 1], [128, 129, 127, 256], [0, 0, 0, 3],
+GROUPS = [[700, 0, 513, 1, 1500, 129, 257, 640], [1025, 128, 1], [0, 5, 1, 0, 130, 17, 0], [1, 1, 1, 1], [128, 129, 127, 256], [0, 0, 0, 3],
           [300, 0, 0, 1], [2] * 40, [0] * 511 + [9], [33, 64, 65, 31, 32, 16, 15]]
 
 
@@ -255,6 +273,7 @@ GROUPS = [[0, 5, 1, 0, 130, 17, 0], [1, 1, 1, 1], [128, 129, 127, 256], [0, 0, 0
 def test_grouped_matches_64_bits(counts, transpose):
     from moe_expert_layer_histogram_gb300 import blockscale_matmul, blockscale_quantize
     E, M, N, K = len(counts), sum(counts), 144, 272
+    N = 1552 if M > 1000 else N                # wide items
     w, s = draw_w(E, *((K, N) if transpose else (N, K)), seed=E)
     codes, scales = blockscale_quantize(draw_x(M, K, M))
     off = offsets_of(counts)
@@ -304,7 +323,8 @@ def swiglu_ref(a, w13, s13, clamp):
 @pytest.mark.parametrize("clamp", [0.0, 1.5])
 @pytest.mark.parametrize("counts,I,K", [([1], 128, 128), ([7, 0, 20], 256, 400),
                                         ([0, 129, 1, 64], 384, 272), ([300, 33], 128, 1040),
-                                        ([2] * 20, 640, 256)])
+                                        ([2] * 20, 640, 256), ([600, 257, 0, 300], 256, 272),
+                                        ([1025], 384, 400)])
 def test_swiglu_codes(counts, I, K, clamp):
     from moe_expert_layer_histogram_gb300 import blockscale_quantize, moe_blockscale_swiglu
     E, M = len(counts), sum(counts)
