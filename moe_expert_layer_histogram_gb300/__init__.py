@@ -404,6 +404,17 @@ class MoELayer:
             pass
 
 
-from .balance import RouterBalance, router_balance, router_balance_backward  # noqa: E402,F401
-from .blockscale import (blockscale_experts, blockscale_linear,  # noqa: E402,F401
-                         blockscale_linear_dx, blockscale_matmul, blockscale_quantize)
+# ---- operators on torch tensors (loaded, with torch, when first asked for) ------
+_OPERATORS = {"RouterBalance": "balance", "router_balance": "balance",
+              "router_balance_backward": "balance", "blockscale_quantize": "blockscale",
+              "blockscale_matmul": "blockscale", "blockscale_linear": "blockscale",
+              "blockscale_linear_dx": "blockscale", "blockscale_experts": "blockscale"}
+
+
+def __getattr__(name):
+    if name not in _OPERATORS:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    import importlib
+    value = getattr(importlib.import_module("." + _OPERATORS[name], __name__), name)
+    globals()[name] = value
+    return value
