@@ -444,16 +444,20 @@ moe_status moe_blockscale_swiglu(const void *a, int64_t lda,
                                  int K, float clamp_limit, void *h, int64_t ldh,
                                  float *h_scales, int64_t ld_hs, void *stream);
 
-/* Workspace bytes for `rows` quantised rows of `cols` columns (inter > 0: and
- * as many of `inter` columns); 0 for sizes out of range.  The contents need
- * no initialisation and mean nothing after the call.                      */
+/* Workspace bytes of moe_blockscale_linear for `rows` rows of `cols` columns
+ * (inter == 0; 0 for at most 16 rows of at most 10240 columns, which need
+ * none) or of
+ * moe_blockscale_experts for rows of H = cols and I = inter; 0 for sizes out
+ * of range.  The contents need no initialisation and mean nothing after the
+ * call.                                                                   */
 size_t moe_blockscale_workspace(int rows, int cols, int inter);
 
 /* moe_blockscale_quantize of the bf16 rows x [M, K] and the product with one
- * matrix w [N, K] (transpose_w: [K, N]) in one call, for which the product's
- * set-up and first weight loads overlap the quantisation.  workspace: device,
- * 16-byte aligned, moe_blockscale_workspace(M, K, 0) bytes, in use until the
- * work is done.  The rest as moe_blockscale_matmul.                        */
+ * matrix w [N, K] (transpose_w: [K, N]) in one call.  Few rows (see
+ * moe_blockscale_workspace) are quantised by the product's own kernel; for
+ * more its set-up and first weight loads overlap the quantisation.  workspace: device, 16-byte aligned,
+ * moe_blockscale_workspace(M, K, 0) bytes (may be NULL when that is 0), in
+ * use until the work is done.  The rest as moe_blockscale_matmul.          */
 moe_status moe_blockscale_linear(const void *x, int64_t ldx, const void *w,
                                  int64_t ldw, const float *w_scales, int M,
                                  int N, int K, int transpose_w, void *out,

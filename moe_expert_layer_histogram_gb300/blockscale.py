@@ -112,10 +112,10 @@ def _linear(x, w, w_scales, transpose_w, out):
     out, ldo = _result(out, M, N, dev)
     L = lib()
     nbytes = L.moe_blockscale_workspace(M, K, 0)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     code = L.moe_blockscale_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, w_scales.data_ptr(), M, N,
-                                   K, transpose_w, out.data_ptr(), ldo, ws.data_ptr(), nbytes,
-                                   stream)
+                                   K, transpose_w, out.data_ptr(), ldo,
+                                   ws.data_ptr() if nbytes else None, nbytes, stream)
     if code:
         raise MoEError(code, "moe_blockscale_linear")
     return out

@@ -54,30 +54,19 @@ __global__ void __launch_bounds__(256)
       v[i] = lo | (hi << 16);
     }
   }
-  float f[16];
-  uint32_t amax = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[2 * i] = __uint_as_float(v[i] << 16);
-    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-    amax = max(amax, max(abs_bits(f[2 * i]), abs_bits(f[2 * i + 1])));
-  }
-#pragma unroll
-  for (int off = 4; off; off >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+  float scale;
+  const uint4 w4 = quantize_16(v, scale);
   if (!real) return;
-  const BlockQuant bq(amax);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = bq.code4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
   uint8_t* d = codes + r * ld_codes + c0;
   if (VEC && c0 + 16 <= cols) {
-    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(d) = w4;
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (c0 + i < cols) d[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
   }
-  if ((threadIdx.x & 7) == 0) scales[b * ld_scales + r] = bq.scale;
+  if ((threadIdx.x & 7) == 0) scales[b * ld_scales + r] = scale;
 }
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -94,6 +83,8 @@ struct Product {
   const int32_t* offsets;
   int E, M, N, K;
   bool transpose;
+  const void* x = nullptr;  // bf16 activations that the product quantises (no codes in `a`)
+  int64_t ldx = 0;
 };
 
 // TMA wants 16-byte aligned bases and row strides; scales and offsets are
@@ -163,7 +154,7 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
   const int boxes = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 3 : 4;
   const cuuint64_t adims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M)};
   const cuuint64_t astr[1] = {static_cast<cuuint64_t>(p.lda)};
-  for (int i = 0; i < boxes; ++i) {
+  for (int i = 0; i < boxes && !p.x; ++i) {
     const cuuint32_t box[2] = {128, 16u << i};
     if (!encode(&maps.a[i], p.a, 2, adims, astr, box)) return MOE_ERR_CUDA;
   }
@@ -192,6 +183,9 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
   a.clamp = clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY;
   a.h_scales = h_scales;
   a.ld_hs = ld_hs;
+  a.x = static_cast<const __nv_bfloat16*>(p.x);
+  a.ldx = p.ldx;
+  a.x_vec = aligned_to(p.x, 16) && p.ldx % 8 == 0;
   a.early = early;
   return launch_blockscale(maps, a, swiglu, p.transpose, early, sms, s) == cudaSuccess
              ? MOE_OK
@@ -284,6 +278,7 @@ moe_status moe_blockscale_swiglu(const void* a, int64_t lda, const float* a_scal
 
 size_t moe_blockscale_workspace(int rows, int cols, int inter) {
   if (rows < 0 || cols < 1 || inter < 0) return 0;
+  if (inter == 0 && blockscale_quantizes(rows, cols)) return 0;
   return static_cast<size_t>(quantized_bytes(rows, cols) +
                              (inter ? quantized_bytes(rows, inter) : 0));
 }
@@ -297,10 +292,17 @@ moe_status moe_blockscale_linear(const void* x, int64_t ldx, const void* w, int6
   if (st != MOE_OK) return st;
   if (ldx < K || ldo < N) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  if (!x || !out || !workspace || !aligned_to(x, 2) || !aligned_to(out, 2) ||
-      !aligned_to(workspace, 16) || workspace_bytes < moe_blockscale_workspace(M, K, 0))
+  const size_t need = moe_blockscale_workspace(M, K, 0);
+  if (!x || !out || !aligned_to(x, 2) || !aligned_to(out, 2) || workspace_bytes < need ||
+      (need && (!workspace || !aligned_to(workspace, 16))))
     return MOE_ERR_INVALID_ARG;
   if (!device_sms()) return MOE_ERR_NO_DEVICE;
+  if (!need) {
+    p.x = x;
+    p.ldx = ldx;
+    return run_product(p, false, out, ldo, 0.0f, nullptr, 0, false,
+                       static_cast<cudaStream_t>(stream));
+  }
   const Quantized q(workspace, M, K);
   p.a = q.codes;
   p.lda = q.ld;

@@ -36,6 +36,12 @@
 // at 128 bytes a cycle against 512 cycles of MMA; in a pair it is 32 KB each
 // way, and both take 512.
 //
+// Few rows of one matrix (QUANT): the CTA's warps but the producer first
+// quantise the bf16 activations of its part of the reduction into shared
+// memory, in the swizzled order the MMAs expect, while the first weight tiles
+// are on their way.  Every CTA does so for itself, but there is no kernel
+// before this one and no workspace.
+//
 // With the weights transposed (input gradient) the reduction runs along the
 // stored rows: the tile is 128 rows of 128 bytes of output columns, an
 // MN-major operand for the tensor cores; nothing is copied or re-laid out.
@@ -319,7 +325,9 @@ __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
 // up rows of the same columns (NT = 256).  SPLIT: the grid is clusters of
 // args.split CTAs, one item each (one expert, at most kBsSplitRows rows).
 // PAIR: the grid is clusters of two CTAs that share each item (NT = 256).
-template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR>
+// QUANT: the activations are args.x, at most kBlockscaleFewRows rows, and
+// every CTA (or split cluster) has one item (NT = 128).
+template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR, bool QUANT>
 __global__ void __launch_bounds__(kBsThreads, 1)
     blockscale_gemm_kernel(const __grid_constant__ BlockscaleMaps maps,
                            const __grid_constant__ BlockscaleArgs p) {
@@ -331,14 +339,18 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   constexpr int kBBytes = NT / kGroup * 128;  // this CTA's part of the weight tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // QUANT: the resident activations, then the ring of weight tiles
   const int a_bytes = p.a_rows * 128;
-  const int stage_bytes = a_bytes + kBBytes;
+  const int stage_bytes = (QUANT ? 0 : a_bytes) + kBBytes;
+  const int b_off = QUANT ? 0 : a_bytes;
   const int stages = p.stages;
+  uint8_t* const s_a = smem;
+  if constexpr (QUANT) smem += p.resident * a_bytes;
   float* s_part = reinterpret_cast<float*>(smem + stages * stage_bytes);  // SPLIT: [32][NT + 4]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_part);                 // SWIGLU: [2][128]
   // [group][block][weight block of the tile][row]
   float* s_scale = s_part + (SPLIT ? kBsSplitRows * (NT + 4) : SWIGLU ? 256 : 0);
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + kBsGroups * kBsAhead * kSets * 128);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + (QUANT ? p.resident * 32 : kBsGroups * kBsAhead * kSets * 128));
   uint64_t* empty = full + kBsMaxStages;
   uint64_t* tfull = empty + kBsMaxStages;
   uint64_t* tempty = tfull + 4;
@@ -401,8 +413,48 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     return map_bs_item(tab, p.E, p.tiles, item, kGroup, PAIR ? rank : 0);
   };
 
+  if (QUANT && warp > 0 && first < total) {
+    // Eight lanes per (row, block), 16 columns each.
+    const int nb = static_cast<int>(kb1 - kb0), units = p.M * nb;
+    const int tile = map_item(first).tile;
+    for (int u0 = 0; u0 < units; u0 += (kBsThreads - 32) / 8) {
+      const int u = u0 + (static_cast<int>(threadIdx.x) - 32) / 8, chunk = lane & 7;
+      const int r = u % p.M, kb = kb0 + u / p.M, c0 = kb * 128 + chunk * 16;
+      const bool real = u < units;
+      const __nv_bfloat16* src = p.x + r * p.ldx + c0;
+      uint32_t v[8];
+      if (real && p.x_vec && c0 + 16 <= p.K) {
+        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src)),
+                    hi = __ldg(reinterpret_cast<const uint4*>(src + 8));
+        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+        v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t lo = 0u, hi = 0u;
+          if (real && c0 + 2 * i < p.K) lo = reinterpret_cast<const uint16_t*>(src)[2 * i];
+          if (real && c0 + 2 * i + 1 < p.K) hi = reinterpret_cast<const uint16_t*>(src)[2 * i + 1];
+          v[i] = lo | (hi << 16);
+        }
+      }
+      const float sw =
+          real ? __ldg(p.w_scales + tile * p.w_stride_n + kb * p.w_stride_k) : 0.0f;
+      float scale;
+      const uint4 codes = quantize_16(v, scale);
+      if (real) {
+        // row r's 16-byte chunk c lies at chunk c ^ (r % 8)
+        *reinterpret_cast<uint4*>(s_a + (kb - kb0) * a_bytes + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+            codes;
+        if (chunk == 0) s_scale[(kb - kb0) * 32 + r] = scale * sw;
+      }
+    }
+    // the codes are read by the tensor core, the scales by the epilogue
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("bar.sync 2, %0;" ::"n"(kBsThreads - 32) : "memory");
+  }
+
   if (warp < kBsEpiWarp0) {
-    regs_release<kBsLeanRegs>();
+    if constexpr (!QUANT) regs_release<kBsLeanRegs>();
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------ TMA producer
       const uint64_t once = l2_policy_evict_first(), reused = l2_policy_evict_normal();
@@ -417,14 +469,14 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         // weights of an expert with one chunk are read once
         const uint64_t policy =
             tab.chunk_off[it.e + 1] - tab.chunk_off[it.e] > 1 ? reused : once;
-        uint8_t* sb = smem + st * stage_bytes + a_bytes;
+        uint8_t* sb = smem + st * stage_bytes + b_off;
         if constexpr (PAIR) {
           if (rank == 0)
             mbar_arrive_expect_tx(&full[st],
                                   a_size(it.rows) + a_size(min(128, tab.end[it.e] - it.row0 - 128)) +
                                       NT * 128u);
         } else {
-          mbar_arrive_expect_tx(&full[st], a_size(it.rows) + NT * 128u);
+          mbar_arrive_expect_tx(&full[st], (QUANT ? 0u : a_size(it.rows)) + NT * 128u);
         }
         // A single CTA's half h is tile columns 128 h..; a pair's CTA `rank`
         // supplies tile columns 128 rank.., 64 of them to each half.  SWIGLU:
@@ -468,7 +520,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
           if constexpr (PAIR) {
             if (it.rows > 0)
               tma_load_2d_pair(sa, &maps.a[box], full_lead + stage * 8, kb * 128, it.row0, reused);
-          } else {
+          } else if constexpr (!QUANT) {
             tma_load_2d(sa, &maps.a[box], &full[stage], kb * 128, it.row0);
           }
           ++slots;
@@ -495,8 +547,8 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       constexpr uint64_t kStepB = TRANS ? 256 : 2;
       constexpr int kHalfB = TRANS && PAIR ? 64 : 16384 / kGroup;
       const int half = warp >> 1;
-      const uint64_t da0 = desc_sw128(smem_u32(smem));
-      const uint64_t db0 = desc_sw128(smem_u32(smem) + a_bytes + half * kHalfB);
+      const uint64_t da0 = desc_sw128(smem_u32(QUANT ? s_a : smem));
+      const uint64_t db0 = desc_sw128(smem_u32(smem) + b_off + half * kHalfB);
       int stage = 0, buf = half;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
@@ -509,7 +561,9 @@ __global__ void __launch_bounds__(kBsThreads, 1)
           }
           tc_fence_after();
           const uint64_t off = static_cast<uint64_t>(stage * (stage_bytes >> 4));
-          const uint64_t da = da0 + off, db = db0 + off;
+          const uint64_t da =
+              da0 + (QUANT ? static_cast<uint64_t>((kb - kb0) * (a_bytes >> 4)) : off);
+          const uint64_t db = db0 + off;
           const uint32_t d = tmem + buf * 128;
           if (elect_one()) {
             mma_e4m3<PAIR>(d, da, db, idesc, 0u);
@@ -543,7 +597,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       __syncwarp();
       if constexpr (!PAIR) mbar_wait_warp(drained, 0, abort_flag);
       if (!ok && lane == 0) report_status(&g_blockscale_status, kStatusTimeout);
-    } else if (warp == 2) {
+    } else if (!QUANT && warp == 2) {
       // ------------------------------------------------ scales
       // Lane l takes rows l, l + 32, ..; four blocks' loads are in flight at a
       // time, and the ring lets the warp run ahead of the tensor pipe.
@@ -613,7 +667,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       cluster_sync();
     }
   } else {
-    regs_claim<kBsEpiRegs>();
+    if constexpr (!QUANT) regs_claim<kBsEpiRegs>();
     // Where warpgroup g's c-th 32 columns lie in the tile (SWIGLU: in its 128
     // gate columns, then its 128 up columns).  NT = 256: the half of its own,
     // two times 64 columns of the halves that a pair's CTAs supplied or that
@@ -635,7 +689,8 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         tc_fence_before();
         __syncwarp();
         mbar_arrive_if(lane == 0, tempty_lead + b * 8);
-        mbar_arrive_if(lane == 0 && group_done, smem_u32(&sempty[group]));
+        if constexpr (!QUANT)
+          mbar_arrive_if(lane == 0 && group_done, smem_u32(&sempty[group]));
         if (group_done && ++group == kBsGroups) {
           group = 0;
           gphase ^= 1u;
@@ -656,11 +711,13 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         uint32_t v[2][32];
         float s0 = 0.0f, s1 = 0.0f;
         // wait for a block's buffer and scales, and read its first columns
-        auto open = [&](int in_group, int b, uint32_t ph, bool known) {
-          if (in_group == 0) ok &= mbar_wait_warp(&sfull[group], gphase, abort_flag);
+        auto open = [&](int block, int b, uint32_t ph, bool known) {
+          const int in_group = block & (kBsAhead - 1);
+          if (!QUANT && in_group == 0) ok &= mbar_wait_warp(&sfull[group], gphase, abort_flag);
           if (!known) ok &= mbar_wait_warp(&tfull[b], ph, abort_flag);
           tc_fence_after();
-          const float* ss = s_scale + (group * kBsAhead + in_group) * kSets * 128 + r;
+          const float* ss = s_scale + r + (QUANT ? block * 32
+                                                 : (group * kBsAhead + in_group) * kSets * 128);
           s0 = ss[kTwoSets || kSets == 1 ? 0 : g * 128];
           if (kTwoSets) s1 = ss[128];
           tmem_ld32(t_lane + b * 128, v[0]);
@@ -685,7 +742,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
             } else {
               hand_back(buf, last_of_group(kb));
               if (kb + 1 < kb1)
-                open((kb + 1 - kb0) & (kBsAhead - 1), nbuf, nphase, __all_sync(0xFFFFFFFFu, next));
+                open(kb + 1 - kb0, nbuf, nphase, __all_sync(0xFFFFFFFFu, next));
             }
             add_scaled(acc + c * 32, v[c & 1], sc);
           }
@@ -696,7 +753,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
 #pragma unroll
         for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
         for (int kb = kb0; kb < kb1 && ok; ++kb) {
-          if (((kb - kb0) & (kBsAhead - 1)) == 0)
+          if (!QUANT && ((kb - kb0) & (kBsAhead - 1)) == 0)
             ok = mbar_wait_warp(&sfull[group], gphase, abort_flag);
           ok = ok && mbar_wait_warp(&tfull[buf], bphase, abort_flag);
           if (!ok) break;
@@ -829,16 +886,18 @@ __global__ void __launch_bounds__(kBsThreads, 1)
 // ---------------------------------------------------------------- host
 using Kernel = void (*)(BlockscaleMaps, BlockscaleArgs);
 
-template <int NT, bool SWIGLU, bool SPLIT>
-constexpr int extra_smem() {
-  return (SPLIT ? kBsSplitRows * (NT + 4) * 4 : SWIGLU ? 1024 : 0) + kBsGroups * kBsAhead * NT * 4 +
+// Shared memory beside the stages (and, QUANT, the resident activations).
+template <int NT, bool SWIGLU, bool SPLIT, bool QUANT>
+int extra_smem(int resident) {
+  return (SPLIT ? kBsSplitRows * (NT + 4) * 4 : SWIGLU ? 1024 : 0) +
+         (QUANT ? resident * 128 : kBsGroups * kBsAhead * NT * 4) +
          (2 * kBsMaxStages + 2 * kBsGroups + 9) * 8 + 8;
 }
 
-template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR = false>
+template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR = false, bool QUANT = false>
 cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bool pdl,
                       cudaStream_t s) {
-  auto k = blockscale_gemm_kernel<NT, SWIGLU, TRANS, SPLIT, PAIR>;
+  auto k = blockscale_gemm_kernel<NT, SWIGLU, TRANS, SPLIT, PAIR, QUANT>;
   // Once per instance: the shared-memory limit, and that the launch
   // allocation covers the register split (setmaxnreg would wait forever).
   static const cudaError_t ready = [&] {
@@ -846,12 +905,15 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmemLimit);
     cudaFuncAttributes fa{};
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, k);
-    if (e == cudaSuccess && fa.numRegs != kBsLaunchRegs) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && !QUANT && fa.numRegs != kBsLaunchRegs) e = cudaErrorInvalidConfiguration;
     return e;
   }();
   if (ready != cudaSuccess) return ready;
-  const int stage = p.a_rows * 128 + NT / (PAIR ? 2 : 1) * 128;
-  const int fixed = 1024 + extra_smem<NT, SWIGLU, SPLIT>() + (3 * p.E + 1) * 4;
+  const int a_bytes = p.a_rows * 128;
+  const int stage = (QUANT ? 0 : a_bytes) + NT / (PAIR ? 2 : 1) * 128;
+  p.resident = QUANT ? ((p.K + 127) / 128 + p.split - 1) / p.split : 0;
+  const int fixed = 1024 + extra_smem<NT, SWIGLU, SPLIT, QUANT>(p.resident) +
+                    p.resident * a_bytes + (3 * p.E + 1) * 4;
   p.stages = std::min(kBsMaxStages, (kBsSmemLimit - fixed) / stage);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
@@ -881,7 +943,7 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
   const int64_t chunks =
       p.E == 1 ? (p.M + 127) / 128 : std::min<int64_t>(p.E, p.M) + p.M / 128;
   p.a_rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const bool wide = swiglu || chunks * ((p.N + 255) / 256) >= sms;
+  const bool wide = swiglu || (!p.x && chunks * ((p.N + 255) / 256) >= sms);
   const int nt = wide ? 256 : 128;
   p.tiles = swiglu ? p.N / 256 : (p.N + nt - 1) / nt;
   const int64_t items = chunks * p.tiles;
@@ -892,10 +954,17 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
       p.split *= 2;
   if (p.split > 1) {
     const int grid = static_cast<int>(items) * p.split;
+    if (p.x)
+      return transpose ? launch_bs<128, false, true, true, false, true>(maps, p, grid, pdl, s)
+                       : launch_bs<128, false, false, true, false, true>(maps, p, grid, pdl, s);
     if (swiglu) return launch_bs<256, true, false, true>(maps, p, grid, pdl, s);
     return transpose ? launch_bs<128, false, true, true>(maps, p, grid, pdl, s)
                      : launch_bs<128, false, false, true>(maps, p, grid, pdl, s);
   }
+  if (p.x)
+    return transpose
+               ? launch_bs<128, false, true, false, false, true>(maps, p, items, pdl, s)
+               : launch_bs<128, false, false, false, false, true>(maps, p, items, pdl, s);
   const int grid = static_cast<int>(std::min<int64_t>(sms, items));
   if (wide && p.M / 256 >= p.E) {
     const int pairs = static_cast<int>(std::min<int64_t>(sms / 2, (items + 1) / 2));

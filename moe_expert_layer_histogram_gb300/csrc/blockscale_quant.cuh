@@ -48,4 +48,23 @@ struct BlockQuant {
   }
 };
 
+// 16 bf16 values (pairs in v) of a block that eight neighbouring lanes share:
+// their codes and the block's scale.  Called by whole warps.
+__device__ __forceinline__ uint4 quantize_16(const uint32_t (&v)[8], float& scale) {
+  float f[16];
+  uint32_t amax = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    amax = max(amax, max(abs_bits(f[2 * i]), abs_bits(f[2 * i + 1])));
+  }
+#pragma unroll
+  for (int off = 4; off; off >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+  const BlockQuant bq(amax);
+  scale = bq.scale;
+  return make_uint4(bq.code4(f[0], f[1], f[2], f[3]), bq.code4(f[4], f[5], f[6], f[7]),
+                    bq.code4(f[8], f[9], f[10], f[11]), bq.code4(f[12], f[13], f[14], f[15]));
+}
+
 }  // namespace moe
