@@ -74,7 +74,7 @@ constexpr int kBsMaxStages = 8;
 constexpr int kBsAhead = 4;       // blocks whose scales are passed on together
 constexpr int kBsGroups = 2;      // such groups in the scale ring
 constexpr int kBsSmemLimit = 232448;
-constexpr int kBsSplitRows = 32;  // largest chunk whose reduction is split
+constexpr int kBsSplitSwigluRows = 32;  // largest chunk of the SwiGLU product that is split
 
 __device__ int g_blockscale_status;
 
@@ -293,9 +293,15 @@ __device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], 
   }
 }
 
-// bf16 of 32 consecutive fp32 columns n0 .. n0 + 31 of one row (n0 + 32 may
-// pass N).
-__device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row, int n0, int N, bool vec,
+// bf16 of 32 consecutive fp32 columns n0 .. n0 + 31 of the warp's 32 rows
+// (lane = row; row0 the first one's, rows how many are real; n0 + 32 may pass
+// N).  Whole 16-byte words where rows allow (VEC): then a lane's 64 bytes are
+// whole sectors.  Else the block is turned in `turn` (32 x kTurnWords words of
+// shared memory, the warp's own), so that a store covers consecutive columns
+// of one row instead of one column of 32 rows.
+constexpr int kTurnWords = 17;  // per row of 32 bf16: odd, so columns differ in bank
+__device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row0, int64_t ldo, int rows, int lane,
+                                              int n0, int N, bool vec, uint32_t* turn,
                                               const float* acc) {
   uint32_t v[16];
 #pragma unroll
@@ -304,15 +310,23 @@ __device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row, int n0, int N,
     v[i] = reinterpret_cast<const uint32_t&>(b);
   }
   if (vec && n0 + 32 <= N) {
-    uint4* d = reinterpret_cast<uint4*>(row + n0);
+    if (lane < rows) {
+      uint4* d = reinterpret_cast<uint4*>(row0 + lane * ldo + n0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int i = 0; i < 4; ++i)
+        d[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
     return;
   }
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (n0 + i < N)
-      reinterpret_cast<uint16_t*>(row)[n0 + i] = static_cast<uint16_t>(v[i >> 1] >> (16 * (i & 1)));
+  for (int i = 0; i < 16; ++i) turn[lane * kTurnWords + i] = v[i];
+  __syncwarp();
+  if (n0 + lane < N) {
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(turn) + lane;
+    uint16_t* d = reinterpret_cast<uint16_t*>(row0) + n0 + lane;
+    for (int r = 0; r < min(rows, 32); ++r) d[r * ldo] = src[r * 2 * kTurnWords];
+  }
 }
 
 __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
@@ -323,7 +337,7 @@ __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
 
 // NT: weight rows per item.  SWIGLU: the tile is 128 gate rows and the 128
 // up rows of the same columns (NT = 256).  SPLIT: the grid is clusters of
-// args.split CTAs, one item each (one expert, at most kBsSplitRows rows).
+// args.split CTAs, one item each (one expert).
 // PAIR: the grid is clusters of two CTAs that share each item (NT = 256).
 // QUANT: the activations are args.x, at most kBlockscaleFewRows rows, and
 // every CTA (or split cluster) has one item (NT = 128).
@@ -346,10 +360,12 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   const int stages = p.stages;
   uint8_t* const s_a = smem;
   if constexpr (QUANT) smem += p.resident * a_bytes;
-  float* s_part = reinterpret_cast<float*>(smem + stages * stage_bytes);  // SPLIT: [32][NT + 4]
+  float* s_part = reinterpret_cast<float*>(smem + stages * stage_bytes);  // SPLIT: [a_rows][NT + 4]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_part);                 // SWIGLU: [2][128]
   // [group][block][weight block of the tile][row]
-  float* s_scale = s_part + (SPLIT ? kBsSplitRows * (NT + 4) : SWIGLU ? 256 : 0);
+  float* s_scale = s_part + (SPLIT    ? p.a_rows * (NT + 4)
+                             : SWIGLU ? 256
+                                      : 8 * 32 * kTurnWords);
   uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + (QUANT ? p.resident * 32 : kBsGroups * kBsAhead * kSets * 128));
   uint64_t* empty = full + kBsMaxStages;
   uint64_t* tfull = empty + kBsMaxStages;
@@ -806,11 +822,13 @@ __global__ void __launch_bounds__(kBsThreads, 1)
             d[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           if (g == 0) p.h_scales[it.tile * p.ld_hs + row] = bq.scale;
         }
-      } else if (live) {
-        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
+      } else if (active) {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + (it.row0 + q * 32) * p.ldo;
+        uint32_t* turn = reinterpret_cast<uint32_t*>(s_part) + (warp - kBsEpiWarp0) * 32 * kTurnWords;
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c)
-          store_bf16_32(d, it.tile * NT + tile_col(c, g), p.N, p.out_vec, acc + c * 32);
+          store_bf16_32(d, p.ldo, it.rows - q * 32, lane, it.tile * NT + tile_col(c, g), p.N,
+                        p.out_vec, turn, acc + c * 32);
       }
     }
     if (!ok && lane == 0) report_status(&g_blockscale_status, kStatusTimeout);
@@ -888,8 +906,10 @@ using Kernel = void (*)(BlockscaleMaps, BlockscaleArgs);
 
 // Shared memory beside the stages (and, QUANT, the resident activations).
 template <int NT, bool SWIGLU, bool SPLIT, bool QUANT>
-int extra_smem(int resident) {
-  return (SPLIT ? kBsSplitRows * (NT + 4) * 4 : SWIGLU ? 1024 : 0) +
+int extra_smem(int a_rows, int resident) {
+  return (SPLIT    ? a_rows * (NT + 4) * 4
+          : SWIGLU ? 1024
+                   : 8 * 32 * kTurnWords * 4) +
          (QUANT ? resident * 128 : kBsGroups * kBsAhead * NT * 4) +
          (2 * kBsMaxStages + 2 * kBsGroups + 9) * 8 + 8;
 }
@@ -912,7 +932,7 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
   const int a_bytes = p.a_rows * 128;
   const int stage = (QUANT ? 0 : a_bytes) + NT / (PAIR ? 2 : 1) * 128;
   p.resident = QUANT ? ((p.K + 127) / 128 + p.split - 1) / p.split : 0;
-  const int fixed = 1024 + extra_smem<NT, SWIGLU, SPLIT, QUANT>(p.resident) +
+  const int fixed = 1024 + extra_smem<NT, SWIGLU, SPLIT, QUANT>(p.a_rows, p.resident) +
                     p.resident * a_bytes + (3 * p.E + 1) * 4;
   p.stages = std::min(kBsMaxStages, (kBsSmemLimit - fixed) / stage);
   cudaLaunchAttribute attr[2];
@@ -949,7 +969,7 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
   const int64_t items = chunks * p.tiles;
   if (items > INT32_MAX) return cudaErrorInvalidValue;
   p.split = 1;
-  if (p.E == 1 && p.M <= kBsSplitRows)
+  if (p.E == 1 && (!swiglu || p.M <= kBsSplitSwigluRows))
     while (p.split < 8 && items * p.split * 2 <= sms && p.split * 2 <= (p.K + 127) / 128)
       p.split *= 2;
   if (p.split > 1) {
