@@ -399,7 +399,7 @@ moe_status moe_balance_backward(const void *logits, int dtype, int64_t ld,
  * gather each expert's rows), or row r; a slot outside x gives a zero row.
  * cols >= 1 of any size, ld_codes >= cols, ld_scales >= rows.  rows == 0 is
  * a no-op.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (more than
- * 2^31 blocks), MOE_ERR_CUDA.                                             */
+ * 2^25 - 512 columns), MOE_ERR_CUDA.                                      */
 moe_status moe_blockscale_quantize(const void *x, int64_t ldx, int x_rows,
                                    const int32_t *slots, int top_k, int rows,
                                    int cols, void *codes, int64_t ld_codes,

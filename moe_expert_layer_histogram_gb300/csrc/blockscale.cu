@@ -21,8 +21,10 @@ constexpr int kBlk = 128;
 __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
 
 // ---------------------------------------------------------------- quantise
-// Eight lanes per (row, block), 16 columns each: with aligned rows two
-// 16-byte loads and one 16-byte store per thread.
+// A warp takes four blocks of a row, eight lanes per block and 16 columns per
+// lane: with aligned rows (VEC) two 16-byte loads and one 16-byte store.
+constexpr int kQuantCols = 4 * kBlk;
+
 template <bool VEC>
 __global__ void __launch_bounds__(256)
     blockscale_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t ldx, int x_rows,
@@ -31,12 +33,11 @@ __global__ void __launch_bounds__(256)
                                float* __restrict__ scales, int64_t ld_scales) {
   // a product that follows may set itself up and load weights meanwhile
   pdl_launch_dependents();
-  const int kb = blocks_of(cols);
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 3);
-  const bool real = unit < static_cast<int64_t>(rows) * kb;
-  const int r = real ? static_cast<int>(unit / kb) : 0;
-  const int b = real ? static_cast<int>(unit - static_cast<int64_t>(r) * kb) : 0;
-  const int c0 = b * kBlk + (threadIdx.x & 7) * 16;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int r = static_cast<int>(row), lane = threadIdx.x & 31;
+  const int c0 = blockIdx.y * kQuantCols + lane * 16, b = c0 / kBlk;
+  const bool real = c0 < cols;
   const int src = slots ? slots[r] / top_k : r;
   const bool in = real && src >= 0 && src < x_rows;
   const __nv_bfloat16* p = x + src * ldx + c0;
@@ -56,6 +57,8 @@ __global__ void __launch_bounds__(256)
   }
   float scale;
   const uint4 w4 = quantize_16(v, scale);
+  const bool first = (lane & 7) == 0 && b * kBlk < cols;
+  if (first) scales[b * ld_scales + r] = scale;
   if (!real) return;
   const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
   uint8_t* d = codes + r * ld_codes + c0;
@@ -66,7 +69,6 @@ __global__ void __launch_bounds__(256)
     for (int i = 0; i < 16; ++i)
       if (c0 + i < cols) d[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
   }
-  if ((threadIdx.x & 7) == 0) scales[b * ld_scales + r] = scale;
 }
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -202,12 +204,12 @@ moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* s
   if ((!x && x_rows > 0) || !codes || !scales || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
       !aligned_to(scales, 4))
     return MOE_ERR_INVALID_ARG;
-  const int64_t grid = (static_cast<int64_t>(rows) * blocks_of(cols) + 31) / 32;
-  if (grid > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid((static_cast<unsigned>(rows) + 7) / 8, (cols - 1) / kQuantCols + 1);
+  if (grid.y > 65535) return MOE_ERR_UNSUPPORTED;
   const bool vec = aligned_to(x, 16) && ldx % 8 == 0 && aligned_to(codes, 16) && ld_codes % 16 == 0;
   const cudaError_t e = launch_pdl(
       false, vec ? blockscale_quantize_kernel<true> : blockscale_quantize_kernel<false>,
-      dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(x),
+      grid, dim3(256), 0, s, static_cast<const __nv_bfloat16*>(x),
       ldx, x_rows, slots, top_k, rows, cols, static_cast<uint8_t*>(codes), ld_codes, scales,
       ld_scales);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

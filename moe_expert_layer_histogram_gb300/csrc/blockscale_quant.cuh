@@ -33,38 +33,52 @@ struct BlockQuant {
     r = amax_bits == 0u ? 0.0f : __frcp_rn(scale);
     slow = scale < 0x1p-80f && amax_bits != 0u;
   }
-  __device__ __forceinline__ float quotient(float x) const {
-    if (slow) return __fdiv_rn(x, scale);
-    const float q = __fmul_rn(x, r);
-    return __fmaf_rn(-__fmaf_rn(q, scale, -x), r, q);
+  // codes of a pair, a's in the low byte
+  __device__ __forceinline__ uint32_t code2(float a, float b) const {
+    const float2 x = make_float2(a, b), s2 = make_float2(scale, scale), r2 = make_float2(r, r);
+    const float2 q = __fmul2_rn(x, r2);
+    const float2 e = __ffma2_rn(q, s2, make_float2(-a, -b));
+    return __nv_cvt_float2_to_fp8x2(__ffma2_rn(make_float2(-e.x, -e.y), r2, q), __NV_SATFINITE,
+                                    __NV_E4M3);
+  }
+  __device__ __forceinline__ uint32_t code2_slow(float a, float b) const {
+    return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)),
+                                    __NV_SATFINITE, __NV_E4M3);
   }
   // four codes, element i in byte i
   __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) const {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(quotient(a), quotient(b)),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(quotient(c), quotient(d)),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+    if (slow) return code2_slow(a, b) | (code2_slow(c, d) << 16);
+    return code2(a, b) | (code2(c, d) << 16);
   }
 };
 
 // 16 bf16 values (pairs in v) of a block that eight neighbouring lanes share:
 // their codes and the block's scale.  Called by whole warps.
 __device__ __forceinline__ uint4 quantize_16(const uint32_t (&v)[8], float& scale) {
-  float f[16];
-  uint32_t amax = 0u;
+  // the larger magnitude of each half-word, then of the two
+  uint32_t m2 = v[0] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[2 * i] = __uint_as_float(v[i] << 16);
-    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-    amax = max(amax, max(abs_bits(f[2 * i]), abs_bits(f[2 * i + 1])));
-  }
+  for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, v[i] & 0x7FFF7FFFu);
+  uint32_t amax = max(m2 << 16, m2 & 0xFFFF0000u);
 #pragma unroll
   for (int off = 4; off; off >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
   const BlockQuant bq(amax);
   scale = bq.scale;
-  return make_uint4(bq.code4(f[0], f[1], f[2], f[3]), bq.code4(f[4], f[5], f[6], f[7]),
-                    bq.code4(f[8], f[9], f[10], f[11]), bq.code4(f[12], f[13], f[14], f[15]));
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
+  uint32_t w[4];
+  if (bq.slow) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = bq.code2_slow(lo(v[2 * i]), hi(v[2 * i])) |
+             (bq.code2_slow(lo(v[2 * i + 1]), hi(v[2 * i + 1])) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = bq.code2(lo(v[2 * i]), hi(v[2 * i])) |
+             (bq.code2(lo(v[2 * i + 1]), hi(v[2 * i + 1])) << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace moe
