@@ -71,7 +71,7 @@ constexpr int kBsEpiRegs = 216;
 constexpr int kBsLaunchRegs = 168;
 static_assert(kBsLeanRegs + 2 * kBsEpiRegs <= 3 * kBsLaunchRegs, "register split");
 constexpr int kBsMaxStages = 8;
-constexpr int kBsAhead = 4;       // blocks whose scales are passed on together
+constexpr int kBsAhead = 4;       // blocks whose scales are passed on together, a float4 per row
 constexpr int kBsGroups = 2;      // such groups in the scale ring
 constexpr int kBsSmemLimit = 232448;
 constexpr int kBsSplitSwigluRows = 32;  // largest chunk of the SwiGLU product that is split
@@ -218,6 +218,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
+// Rows of 32 scales for QUANT's resident blocks: the epilogue reads them
+// kBsAhead at a time.
+__host__ __device__ constexpr int scale_rows(int resident) {
+  return (resident + kBsAhead - 1) / kBsAhead * kBsAhead;
+}
+
 struct BsItem {
   int e, tile, row0, rows;
 };
@@ -362,11 +368,11 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   if constexpr (QUANT) smem += p.resident * a_bytes;
   float* s_part = reinterpret_cast<float*>(smem + stages * stage_bytes);  // SPLIT: [a_rows][NT + 4]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_part);                 // SWIGLU: [2][128]
-  // [group][block][weight block of the tile][row]
+  // [group][weight block of the tile][row][block] (QUANT: [block][row])
   float* s_scale = s_part + (SPLIT    ? p.a_rows * (NT + 4)
                              : SWIGLU ? 256
                                       : 8 * 32 * kTurnWords);
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + (QUANT ? p.resident * 32 : kBsGroups * kBsAhead * kSets * 128));
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + (QUANT ? scale_rows(p.resident) * 32 : kBsGroups * kBsAhead * kSets * 128));
   uint64_t* empty = full + kBsMaxStages;
   uint64_t* tfull = empty + kBsMaxStages;
   uint64_t* tempty = tfull + 4;
@@ -655,13 +661,13 @@ __global__ void __launch_bounds__(kBsThreads, 1)
           ok = false;
           return;
         }
-        float* d = s_scale + group * kBsAhead * kSets * 128 + lane;
+        float4* d = reinterpret_cast<float4*>(s_scale) + group * kSets * 128 + lane;
 #pragma unroll
-        for (int i = 0; i < kBsAhead; ++i)
+        for (int h = 0; h < kSets; ++h)
 #pragma unroll
-          for (int h = 0; h < kSets; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[(i * kSets + h) * 128 + 32 * j] = a[i][j] * w[i][h];
+          for (int j = 0; j < 4; ++j)
+            d[h * 128 + 32 * j] = make_float4(a[0][j] * w[0][h], a[1][j] * w[1][h],
+                                              a[2][j] * w[2][h], a[3][j] * w[3][h]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfull[group]);
         if (++group == kBsGroups) {
@@ -725,17 +731,27 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         const uint32_t t_lane =
             tmem + (static_cast<uint32_t>(q * 32) << 16) + (kHalves == 1 ? g * kCols : 0);
         uint32_t v[2][32];
-        float s0 = 0.0f, s1 = 0.0f;
+        float4 s0, s1;  // the scales of kBsAhead blocks
+        s0 = s1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         // wait for a block's buffer and scales, and read its first columns
         auto open = [&](int block, int b, uint32_t ph, bool known) {
-          const int in_group = block & (kBsAhead - 1);
-          if (!QUANT && in_group == 0) ok &= mbar_wait_warp(&sfull[group], gphase, abort_flag);
+          if ((block & (kBsAhead - 1)) == 0) {
+            if constexpr (QUANT) {
+              const float* ss = s_scale + block * 32 + r;
+              s0 = make_float4(ss[0], ss[32], ss[64], ss[96]);
+            } else {
+              ok &= mbar_wait_warp(&sfull[group], gphase, abort_flag);
+              const float4* ss = reinterpret_cast<const float4*>(s_scale) + group * kSets * 128 + r;
+              s0 = ss[kTwoSets || kSets == 1 ? 0 : g * 128];
+              if (kTwoSets) s1 = ss[128];
+            }
+          } else {
+            // the next block's scales move to the front
+            s0 = make_float4(s0.y, s0.z, s0.w, 0.0f);
+            if (kTwoSets) s1 = make_float4(s1.y, s1.z, s1.w, 0.0f);
+          }
           if (!known) ok &= mbar_wait_warp(&tfull[b], ph, abort_flag);
           tc_fence_after();
-          const float* ss = s_scale + r + (QUANT ? block * 32
-                                                 : (group * kBsAhead + in_group) * kSets * 128);
-          s0 = ss[kTwoSets || kSets == 1 ? 0 : g * 128];
-          if (kTwoSets) s1 = ss[128];
           tmem_ld32(t_lane + b * 128, v[0]);
         };
 #pragma unroll
@@ -747,9 +763,10 @@ __global__ void __launch_bounds__(kBsThreads, 1)
           const int nbuf = (buf + kHalves) & (kBufs - 1);
           const uint32_t nphase = bphase ^ (nbuf < kHalves ? 1u : 0u);
           bool next = false;
+          const float c0 = s0.x, c1 = s1.x;
 #pragma unroll
           for (int c = 0; c < kParts; ++c) {
-            const float sc = kTwoSets && c >= 2 ? s1 : s0;
+            const float sc = kTwoSets && c >= 2 ? c1 : c0;
             tmem_ld_wait();
             reg_fence32(v[c & 1]);
             if (c + 1 < kParts) {
@@ -910,7 +927,7 @@ int extra_smem(int a_rows, int resident) {
   return (SPLIT    ? a_rows * (NT + 4) * 4
           : SWIGLU ? 1024
                    : 8 * 32 * kTurnWords * 4) +
-         (QUANT ? resident * 128 : kBsGroups * kBsAhead * NT * 4) +
+         (QUANT ? scale_rows(resident) * 128 : kBsGroups * kBsAhead * NT * 4) +
          (2 * kBsMaxStages + 2 * kBsGroups + 9) * 8 + 8;
 }
 
