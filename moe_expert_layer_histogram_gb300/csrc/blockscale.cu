@@ -181,7 +181,7 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
   a.K = p.K;
   a.out = out;
   a.ldo = ldo;
-  a.out_vec = aligned_to(out, 16) && ldo % 8 == 0;
+  a.out_vec = aligned_to(out, 32) && ldo % 16 == 0;
   a.clamp = clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY;
   a.h_scales = h_scales;
   a.ld_hs = ld_hs;

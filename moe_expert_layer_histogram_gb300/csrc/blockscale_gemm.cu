@@ -238,22 +238,19 @@ struct BsTable {
 };
 
 // group: chunks per item (a pair's two; the second may have no rows), rank:
-// the chunk of the item that is wanted.
-__device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int E, int tiles, int item,
-                                              int group, int rank) {
-  int lo = 0, hi = E;  // chunk_off[lo] * tiles <= item < chunk_off[hi] * tiles
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.chunk_off[mid] * tiles <= item) lo = mid;
-    else hi = mid;
-  }
-  const int chunks = t.chunk_off[lo + 1] - t.chunk_off[lo];
-  const int local = item - t.chunk_off[lo] * tiles;
+// the chunk of the item that is wanted.  e: the expert of this or an earlier
+// item, moved up to the item's: a CTA's items come in expert order, so the
+// search is a step or two of the way.
+__device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int tiles, int item, int group,
+                                              int rank, int& e) {
+  while (t.chunk_off[e + 1] * tiles <= item) ++e;
+  const int chunks = t.chunk_off[e + 1] - t.chunk_off[e];
+  const int local = item - t.chunk_off[e] * tiles;
   BsItem it;
-  it.e = lo;
+  it.e = e;
   it.tile = local / chunks;
-  it.row0 = t.start[lo] + (local % chunks * group + rank) * 128;
-  it.rows = min(128, t.end[lo] - it.row0);
+  it.row0 = t.start[e] + (local - it.tile * chunks) * (128 * group) + rank * 128;
+  it.rows = min(128, t.end[e] - it.row0);
   return it;
 }
 
@@ -301,8 +298,7 @@ __device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], 
 
 // bf16 of 32 consecutive fp32 columns n0 .. n0 + 31 of the warp's 32 rows
 // (lane = row; row0 the first one's, rows how many are real; n0 + 32 may pass
-// N).  Whole 16-byte words where rows allow (VEC): then a lane's 64 bytes are
-// whole sectors.  Else the block is turned in `turn` (32 x kTurnWords words of
+// N).  Whole sectors where the rows start on one (vec).  Else the block is turned in `turn` (32 x kTurnWords words of
 // shared memory, the warp's own), so that a store covers consecutive columns
 // of one row instead of one column of 32 rows.
 constexpr int kTurnWords = 17;  // per row of 32 bf16: odd, so columns differ in bank
@@ -317,10 +313,10 @@ __device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row0, int64_t ldo, 
   }
   if (vec && n0 + 32 <= N) {
     if (lane < rows) {
-      uint4* d = reinterpret_cast<uint4*>(row0 + lane * ldo + n0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        d[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      // (32 bytes each: whole sectors)
+      __nv_bfloat16* d = row0 + lane * ldo + n0;
+      st_global_v8(d, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+      st_global_v8(d + 16, v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]);
     }
     return;
   }
@@ -338,7 +334,11 @@ __device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row0, int64_t ldo, 
 __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
   g = fminf(fmaxf(g, -clamp), clamp);
   u = fminf(fmaxf(u, -clamp), clamp);
-  return g / (1.0f + expf(-g)) * u;
+  // e^-g by the hardware's power of two and an approximate quotient, a few ulp:
+  // as near as the sums of the product
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  return __fdividef(g, 1.0f + e) * u;
 }
 
 // NT: weight rows per item.  SWIGLU: the tile is 128 gate rows and the 128
@@ -431,8 +431,9 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   const int first = blockIdx.x / (SPLIT ? p.split : kGroup);
   const int step = gridDim.x / (SPLIT ? p.split : kGroup);
   const int total = tab.chunk_off[p.E] * p.tiles;
+  int expert = 0;  // of the role's latest item
   auto map_item = [&](int item) {
-    return map_bs_item(tab, p.E, p.tiles, item, kGroup, PAIR ? rank : 0);
+    return map_bs_item(tab, p.tiles, item, kGroup, PAIR ? rank : 0, expert);
   };
 
   if (QUANT && warp > 0 && first < total) {

@@ -211,7 +211,7 @@ struct BlockscaleArgs {
   int E, M, N, K;
   void* out;               // bf16 [M, ldo], or (SwiGLU) codes [M, ldo]
   int64_t ldo;
-  int out_vec;             // bf16 rows start on 16-byte boundaries
+  int out_vec;             // bf16 rows start on 32-byte boundaries
   float clamp;             // SwiGLU (+inf: none)
   float* h_scales;         // SwiGLU [N/256, ld_hs]
   int64_t ld_hs;
