@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     }
     // the codes are read by the tensor core, the scales by the epilogue
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    asm volatile("bar.sync 2, %0;" ::"n"(kBsThreads - 32) : "memory");
+    asm volatile("bar.sync 5, %0;" ::"n"(kBsThreads - 32) : "memory");
   }
 
   if (warp < kBsEpiWarp0) {
@@ -815,18 +815,20 @@ __global__ void __launch_bounds__(kBsThreads, 1)
           }
         }
       } else if constexpr (SWIGLU) {
-        // h of 64 columns, in place of the gate; the block's maximum is over
-        // both warpgroups
+        // h of 64 columns, in place of the gate; the block's maximum is that of
+        // both warps with these rows
         uint32_t amax = 0u;
+        if (active) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          acc[i] = swiglu(acc[i], acc[64 + i], p.clamp);
-          amax = max(amax, abs_bits(acc[i]));
+          for (int i = 0; i < 64; ++i) {
+            acc[i] = swiglu(acc[i], acc[64 + i], p.clamp);
+            amax = max(amax, abs_bits(acc[i]));
+          }
+          s_amax[g * 128 + r] = amax;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+          amax = max(amax, s_amax[(1 - g) * 128 + r]);
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
         }
-        s_amax[g * 128 + r] = amax;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        amax = max(s_amax[r], s_amax[128 + r]);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
         if (live) {
           const BlockQuant bq(amax);
           uint32_t w[16];

@@ -405,6 +405,68 @@ def test_experts_match_64_bits(T, E, topk, H, I, clamp):
     assert err <= 1e-2, err
 
 
+def _route(T, E, topk, seed):
+    from moe_expert_layer_histogram_gb300 import moe_route_permute_static
+    g = torch.Generator().manual_seed(seed)
+    logits = torch.randn(T, E, generator=g).cuda()
+    ids = torch.empty(T, topk, dtype=torch.int32, device="cuda")
+    wt = torch.empty(T, topk, device="cuda")
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    perm = torch.empty(T * topk, dtype=torch.int32, device="cuda")
+    moe_route_permute_static(logits, T, E, topk, ids, wt, off, perm,
+                             torch.cuda.current_stream().cuda_stream)
+    return off, perm
+
+
+@pytest.mark.parametrize("T,E,topk,H,I", [(700, 2, 1, 400, 256), (1500, 3, 2, 272, 128),
+                                          (90, 5, 3, 1040, 128)])
+def test_experts_however_their_rows_are_gathered(T, E, topk, H, I):
+    # all rows against the slices of one
+    # expert each, beside an empty one (fewer rows than tokens: gathered by the
+    # quantiser), and against the two products called one by one: the same
+    # sums in the same order, so the same bits
+    from moe_expert_layer_histogram_gb300 import (blockscale_experts, blockscale_matmul,
+                                                  blockscale_quantize, moe_blockscale_swiglu)
+    x = draw_x(T, H, T)
+    w13, s13 = draw_w(E, 2 * I, H, 1)
+    w2, s2 = draw_w(E, H, I, 2)
+    s13 = s13 * (8.5 / H ** 0.5)
+    off, perm = _route(T, E, topk, 7)
+    y = blockscale_experts(x, perm, off, topk, w13, s13, w2, s2)
+    o = off.tolist()
+    for e in range(E):
+        n, pick = o[e + 1] - o[e], [e, (e + 1) % E]
+        own = torch.tensor([0, n, n], dtype=torch.int32, device="cuda")
+        # (indexing drops the padding of the rows, which H is a multiple of 16 without)
+        part = blockscale_experts(x, perm[o[e]:o[e + 1]].clone(), own, topk,
+                                  w13.view(torch.uint8)[pick].view(torch.float8_e4m3fn), s13[pick],
+                                  w2.view(torch.uint8)[pick].view(torch.float8_e4m3fn), s2[pick])
+        assert torch.equal(part, y[o[e]:o[e + 1]])
+    R = T * topk
+    codes, scales = blockscale_quantize(x, perm, topk)
+    h = torch.empty(R, I, dtype=torch.float8_e4m3fn, device="cuda")
+    hs = torch.empty(I // 128, R, device="cuda")
+    moe_blockscale_swiglu(codes, H, scales, R, w13, H, s13, off, E, R, I, H, 0.0, h, I, hs, R,
+                          torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(blockscale_matmul(h, hs, w2, s2, off), y)
+
+
+def test_slots_outside_the_tokens_give_zero_rows():
+    from moe_expert_layer_histogram_gb300 import blockscale_experts
+    T, E, topk, H, I = 40, 4, 2, 256, 128
+    x = draw_x(T, H, 1)
+    w13, s13 = draw_w(E, 2 * I, H, 1)
+    w2, s2 = draw_w(E, H, I, 2)
+    off, perm = _route(T, E, topk, 3)
+    want = blockscale_experts(x, perm, off, topk, w13, s13, w2, s2)
+    bad = perm.clone()
+    rows = [0, 5, 33, 79]
+    bad[rows] = torch.tensor([-1, T * topk, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+    got = blockscale_experts(x, bad, off, topk, w13, s13, w2, s2)
+    keep = [r for r in range(T * topk) if r not in rows]
+    assert torch.equal(got[keep], want[keep]) and not bool(got[rows].any())
+
+
 def test_same_bits_every_time_streams_and_graphs():
     from moe_expert_layer_histogram_gb300 import blockscale_linear
     x = draw_x(37, 1024, 1)
