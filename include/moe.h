@@ -444,20 +444,19 @@ moe_status moe_blockscale_swiglu(const void *a, int64_t lda,
                                  int K, float clamp_limit, void *h, int64_t ldh,
                                  float *h_scales, int64_t ld_hs, void *stream);
 
-/* Workspace bytes of moe_blockscale_linear for `rows` rows of `cols` columns
- * (inter == 0; 0 for at most 16 rows of at most 10240 columns, which need
- * none) or of
- * moe_blockscale_experts for rows of H = cols and I = inter; 0 for sizes out
- * of range.  The contents need no initialisation and mean nothing after the
- * call.                                                                   */
-size_t moe_blockscale_workspace(int rows, int cols, int inter);
+/* Workspace bytes of moe_blockscale_linear on the current device (0 for small
+ * products, which need none, and for sizes out of range) and of
+ * moe_blockscale_experts.  The contents need no initialisation and mean
+ * nothing after the call.                                                 */
+size_t moe_blockscale_linear_workspace(int M, int N, int K);
+size_t moe_blockscale_experts_workspace(int rows, int H, int I);
 
 /* moe_blockscale_quantize of the bf16 rows x [M, K] and the product with one
- * matrix w [N, K] (transpose_w: [K, N]) in one call.  Few rows (see
- * moe_blockscale_workspace) are quantised by the product's own kernel; for
- * more its set-up and first weight loads overlap the quantisation.  workspace: device, 16-byte aligned,
- * moe_blockscale_workspace(M, K, 0) bytes (may be NULL when that is 0), in
- * use until the work is done.  The rest as moe_blockscale_matmul.          */
+ * matrix w [N, K] (transpose_w: [K, N]) in one call.  Small products quantise
+ * their rows in their own kernel; the others' set-up and first weight loads
+ * overlap the quantisation.  workspace: device, 16-byte aligned,
+ * moe_blockscale_linear_workspace(M, N, K) bytes (may be NULL when that is
+ * 0), in use until the work is done.  The rest as moe_blockscale_matmul.   */
 moe_status moe_blockscale_linear(const void *x, int64_t ldx, const void *w,
                                  int64_t ldw, const float *w_scales, int M,
                                  int N, int K, int transpose_w, void *out,
@@ -471,8 +470,8 @@ moe_status moe_blockscale_linear(const void *x, int64_t ldx, const void *w,
  * through w2 [E, H, I]; both contiguous.  slots int32 [rows] and offsets
  * int32 [E+1] as moe_route_permute_static writes perm and offsets.  H a
  * multiple of 16 and I of 128 (else MOE_ERR_UNSUPPORTED).  workspace: device,
- * 16-byte aligned, moe_blockscale_workspace(rows, H, I) bytes.  rows == 0 is
- * a no-op.  The rest as moe_blockscale_swiglu and moe_blockscale_matmul.   */
+ * 16-byte aligned, moe_blockscale_experts_workspace(rows, H, I) bytes.
+ * rows == 0 is a no-op.  The rest as moe_blockscale_swiglu and moe_blockscale_matmul.   */
 moe_status moe_blockscale_experts(const void *x, int64_t ldx, int T,
                                   const int32_t *slots, int top_k, int rows,
                                   const int32_t *offsets, int E,

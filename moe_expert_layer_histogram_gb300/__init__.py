@@ -48,7 +48,8 @@ EXPORTS = ("moe_create", "moe_prepare_weights", "moe_forward", "moe_forward_batc
            "moe_gemm_ctas",
            "moe_route_permute_static", "moe_balance_workspace", "moe_balance_forward",
            "moe_balance_backward", "moe_blockscale_quantize", "moe_blockscale_matmul",
-           "moe_blockscale_swiglu", "moe_blockscale_workspace", "moe_blockscale_linear",
+           "moe_blockscale_swiglu", "moe_blockscale_linear_workspace",
+           "moe_blockscale_experts_workspace", "moe_blockscale_linear",
            "moe_blockscale_experts", "moe_blockscale_status", "moe_measure_mma_rate", "moe_status_string",
            "moe_destroy")
 
@@ -91,7 +92,8 @@ def lib():
                                         i64, vp]
     L.moe_blockscale_swiglu.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, cf, vp,
                                         i64, vp, i64, vp]
-    L.moe_blockscale_workspace.argtypes = [ci, ci, ci]
+    L.moe_blockscale_linear_workspace.argtypes = [ci, ci, ci]
+    L.moe_blockscale_experts_workspace.argtypes = [ci, ci, ci]
     L.moe_blockscale_linear.argtypes = [vp, i64, vp, i64, vp, ci, ci, ci, ci, vp, i64, vp,
                                         ctypes.c_size_t, vp]
     L.moe_blockscale_experts.argtypes = [vp, i64, ci, vp, ci, ci, vp, ci, vp, vp, vp, vp, ci, ci,
@@ -105,7 +107,9 @@ def lib():
     for name in EXPORTS:
         if name not in ("moe_status_string", "moe_destroy"):
             getattr(L, name).restype = ci
-    L.moe_balance_workspace.restype = L.moe_blockscale_workspace.restype = ctypes.c_size_t
+    for name in ("moe_balance_workspace", "moe_blockscale_linear_workspace",
+                 "moe_blockscale_experts_workspace"):
+        getattr(L, name).restype = ctypes.c_size_t
     _lib = L
     return L
 
@@ -273,8 +277,12 @@ def moe_blockscale_swiglu(a, lda, a_scales, ld_as, w13, ldw, w13_scales, offsets
            "moe_blockscale_swiglu")
 
 
-def moe_blockscale_workspace(rows, cols, inter=0):
-    return lib().moe_blockscale_workspace(rows, cols, inter)
+def moe_blockscale_linear_workspace(M, N, K):
+    return lib().moe_blockscale_linear_workspace(M, N, K)
+
+
+def moe_blockscale_experts_workspace(rows, H, I):
+    return lib().moe_blockscale_experts_workspace(rows, H, I)
 
 
 def moe_blockscale_linear(x, ldx, w, ldw, w_scales, M, N, K, transpose_w, out, ldo, workspace,

@@ -111,7 +111,7 @@ def _linear(x, w, w_scales, transpose_w, out):
         raise ValueError("x: [M, %d] on %s" % (K, dev))
     out, ldo = _result(out, M, N, dev)
     L = lib()
-    nbytes = L.moe_blockscale_workspace(M, K, 0)
+    nbytes = L.moe_blockscale_linear_workspace(M, N, K)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     code = L.moe_blockscale_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, w_scales.data_ptr(), M, N,
                                    K, transpose_w, out.data_ptr(), ldo,
@@ -156,7 +156,7 @@ def blockscale_experts(x, slots, offsets, top_k, w13, w13_scales, w2, w2_scales,
     check(offsets, _I32, (E + 1,), dev, "offsets")
     out, ldo = _result(out, R, H, dev)
     L = lib()
-    nbytes = L.moe_blockscale_workspace(R, H, I)
+    nbytes = L.moe_blockscale_experts_workspace(R, H, I)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     code = L.moe_blockscale_experts(
         x.data_ptr(), ldx, T, slots.data_ptr(), top_k, R, offsets.data_ptr(), E, w13.data_ptr(),

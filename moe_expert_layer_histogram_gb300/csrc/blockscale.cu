@@ -187,10 +187,11 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
   const int sms = device_sms();
   if (!sms) return MOE_ERR_NO_DEVICE;
   BlockscaleMaps maps;
+  // (one expert: all chunks take the largest box)
   const int boxes = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 3 : 4;
   const cuuint64_t adims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M)};
   const cuuint64_t astr[1] = {static_cast<cuuint64_t>(p.lda)};
-  for (int i = 0; i < boxes && !p.x; ++i) {
+  for (int i = p.E == 1 ? boxes - 1 : 0; i < boxes && !p.x; ++i) {
     const cuuint32_t box[2] = {128, 16u << i};
     if (!encode(&maps.a[i], p.a, 2, adims, astr, box)) return MOE_ERR_CUDA;
   }
@@ -323,11 +324,16 @@ moe_status moe_blockscale_swiglu(const void* a, int64_t lda, const float* a_scal
                      static_cast<cudaStream_t>(stream));
 }
 
-size_t moe_blockscale_workspace(int rows, int cols, int inter) {
-  if (rows < 0 || cols < 1 || inter < 0) return 0;
-  if (inter == 0 && blockscale_quantizes(rows, cols)) return 0;
-  return static_cast<size_t>(quantized_bytes(rows, cols) +
-                             (inter ? quantized_bytes(rows, inter) : 0));
+size_t moe_blockscale_linear_workspace(int M, int N, int K) {
+  if (M < 1 || N < 1 || K < 1) return 0;
+  const int sms = device_sms();
+  return blockscale_quantizes(M, N, K, sms ? sms : 152) ? 0
+                                                        : static_cast<size_t>(quantized_bytes(M, K));
+}
+
+size_t moe_blockscale_experts_workspace(int rows, int H, int I) {
+  if (rows < 1 || H < 1 || I < 1) return 0;
+  return static_cast<size_t>(quantized_bytes(rows, H) + quantized_bytes(rows, I));
 }
 
 moe_status moe_blockscale_linear(const void* x, int64_t ldx, const void* w, int64_t ldw,
@@ -339,7 +345,7 @@ moe_status moe_blockscale_linear(const void* x, int64_t ldx, const void* w, int6
   if (st != MOE_OK) return st;
   if (ldx < K || ldo < N) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  const size_t need = moe_blockscale_workspace(M, K, 0);
+  const size_t need = moe_blockscale_linear_workspace(M, N, K);
   if (!x || !out || !aligned_to(x, 2) || !aligned_to(out, 2) || workspace_bytes < need ||
       (need && (!workspace || !aligned_to(workspace, 16))))
     return MOE_ERR_INVALID_ARG;
@@ -379,7 +385,7 @@ moe_status moe_blockscale_experts(const void* x, int64_t ldx, int T, const int32
   if (rows == 0) return MOE_OK;
   if ((!x && T > 0) || !slots || !out || !workspace || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
       !aligned_to(out, 2) || !aligned_to(workspace, 16) ||
-      workspace_bytes < moe_blockscale_workspace(rows, H, I))
+      workspace_bytes < moe_blockscale_experts_workspace(rows, H, I))
     return MOE_ERR_INVALID_ARG;
   if (!device_sms()) return MOE_ERR_NO_DEVICE;
   const Quantized q(workspace, rows, H);

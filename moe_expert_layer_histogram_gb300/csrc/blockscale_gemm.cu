@@ -36,11 +36,12 @@
 // at 128 bytes a cycle against 512 cycles of MMA; in a pair it is 32 KB each
 // way, and both take 512.
 //
-// Few rows of one matrix (QUANT): the CTA's warps but the producer first
-// quantise the bf16 activations of its part of the reduction into shared
-// memory, in the swizzled order the MMAs expect, while the first weight tiles
-// are on their way.  Every CTA does so for itself, but there is no kernel
-// before this one and no workspace.
+// Small products of one matrix (QUANT): the CTA's warps but the producer first
+// quantise the bf16 activations of its rows and its part of the reduction
+// into shared memory, in the swizzled order the MMAs expect, while the first
+// weight tiles are on their way.  Every CTA does so for itself, but there is
+// no kernel before this one and no workspace, which is most of such a call's
+// time.
 //
 // With the weights transposed (input gradient) the reduction runs along the
 // stored rows: the tile is 128 rows of 128 bytes of output columns, an
@@ -218,8 +219,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
-// Rows of 32 scales for QUANT's resident blocks: the epilogue reads them
-// kBsAhead at a time.
+// Rows of scales (one per activation row) for QUANT's resident blocks: the
+// epilogue reads them kBsAhead at a time.
 __host__ __device__ constexpr int scale_rows(int resident) {
   return (resident + kBsAhead - 1) / kBsAhead * kBsAhead;
 }
@@ -345,8 +346,8 @@ __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
 // up rows of the same columns (NT = 256).  SPLIT: the grid is clusters of
 // args.split CTAs, one item each (one expert).
 // PAIR: the grid is clusters of two CTAs that share each item (NT = 256).
-// QUANT: the activations are args.x, at most kBlockscaleFewRows rows, and
-// every CTA (or split cluster) has one item (NT = 128).
+// QUANT: the activations are args.x, and every CTA (or split cluster) has one
+// item (NT = 128, one expert).
 template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR, bool QUANT>
 __global__ void __launch_bounds__(kBsThreads, 1)
     blockscale_gemm_kernel(const __grid_constant__ BlockscaleMaps maps,
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   float* s_scale = s_part + (SPLIT    ? p.a_rows * (NT + 4)
                              : SWIGLU ? 256
                                       : 8 * 32 * kTurnWords);
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + (QUANT ? scale_rows(p.resident) * 32 : kBsGroups * kBsAhead * kSets * 128));
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + (QUANT ? scale_rows(p.resident) * p.a_rows : kBsGroups * kBsAhead * kSets * 128));
   uint64_t* empty = full + kBsMaxStages;
   uint64_t* tfull = empty + kBsMaxStages;
   uint64_t* tempty = tfull + 4;
@@ -437,38 +438,57 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   };
 
   if (QUANT && warp > 0 && first < total) {
-    // Eight lanes per (row, block), 16 columns each.
-    const int nb = static_cast<int>(kb1 - kb0), units = p.M * nb;
-    const int tile = map_item(first).tile;
-    for (int u0 = 0; u0 < units; u0 += (kBsThreads - 32) / 8) {
-      const int u = u0 + (static_cast<int>(threadIdx.x) - 32) / 8, chunk = lane & 7;
-      const int r = u % p.M, kb = kb0 + u / p.M, c0 = kb * 128 + chunk * 16;
-      const bool real = u < units;
-      const __nv_bfloat16* src = p.x + r * p.ldx + c0;
-      uint32_t v[8];
-      if (real && p.x_vec && c0 + 16 <= p.K) {
-        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src)),
-                    hi = __ldg(reinterpret_cast<const uint4*>(src + 8));
-        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
-        v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-      } else {
+    // Eight lanes per (row, block), 16 columns each; four of them are loaded
+    // before the first is quantised.
+    constexpr int kUnits = (kBsThreads - 32) / 8, kBatch = 4;
+    const BsItem it = map_item(first);
+    const int units = it.rows * (kb1 - kb0), chunk = lane & 7;
+    const float* sw = p.w_scales + it.tile * p.w_stride_n;
+    // u / rows by a multiplication (exact: u and rows stay far below 2^16)
+    const uint32_t inv = 0xFFFFFFFFu / static_cast<uint32_t>(it.rows) + 1u;
+    auto block_of = [&](int u) {
+      return it.rows == 1 ? u : static_cast<int>(__umulhi(static_cast<uint32_t>(u), inv));
+    };
+    for (int u0 = (static_cast<int>(threadIdx.x) - 32) / 8; u0 - (u0 % kUnits) < units;
+         u0 += kUnits * kBatch) {
+      uint32_t v[kBatch][8];
+      float w[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t lo = 0u, hi = 0u;
-          if (real && c0 + 2 * i < p.K) lo = reinterpret_cast<const uint16_t*>(src)[2 * i];
-          if (real && c0 + 2 * i + 1 < p.K) hi = reinterpret_cast<const uint16_t*>(src)[2 * i + 1];
-          v[i] = lo | (hi << 16);
+      for (int k = 0; k < kBatch; ++k) {
+        const int u = u0 + k * kUnits;
+        const bool real = u < units;
+        const int block = block_of(u), r = u - block * it.rows, kb = kb0 + block;
+        const int c0 = kb * 128 + chunk * 16;
+        const __nv_bfloat16* src = p.x + (it.row0 + r) * p.ldx + c0;
+        if (real && p.x_vec && c0 + 16 <= p.K) {
+          const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src)),
+                      hi = __ldg(reinterpret_cast<const uint4*>(src + 8));
+          v[k][0] = lo.x, v[k][1] = lo.y, v[k][2] = lo.z, v[k][3] = lo.w;
+          v[k][4] = hi.x, v[k][5] = hi.y, v[k][6] = hi.z, v[k][7] = hi.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t lo = 0u, hi = 0u;
+            if (real && c0 + 2 * i < p.K) lo = reinterpret_cast<const uint16_t*>(src)[2 * i];
+            if (real && c0 + 2 * i + 1 < p.K) hi = reinterpret_cast<const uint16_t*>(src)[2 * i + 1];
+            v[k][i] = lo | (hi << 16);
+          }
         }
+        w[k] = real ? __ldg(sw + kb * p.w_stride_k) : 0.0f;
       }
-      const float sw =
-          real ? __ldg(p.w_scales + tile * p.w_stride_n + kb * p.w_stride_k) : 0.0f;
-      float scale;
-      const uint4 codes = quantize_16(v, scale);
-      if (real) {
-        // row r's 16-byte chunk c lies at chunk c ^ (r % 8)
-        *reinterpret_cast<uint4*>(s_a + (kb - kb0) * a_bytes + r * 128 + ((chunk ^ (r & 7)) << 4)) =
-            codes;
-        if (chunk == 0) s_scale[(kb - kb0) * 32 + r] = scale * sw;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int u = u0 + k * kUnits;
+        if (u - (u % kUnits) >= units) break;  // (the whole warp's)
+        const int block = block_of(u), r = u - block * it.rows;
+        float scale;
+        const uint4 codes = quantize_16(v[k], scale);
+        if (u < units) {
+          // row r's 16-byte chunk c lies at chunk c ^ (r % 8)
+          *reinterpret_cast<uint4*>(s_a + block * a_bytes + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+              codes;
+          if (chunk == 0) s_scale[block * p.a_rows + r] = scale * w[k];
+        }
       }
     }
     // the codes are read by the tensor core, the scales by the epilogue
@@ -484,7 +504,11 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       int stage = 0, slots = 0;
       uint32_t phase = 0;
       bool ok = true;
-      auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
+      // (one expert: the box that all its chunks take, the last one short)
+      auto box_of = [&](int rows) {
+        rows = p.E == 1 ? p.a_rows : rows;
+        return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3;
+      };
       auto a_size = [&](int rows) { return rows > 0 ? (16u << box_of(rows)) * 128u : 0u; };
       const uint32_t full_lead = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
       // announce a stage's bytes (a pair's on rank 0) and load its weight tile
@@ -738,8 +762,8 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         auto open = [&](int block, int b, uint32_t ph, bool known) {
           if ((block & (kBsAhead - 1)) == 0) {
             if constexpr (QUANT) {
-              const float* ss = s_scale + block * 32 + r;
-              s0 = make_float4(ss[0], ss[32], ss[64], ss[96]);
+              const float* ss = s_scale + block * p.a_rows + r;
+              s0 = make_float4(ss[0], ss[p.a_rows], ss[2 * p.a_rows], ss[3 * p.a_rows]);
             } else {
               ok &= mbar_wait_warp(&sfull[group], gphase, abort_flag);
               const float4* ss = reinterpret_cast<const float4*>(s_scale) + group * kSets * 128 + r;
@@ -930,7 +954,7 @@ int extra_smem(int a_rows, int resident) {
   return (SPLIT    ? a_rows * (NT + 4) * 4
           : SWIGLU ? 1024
                    : 8 * 32 * kTurnWords * 4) +
-         (QUANT ? scale_rows(resident) * 128 : kBsGroups * kBsAhead * NT * 4) +
+         (QUANT ? scale_rows(resident) * a_rows * 4 : kBsGroups * kBsAhead * NT * 4) +
          (2 * kBsMaxStages + 2 * kBsGroups + 9) * 8 + 8;
 }
 
@@ -951,7 +975,6 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
   if (ready != cudaSuccess) return ready;
   const int a_bytes = p.a_rows * 128;
   const int stage = (QUANT ? 0 : a_bytes) + NT / (PAIR ? 2 : 1) * 128;
-  p.resident = QUANT ? ((p.K + 127) / 128 + p.split - 1) / p.split : 0;
   const int fixed = 1024 + extra_smem<NT, SWIGLU, SPLIT, QUANT>(p.a_rows, p.resident) +
                     p.resident * a_bytes + (3 * p.E + 1) * 4;
   p.stages = std::min(kBsMaxStages, (kBsSmemLimit - fixed) / stage);
@@ -977,23 +1000,62 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
 
 }  // namespace
 
+namespace {
+
+// How a product is cut up.  NT = 256 once its items fill the SMs, else 128
+// and, for one expert, a reduction split over a cluster until they do.
+struct Plan {
+  bool wide;
+  int a_rows, tiles, split, resident;
+  int64_t items;  // an upper bound where the experts' rows are not known
+};
+
+Plan plan_product(int M, int N, int K, int E, bool swiglu, int sms) {
+  Plan p{};
+  const int64_t chunks = E == 1 ? (M + 127) / 128 : std::min<int64_t>(E, M) + M / 128;
+  const int kb = (K + 127) / 128;
+  p.a_rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  p.wide = swiglu || chunks * ((N + 255) / 256) >= sms;
+  const int nt = p.wide ? 256 : 128;
+  p.tiles = swiglu ? N / 256 : (N + nt - 1) / nt;
+  p.items = chunks * p.tiles;
+  p.split = 1;
+  if (E == 1 && (!swiglu || M <= kBsSplitSwigluRows))
+    while (p.split < 8 && p.items * p.split * 2 <= sms && p.split * 2 <= kb) p.split *= 2;
+  p.resident = (kb + p.split - 1) / p.split;
+  return p;
+}
+
+// Row blocks that a CTA quantises for itself at most (QUANT).  48 rows x 2048
+// into 7168 (384 a CTA): 14.1 us on the GPU where a quantising kernel and the
+// product take 9.7, but 16.4 us a call where their two launches and the
+// workspace take 23.4; one row x 7168 into 4096: 10.4 against 11.3, and 12.3
+// against 24.
+constexpr int kBsQuantUnits = 640;
+
+}  // namespace
+
 // See internal.h.
+bool blockscale_quantizes(int M, int N, int K, int sms) {
+  const Plan p = plan_product(M, N, K, 1, false, sms);
+  const int64_t smem = p.resident * p.a_rows * 128 + 2 * 128 * 128 + 1024 +
+                       extra_smem<128, false, true, true>(p.a_rows, p.resident) + 16;
+  return !p.wide && std::min(M, 128) * p.resident <= kBsQuantUnits && smem <= kBsSmemLimit &&
+         (p.items * p.split <= sms || M <= 16);
+}
+
 cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool swiglu,
                               bool transpose, bool pdl, int sms, cudaStream_t s) {
-  const int64_t chunks =
-      p.E == 1 ? (p.M + 127) / 128 : std::min<int64_t>(p.E, p.M) + p.M / 128;
-  p.a_rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const bool wide = swiglu || (!p.x && chunks * ((p.N + 255) / 256) >= sms);
-  const int nt = wide ? 256 : 128;
-  p.tiles = swiglu ? p.N / 256 : (p.N + nt - 1) / nt;
-  const int64_t items = chunks * p.tiles;
-  if (items > INT32_MAX) return cudaErrorInvalidValue;
-  p.split = 1;
-  if (p.E == 1 && (!swiglu || p.M <= kBsSplitSwigluRows))
-    while (p.split < 8 && items * p.split * 2 <= sms && p.split * 2 <= (p.K + 127) / 128)
-      p.split *= 2;
+  const Plan plan = plan_product(p.M, p.N, p.K, p.E, swiglu, sms);
+  if (plan.items * plan.split > INT32_MAX) return cudaErrorInvalidValue;
+  p.a_rows = plan.a_rows;
+  p.tiles = plan.tiles;
+  p.split = plan.split;
+  p.resident = p.x ? plan.resident : 0;
+  const bool wide = plan.wide;
+  const int items = static_cast<int>(plan.items);
   if (p.split > 1) {
-    const int grid = static_cast<int>(items) * p.split;
+    const int grid = items * p.split;
     if (p.x)
       return transpose ? launch_bs<128, false, true, true, false, true>(maps, p, grid, pdl, s)
                        : launch_bs<128, false, false, true, false, true>(maps, p, grid, pdl, s);
@@ -1002,12 +1064,11 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
                      : launch_bs<128, false, false, true>(maps, p, grid, pdl, s);
   }
   if (p.x)
-    return transpose
-               ? launch_bs<128, false, true, false, false, true>(maps, p, items, pdl, s)
-               : launch_bs<128, false, false, false, false, true>(maps, p, items, pdl, s);
-  const int grid = static_cast<int>(std::min<int64_t>(sms, items));
+    return transpose ? launch_bs<128, false, true, false, false, true>(maps, p, items, pdl, s)
+                     : launch_bs<128, false, false, false, false, true>(maps, p, items, pdl, s);
+  const int grid = std::min(sms, items);
   if (wide && p.M / 256 >= p.E) {
-    const int pairs = static_cast<int>(std::min<int64_t>(sms / 2, (items + 1) / 2));
+    const int pairs = std::min(sms / 2, (items + 1) / 2);
     if (swiglu) return launch_bs<256, true, false, false, true>(maps, p, 2 * pairs, pdl, s);
     return transpose ? launch_bs<256, false, true, false, true>(maps, p, 2 * pairs, pdl, s)
                      : launch_bs<256, false, false, false, true>(maps, p, 2 * pairs, pdl, s);

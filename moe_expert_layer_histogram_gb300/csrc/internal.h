@@ -193,14 +193,6 @@ struct BlockscaleMaps {
   CUtensorMap w;     // codes [E, N, K] (transposed: [E, K, N]), boxes of 128 x 128
 };
 
-// Activations of so few rows and columns are quantised by the product kernel:
-// 80 blocks of 16 rows are 160 KB of codes and 10 KB of scales in shared
-// memory, beside three stages of weights.
-constexpr int kBlockscaleFewRows = 16, kBlockscaleFewCols = 80 * 128;
-inline bool blockscale_quantizes(int rows, int cols) {
-  return rows <= kBlockscaleFewRows && cols <= kBlockscaleFewCols;
-}
-
 struct BlockscaleArgs {
   const float* a_scales;   // [ceil(K/128), ld_as]
   int64_t ld_as;
@@ -216,7 +208,7 @@ struct BlockscaleArgs {
   float* h_scales;         // SwiGLU [N/256, ld_hs]
   int64_t ld_hs;
   const __nv_bfloat16* x;  // the activations in bf16, quantised by the product kernel (then
-  int64_t ldx;             // blockscale_quantizes(M, K), E = 1, a_scales unused), or null
+  int64_t ldx;             // blockscale_quantizes, E = 1, a_scales unused), or null
   int x_vec;               // x's rows start on 16-byte boundaries
   int early;               // the kernel before this one is the library's own and writes
                            // neither weights nor offsets
@@ -224,6 +216,9 @@ struct BlockscaleArgs {
   int a_rows, tiles, stages, split, resident;
 };
 
+// Whether a product of one matrix is small enough to quantise its activations
+// itself (args.x): a CTA's share of them stays in its shared memory.
+bool blockscale_quantizes(int M, int N, int K, int sms);
 // swiglu: N = 2 I, gate and up rows; transpose: weights stored [E, K, N].
 // pdl: programmatic dependent launch.
 cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs args, bool swiglu,
