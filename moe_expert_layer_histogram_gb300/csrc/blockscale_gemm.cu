@@ -255,35 +255,49 @@ __device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int tiles, int i
   return it;
 }
 
-// One warp fills the table: lane l takes kMaxExperts / 32 consecutive experts.
+// One warp fills the table, 32 experts at a time; all offsets are on their way
+// before the first is used.
 __device__ __forceinline__ void fill_bs_table(const BlockscaleArgs& p, const BsTable& t, int group,
                                               int lane) {
-  const int per_item = 128 * group;
+  if (!p.offsets) {
+    if (lane == 0) {
+      t.start[0] = 0;
+      t.end[0] = p.M;
+      t.chunk_off[0] = 0;
+      t.chunk_off[1] = (p.M + 128 * group - 1) / (128 * group);
+    }
+    return;
+  }
   constexpr int kPer = kMaxExperts / 32;
-  int chunks = 0;
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane * kPer + i;
-    if (e >= p.E) break;
-    const int r0 = p.offsets ? min(max(p.offsets[e], 0), p.M) : 0;
-    const int r1 = p.offsets ? min(max(p.offsets[e + 1], r0), p.M) : p.M;
-    t.start[e] = r0;
-    t.end[e] = r1;
-    chunks += (r1 - r0 + per_item - 1) / per_item;
-  }
-  int inc = chunks;
+  const int per_item = 128 * group;
+  int first[kPer], last[kPer];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-    if (lane >= off) inc += o;
-  }
-  int run = inc - chunks;
   for (int i = 0; i < kPer; ++i) {
-    const int e = lane * kPer + i;
-    if (e >= p.E) break;
-    t.chunk_off[e] = run;
-    run += (t.end[e] - t.start[e] + per_item - 1) / per_item;
-    if (e == p.E - 1) t.chunk_off[p.E] = run;
+    const int e = 32 * i + lane;
+    first[i] = e < p.E ? p.offsets[e] : 0;
+    last[i] = e < p.E ? p.offsets[e + 1] : 0;
   }
+  int run = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (32 * i >= p.E) break;
+    const int e = 32 * i + lane;
+    const int r0 = min(max(first[i], 0), p.M), r1 = min(max(last[i], r0), p.M);
+    const int chunks = e < p.E ? (r1 - r0 + per_item - 1) / per_item : 0;
+    int inc = chunks;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    if (e < p.E) {
+      t.start[e] = r0;
+      t.end[e] = r1;
+      t.chunk_off[e] = run + inc - chunks;
+    }
+    run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+  }
+  if (lane == 0) t.chunk_off[p.E] = run;
 }
 
 // acc += s v for 32 columns.
