@@ -21,6 +21,13 @@ import torch
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def no_wait_gave_up():
+    from moe_expert_layer_histogram_gb300 import moe_blockscale_status
+    yield
+    assert moe_blockscale_status() == 0
+
+
 def cdiv(a, b):
     return (a + b - 1) // b
 
@@ -486,6 +493,22 @@ def test_same_bits_every_time_streams_and_graphs():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, blockscale_linear(x2, w[0], s[0]))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 7168), (16, 1024, 2000), (48, 2048, 2048),
+                                   (300, 600, 1536)])
+def test_many_calls_in_a_row(M, N, K):
+    # launches that find the weights in L2 and launches that do not: the copies
+    # and the tensor pipe take turns in being first
+    from moe_expert_layer_histogram_gb300 import blockscale_linear
+    x = draw_x(M, K, 1)
+    w, s = draw_w(1, N, K, 2)
+    want = blockscale_linear(x, w[0], s[0])
+    flush = torch.empty(1 << 27, dtype=torch.int16, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            flush.fill_(i)
+        assert torch.equal(blockscale_linear(x, w[0], s[0]), want)
 
 
 def test_back_to_back_calls_do_not_disturb_each_other():
