@@ -294,7 +294,10 @@ __global__ void __launch_bounds__(32 * kBalanceWarps)
 
 // Few tokens: the whole forward in one cluster of up to eight CTAs, one warp
 // per token; the CTAs' sums are joined in rank order through distributed
-// shared memory, so there is no second launch and no workspace.
+// shared memory, so there is no second launch and no workspace.  Against the
+// kernels for many tokens: 64 tokens of 64 experts 4.9 us and 7.1, 256 5.7 and
+// 7.3, 512 7.6 and 7.5, 512 of 384 experts 10.4 and 8.8 (with a launch less on
+// the host), 1024 of 64 11.0 and 7.3.
 constexpr int kSmallCluster = 8;
 constexpr int kSmallTokens = 2 * kBalanceWarps * kSmallCluster;
 

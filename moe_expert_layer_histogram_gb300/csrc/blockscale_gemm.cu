@@ -8,33 +8,35 @@
 // e4m3 product therefore goes into a TMEM buffer of its own (four MMAs of
 // K = 32, the first one overwriting), and the epilogue warps add it, times
 // sa sw, to fp32 accumulators that stay in registers for the whole item: one
-// fused multiply-add per output and block.  (Plain ones: the packed pair
-// instruction took 333 cycles per 128 x 256 block where these take 263.)
+// fused multiply-add per output and block, two outputs to an instruction.
 //
 // A buffer's turn is an MMA, the hand-off to the epilogue, its reads and the
-// hand-off back.  TMEM holds two buffers of 256 columns (or four of 128), and
-// the epilogue hands a buffer back as soon as it has read it.  The issuing
-// warp stays whole and elects a thread for each group of MMAs: the same code
-// under `lane == 0` spent 631 cycles on a block (two waits, four MMAs, two
-// commits), longer than the tensor pipe's 512.
+// hand-off back, about 600 cycles besides the work.  So TMEM holds four buffers
+// of 128 columns, and the epilogue hands a buffer back as soon as it has read
+// it.  An issuing warp stays whole and elects a thread for each group of MMAs:
+// the same code under `lane == 0` spent 631 cycles on a block, longer than the
+// tensor pipe's 512.  For the same reason the epilogue's waits branch on votes
+// and its arrivals are predicated.
 //
 // Structure: one persistent CTA per SM walks the items (expert, tile of NT
 // weight rows, chunk of at most 128 rows), expert-major, then tile, then
 // chunk, so that CTAs running together share a weight tile in L2.  Warp 0
 // (one thread) fills a ring of stages by TMA: 128 columns of the chunk's
 // rows (box height 16 / 32 / 64 / 128, so short chunks pull no padding) and
-// of the NT weight rows.  Warp 1 issues the MMAs.  Warp 2 runs ahead through
-// the same blocks and leaves every row's scale product in a ring in shared
-// memory.  Warps 4-11 are the epilogue: warp w reads TMEM lanes
-// 32 (w % 4).. and half of the tile's columns, so a thread owns one row and
-// NT / 2 columns.
+// of the NT weight rows.  Of a tile of 256 rows each half is a product of its
+// own: warp 1 issues the first half's MMAs and warp 3 the second's, into two
+// buffers each, read by one epilogue warpgroup each (warps 4-7 and 8-11; warp
+// w reads TMEM lanes 32 (w % 4)..).  A tile of 128 has one issuer and all four
+// buffers, and each warpgroup reads half of the columns.  Warp 2 runs ahead
+// through the same blocks and leaves the product of the scales of every row,
+// four blocks at a time, in a ring in shared memory.
 //
-// Chunks of full experts come in pairs (PAIR): a cluster of two CTAs shares
-// one MMA of 256 rows x 256 columns (cta_group::2), each CTA loading its own
-// 128 rows and half of the weight tile.  A single CTA's 128 x 256 block moves
-// 48 KB into shared memory and reads 48 KB of operands back out, 768 cycles
-// at 128 bytes a cycle against 512 cycles of MMA; in a pair it is 32 KB each
-// way, and both take 512.
+// Full chunks come in pairs (PAIR): a cluster of two CTAs shares MMAs of 256
+// rows x 128 columns (cta_group::2), each CTA loading its own 128 rows and
+// half of the weight tile.  A single CTA's 128 x 256 block moves 48 KB into
+// shared memory and reads 64 KB of operands back out (the rows once for each
+// half), 875 cycles at 128 bytes a cycle against 512 of MMA; in a pair it is
+// 32 and 48 KB, 640 cycles.
 //
 // Small products of one matrix (QUANT): the CTA's warps but the producer first
 // quantise the bf16 activations of its rows and its part of the reduction
@@ -51,6 +53,11 @@
 // 2, 4 or 8 CTAs splits the reduction of each item and joins its fp32
 // partial sums through distributed shared memory, in rank order, so the
 // result does not depend on timing.
+//
+// What bounds it: with many rows, the shared memory that feeds the MMAs
+// (8192 x 4096 x 7168: 183 us, 2620 TFLOP/s; a build without the epilogue's
+// sums took 163); with few rows per expert, the weights' bytes (64 tokens over
+// 64 experts of 44 MB: 420 us, 6.7 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -75,7 +82,11 @@ constexpr int kBsMaxStages = 8;
 constexpr int kBsAhead = 4;       // blocks whose scales are passed on together, a float4 per row
 constexpr int kBsGroups = 2;      // such groups in the scale ring
 constexpr int kBsSmemLimit = 232448;
-constexpr int kBsSplitSwigluRows = 32;  // largest chunk of the SwiGLU product that is split
+// Most rows of one expert whose SwiGLU product is split: the partial sums lie
+// beside the ring of stages.  A whole call, split against not, 7168 -> 2048:
+// 32 rows 30.4 us against 40.4, 64 rows 32.9 against 41, 100 rows 46.1 against
+// 41.7 (two stages are left).
+constexpr int kBsSplitSwigluRows = 64;
 
 __device__ int g_blockscale_status;
 
@@ -313,9 +324,10 @@ __device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], 
 
 // bf16 of 32 consecutive fp32 columns n0 .. n0 + 31 of the warp's 32 rows
 // (lane = row; row0 the first one's, rows how many are real; n0 + 32 may pass
-// N).  Whole sectors where the rows start on one (vec).  Else the block is turned in `turn` (32 x kTurnWords words of
-// shared memory, the warp's own), so that a store covers consecutive columns
-// of one row instead of one column of 32 rows.
+// N).  Whole sectors where the rows start on one (vec).  Else the block is
+// turned in `turn` (32 x kTurnWords words of shared memory, the warp's own),
+// so that a store covers consecutive columns of one row instead of one column
+// of 32 rows.
 constexpr int kTurnWords = 17;  // per row of 32 bf16: odd, so columns differ in bank
 __device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row0, int64_t ldo, int rows, int lane,
                                               int n0, int N, bool vec, uint32_t* turn,
@@ -387,7 +399,9 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   float* s_scale = s_part + (SPLIT    ? p.a_rows * (NT + 4)
                              : SWIGLU ? 256
                                       : 8 * 32 * kTurnWords);
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + (QUANT ? scale_rows(p.resident) * p.a_rows : kBsGroups * kBsAhead * kSets * 128));
+  const int scale_words =
+      QUANT ? scale_rows(p.resident) * p.a_rows : kBsGroups * kBsAhead * kSets * 128;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + scale_words);
   uint64_t* empty = full + kBsMaxStages;
   uint64_t* tfull = empty + kBsMaxStages;
   uint64_t* tempty = tfull + 4;
@@ -991,6 +1005,8 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
   const int stage = (QUANT ? 0 : a_bytes) + NT / (PAIR ? 2 : 1) * 128;
   const int fixed = 1024 + extra_smem<NT, SWIGLU, SPLIT, QUANT>(p.a_rows, p.resident) +
                     p.resident * a_bytes + (3 * p.E + 1) * 4;
+  // (either eight stages of 16 KB and more or all that there is: one CTA to an
+  // SM, so no CTA waits for TMEM that another of its cluster holds)
   p.stages = std::min(kBsMaxStages, (kBsSmemLimit - fixed) / stage);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
@@ -1016,8 +1032,14 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
 
 namespace {
 
-// How a product is cut up.  NT = 256 once its items fill the SMs, else 128
-// and, for one expert, a reduction split over a cluster until they do.
+// How a product is cut up.  An item of 256 columns takes about 1.5 times as
+// long as one of 128 (4096 x 4096 x 7168: 105 us in 256s, 133 in 128s), so
+// NT = 256 where its rounds of items over the SMs are at most two thirds of
+// those of NT = 128 (1024 x 4096 x 7168, one round against two: 30 us, 41 in
+// 128s; 512 rows, one round of either: 128).  Fewer items than half the SMs,
+// of one expert: the reduction is split over a cluster until they fill them
+// (333 x 1001 x 2000: 8.2 us, 10.7 in one piece; 512 x 1024 x 7168: 11.5 and
+// 21.6).
 struct Plan {
   bool wide;
   int a_rows, tiles, split, resident;
@@ -1029,12 +1051,13 @@ Plan plan_product(int M, int N, int K, int E, bool swiglu, int sms) {
   const int64_t chunks = E == 1 ? (M + 127) / 128 : std::min<int64_t>(E, M) + M / 128;
   const int kb = (K + 127) / 128;
   p.a_rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  p.wide = swiglu || chunks * ((N + 255) / 256) >= sms;
+  auto rounds = [&](int nt) { return (chunks * ((N + nt - 1) / nt) + sms - 1) / sms; };
+  p.wide = swiglu || 3 * rounds(256) <= 2 * rounds(128);
   const int nt = p.wide ? 256 : 128;
   p.tiles = swiglu ? N / 256 : (N + nt - 1) / nt;
   p.items = chunks * p.tiles;
   p.split = 1;
-  if (E == 1 && (!swiglu || M <= kBsSplitSwigluRows))
+  if (E == 1 && (swiglu ? M <= kBsSplitSwigluRows : !p.wide))
     while (p.split < 8 && p.items * p.split * 2 <= sms && p.split * 2 <= kb) p.split *= 2;
   p.resident = (kb + p.split - 1) / p.split;
   return p;
@@ -1081,7 +1104,10 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
     return transpose ? launch_bs<128, false, true, false, false, true>(maps, p, items, pdl, s)
                      : launch_bs<128, false, false, false, false, true>(maps, p, items, pdl, s);
   const int grid = std::min(sms, items);
-  if (wide && p.M / 256 >= p.E) {
+  // (pairs for full chunks: one expert of 8192 rows, 4096 x 7168, 183 us
+  // against 192; 8 experts of 1024 rows, a whole call, 93 against 100; 64 of
+  // 256 rows, where the second chunk is often short, 195 against 174)
+  if (wide && p.M / 1024 >= p.E) {
     const int pairs = std::min(sms / 2, (items + 1) / 2);
     if (swiglu) return launch_bs<256, true, false, false, true>(maps, p, 2 * pairs, pdl, s);
     return transpose ? launch_bs<256, false, true, false, true>(maps, p, 2 * pairs, pdl, s)

@@ -271,8 +271,9 @@ def offsets_of(counts, first=0):
     return (off + first).cuda()
 
 
-GROUPS = [[700, 0, 513, 1, 1500, 129, 257, 640], [1025, 128, 1], [0, 5, 1, 0, 130, 17, 0], [1, 1, 1, 1], [128, 129, 127, 256], [0, 0, 0, 3],
-          [300, 0, 0, 1], [2] * 40, [0] * 511 + [9], [33, 64, 65, 31, 32, 16, 15]]
+GROUPS = [[700, 0, 513, 1, 1500, 129, 257, 640], [1025, 128, 1], [0, 5, 1, 0, 130, 17, 0],
+          [1, 1, 1, 1], [128, 129, 127, 256], [0, 0, 0, 3], [300, 0, 0, 1], [2] * 40,
+          [0] * 511 + [9], [33, 64, 65, 31, 32, 16, 15], [2100, 77], [1, 3300, 129], [0, 2049]]
 
 
 @pytest.mark.parametrize("transpose", [False, True])
@@ -331,7 +332,9 @@ def swiglu_ref(a, w13, s13, clamp):
 @pytest.mark.parametrize("counts,I,K", [([1], 128, 128), ([7, 0, 20], 256, 400),
                                         ([0, 129, 1, 64], 384, 272), ([300, 33], 128, 1040),
                                         ([2] * 20, 640, 256), ([600, 257, 0, 300], 256, 272),
-                                        ([1025], 384, 400)])
+                                        ([1025], 384, 400), ([64], 256, 1040), ([37], 128, 528),
+                                        ([65], 256, 1040), ([2500, 300], 256, 272),
+                                        ([5, 3200, 0], 128, 144)])
 def test_swiglu_codes(counts, I, K, clamp):
     from moe_expert_layer_histogram_gb300 import blockscale_quantize, moe_blockscale_swiglu
     E, M = len(counts), sum(counts)
