@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "blockscale_quant.cuh"
 #include "internal.h"
@@ -41,7 +42,8 @@ __global__ void __launch_bounds__(256)
   const int slot = slots ? slots[r] : r, src = slots ? slot / top_k : r;
   const bool in = real && slot >= 0 && src < x_rows;
   const __nv_bfloat16* p = x + src * ldx + c0;
-  uint32_t v[8];  // pairs of bf16
+  uint32_t vs[1][8];  // pairs of bf16
+  uint32_t(&v)[8] = vs[0];
   if (VEC && in && c0 + 16 <= cols) {
     const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 8);
     v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
@@ -55,8 +57,11 @@ __global__ void __launch_bounds__(256)
       v[i] = lo | (hi << 16);
     }
   }
-  float scale;
-  const uint4 w4 = quantize_16(v, scale);
+  float scales1[1];
+  uint4 codes1[1];
+  quantize_16(vs, codes1, scales1);
+  const float scale = scales1[0];
+  const uint4 w4 = codes1[0];
   const bool first = (lane & 7) == 0 && b * kBlk < cols;
   if (first) scales[b * ld_scales + r] = scale;
   if (!real) return;
@@ -160,32 +165,40 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// SM count of the current device, 0 unless it is an sm_103 one (looked up
-// once per device).
-int device_sms() {
+// The current device, null unless it is an sm_103 one (looked up once per
+// device).
+const BlockscaleDevice* current_device() {
   constexpr int kMaxDevices = 64;
-  static int cached[kMaxDevices] = {};  // 0: not looked up, -1: not usable
+  struct Entry {
+    std::once_flag once;
+    bool usable = false;
+    BlockscaleDevice d{};
+  };
+  static Entry entries[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
-    return 0;
+    return nullptr;
   }
-  if (cached[dev] == 0) {
-    int major = 0, minor = 0, sms = 0;
+  Entry& e = entries[dev];
+  std::call_once(e.once, [&] {
+    int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cached[dev] = major == 10 && minor == 3 && tensor_map_encoder() ? sms : -1;
-  }
-  return std::max(cached[dev], 0);
+    cudaDeviceGetAttribute(&e.d.sms, cudaDevAttrMultiProcessorCount, dev);
+    e.usable = major == 10 && minor == 3 && tensor_map_encoder() &&
+               blockscale_clusters(&e.d) == cudaSuccess;
+    cudaGetLastError();
+  });
+  return e.usable ? &e.d : nullptr;
 }
 
 // early: the product follows the library's own kernel on the stream and may
 // start while it runs (programmatic dependent launch).
 moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, float clamp,
                        float* h_scales, int64_t ld_hs, bool early, cudaStream_t s) {
-  const int sms = device_sms();
-  if (!sms) return MOE_ERR_NO_DEVICE;
+  const BlockscaleDevice* d = current_device();
+  if (!d) return MOE_ERR_NO_DEVICE;
   BlockscaleMaps maps;
   // (one expert: all chunks take the largest box)
   const int boxes = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 3 : 4;
@@ -224,7 +237,7 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
   a.ldx = p.ldx;
   a.x_vec = aligned_to(p.x, 16) && p.ldx % 8 == 0;
   a.early = early;
-  return launch_blockscale(maps, a, swiglu, p.transpose, early, sms, s) == cudaSuccess
+  return launch_blockscale(maps, a, swiglu, p.transpose, early, *d, s) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -328,9 +341,8 @@ moe_status moe_blockscale_swiglu(const void* a, int64_t lda, const float* a_scal
 
 size_t moe_blockscale_linear_workspace(int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1) return 0;
-  const int sms = device_sms();
-  return blockscale_quantizes(M, N, K, sms ? sms : 152) ? 0
-                                                        : static_cast<size_t>(quantized_bytes(M, K));
+  const BlockscaleDevice* d = current_device();
+  return d && blockscale_quantizes(M, N, K, *d) ? 0 : static_cast<size_t>(quantized_bytes(M, K));
 }
 
 size_t moe_blockscale_experts_workspace(int rows, int H, int I) {
@@ -351,7 +363,7 @@ moe_status moe_blockscale_linear(const void* x, int64_t ldx, const void* w, int6
   if (!x || !out || !aligned_to(x, 2) || !aligned_to(out, 2) || workspace_bytes < need ||
       (need && (!workspace || !aligned_to(workspace, 16))))
     return MOE_ERR_INVALID_ARG;
-  if (!device_sms()) return MOE_ERR_NO_DEVICE;
+  if (!current_device()) return MOE_ERR_NO_DEVICE;
   if (!need) {
     p.x = x;
     p.ldx = ldx;
@@ -389,7 +401,7 @@ moe_status moe_blockscale_experts(const void* x, int64_t ldx, int T, const int32
       !aligned_to(out, 2) || !aligned_to(workspace, 16) ||
       workspace_bytes < moe_blockscale_experts_workspace(rows, H, I))
     return MOE_ERR_INVALID_ARG;
-  if (!device_sms()) return MOE_ERR_NO_DEVICE;
+  if (!current_device()) return MOE_ERR_NO_DEVICE;
   const Quantized q(workspace, rows, H);
   uint8_t* rest = static_cast<uint8_t*>(workspace) + quantized_bytes(rows, H);
   const Quantized h(rest, rows, I);

@@ -61,6 +61,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "blockscale_quant.cuh"
 #include "internal.h"
@@ -466,9 +467,10 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   };
 
   if (QUANT && warp > 0 && first < total) {
-    // Eight lanes per (row, block), 16 columns each; four of them are loaded
-    // before the first is quantised.
-    constexpr int kUnits = (kBsThreads - 32) / 8, kBatch = 4;
+    // Eight lanes per (row, block), 16 columns each: kUnits of those at a time,
+    // three times over (all loads before the first is used) while more than
+    // one time is left.
+    constexpr int kUnits = (kBsThreads - 32) / 8;
     const BsItem it = map_item(first);
     const int units = it.rows * (kb1 - kb0), chunk = lane & 7;
     const float* sw = p.w_scales + it.tile * p.w_stride_n;
@@ -477,48 +479,56 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     auto block_of = [&](int u) {
       return it.rows == 1 ? u : static_cast<int>(__umulhi(static_cast<uint32_t>(u), inv));
     };
-    for (int u0 = (static_cast<int>(threadIdx.x) - 32) / 8; u0 - (u0 % kUnits) < units;
-         u0 += kUnits * kBatch) {
-      uint32_t v[kBatch][8];
-      float w[kBatch];
+    auto quantise = [&](auto batch, int u0) {
+      constexpr int N = decltype(batch)::value;
+      uint32_t v[N][8];
+      float w[N];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < N; ++k) {
         const int u = u0 + k * kUnits;
-        const bool real = u < units;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = 0u;
+        w[k] = 0.0f;
+        if (u >= units) continue;
         const int block = block_of(u), r = u - block * it.rows, kb = kb0 + block;
         const int c0 = kb * 128 + chunk * 16;
         const __nv_bfloat16* src = p.x + (it.row0 + r) * p.ldx + c0;
-        if (real && p.x_vec && c0 + 16 <= p.K) {
+        w[k] = __ldg(sw + kb * p.w_stride_k);
+        if (p.x_vec && c0 + 16 <= p.K) {
           const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src)),
                       hi = __ldg(reinterpret_cast<const uint4*>(src + 8));
           v[k][0] = lo.x, v[k][1] = lo.y, v[k][2] = lo.z, v[k][3] = lo.w;
           v[k][4] = hi.x, v[k][5] = hi.y, v[k][6] = hi.z, v[k][7] = hi.w;
-        } else {
+        } else if (c0 < p.K) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t lo = 0u, hi = 0u;
-            if (real && c0 + 2 * i < p.K) lo = reinterpret_cast<const uint16_t*>(src)[2 * i];
-            if (real && c0 + 2 * i + 1 < p.K) hi = reinterpret_cast<const uint16_t*>(src)[2 * i + 1];
+            if (c0 + 2 * i < p.K) lo = reinterpret_cast<const uint16_t*>(src)[2 * i];
+            if (c0 + 2 * i + 1 < p.K) hi = reinterpret_cast<const uint16_t*>(src)[2 * i + 1];
             v[k][i] = lo | (hi << 16);
           }
         }
-        w[k] = real ? __ldg(sw + kb * p.w_stride_k) : 0.0f;
       }
+      uint4 codes[N];
+      float scale[N];
+      quantize_16(v, codes, scale);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < N; ++k) {
         const int u = u0 + k * kUnits;
-        if (u - (u % kUnits) >= units) break;  // (the whole warp's)
-        const int block = block_of(u), r = u - block * it.rows;
-        float scale;
-        const uint4 codes = quantize_16(v[k], scale);
         if (u < units) {
+          const int block = block_of(u), r = u - block * it.rows;
           // row r's 16-byte chunk c lies at chunk c ^ (r % 8)
           *reinterpret_cast<uint4*>(s_a + block * a_bytes + r * 128 + ((chunk ^ (r & 7)) << 4)) =
-              codes;
-          if (chunk == 0) s_scale[block * p.a_rows + r] = scale * w[k];
+              codes[k];
+          if (chunk == 0) s_scale[block * p.a_rows + r] = scale[k] * w[k];
         }
       }
-    }
+    };
+    const int unit = (static_cast<int>(threadIdx.x) - 32) / 8;
+    int done = 0;
+    for (; done + kUnits < units; done += 3 * kUnits)
+      quantise(std::integral_constant<int, 3>(), done + unit);
+    if (done < units) quantise(std::integral_constant<int, 1>(), done + unit);
     // the codes are read by the tensor core, the scales by the epilogue
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("bar.sync 5, %0;" ::"n"(kBsThreads - 32) : "memory");
@@ -1037,53 +1047,78 @@ namespace {
 // NT = 256 where its rounds of items over the SMs are at most two thirds of
 // those of NT = 128 (1024 x 4096 x 7168, one round against two: 30 us, 41 in
 // 128s; 512 rows, one round of either: 128).  Fewer items than half the SMs,
-// of one expert: the reduction is split over a cluster until they fill them
-// (333 x 1001 x 2000: 8.2 us, 10.7 in one piece; 512 x 1024 x 7168: 11.5 and
-// 21.6).
+// of one expert: the reduction is split over clusters of as many CTAs (up to
+// eight) as still run all at once, which is fewer than SMs / items: 16 items
+// in eight pieces each, 15 of 16 clusters at a time, took 15.1 us where four
+// pieces take 8.5 and six 9.1 (128 x 2048 x 2048 with a kernel that quantises;
+// 16 x 2048 x 7168 in one kernel: four pieces 10.9, six 9.5).  333 x 1001 x
+// 2000: 8.2 us in four pieces, 10.7 in one; 512 x 1024 x 7168: 11.5 and 21.6.
 struct Plan {
   bool wide;
   int a_rows, tiles, split, resident;
   int64_t items;  // an upper bound where the experts' rows are not known
 };
 
-Plan plan_product(int M, int N, int K, int E, bool swiglu, int sms) {
+Plan plan_product(int M, int N, int K, int E, bool swiglu, const BlockscaleDevice& d) {
   Plan p{};
   const int64_t chunks = E == 1 ? (M + 127) / 128 : std::min<int64_t>(E, M) + M / 128;
   const int kb = (K + 127) / 128;
   p.a_rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  auto rounds = [&](int nt) { return (chunks * ((N + nt - 1) / nt) + sms - 1) / sms; };
+  auto rounds = [&](int nt) { return (chunks * ((N + nt - 1) / nt) + d.sms - 1) / d.sms; };
   p.wide = swiglu || 3 * rounds(256) <= 2 * rounds(128);
   const int nt = p.wide ? 256 : 128;
   p.tiles = swiglu ? N / 256 : (N + nt - 1) / nt;
   p.items = chunks * p.tiles;
   p.split = 1;
   if (E == 1 && (swiglu ? M <= kBsSplitSwigluRows : !p.wide))
-    while (p.split < 8 && p.items * p.split * 2 <= sms && p.split * 2 <= kb) p.split *= 2;
+    for (int s = 2; s <= std::min(kBsMaxSplit, kb); ++s)
+      if (p.items <= d.clusters[s] && (kb + s - 1) / s < (kb + p.split - 1) / p.split) p.split = s;
   p.resident = (kb + p.split - 1) / p.split;
   return p;
 }
 
-// Row blocks that a CTA quantises for itself at most (QUANT).  48 rows x 2048
-// into 7168 (384 a CTA): 14.1 us on the GPU where a quantising kernel and the
-// product take 9.7, but 16.4 us a call where their two launches and the
-// workspace take 23.4; one row x 7168 into 4096: 10.4 against 11.3, and 12.3
-// against 24.
-constexpr int kBsQuantUnits = 640;
+// Row blocks that a CTA quantises for itself at most (QUANT).  On the GPU one
+// row x 7168 into 4096 takes 8.9 us where a quantising kernel and the product
+// take 10.5; 16 rows 10.9 and 10.9; 48 rows x 2048 into 7168 (384 a CTA) 11.0
+// and 9.6; 333 x 2000 into 1001 (512) 12.3 and 9.2; 64 x 7168 into 2048 (640)
+// 14.6 and 10.8.  But the second launch and the workspace make a call 20 us
+// for the host, against 14, so up to 512 the one kernel is the faster call.
+constexpr int kBsQuantUnits = 512;
 
 }  // namespace
 
 // See internal.h.
-bool blockscale_quantizes(int M, int N, int K, int sms) {
-  const Plan p = plan_product(M, N, K, 1, false, sms);
+cudaError_t blockscale_clusters(BlockscaleDevice* d) {
+  auto k = blockscale_gemm_kernel<128, false, false, true, false, false>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmemLimit);
+  for (int n = 1; n <= kBsMaxSplit && e == cudaSuccess; ++n) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(n * d->sms);
+    cfg.blockDim = dim3(kBsThreads);
+    cfg.dynamicSmemBytes = kBsSmemLimit;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&d->clusters[n], k, &cfg);
+  }
+  return e;
+}
+
+bool blockscale_quantizes(int M, int N, int K, const BlockscaleDevice& d) {
+  const Plan p = plan_product(M, N, K, 1, false, d);
   const int64_t smem = p.resident * p.a_rows * 128 + 2 * 128 * 128 + 1024 +
                        extra_smem<128, false, true, true>(p.a_rows, p.resident) + 16;
   return !p.wide && std::min(M, 128) * p.resident <= kBsQuantUnits && smem <= kBsSmemLimit &&
-         (p.items * p.split <= sms || M <= 16);
+         (p.items * p.split <= d.sms || M <= 16);
 }
 
 cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool swiglu,
-                              bool transpose, bool pdl, int sms, cudaStream_t s) {
-  const Plan plan = plan_product(p.M, p.N, p.K, p.E, swiglu, sms);
+                              bool transpose, bool pdl, const BlockscaleDevice& d,
+                              cudaStream_t s) {
+  const Plan plan = plan_product(p.M, p.N, p.K, p.E, swiglu, d);
   if (plan.items * plan.split > INT32_MAX) return cudaErrorInvalidValue;
   p.a_rows = plan.a_rows;
   p.tiles = plan.tiles;
@@ -1103,12 +1138,12 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
   if (p.x)
     return transpose ? launch_bs<128, false, true, false, false, true>(maps, p, items, pdl, s)
                      : launch_bs<128, false, false, false, false, true>(maps, p, items, pdl, s);
-  const int grid = std::min(sms, items);
+  const int grid = std::min(d.sms, items);
   // (pairs for full chunks: one expert of 8192 rows, 4096 x 7168, 183 us
   // against 192; 8 experts of 1024 rows, a whole call, 93 against 100; 64 of
   // 256 rows, where the second chunk is often short, 195 against 174)
   if (wide && p.M / 1024 >= p.E) {
-    const int pairs = std::min(sms / 2, (items + 1) / 2);
+    const int pairs = std::min(d.clusters[2], (items + 1) / 2);
     if (swiglu) return launch_bs<256, true, false, false, true>(maps, p, 2 * pairs, pdl, s);
     return transpose ? launch_bs<256, false, true, false, true>(maps, p, 2 * pairs, pdl, s)
                      : launch_bs<256, false, false, false, true>(maps, p, 2 * pairs, pdl, s);

@@ -9,6 +9,7 @@
 namespace moe {
 
 constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr uint32_t kFastBits = (127u - 71u) << 23;  // 2^-71: 448 times and more of it, s >= 2^-80
 
 // The bits of |x|: ordered like the magnitudes, with NaN above infinity, so
 // an integer maximum finds the largest magnitude and keeps a NaN.
@@ -27,11 +28,29 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 struct BlockQuant {
   float scale, r;
   bool slow;
+  BlockQuant() = default;
   __device__ __forceinline__ explicit BlockQuant(uint32_t amax_bits) {
     scale = amax_bits >= kInfBits ? __uint_as_float(0x7FC00000u)
                                   : __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
     r = amax_bits == 0u ? 0.0f : __frcp_rn(scale);
     slow = scale < 0x1p-80f && amax_bits != 0u;
+  }
+  // The same for a bf16 block with is_fast(amax), without a branch: the
+  // scale by the Newton step of the codes (exact in the same way), r by the
+  // approximate reciprocal and one step of its own.
+  __device__ __forceinline__ static bool is_fast(uint32_t amax_bits) {
+    return amax_bits - kFastBits < kInfBits - kFastBits || amax_bits == 0u;
+  }
+  __device__ __forceinline__ static BlockQuant of_bf16(uint32_t amax_bits) {
+    BlockQuant b;
+    const float a = __uint_as_float(amax_bits), q = a * (1.0f / 448.0f);
+    b.scale = fmaf(-fmaf(q, 448.0f, -a), 1.0f / 448.0f, q);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b.scale));
+    r = fmaf(-fmaf(r, b.scale, -1.0f), r, r);
+    b.r = amax_bits == 0u ? 0.0f : r;
+    b.slow = false;
+    return b;
   }
   // codes of a pair, a's in the low byte
   __device__ __forceinline__ uint32_t code2(float a, float b) const {
@@ -52,33 +71,55 @@ struct BlockQuant {
   }
 };
 
-// 16 bf16 values (pairs in v) of a block that eight neighbouring lanes share:
-// their codes and the block's scale.  Called by whole warps.
-__device__ __forceinline__ uint4 quantize_16(const uint32_t (&v)[8], float& scale) {
-  // the larger magnitude of each half-word, then of the two
-  uint32_t m2 = v[0] & 0x7FFF7FFFu;
+// N times 16 bf16 values (pairs in v[k]), each of a block that eight
+// neighbouring lanes share: their codes and the blocks' scales.  Called by
+// whole warps.  There is one branch for all of them, so that the N chains of
+// shuffles and quotients overlap.
+template <int N>
+__device__ __forceinline__ void quantize_16(const uint32_t (&v)[N][8], uint4 (&codes)[N],
+                                            float (&scale)[N]) {
+  uint32_t amax[N];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, v[i] & 0x7FFF7FFFu);
-  uint32_t amax = max(m2 << 16, m2 & 0xFFFF0000u);
+  for (int k = 0; k < N; ++k) {
+    // the larger magnitude of each half-word, then of the two
+    uint32_t m2 = v[k][0] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int off = 4; off; off >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-  const BlockQuant bq(amax);
-  scale = bq.scale;
+    for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, v[k][i] & 0x7FFF7FFFu);
+    amax[k] = max(m2 << 16, m2 & 0xFFFF0000u);
+  }
+#pragma unroll
+  for (int off = 4; off; off >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) amax[k] = max(amax[k], __shfl_xor_sync(0xFFFFFFFFu, amax[k], off));
+  bool fast = true;
+#pragma unroll
+  for (int k = 0; k < N; ++k) fast &= BlockQuant::is_fast(amax[k]);
   auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
   auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
-  uint32_t w[4];
-  if (bq.slow) {
+  if (__all_sync(0xFFFFFFFFu, fast)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = bq.code2_slow(lo(v[2 * i]), hi(v[2 * i])) |
-             (bq.code2_slow(lo(v[2 * i + 1]), hi(v[2 * i + 1])) << 16);
-  } else {
+    for (int k = 0; k < N; ++k) {
+      const BlockQuant bq = BlockQuant::of_bf16(amax[k]);
+      scale[k] = bq.scale;
+      uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = bq.code2(lo(v[2 * i]), hi(v[2 * i])) |
-             (bq.code2(lo(v[2 * i + 1]), hi(v[2 * i + 1])) << 16);
+      for (int i = 0; i < 4; ++i)
+        w[i] = bq.code2(lo(v[k][2 * i]), hi(v[k][2 * i])) |
+               (bq.code2(lo(v[k][2 * i + 1]), hi(v[k][2 * i + 1])) << 16);
+      codes[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const BlockQuant bq(amax[k]);
+    scale[k] = bq.scale;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = bq.code4(lo(v[k][2 * i]), hi(v[k][2 * i]), lo(v[k][2 * i + 1]), hi(v[k][2 * i + 1]));
+    codes[k] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 }  // namespace moe

@@ -216,13 +216,22 @@ struct BlockscaleArgs {
   int a_rows, tiles, stages, split, resident;
 };
 
+// What the plan of a product goes by: clusters[n] clusters of n CTAs of its
+// kernels run at a time (a cluster stays inside one GPC).
+constexpr int kBsMaxSplit = 8;
+struct BlockscaleDevice {
+  int sms;
+  int clusters[kBsMaxSplit + 1];
+};
+cudaError_t blockscale_clusters(BlockscaleDevice* d);  // the current device's
 // Whether a product of one matrix is small enough to quantise its activations
 // itself (args.x): a CTA's share of them stays in its shared memory.
-bool blockscale_quantizes(int M, int N, int K, int sms);
+bool blockscale_quantizes(int M, int N, int K, const BlockscaleDevice& d);
 // swiglu: N = 2 I, gate and up rows; transpose: weights stored [E, K, N].
 // pdl: programmatic dependent launch.
 cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs args, bool swiglu,
-                              bool transpose, bool pdl, int sms, cudaStream_t s);
+                              bool transpose, bool pdl, const BlockscaleDevice& d,
+                              cudaStream_t s);
 // The first status code its kernels recorded on the current device since the
 // last call (0: none).
 cudaError_t blockscale_status(int* code);

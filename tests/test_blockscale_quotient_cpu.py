@@ -42,3 +42,13 @@ def test_quotient_is_correctly_rounded_for_all_bf16_significands():
             q = rn32(x * r)
             e = rn32(q * s - x)
             assert rn32(q - e * r) == rn32(x / s), (a, m)
+
+
+def test_scale_without_a_divide_is_correctly_rounded():
+    """s = RN(amax / 448) by one step on amax RN(1 / 448)."""
+    r = rn32(Fraction(1, 448))
+    for a in range(128, 256):
+        v = Fraction(a, 128)
+        q = rn32(v * r)
+        e = rn32(q * 448 - v)
+        assert rn32(q - e * r) == rn32(v / 448), a

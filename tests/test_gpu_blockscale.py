@@ -134,6 +134,25 @@ def test_quantize_hard_blocks():
     assert np.array_equal(codes.double().cpu().numpy(), want_c)
 
 
+def test_quantize_all_significands():
+    """Every pair of a block maximum's and a value's significand, the value at
+    every exponent that has a code."""
+    from moe_expert_layer_histogram_gb300 import blockscale_quantize
+    a = torch.arange(128, 256).double() / 128
+    m = torch.arange(128, 256).double() / 128
+    e = 2.0 ** -torch.arange(1, 21).double()
+    x = m[None, None, :] * e[None, :, None] * torch.ones(128, 1, 1)     # [a, e, m]
+    x = torch.cat([x[..., :64], a[:, None, None].expand(128, 20, 1), -x[..., 64:],
+                   torch.zeros(128, 20, 127)], 2).reshape(-1, 256)
+    x[:, 255] = x[:, 64]                                                # (its own block's maximum)
+    x[:, 129:255] = -x[:, 1:127]
+    x = x.bfloat16().cuda()
+    codes, scales = blockscale_quantize(x)
+    want_c, want_s = ref_quantize(x.double().cpu().numpy())
+    assert np.array_equal(scales.cpu().numpy(), want_s)
+    assert np.array_equal(codes.double().cpu().numpy(), want_c)
+
+
 def test_quantize_non_finite_blocks_are_nan():
     from moe_expert_layer_histogram_gb300 import blockscale_quantize
     x = draw_x(4, 300, 1)
