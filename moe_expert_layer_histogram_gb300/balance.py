@@ -51,14 +51,17 @@ def router_balance(logits, top_k, coef=1.0, mask=None):
     ids = torch.empty(T, k, dtype=torch.int32, device=dev)
     weights = torch.empty(T, k, dtype=_F32, device=dev)
     counts = torch.empty(E, dtype=torch.int32, device=dev)
-    # loss, mean_probs (from word 4) and the workspace (16-byte aligned)
+    # loss and mean_probs (from word 4); a small workspace behind them (16-byte
+    # aligned), a large one apart, so that a loss that is kept keeps none of it
     words = 4 + (E + 3) // 4 * 4
-    stats = torch.empty(words + (nbytes + 3) // 4, dtype=_F32, device=dev)
+    large = nbytes > 16
+    stats = torch.empty(words if large else words + 4, dtype=_F32, device=dev)
     base = stats.data_ptr()
+    work = torch.empty(nbytes, dtype=torch.uint8, device=dev) if large else None
     code = L.moe_balance_forward(
         logits.data_ptr(), dtype, ld, None if mask is None else mask.data_ptr(), T, E, top_k, coef,
-        ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), base + 16, base, base + 4 * words,
-        nbytes, stream)
+        ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), base + 16, base,
+        work.data_ptr() if large else base + 4 * words, nbytes, stream)
     if code:
         raise MoEError(code, "moe_balance_forward")
     return RouterBalance(ids, weights, counts, stats, top_k, coef)

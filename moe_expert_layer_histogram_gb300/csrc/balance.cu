@@ -566,11 +566,11 @@ cudaError_t run_forward(const T* logits, int64_t ld, const uint8_t* mask, int to
     static const cudaError_t ready =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (ready != cudaSuccess) return ready;
-    cudaError_t e = launch_pdl(false, k, dim3(blocks), dim3(32 * kBalanceWarps), smem, s, logits, ld, mask, tokens, E, K, ids,
-                               weights, psum, count);
+    cudaError_t e = launch_pdl(false, k, dim3(blocks), dim3(32 * kBalanceWarps), smem, s, logits,
+                               ld, mask, tokens, E, K, ids, weights, psum, count);
     if (e == cudaSuccess)
-      e = launch_pdl(true, balance_finish_kernel, dim3(kFinishRanks), dim3(kFinishThreads), 0, s, psum, count,
-                     blocks, E, K, coef, counts, mean_probs, loss);
+      e = launch_pdl(true, balance_finish_kernel, dim3(kFinishRanks), dim3(kFinishThreads), 0, s,
+                     psum, count, blocks, E, K, coef, counts, mean_probs, loss);
     return e;
   });
 }
@@ -585,7 +585,8 @@ cudaError_t run_backward(const T* logits, int64_t ld, int tokens, int E, int K, 
     return launch_pdl(false,
                       balance_backward_kernel<decltype(maxi)::value, decltype(vec)::value, T>,
                       dim3(std::min(kBackBlocks, (tokens + kBackWarps - 1) / kBackWarps)),
-                      dim3(32 * kBackWarps), 0, s, logits, ld, tokens, E, K, coef, ids, weights, counts, d_loss, d_weights, d_logits, ld_d);
+                      dim3(32 * kBackWarps), 0, s, logits, ld, tokens, E, K, coef, ids, weights,
+                      counts, d_loss, d_weights, d_logits, ld_d);
   });
 }
 

@@ -27,7 +27,7 @@ __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlk - 1)
 constexpr int kQuantCols = 4 * kBlk;
 
 template <bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, VEC ? 8 : 5)
     blockscale_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t ldx, int x_rows,
                                const int32_t* __restrict__ slots, int top_k, int rows, int cols,
                                uint8_t* __restrict__ codes, int64_t ld_codes,
@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(256)
   const int slot = slots ? slots[r] : r, src = slots ? slot / top_k : r;
   const bool in = real && slot >= 0 && src < x_rows;
   const __nv_bfloat16* p = x + src * ldx + c0;
-  uint32_t vs[1][8];  // pairs of bf16
-  uint32_t(&v)[8] = vs[0];
+  uint32_t values[1][8];  // pairs of bf16
+  uint32_t(&v)[8] = values[0];
   if (VEC && in && c0 + 16 <= cols) {
     const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 8);
     v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
@@ -57,18 +57,16 @@ __global__ void __launch_bounds__(256)
       v[i] = lo | (hi << 16);
     }
   }
-  float scales1[1];
-  uint4 codes1[1];
-  quantize_16(vs, codes1, scales1);
-  const float scale = scales1[0];
-  const uint4 w4 = codes1[0];
+  float scale[1];
+  uint4 w4[1];
+  quantize_16(values, w4, scale);
   const bool first = (lane & 7) == 0 && b * kBlk < cols;
-  if (first) scales[b * ld_scales + r] = scale;
+  if (first) scales[b * ld_scales + r] = scale[0];
   if (!real) return;
-  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+  const uint32_t w[4] = {w4[0].x, w4[0].y, w4[0].z, w4[0].w};
   uint8_t* d = codes + r * ld_codes + c0;
   if (VEC && c0 + 16 <= cols) {
-    *reinterpret_cast<uint4*>(d) = w4;
+    *reinterpret_cast<uint4*>(d) = w4[0];
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
