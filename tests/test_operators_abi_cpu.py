@@ -30,7 +30,8 @@ def forward(lib, **over):
     (dict(loss=None), INVALID), (dict(ws=None), INVALID), (dict(ids=GOOD + 2), INVALID),
     (dict(weights=GOOD + 1), INVALID), (dict(counts=GOOD + 3), INVALID),
     (dict(mean=GOOD + 2), INVALID), (dict(loss=GOOD + 2), INVALID), (dict(ws=GOOD + 8), INVALID),
-    (dict(nbytes=100), INVALID), (dict(E=513, ld=513), UNSUPPORTED), (dict(K=17), UNSUPPORTED),
+    (dict(nbytes=15), INVALID), (dict(T=4096, nbytes=100), INVALID),
+    (dict(E=513, ld=513), UNSUPPORTED), (dict(K=17), UNSUPPORTED),
     (dict(T=1 << 30), UNSUPPORTED)])
 def test_balance_forward_refusals(lib, over, code):
     assert forward(lib, **over) == code
