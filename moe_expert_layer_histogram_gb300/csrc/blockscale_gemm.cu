@@ -1043,16 +1043,20 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
 namespace {
 
 // How a product is cut up.  An item of 256 columns takes about 1.5 times as
-// long as one of 128 (4096 x 4096 x 7168: 105 us in 256s, 133 in 128s), so
-// NT = 256 where its rounds of items over the SMs are at most two thirds of
+// long as one of 128 (4096 x 4096 x 7168: 105 us in 256s, 133 in 128s), so NT
+// = 256 where its rounds of items over the SMs are at most two thirds of
 // those of NT = 128 (1024 x 4096 x 7168, one round against two: 30 us, 41 in
-// 128s; 512 rows, one round of either: 128).  Fewer items than half the SMs,
-// of one expert: the reduction is split over clusters of as many CTAs (up to
-// eight) as still run all at once, which is fewer than SMs / items: 16 items
-// in eight pieces each, 15 of 16 clusters at a time, took 15.1 us where four
-// pieces take 8.5 and six 9.1 (128 x 2048 x 2048 with a kernel that quantises;
-// 16 x 2048 x 7168 in one kernel: four pieces 10.9, six 9.5).  333 x 1001 x
-// 2000: 8.2 us in four pieces, 10.7 in one; 512 x 1024 x 7168: 11.5 and 21.6.
+// 128s; 512 rows, one round of either: 128).  With few rows per expert the
+// weights' bytes are what takes the time, and finer items share them out more
+// evenly (64 experts of 64 rows, 2048 -> 2048: a whole call 144 us in 128s,
+// 147 in 256s; of 128 rows 128.5 and 128; of 512 rows 299 and 285).  Fewer
+// items than half the SMs, of one expert: the reduction is split over
+// clusters of as many CTAs (up to eight) as still run all at once, which is
+// fewer than SMs / items: 16 items in eight pieces each, 15 of 16 clusters at
+// a time, took 15.1 us where four pieces take 8.5 and six 9.1 (128 x 2048 x
+// 2048 with a kernel that quantises; 16 x 2048 x 7168 in one kernel: four
+// pieces 10.9, six 9.5).  333 x 1001 x 2000: 8.2 us in four pieces, 10.7 in
+// one; 512 x 1024 x 7168: 11.5 and 21.6.
 struct Plan {
   bool wide;
   int a_rows, tiles, split, resident;
@@ -1065,7 +1069,7 @@ Plan plan_product(int M, int N, int K, int E, bool swiglu, const BlockscaleDevic
   const int kb = (K + 127) / 128;
   p.a_rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   auto rounds = [&](int nt) { return (chunks * ((N + nt - 1) / nt) + d.sms - 1) / d.sms; };
-  p.wide = swiglu || 3 * rounds(256) <= 2 * rounds(128);
+  p.wide = swiglu || (3 * rounds(256) <= 2 * rounds(128) && (E == 1 || M > 64 * E));
   const int nt = p.wide ? 256 : 128;
   p.tiles = swiglu ? N / 256 : (N + nt - 1) / nt;
   p.items = chunks * p.tiles;
