@@ -318,9 +318,8 @@ constexpr int kFinishThreads = 1024;
 constexpr int kFinishRanks = 8;
 
 __global__ void __cluster_dims__(kFinishRanks, 1, 1) __launch_bounds__(kFinishThreads)
-    balance_finish_kernel(const float* __restrict__ psum, const int32_t* __restrict__ count,
-                          int blocks, int E, int K, float coef, int32_t* __restrict__ counts,
-                          float* __restrict__ mean_probs, float* __restrict__ loss) {
+    balance_finish_kernel(const float* psum, const int32_t* count, int blocks, int E, int K,
+                          float coef, int32_t* counts, float* mean_probs, float* loss) {
   __shared__ float s_p[kFinishThreads];
   __shared__ int s_c[kFinishThreads];
   pdl_wait();

@@ -28,11 +28,13 @@ constexpr int kQuantCols = 4 * kBlk;
 
 template <bool VEC>
 __global__ void __launch_bounds__(256, VEC ? 8 : 5)
-    blockscale_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t ldx, int x_rows,
-                               const int32_t* __restrict__ slots, int top_k, int rows, int cols,
+    blockscale_quantize_kernel(const __nv_bfloat16* x, int64_t ldx, int x_rows,
+                               const int32_t* slots, int top_k, int rows, int cols,
                                uint8_t* __restrict__ codes, int64_t ld_codes,
                                float* __restrict__ scales, int64_t ld_scales) {
-  // a product that follows may set itself up and load weights meanwhile
+  // What came before is over when a product that follows may set itself up and
+  // load weights meanwhile.
+  pdl_wait();
   pdl_launch_dependents();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
@@ -81,10 +83,9 @@ __global__ void __launch_bounds__(256, VEC ? 8 : 5)
 constexpr int kCopyWords = 128;
 
 __global__ void __launch_bounds__(256)
-    blockscale_copy_rows_kernel(const uint4* __restrict__ codes, const float* __restrict__ scales,
-                                int x_rows, int blocks, int words, const int32_t* __restrict__ slots,
-                                int top_k, int rows, uint4* __restrict__ out,
-                                float* __restrict__ out_scales) {
+    blockscale_copy_rows_kernel(const uint4* codes, const float* scales, int x_rows, int blocks,
+                                int words, const int32_t* slots, int top_k, int rows, uint4* out,
+                                float* out_scales) {
   pdl_launch_dependents();
   pdl_wait();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(256)
   uint4 v[kCopyWords / 32];
 #pragma unroll
   for (int i = 0; i < kCopyWords / 32; ++i)
-    v[i] = in && w0 + 32 * i < words ? __ldg(s + w0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+    v[i] = in && w0 + 32 * i < words ? s[w0 + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
   for (int i = 0; i < kCopyWords / 32; ++i)
     if (w0 + 32 * i < words) d[w0 + 32 * i] = v[i];
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(256)
   const int b = blockIdx.y * (kCopyWords / 8) + lane;
   if (lane < kCopyWords / 8 && b < blocks)
     out_scales[static_cast<int64_t>(b) * rows + row] =
-        in ? __ldg(scales + static_cast<int64_t>(b) * x_rows + src) : 0.0f;
+        in ? scales[static_cast<int64_t>(b) * x_rows + src] : 0.0f;
 }
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -235,7 +236,7 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
   a.ldx = p.ldx;
   a.x_vec = aligned_to(p.x, 16) && p.ldx % 8 == 0;
   a.early = early;
-  return launch_blockscale(maps, a, swiglu, p.transpose, early, *d, s) == cudaSuccess
+  return launch_blockscale(maps, a, swiglu, p.transpose, *d, s) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -254,7 +255,7 @@ moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* s
   if (grid.y > 65535) return MOE_ERR_UNSUPPORTED;
   const bool vec = aligned_to(x, 16) && ldx % 8 == 0 && aligned_to(codes, 16) && ld_codes % 16 == 0;
   const cudaError_t e = launch_pdl(
-      false, vec ? blockscale_quantize_kernel<true> : blockscale_quantize_kernel<false>,
+      true, vec ? blockscale_quantize_kernel<true> : blockscale_quantize_kernel<false>,
       grid, dim3(256), 0, s, static_cast<const __nv_bfloat16*>(x),
       ldx, x_rows, slots, top_k, rows, cols, static_cast<uint8_t*>(codes), ld_codes, scales,
       ld_scales);

@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   const BsTable tab{s_tab, s_tab + p.E + 1, s_tab + 2 * p.E + 1};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_launch_dependents();
+  // (not early: below)
+  if (p.early) pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -434,6 +435,17 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // The launch may overlap the kernel before it.  Early: that is the library's
+  // own, which writes the activations and their scales but no offsets or
+  // weights, and which has let this one start only when all before it was
+  // over.  Else nothing is read, no TMEM held that the other could be waiting
+  // for, and no kernel after this one started, before it is over.  (What it
+  // may have written is not read with __ldg, which is for memory that stays as
+  // it is.)
+  if (!p.early) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   if (warp == 1) {
     if constexpr (PAIR) {
       tmem_alloc_pair(tmem_holder, 512);
@@ -443,10 +455,6 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       tmem_relinquish();
     }
   }
-  // (early: the only kernel this one may overlap is the library's own before
-  // it, which writes the activations and their scales but no offsets or
-  // weights)
-  if (!p.early) pdl_wait();
   if (warp == 2) fill_bs_table(p, tab, kGroup, lane);
   tc_fence_before();
   __syncthreads();
@@ -493,10 +501,10 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         const int block = block_of(u), r = u - block * it.rows, kb = kb0 + block;
         const int c0 = kb * 128 + chunk * 16;
         const __nv_bfloat16* src = p.x + (it.row0 + r) * p.ldx + c0;
-        w[k] = __ldg(sw + kb * p.w_stride_k);
+        w[k] = sw[kb * p.w_stride_k];
         if (p.x_vec && c0 + 16 <= p.K) {
-          const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src)),
-                      hi = __ldg(reinterpret_cast<const uint4*>(src + 8));
+          const uint4 lo = *reinterpret_cast<const uint4*>(src),
+                      hi = *reinterpret_cast<const uint4*>(src + 8);
           v[k][0] = lo.x, v[k][1] = lo.y, v[k][2] = lo.z, v[k][3] = lo.w;
           v[k][4] = hi.x, v[k][5] = hi.y, v[k][6] = hi.z, v[k][7] = hi.w;
         } else if (c0 < p.K) {
@@ -699,7 +707,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
         for (int i = 0; i < kBsAhead; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            a[i][j] = i < n && lane + 32 * j < it.rows ? __ldg(sa + i * p.ld_as + 32 * j) : 0.0f;
+            a[i][j] = i < n && lane + 32 * j < it.rows ? sa[i * p.ld_as + 32 * j] : 0.0f;
         // SWIGLU: the gate's block and the up half's; else the tile's blocks
         // (one past N has no scale of its own and is not stored)
 #pragma unroll
@@ -708,7 +716,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
                                 : min(it.tile * kSets + h, (p.N + 127) / 128 - 1);
           const float* sw = p.w_scales + it.e * p.w_blocks + nb * p.w_stride_n + kb * p.w_stride_k;
 #pragma unroll
-          for (int i = 0; i < kBsAhead; ++i) w[i][h] = i < n ? __ldg(sw + i * p.w_stride_k) : 0.0f;
+          for (int i = 0; i < kBsAhead; ++i) w[i][h] = i < n ? sw[i * p.w_stride_k] : 0.0f;
         }
         kb += n;
         if (kb == kb1) {
@@ -997,8 +1005,7 @@ int extra_smem(int a_rows, int resident) {
 }
 
 template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR = false, bool QUANT = false>
-cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bool pdl,
-                      cudaStream_t s) {
+cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, cudaStream_t s) {
   auto k = blockscale_gemm_kernel<NT, SWIGLU, TRANS, SPLIT, PAIR, QUANT>;
   // Once per instance: the shared-memory limit, and that the launch
   // allocation covers the register split (setmaxnreg would wait forever).
@@ -1025,10 +1032,8 @@ cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, bo
   cfg.dynamicSmemBytes = fixed + p.stages * stage;
   cfg.stream = s;
   cfg.attrs = attr;
-  if (pdl) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
+  attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
   if (SPLIT || PAIR) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs].val.clusterDim.x = PAIR ? 2 : p.split;
@@ -1120,8 +1125,7 @@ bool blockscale_quantizes(int M, int N, int K, const BlockscaleDevice& d) {
 }
 
 cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool swiglu,
-                              bool transpose, bool pdl, const BlockscaleDevice& d,
-                              cudaStream_t s) {
+                              bool transpose, const BlockscaleDevice& d, cudaStream_t s) {
   const Plan plan = plan_product(p.M, p.N, p.K, p.E, swiglu, d);
   if (plan.items * plan.split > INT32_MAX) return cudaErrorInvalidValue;
   p.a_rows = plan.a_rows;
@@ -1133,31 +1137,31 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
   if (p.split > 1) {
     const int grid = items * p.split;
     if (p.x)
-      return transpose ? launch_bs<128, false, true, true, false, true>(maps, p, grid, pdl, s)
-                       : launch_bs<128, false, false, true, false, true>(maps, p, grid, pdl, s);
-    if (swiglu) return launch_bs<256, true, false, true>(maps, p, grid, pdl, s);
-    return transpose ? launch_bs<128, false, true, true>(maps, p, grid, pdl, s)
-                     : launch_bs<128, false, false, true>(maps, p, grid, pdl, s);
+      return transpose ? launch_bs<128, false, true, true, false, true>(maps, p, grid, s)
+                       : launch_bs<128, false, false, true, false, true>(maps, p, grid, s);
+    if (swiglu) return launch_bs<256, true, false, true>(maps, p, grid, s);
+    return transpose ? launch_bs<128, false, true, true>(maps, p, grid, s)
+                     : launch_bs<128, false, false, true>(maps, p, grid, s);
   }
   if (p.x)
-    return transpose ? launch_bs<128, false, true, false, false, true>(maps, p, items, pdl, s)
-                     : launch_bs<128, false, false, false, false, true>(maps, p, items, pdl, s);
+    return transpose ? launch_bs<128, false, true, false, false, true>(maps, p, items, s)
+                     : launch_bs<128, false, false, false, false, true>(maps, p, items, s);
   const int grid = std::min(d.sms, items);
   // (pairs for full chunks: one expert of 8192 rows, 4096 x 7168, 183 us
   // against 192; 8 experts of 1024 rows, a whole call, 93 against 100; 64 of
   // 256 rows, where the second chunk is often short, 195 against 174)
   if (wide && p.M / 1024 >= p.E) {
     const int pairs = std::min(d.clusters[2], (items + 1) / 2);
-    if (swiglu) return launch_bs<256, true, false, false, true>(maps, p, 2 * pairs, pdl, s);
-    return transpose ? launch_bs<256, false, true, false, true>(maps, p, 2 * pairs, pdl, s)
-                     : launch_bs<256, false, false, false, true>(maps, p, 2 * pairs, pdl, s);
+    if (swiglu) return launch_bs<256, true, false, false, true>(maps, p, 2 * pairs, s);
+    return transpose ? launch_bs<256, false, true, false, true>(maps, p, 2 * pairs, s)
+                     : launch_bs<256, false, false, false, true>(maps, p, 2 * pairs, s);
   }
-  if (swiglu) return launch_bs<256, true, false, false>(maps, p, grid, pdl, s);
+  if (swiglu) return launch_bs<256, true, false, false>(maps, p, grid, s);
   if (wide)
-    return transpose ? launch_bs<256, false, true, false>(maps, p, grid, pdl, s)
-                     : launch_bs<256, false, false, false>(maps, p, grid, pdl, s);
-  return transpose ? launch_bs<128, false, true, false>(maps, p, grid, pdl, s)
-                   : launch_bs<128, false, false, false>(maps, p, grid, pdl, s);
+    return transpose ? launch_bs<256, false, true, false>(maps, p, grid, s)
+                     : launch_bs<256, false, false, false>(maps, p, grid, s);
+  return transpose ? launch_bs<128, false, true, false>(maps, p, grid, s)
+                   : launch_bs<128, false, false, false>(maps, p, grid, s);
 }
 
 cudaError_t blockscale_status(int* code) {

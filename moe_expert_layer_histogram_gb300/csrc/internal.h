@@ -228,10 +228,8 @@ cudaError_t blockscale_clusters(BlockscaleDevice* d);  // the current device's
 // itself (args.x): a CTA's share of them stays in its shared memory.
 bool blockscale_quantizes(int M, int N, int K, const BlockscaleDevice& d);
 // swiglu: N = 2 I, gate and up rows; transpose: weights stored [E, K, N].
-// pdl: programmatic dependent launch.
 cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs args, bool swiglu,
-                              bool transpose, bool pdl, const BlockscaleDevice& d,
-                              cudaStream_t s);
+                              bool transpose, const BlockscaleDevice& d, cudaStream_t s);
 // The first status code its kernels recorded on the current device since the
 // last call (0: none).
 cudaError_t blockscale_status(int* code);
