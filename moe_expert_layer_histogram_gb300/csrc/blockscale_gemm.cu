@@ -1087,11 +1087,11 @@ Plan plan_product(int M, int N, int K, int E, bool swiglu, const BlockscaleDevic
 }
 
 // Row blocks that a CTA quantises for itself at most (QUANT).  On the GPU one
-// row x 7168 into 4096 takes 8.9 us where a quantising kernel and the product
-// take 10.5; 16 rows 10.9 and 10.9; 48 rows x 2048 into 7168 (384 a CTA) 11.0
-// and 9.6; 333 x 2000 into 1001 (512) 12.3 and 9.2; 64 x 7168 into 2048 (640)
-// 14.6 and 10.8.  But the second launch and the workspace make a call 20 us
-// for the host, against 14, so up to 512 the one kernel is the faster call.
+// row x 7168 into 4096 takes 8.5 us where a quantising kernel and the product
+// take 10.1; 16 rows 10.4 and 10.6; 48 rows x 2048 into 7168 (384 a CTA) 10.4
+// and 9.1; 333 x 2000 into 1001 (512) 11.6 and 8.8; 64 x 7168 into 2048 (640)
+// 13.7 and 10.5.  But the second launch and the workspace make a call 21 us
+// for the host, against 12, so up to 512 the one kernel is the faster call.
 constexpr int kBsQuantUnits = 512;
 
 }  // namespace
