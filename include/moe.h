@@ -415,6 +415,9 @@ moe_status moe_blockscale_quantize(const void *x, int64_t ldx, int x_rows,
  * gradient from the weights as they are stored; w_scales keeps the stored
  * orientation).  out: bf16 [M, N], row stride ldo.  Rows of no expert are
  * not written; offsets outside [0, M] or falling are clamped into range.
+ * The order of a row's sums depends on E, M, N, K and the device alone (one
+ * expert, or 16 rows and fewer, may split the reduction), so the same call
+ * gives the same bits.
  * N, K, M of any size; a and w 16-byte aligned with row strides that are
  * multiples of 16 (ld >= the row), E <= 512.  M == 0 is a no-op.
  * Asynchronous on `stream`, allocates nothing, no workspace.  Errors:

@@ -49,10 +49,10 @@
 // stored rows: the tile is 128 rows of 128 bytes of output columns, an
 // MN-major operand for the tensor cores; nothing is copied or re-laid out.
 //
-// Few rows of one expert leave most SMs without an item; there a cluster of
-// 2, 4 or 8 CTAs splits the reduction of each item and joins its fp32
-// partial sums through distributed shared memory, in rank order, so the
-// result does not depend on timing.
+// Few rows leave most SMs without an item; there a cluster of two to eight
+// CTAs splits the reduction of each item and joins its fp32 partial sums
+// through distributed shared memory, in rank order, so the result does not
+// depend on timing.
 //
 // What bounds it: with many rows, the shared memory that feeds the MMAs
 // (8192 x 4096 x 7168: 183 us, 2620 TFLOP/s; a build without the epilogue's
@@ -83,11 +83,16 @@ constexpr int kBsMaxStages = 8;
 constexpr int kBsAhead = 4;       // blocks whose scales are passed on together, a float4 per row
 constexpr int kBsGroups = 2;      // such groups in the scale ring
 constexpr int kBsSmemLimit = 232448;
-// Most rows of one expert whose SwiGLU product is split: the partial sums lie
-// beside the ring of stages.  A whole call, split against not, 7168 -> 2048:
+// Most rows of a SwiGLU product that is split: the partial sums lie beside the
+// ring of stages.  A whole call of one expert, split against not, 7168 -> 2048:
 // 32 rows 30.4 us against 40.4, 64 rows 32.9 against 41, 100 rows 46.1 against
 // 41.7 (two stages are left).
 constexpr int kBsSplitSwigluRows = 64;
+// Most rows in all of several experts whose products are split: a token's or
+// two (a whole call of one token, 64 x (2048, 1024), top-6: 20.9 us against
+// 24.6 in one piece; 64 x (7168, 2048), top-2: 28.2 against 42.8).  With more
+// rows a row's sums keep their order whatever the other experts' number.
+constexpr int kBsSplitGroupRows = 16;
 
 __device__ int g_blockscale_status;
 
@@ -371,7 +376,7 @@ __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
 
 // NT: weight rows per item.  SWIGLU: the tile is 128 gate rows and the 128
 // up rows of the same columns (NT = 256).  SPLIT: the grid is clusters of
-// args.split CTAs, one item each (one expert).
+// args.split CTAs, one item each at most.
 // PAIR: the grid is clusters of two CTAs that share each item (NT = 256).
 // QUANT: the activations are args.x, and every CTA (or split cluster) has one
 // item (NT = 128, one expert).
@@ -1055,13 +1060,13 @@ namespace {
 // weights' bytes are what takes the time, and finer items share them out more
 // evenly (64 experts of 64 rows, 2048 -> 2048: a whole call 144 us in 128s,
 // 147 in 256s; of 128 rows 128.5 and 128; of 512 rows 299 and 285).  Fewer
-// items than half the SMs, of one expert: the reduction is split over
-// clusters of as many CTAs (up to eight) as still run all at once, which is
-// fewer than SMs / items: 16 items in eight pieces each, 15 of 16 clusters at
-// a time, took 15.1 us where four pieces take 8.5 and six 9.1 (128 x 2048 x
-// 2048 with a kernel that quantises; 16 x 2048 x 7168 in one kernel: four
-// pieces 10.9, six 9.5).  333 x 1001 x 2000: 8.2 us in four pieces, 10.7 in
-// one; 512 x 1024 x 7168: 11.5 and 21.6.
+// items than half the SMs: the reduction is split over clusters of as many
+// CTAs (up to eight) as still run all at once, which is fewer than SMs /
+// items: 16 items in eight pieces each, 15 of 16 clusters at a time, took
+// 15.1 us where four pieces take 8.5 and six 9.1 (128 x 2048 x 2048 with a
+// kernel that quantises; 16 x 2048 x 7168 in one kernel: four pieces 10.9,
+// six 9.5).  333 x 1001 x 2000: 8.2 us in four pieces, 10.7 in one; 512 x
+// 1024 x 7168: 11.5 and 21.6.
 struct Plan {
   bool wide;
   int a_rows, tiles, split, resident;
@@ -1079,7 +1084,7 @@ Plan plan_product(int M, int N, int K, int E, bool swiglu, const BlockscaleDevic
   p.tiles = swiglu ? N / 256 : (N + nt - 1) / nt;
   p.items = chunks * p.tiles;
   p.split = 1;
-  if (E == 1 && (swiglu ? M <= kBsSplitSwigluRows : !p.wide))
+  if (E > 1 ? M <= kBsSplitGroupRows : !p.wide || M <= kBsSplitSwigluRows)
     for (int s = 2; s <= std::min(kBsMaxSplit, kb); ++s)
       if (p.items <= d.clusters[s] && (kb + s - 1) / s < (kb + p.split - 1) / p.split) p.split = s;
   p.resident = (kb + p.split - 1) / p.split;

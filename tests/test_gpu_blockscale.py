@@ -292,7 +292,8 @@ def offsets_of(counts, first=0):
 
 GROUPS = [[700, 0, 513, 1, 1500, 129, 257, 640], [1025, 128, 1], [0, 5, 1, 0, 130, 17, 0],
           [1, 1, 1, 1], [128, 129, 127, 256], [0, 0, 0, 3], [300, 0, 0, 1], [2] * 40,
-          [0] * 511 + [9], [33, 64, 65, 31, 32, 16, 15], [2100, 77], [1, 3300, 129], [0, 2049]]
+          [0] * 511 + [9], [33, 64, 65, 31, 32, 16, 15], [2100, 77], [1, 3300, 129], [0, 2049],
+          [30, 0, 34], [1] * 3 + [0] * 5, [63], [0, 16, 0, 0], [8, 8], [3, 14]]
 
 
 @pytest.mark.parametrize("transpose", [False, True])
@@ -353,7 +354,8 @@ def swiglu_ref(a, w13, s13, clamp):
                                         ([2] * 20, 640, 256), ([600, 257, 0, 300], 256, 272),
                                         ([1025], 384, 400), ([64], 256, 1040), ([37], 128, 528),
                                         ([65], 256, 1040), ([2500, 300], 256, 272),
-                                        ([5, 3200, 0], 128, 144)])
+                                        ([5, 3200, 0], 128, 144), ([1, 0, 1, 3], 256, 1040),
+                                        ([0, 9, 4], 256, 528), ([16, 0, 1], 256, 528), ([1, 0, 0, 0, 0, 0, 1], 128, 2000)])
 def test_swiglu_codes(counts, I, K, clamp):
     from moe_expert_layer_histogram_gb300 import blockscale_quantize, moe_blockscale_swiglu
     E, M = len(counts), sum(counts)
