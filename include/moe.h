@@ -414,7 +414,8 @@ moe_status moe_blockscale_quantize(const void *x, int64_t ldx, int x_rows,
  * [E, K, N], the same product with the weights' transpose, i.e. the input
  * gradient from the weights as they are stored; w_scales keeps the stored
  * orientation).  out: bf16 [M, N], row stride ldo.  Rows of no expert are
- * not written; offsets outside [0, M] or falling are clamped into range.
+ * not written; offsets are clamped into [0, M], and one that is below an
+ * earlier offset counts as that one (a row has one expert at most).
  * The order of a row's sums depends on E, M, N, K and the device alone (one
  * expert, or 16 rows and fewer, may split the reduction), so the same call
  * gives the same bits.

@@ -248,7 +248,10 @@ struct BsItem {
 
 // Chunk table in shared memory: exclusive counts of the items' chunk groups
 // (`group` chunks of 128 rows each), and the first and last row of every
-// expert, clamped into [0, M].
+// expert.  The offsets are clamped into [0, M] and each is raised to the
+// largest before it, so no row has two experts and the host's bound on the
+// number of items holds whatever the offsets are: the split products have one
+// item per cluster and no more.
 struct BsTable {
   int* chunk_off;  // [E + 1]
   int* start;      // [E]
@@ -293,6 +296,27 @@ __device__ __forceinline__ void fill_bs_table(const BlockscaleArgs& p, const BsT
     const int e = 32 * i + lane;
     first[i] = e < p.E ? p.offsets[e] : 0;
     last[i] = e < p.E ? p.offsets[e + 1] : 0;
+  }
+  bool falls = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) falls |= last[i] < first[i];
+  if (__any_sync(0xFFFFFFFFu, falls)) {
+    int top = 0;
+    for (int i = 0; i < kPer && 32 * i < p.E; ++i) {
+      const int e = 32 * i + lane;
+      int m = max(e < p.E ? p.offsets[e] : 0, top);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, m, off);
+        if (lane >= off) m = max(m, o);
+      }
+      if (e < p.E) t.start[e] = m;
+      top = __shfl_sync(0xFFFFFFFFu, m, 31);
+    }
+    // (every lane reads back what it wrote itself)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (32 * i + lane < p.E) first[i] = t.start[32 * i + lane];
   }
   int run = 0;
 #pragma unroll
