@@ -26,13 +26,16 @@ def _weights(w, w_scales):
     elif len(shape) == 3:
         (E, N, K), (ld_e, ldw, one) = shape, strides
         blocks = (E, (N + 127) // 128, (K + 127) // 128)
-        if E > 1 and ld_e != N * ldw:
-            raise ValueError("w: experts at a stride of N rows")
+        if E > 1:
+            if N == 1:  # (the stride of a single row says nothing)
+                ldw = ld_e
+            if ld_e != N * ldw or ldw < K:
+                raise ValueError("w: experts at a stride of N rows of at least K codes")
     else:
         raise ValueError("w: [N, K] or [E, N, K]")
     if one != 1 and K > 1:
         raise ValueError("w: contiguous rows")
-    if N == 1 and ldw < K:
+    if N == 1 and ldw < K:  # (one expert)
         ldw = K
     check(w_scales, _F32, blocks, w.device, "w_scales")
     return E, N, K, ldw
