@@ -419,8 +419,9 @@ moe_status moe_blockscale_quantize(const void *x, int64_t ldx, int x_rows,
  * The order of a row's sums depends on E, M, N, K and the device alone (one
  * expert, or 16 rows and fewer, may split the reduction), so the same call
  * gives the same bits.
- * N, K, M of any size; a and w 16-byte aligned with row strides that are
- * multiples of 16 (ld >= the row), E <= 512.  M == 0 is a no-op.
+ * N, K, M of any size up to 2^31 - 256; a and w 16-byte aligned with row
+ * strides that are multiples of 16 (ld >= the row), E <= 512.  M == 0 is a
+ * no-op.
  * Asynchronous on `stream`, allocates nothing, no workspace.  Errors:
  * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_NO_DEVICE,
  * MOE_ERR_CUDA.  A kernel that gives up a bounded wait leaves its output

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include <mutex>
 
 #include "blockscale_quant.cuh"
@@ -18,6 +19,8 @@ namespace moe {
 namespace {
 
 constexpr int kBlk = 128;
+// Largest M, N and K of a product: rounding one up to a tile stays in 32 bits.
+constexpr int kMaxExtent = INT32_MAX - 255;
 
 __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
 
@@ -132,7 +135,8 @@ struct Product {
 moe_status check_weights(const Product& p) {
   if (p.M < 0 || p.N < 1 || p.K < 1 || p.E < 1 || (!p.offsets && p.E != 1))
     return MOE_ERR_INVALID_ARG;
-  if (p.E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+  if (p.E > kMaxExperts || p.M > kMaxExtent || p.N > kMaxExtent || p.K > kMaxExtent)
+    return MOE_ERR_UNSUPPORTED;
   if (p.ldw < (p.transpose ? p.N : p.K)) return MOE_ERR_INVALID_ARG;
   if (p.M == 0) return MOE_OK;
   if (!p.w || !p.w_scales || !aligned_to(p.w, 16) || p.ldw % 16 || !aligned_to(p.w_scales, 4) ||
@@ -339,13 +343,13 @@ moe_status moe_blockscale_swiglu(const void* a, int64_t lda, const float* a_scal
 }
 
 size_t moe_blockscale_linear_workspace(int M, int N, int K) {
-  if (M < 1 || N < 1 || K < 1) return 0;
+  if (M < 1 || N < 1 || K < 1 || M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return 0;
   const BlockscaleDevice* d = current_device();
   return d && blockscale_quantizes(M, N, K, *d) ? 0 : static_cast<size_t>(quantized_bytes(M, K));
 }
 
 size_t moe_blockscale_experts_workspace(int rows, int H, int I) {
-  if (rows < 1 || H < 1 || I < 1) return 0;
+  if (rows < 1 || H < 1 || I < 1 || rows > kMaxExtent || H > kMaxExtent || I > kMaxExtent) return 0;
   return static_cast<size_t>(quantized_bytes(rows, H) + quantized_bytes(rows, I));
 }
 

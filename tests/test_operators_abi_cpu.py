@@ -102,3 +102,41 @@ def test_swiglu_refusals(lib, over, code):
         over = {("w13" if k == "w" else k): v for k, v in over.items()}
     a.update(over)
     assert lib.moe_blockscale_swiglu(*a.values(), None) == code
+
+
+# Sizes whose round-up to a tile would pass 32 bits.
+LARGEST = 2 ** 31 - 256
+
+
+@pytest.mark.parametrize("over", [dict(N=LARGEST + 1, ldo=1 << 31), dict(N=2 ** 31 - 1, ldo=1 << 31),
+                                  dict(K=LARGEST + 1, lda=1 << 31, ldw=1 << 31, N=1),
+                                  dict(M=LARGEST + 1, ld_as=1 << 31, N=1, E=1),
+                                  dict(M=2 ** 31 - 1, ld_as=1 << 31, N=1, E=1),
+                                  dict(N=2 ** 31 - 1, ldo=1 << 31, ldw=1 << 31, K=16,
+                                       transpose_w=1)])
+def test_matmul_sizes_near_32_bits(lib, over):
+    a = dict(a=GOOD, lda=256, a_scales=GOOD, ld_as=8, w=GOOD, ldw=16, w_scales=GOOD, offsets=GOOD,
+             E=1, M=8, N=512, K=16, transpose_w=0, out=GOOD, ldo=512)
+    a.update(over)
+    assert lib.moe_blockscale_matmul(*a.values(), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("over", [dict(M=2 ** 31 - 1), dict(N=2 ** 31 - 1), dict(K=2 ** 31 - 1)])
+def test_linear_sizes_near_32_bits(lib, over):
+    a = dict(x=GOOD, ldx=1 << 31, w=GOOD, ldw=1 << 31, w_scales=GOOD, M=8, N=1, K=16, transpose_w=0,
+             out=GOOD, ldo=1 << 31, ws=GOOD, nbytes=1 << 60)
+    if "N" in over:
+        a["ldw"] = 16
+    a.update(over)
+    assert lib.moe_blockscale_linear_workspace(a["M"], a["N"], a["K"]) == 0
+    assert lib.moe_blockscale_linear(*a.values(), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("over", [dict(rows=2 ** 31 - 1), dict(H=2 ** 31 - 16)])
+def test_experts_sizes_near_32_bits(lib, over):
+    a = dict(x=GOOD, ldx=1 << 31, T=8, slots=GOOD, top_k=1, rows=8, offsets=GOOD, E=1, w13=GOOD,
+             s13=GOOD, w2=GOOD, s2=GOOD, H=16, I=128, clamp=0.0, out=GOOD, ldo=1 << 31, ws=GOOD,
+             nbytes=1 << 62)
+    a.update(over)
+    assert lib.moe_blockscale_experts_workspace(a["rows"], a["H"], a["I"]) == 0
+    assert lib.moe_blockscale_experts(*a.values(), None) == UNSUPPORTED
