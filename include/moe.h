@@ -351,8 +351,8 @@ size_t moe_balance_workspace(int T, int E);
  * f_e = counts_e * E / (K * n), the loss whose minimum is an even load; 0
  * when no token is live.  Sums are in fp32 in a fixed order: the same inputs
  * give the same bits.  A NaN logit makes its token's weights and the loss
- * NaN.  T == 0 writes zero counts and loss.  1 <= E <= 512, K <= min(E, 16)
- * and T * K < 2^31, else MOE_ERR_UNSUPPORTED.  Asynchronous on `stream`;
+ * NaN.  T == 0 writes zero counts and loss.  1 <= E <= 512, K <= min(E, 16),
+ * T <= 2^31 - 65536 and T * K < 2^31, else MOE_ERR_UNSUPPORTED.  Asynchronous on `stream`;
  * the workspace must stay until the work is done.  Errors:
  * MOE_ERR_INVALID_ARG (sizes, a NULL or misaligned pointer: logits to their
  * element, the workspace to 16 bytes, the others to 4; workspace_bytes below

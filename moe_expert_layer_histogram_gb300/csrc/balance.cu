@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstdint>
 #include <type_traits>
 
 #include "internal.h"
@@ -493,6 +494,9 @@ __global__ void __launch_bounds__(32 * kBackWarps)
 // per warp until there are more.  Backward: blocks of 8 warps, four to an SM.
 constexpr int kBalanceBlocks = 152;
 constexpr int kBackBlocks = 4 * 152;
+// Most tokens: a warp's next token (the stride is that of all warps) stays in 32 bits.
+constexpr int kBalanceMaxTokens = INT32_MAX - 65535;
+static_assert(kBalanceBlocks * kBalanceWarps <= 65535 && kBackBlocks * kBackWarps <= 65535);
 
 int balance_blocks(int T) {
   return std::max(1, std::min(kBalanceBlocks, (T + kBalanceWarps - 1) / kBalanceWarps));
@@ -503,7 +507,8 @@ bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 moe_status check_logits(const void* logits, int dtype, int64_t ld, int T, int E, int K) {
   if (T < 0 || E < 1 || K < 1 || K > E || ld < E) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
-  if (E > kMaxExperts || K > kMaxTopK || static_cast<int64_t>(T) * K > INT32_MAX)
+  if (E > kMaxExperts || K > kMaxTopK || T > kBalanceMaxTokens ||
+      static_cast<int64_t>(T) * K > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!logits || !aligned_to(logits, dtype == MOE_DTYPE_F32 ? 4 : 2)))
     return MOE_ERR_INVALID_ARG;
@@ -598,7 +603,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_balance_workspace(int T, int E) {
-  if (T < 0 || E < 1 || E > kMaxExperts) return 0;
+  if (T < 0 || T > kBalanceMaxTokens || E < 1 || E > kMaxExperts) return 0;
   return T <= kSmallTokens ? 16 : static_cast<size_t>(balance_blocks(T)) * E * 8;
 }
 

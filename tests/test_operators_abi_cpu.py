@@ -140,3 +140,14 @@ def test_experts_sizes_near_32_bits(lib, over):
     a.update(over)
     assert lib.moe_blockscale_experts_workspace(a["rows"], a["H"], a["I"]) == 0
     assert lib.moe_blockscale_experts(*a.values(), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 4865, 2 ** 31 - 65535])
+def test_balance_tokens_near_32_bits(lib, T):
+    # (the warps' stride over the tokens passes T)
+    assert lib.moe_balance_workspace(T, 8) == 0
+    assert forward(lib, T=T, E=8, K=1) == UNSUPPORTED
+    a = dict(logits=GOOD, dtype=0, ld=8, T=T, E=8, K=1, coef=0.1, ids=GOOD, weights=GOOD,
+             counts=GOOD, d_loss=GOOD, d_weights=GOOD, d_logits=GOOD, ld_d=8)
+    assert lib.moe_balance_backward(*a.values(), None) == UNSUPPORTED
+    assert lib.moe_balance_workspace(2 ** 31 - 65536, 8) > 0
