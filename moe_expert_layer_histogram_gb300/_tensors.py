@@ -4,6 +4,13 @@ import torch
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_LARGEST = 2 ** 31 - 1
+
+
+def fits(n, name):
+    """The library takes sizes as 32-bit integers (and ctypes would cut them)."""
+    if n > _LARGEST:
+        raise ValueError("%s: %d is above 2^31 - 1" % (name, n))
 
 
 def stream_on(device):
@@ -23,11 +30,15 @@ def row_stride(t, dtype, name):
     (rows, cols), (ld, one) = t.shape, t.stride()
     if one != 1 and cols > 1:
         raise ValueError("%s: a matrix with contiguous rows" % name)
+    if rows > _LARGEST or cols > _LARGEST:
+        raise ValueError("%s: more than 2^31 - 1 rows or columns" % name)
     return ld if rows > 1 or ld > cols else cols
 
 
 def check(t, dtype, shape, device, name):
-    """A contiguous tensor of this type, shape and device."""
+    """A contiguous tensor of this type, shape and device, at most 2^31 - 1 in
+    its first dimension."""
     if (t.dtype is not dtype or t.shape != shape or t.device != device
             or not t.is_contiguous()):
         raise ValueError("%s: contiguous %s %s on %s" % (name, dtype, tuple(shape), device))
+    fits(shape[0], name)

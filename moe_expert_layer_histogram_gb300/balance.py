@@ -7,7 +7,7 @@ Thin wrappers of ``moe_balance_forward`` and ``moe_balance_backward``
 import torch
 
 from . import MoEError, lib
-from ._tensors import check, row_stride, stream_on
+from ._tensors import check, fits, row_stride, stream_on
 
 _F32, _BF16 = torch.float32, torch.bfloat16
 
@@ -47,6 +47,7 @@ def router_balance(logits, top_k, coef=1.0, mask=None):
         check(mask, torch.bool if mask.dtype is torch.bool else torch.uint8, (T,), dev, "mask")
     L = lib()
     nbytes = L.moe_balance_workspace(T, E)
+    fits(top_k, "top_k")
     k = max(top_k, 0)
     ids = torch.empty(T, k, dtype=torch.int32, device=dev)
     weights = torch.empty(T, k, dtype=_F32, device=dev)

@@ -10,7 +10,7 @@ allocator for the length of the call.
 import torch
 
 from . import MoEError, lib
-from ._tensors import check, row_stride, stream_on
+from ._tensors import check, fits, row_stride, stream_on
 
 _F32, _BF16, _E4M3, _I32 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int32
 
@@ -35,6 +35,7 @@ def _weights(w, w_scales):
         raise ValueError("w: [N, K] or [E, N, K]")
     if one != 1 and K > 1:
         raise ValueError("w: contiguous rows")
+    fits(max(E, N, K), "w")
     if N == 1 and ldw < K:  # (one expert)
         ldw = K
     check(w_scales, _F32, blocks, w.device, "w_scales")
@@ -59,6 +60,7 @@ def blockscale_quantize(x, slots=None, top_k=1):
     (T, C), dev = x.shape, x.device
     stream = stream_on(dev)
     R = T
+    fits(top_k, "top_k")
     if slots is not None:
         R = slots.numel()
         check(slots, _I32, (R,), dev, "slots")
@@ -155,6 +157,7 @@ def blockscale_experts(x, slots, offsets, top_k, w13, w13_scales, w2, w2_scales,
     if x.shape[1] != H or x.device != dev or w2.device != dev:
         raise ValueError("x: [T, %d], all on %s" % (H, dev))
     R = slots.numel()
+    fits(top_k, "top_k")
     check(slots, _I32, (R,), dev, "slots")
     check(offsets, _I32, (E + 1,), dev, "offsets")
     out, ldo = _result(out, R, H, dev)

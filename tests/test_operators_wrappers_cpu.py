@@ -3,7 +3,7 @@ attributes that the wrappers read take the place of CUDA tensors."""
 import pytest
 import torch
 
-from moe_expert_layer_histogram_gb300 import blockscale
+from moe_expert_layer_histogram_gb300 import _tensors, blockscale
 
 CUDA = torch.device("cuda:0")
 
@@ -59,3 +59,30 @@ def test_weight_strides(shape, strides, want):
 def test_weight_strides_refused(shape, strides):
     with pytest.raises(ValueError):
         blockscale._weights(*weights(shape, strides))
+
+
+BIG = 2 ** 32 + 4                                     # 4, if cut to 32 bits
+
+
+@pytest.mark.parametrize("shape", [(BIG, 16), (16, BIG), (2 ** 31, 16)])
+def test_matrices_past_32_bits_are_refused(shape):
+    # (the library takes its sizes as 32-bit integers)
+    with pytest.raises(ValueError):
+        _tensors.row_stride(Fake(torch.bfloat16, shape), torch.bfloat16, "x")
+    with pytest.raises(ValueError):
+        blockscale._weights(*weights(shape))
+    with pytest.raises(ValueError):
+        blockscale._weights(*weights((2,) + shape))
+
+
+def test_more_slots_than_32_bits_are_refused():
+    with pytest.raises(ValueError):
+        _tensors.check(Fake(torch.int32, (BIG,)), torch.int32, (BIG,), CUDA, "slots")
+    assert _tensors.check(Fake(torch.int32, (4,)), torch.int32, (4,), CUDA, "slots") is None
+
+
+def test_numbers_past_32_bits_are_refused():
+    assert _tensors.fits(2 ** 31 - 1, "top_k") is None
+    for n in (2 ** 31, BIG):
+        with pytest.raises(ValueError):
+            _tensors.fits(n, "top_k")
