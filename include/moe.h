@@ -436,7 +436,8 @@ moe_status moe_blockscale_matmul(const void *a, int64_t lda,
 /* The gate/up product with SwiGLU and re-quantisation: w13 [E, 2I, K], rows
  * 0..I-1 of an expert the gate and I..2I-1 the up projection (as
  * moe_prepare_weights takes them); h = silu(gate) * up in fp32, gate and up
- * clamped to [-clamp_limit, clamp_limit] first when that is > 0 and finite;
+ * clamped to [-clamp_limit, clamp_limit] first when that is > 0 and finite
+ * (a NaN stays one);
  * h quantised as moe_blockscale_quantize does, without an intermediate
  * rounding, into codes h [M, I] (16-byte aligned, ldh a multiple of 16) and
  * h_scales [I / 128, ld_hs].  I a multiple of 128 (else

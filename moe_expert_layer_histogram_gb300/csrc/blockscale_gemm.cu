@@ -388,9 +388,16 @@ __device__ __forceinline__ void store_bf16_32(__nv_bfloat16* row0, int64_t ldo, 
   }
 }
 
+// v in [-limit, limit]; a NaN stays one (fminf and fmaxf would drop it).
+__device__ __forceinline__ float clamp_to(float v, float limit) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-limit));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(limit));
+  return v;
+}
+
 __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
-  g = fminf(fmaxf(g, -clamp), clamp);
-  u = fminf(fmaxf(u, -clamp), clamp);
+  g = clamp_to(g, clamp);
+  u = clamp_to(u, clamp);
   // e^-g by the hardware's power of two and an approximate quotient, a few ulp:
   // as near as the sums of the product
   float e;

@@ -75,3 +75,53 @@ def test_experts_with_offsets_out_of_order(kind, E, M):
                                   s13, w2, s2, out=out)
 
     assert torch.equal(call(off), call(in_order(off, M)))
+
+
+# ---------------------------------------------------------------- non-finite values
+# rows split over a cluster, rows of one chunk, several chunks, CTA pairs
+@pytest.mark.parametrize("clamp", [0.0, 7.0])
+@pytest.mark.parametrize("M,K", [(6, 1040), (100, 256), (300, 272), (3000, 272)])
+def test_swiglu_keeps_non_finite_rows(M, K, clamp):
+    from moe_expert_layer_histogram_gb300 import blockscale_quantize, moe_blockscale_swiglu
+    I = 256
+    w, s = draw_w(1, 2 * I, K, 3)
+    s = s * (8.5 / K ** 0.5)
+    x = draw_x(M, K, 1)
+    bad = sorted({2, M // 2, M - 1})
+    for r, v in zip(bad, (float("inf"), float("nan"), -float("inf"))):
+        x[r, 3 + r % 100] = v
+    codes, scales = blockscale_quantize(x)
+    h = torch.empty(M, I, dtype=torch.float8_e4m3fn, device="cuda")
+    hs = torch.empty(I // 128, M, device="cuda")
+    moe_blockscale_swiglu(codes, codes.stride(0), scales, M, w, w.stride(1), s, None, 1, M, I, K,
+                          clamp, h, I, hs, M, torch.cuda.current_stream().cuda_stream)
+    is_bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    is_bad[bad] = True
+    assert torch.equal(torch.isnan(hs).all(0), is_bad) and torch.equal(torch.isnan(hs).any(0), is_bad)
+    nan = torch.isnan(h.float())
+    assert torch.equal(nan.all(1), is_bad) and torch.equal(nan.any(1), is_bad)
+
+
+@pytest.mark.parametrize("clamp", [0.0, 7.0])
+@pytest.mark.parametrize("T,E,topk", [(3, 8, 2), (60, 4, 2), (1500, 3, 2)])
+def test_experts_keep_non_finite_tokens(T, E, topk, clamp):
+    # a token with an infinity or NaN gives NaN rows, the others stay as they are
+    from moe_expert_layer_histogram_gb300 import blockscale_experts
+    H, I = 400, 256
+    w13, s13 = draw_w(E, 2 * I, H, 1)
+    w2, s2 = draw_w(E, H, I, 2)
+    s13 = s13 * (8.5 / H ** 0.5)
+    g = torch.Generator().manual_seed(T)
+    ids = torch.rand(T, E, generator=g).topk(topk, 1).indices.reshape(-1)
+    slots = torch.sort(ids, stable=True).indices.to(torch.int32).cuda()
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = torch.bincount(ids, minlength=E).cumsum(0)
+    x = draw_x(T, H, 5)
+    want = blockscale_experts(x, slots, off.cuda(), topk, w13, s13, w2, s2, clamp=clamp)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[0] = bad[T - 1] = True
+    x[0, 399], x[T - 1, 0] = float("nan"), float("inf")
+    y = blockscale_experts(x, slots, off.cuda(), topk, w13, s13, w2, s2, clamp=clamp)
+    rows = bad[slots.long() // topk]
+    assert bool(torch.isfinite(want).all())
+    assert bool(torch.isnan(y[rows]).all()) and torch.equal(y[~rows], want[~rows])
