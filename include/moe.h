@@ -438,8 +438,8 @@ moe_status moe_blockscale_matmul(const void *a, int64_t lda,
  * moe_prepare_weights takes them); h = silu(gate) * up in fp32, gate and up
  * clamped to [-clamp_limit, clamp_limit] first when that is > 0 and finite
  * (a NaN stays one);
- * h quantised as moe_blockscale_quantize does, without an intermediate
- * rounding, into codes h [M, I] (16-byte aligned, ldh a multiple of 16) and
+ * h quantised as moe_blockscale_quantize does (a block whose scale rounds to
+ * 0 is a zero block), without an intermediate rounding, into codes h [M, I] (16-byte aligned, ldh a multiple of 16) and
  * h_scales [I / 128, ld_hs].  I a multiple of 128 (else
  * MOE_ERR_UNSUPPORTED); the rest as moe_blockscale_matmul.                */
 moe_status moe_blockscale_swiglu(const void *a, int64_t lda,

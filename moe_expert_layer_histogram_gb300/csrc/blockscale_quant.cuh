@@ -23,8 +23,8 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 // subnormal is then below 2^-22 s, far under the smallest code.  For the
 // fp32 values of the fused SwiGLU it is within an ulp.  The signs are
 // arranged so that -0 stays -0.  Blocks of smaller scale take divides.
-// amax == 0: s = 0 and zero codes; an infinity or NaN in the block: s = NaN
-// and NaN codes.
+// s == 0 (amax 0, or an fp32 amax up to 2^-149 * 224, whose quotient rounds to
+// 0): zero codes; an infinity or NaN in the block: s = NaN and NaN codes.
 struct BlockQuant {
   float scale, r;
   bool slow;
@@ -32,8 +32,8 @@ struct BlockQuant {
   __device__ __forceinline__ explicit BlockQuant(uint32_t amax_bits) {
     scale = amax_bits >= kInfBits ? __uint_as_float(0x7FC00000u)
                                   : __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
-    r = amax_bits == 0u ? 0.0f : __frcp_rn(scale);
-    slow = scale < 0x1p-80f && amax_bits != 0u;
+    r = scale == 0.0f ? 0.0f : __frcp_rn(scale);
+    slow = scale < 0x1p-80f && scale != 0.0f;
   }
   // The same for a bf16 block with is_fast(amax), without a branch: the
   // scale by the Newton step of the codes (exact in the same way), r by the

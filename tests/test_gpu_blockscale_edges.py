@@ -125,3 +125,55 @@ def test_experts_keep_non_finite_tokens(T, E, topk, clamp):
     rows = bad[slots.long() // topk]
     assert bool(torch.isfinite(want).all())
     assert bool(torch.isnan(y[rows]).all()) and torch.equal(y[~rows], want[~rows])
+
+
+# ---------------------------------------------------------------- tiny values
+def tiny_rows(M, K, seed):
+    """Rows whose gate and up shrink row by row: h's block maxima run from about
+    2^-120 through fp32's subnormal range to 0."""
+    x = draw_x(M, K, seed).float()
+    x = x * torch.exp2(-torch.linspace(57, 78, M, device="cuda"))[:, None]
+    return x.bfloat16()
+
+
+@pytest.mark.parametrize("clamp", [0.0, 7.0])
+@pytest.mark.parametrize("M", [7, 60, 300, 3000])
+def test_swiglu_of_tiny_values(M, clamp):
+    # h is stored as code * s: s = RN(amax / 448) is off by up to 2^-150, which
+    # moves (and at the top cuts) a value by up to 448 times that; a code is off
+    # by 2^-4 of its value, or 2^-10 s, twice that where h's own error moves it
+    # across a rounding boundary; h's error is 2^-13 of it and a few 2^-149.
+    from moe_expert_layer_histogram_gb300 import blockscale_quantize, moe_blockscale_swiglu
+    from .test_gpu_blockscale import dequant_rows, swiglu_ref
+    I, K = 256, 272
+    w, s = draw_w(1, 2 * I, K, 3)
+    s = s * (8.5 / K ** 0.5)
+    codes, scales = blockscale_quantize(tiny_rows(M, K, 1))
+    h = torch.empty(M, I, dtype=torch.float8_e4m3fn, device="cuda")
+    hs = torch.empty(I // 128, M, device="cuda")
+    moe_blockscale_swiglu(codes, codes.stride(0), scales, M, w, w.stride(1), s, None, 1, M, I, K,
+                          clamp, h, I, hs, M, torch.cuda.current_stream().cuda_stream)
+    ref = swiglu_ref(dequant_rows(codes, scales).cpu(), w[0], s[0], clamp)
+    top = ref.abs().amax(1)
+    assert float(top.max()) > 2.0 ** -126 and float(top.min()) < 2.0 ** -149
+    assert bool(torch.isfinite(hs).all()) and bool(torch.isfinite(h.float()).all())
+    amax = ref.abs().view(M, 2, 128).amax(2)
+    got_s = hs.t().double().cpu()
+    assert bool(((got_s - amax / 448).abs() <= 2.0 ** -13 * amax / 448 + 2.0 ** -149).all())
+    err = (dequant_rows(h, hs).cpu() - ref).abs()
+    tol = (2.0 ** -3 + 2.0 ** -13) * ref.abs() + 2.0 ** -9 * got_s.repeat_interleave(128, 1) + 2.0 ** -141
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("M", [7, 60, 300])
+def test_experts_of_tiny_values(M):
+    # the tokens' h is far below bf16's normal range: finite and next to nothing
+    from moe_expert_layer_histogram_gb300 import blockscale_experts
+    H, I = 272, 256
+    w13, s13 = draw_w(2, 2 * I, H, 1)
+    w2, s2 = draw_w(2, H, I, 2)
+    x = tiny_rows(M, H, 4)
+    off = torch.tensor([0, M // 2, M], dtype=torch.int32, device="cuda")
+    slots = torch.arange(M, dtype=torch.int32, device="cuda")
+    y = blockscale_experts(x, slots, off, 1, w13, s13 * (8.5 / H ** 0.5), w2, s2)
+    assert bool(torch.isfinite(y).all()) and float(y.abs().max()) < 2.0 ** -90
