@@ -129,7 +129,7 @@ __device__ __forceinline__ int top_k(const float (&x)[4 * MAXI], int E, int K, i
   for (int j = 0; j < 4 * MAXI; ++j) {
     const int e = 128 * (j >> 2) + 4 * lane + (j & 3);
     // the key: sign bit flipped, the other bits too where it was set (x + 0
-    // turns -0 into +0)
+    // turns -0 into +0 and any NaN into the positive one, which comes first)
     const int32_t b = __float_as_int(x[j] + 0.0f);
     const uint32_t key = static_cast<uint32_t>(b) ^ (static_cast<uint32_t>(b >> 31) | 0x80000000u);
     word[j] = e < E ? (key & 0xFFFFFE00u) | static_cast<uint32_t>(511 - e) : 0u;
@@ -158,8 +158,8 @@ __device__ __forceinline__ int top_k(const float (&x)[4 * MAXI], int E, int K, i
       uint32_t key[4 * MAXI];
 #pragma unroll
       for (int j = 0; j < 4 * MAXI; ++j)
-        // (a NaN's key may be 0, which marks an empty slot)
-        key[j] = 128 * (j >> 2) + 4 * lane + (j & 3) < E ? max(logit_key(x[j]), 1u) : 0u;
+        // (x + 0 again: every NaN is the same positive one, the largest key)
+        key[j] = 128 * (j >> 2) + 4 * lane + (j & 3) < E ? logit_key(x[j] + 0.0f) : 0u;
       int id = 0;
       for (int k = 0; k < K; ++k) {
         uint32_t m = 0u;
