@@ -544,8 +544,10 @@ cudaError_t run_forward(const T* logits, int64_t ld, const uint8_t* mask, int to
     constexpr int smem = kBalanceWarps * kI * 128 * 4;
     if (tokens <= kSmallTokens) {
       auto k = balance_small_kernel<kI, kV, T>;
-      static const cudaError_t ready =
-          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      static OncePerDevice prepared;
+      const cudaError_t ready = prepared([&] {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      });
       if (ready != cudaSuccess) return ready;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -567,8 +569,10 @@ cudaError_t run_forward(const T* logits, int64_t ld, const uint8_t* mask, int to
     float* psum = static_cast<float*>(workspace);
     int32_t* count = reinterpret_cast<int32_t*>(psum + static_cast<int64_t>(blocks) * E);
     auto k = balance_forward_kernel<kI, kV, T>;
-    static const cudaError_t ready =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static OncePerDevice prepared;
+    const cudaError_t ready = prepared([&] {
+      return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
     if (ready != cudaSuccess) return ready;
     cudaError_t e = launch_pdl(false, k, dim3(blocks), dim3(32 * kBalanceWarps), smem, s, logits,
                                ld, mask, tokens, E, K, ids, weights, psum, count);

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -168,32 +169,38 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The current device, null unless it is an sm_103 one (looked up once per
-// device).
+// The current device, null unless it is an sm_103 one.  What was found out about
+// a device is kept; a look-up that failed is tried again.
 const BlockscaleDevice* current_device() {
   constexpr int kMaxDevices = 64;
   struct Entry {
-    std::once_flag once;
-    bool usable = false;
+    std::atomic<bool> known{false};
     BlockscaleDevice d{};
   };
   static Entry entries[kMaxDevices];
+  static std::mutex looking_up;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
     return nullptr;
   }
   Entry& e = entries[dev];
-  std::call_once(e.once, [&] {
+  if (e.known.load(std::memory_order_acquire)) return &e.d;
+  std::lock_guard<std::mutex> lock(looking_up);
+  if (!e.known.load(std::memory_order_relaxed)) {
     int major = 0, minor = 0;
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    cudaDeviceGetAttribute(&e.d.sms, cudaDevAttrMultiProcessorCount, dev);
-    e.usable = major == 10 && minor == 3 && tensor_map_encoder() &&
-               blockscale_clusters(&e.d) == cudaSuccess;
-    cudaGetLastError();
-  });
-  return e.usable ? &e.d : nullptr;
+    const bool usable =
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&e.d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+        major == 10 && minor == 3 && tensor_map_encoder() && blockscale_clusters(&e.d) == cudaSuccess;
+    if (!usable) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    e.known.store(true, std::memory_order_release);
+  }
+  return &e.d;
 }
 
 // early: the product follows the library's own kernel on the stream and may

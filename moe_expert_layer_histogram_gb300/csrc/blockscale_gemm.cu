@@ -1043,16 +1043,17 @@ int extra_smem(int a_rows, int resident) {
 template <int NT, bool SWIGLU, bool TRANS, bool SPLIT, bool PAIR = false, bool QUANT = false>
 cudaError_t launch_bs(const BlockscaleMaps& maps, BlockscaleArgs p, int grid, cudaStream_t s) {
   auto k = blockscale_gemm_kernel<NT, SWIGLU, TRANS, SPLIT, PAIR, QUANT>;
-  // Once per instance: the shared-memory limit, and that the launch
+  // Once per instance and device: the shared-memory limit, and that the launch
   // allocation covers the register split (setmaxnreg would wait forever).
-  static const cudaError_t ready = [&] {
+  static OncePerDevice prepared;
+  const cudaError_t ready = prepared([&] {
     cudaError_t e =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmemLimit);
     cudaFuncAttributes fa{};
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, k);
     if (e == cudaSuccess && !QUANT && fa.numRegs != kBsLaunchRegs) e = cudaErrorInvalidConfiguration;
     return e;
-  }();
+  });
   if (ready != cudaSuccess) return ready;
   const int a_bytes = p.a_rows * 128;
   const int stage = (QUANT ? 0 : a_bytes) + NT / (PAIR ? 2 : 1) * 128;

@@ -2,6 +2,7 @@
 // translation units of the GB300 MoE expert-layer library.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -119,6 +120,28 @@ cudaError_t launch_pdl(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+
+// Preparation of a kernel that belongs to the device it is done on (its
+// shared-memory limit, say): the first call on each device runs `prepare`, and
+// one that failed is tried again.  Threads that come first together both run
+// it, so it is something that may be done twice.
+class OncePerDevice {
+ public:
+  template <typename F>
+  cudaError_t operator()(F&& prepare) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (ready_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = prepare();
+    if (e == cudaSuccess) ready_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> ready_{0};
+};
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_launch_dependents() {
