@@ -629,7 +629,7 @@ moe_status moe_balance_forward(const void* logits, int dtype, int64_t ld, const 
                         counts, mean_probs, loss, workspace, s)
           : run_forward(static_cast<const __nv_bfloat16*>(logits), ld, mask, T, E, K, coef, ids,
                         weights, counts, mean_probs, loss, workspace, s);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_balance_backward(const void* logits, int dtype, int64_t ld, int T, int E, int K,
@@ -654,7 +654,7 @@ moe_status moe_balance_backward(const void* logits, int dtype, int64_t ld, int T
           : run_backward(static_cast<const __nv_bfloat16*>(logits), ld, T, E, K, coef, ids,
                          weights, counts, d_loss, d_weights,
                          static_cast<__nv_bfloat16*>(d_logits), ld_d, s);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

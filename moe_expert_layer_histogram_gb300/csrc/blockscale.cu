@@ -247,7 +247,7 @@ moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, fl
   a.ldx = p.ldx;
   a.x_vec = aligned_to(p.x, 16) && p.ldx % 8 == 0;
   a.early = early;
-  return launch_blockscale(maps, a, swiglu, p.transpose, *d, s) == cudaSuccess
+  return take_error(launch_blockscale(maps, a, swiglu, p.transpose, *d, s)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -270,7 +270,7 @@ moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* s
       grid, dim3(256), 0, s, static_cast<const __nv_bfloat16*>(x),
       ldx, x_rows, slots, top_k, rows, cols, static_cast<uint8_t*>(codes), ld_codes, scales,
       ld_scales);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Quantised activations in a workspace: codes in rows of a multiple of 16
@@ -425,9 +425,10 @@ moe_status moe_blockscale_experts(const void* x, int64_t ldx, int T, const int32
     const int words = static_cast<int>(t.ld / 16);
     const dim3 grid((static_cast<unsigned>(rows) + 7) / 8, (words + kCopyWords - 1) / kCopyWords);
     if (st == MOE_OK &&
-        launch_pdl(true, blockscale_copy_rows_kernel, grid, dim3(256), 0, s,
-                   reinterpret_cast<const uint4*>(t.codes), t.scales, T, blocks_of(H), words,
-                   slots, top_k, rows, reinterpret_cast<uint4*>(q.codes), q.scales) != cudaSuccess)
+        take_error(launch_pdl(true, blockscale_copy_rows_kernel, grid, dim3(256), 0, s,
+                              reinterpret_cast<const uint4*>(t.codes), t.scales, T, blocks_of(H),
+                              words, slots, top_k, rows, reinterpret_cast<uint4*>(q.codes),
+                              q.scales)) != cudaSuccess)
       st = MOE_ERR_CUDA;
   } else {
     st = run_quantize(x, ldx, T, slots, top_k, rows, H, q.codes, q.ld, q.scales, q.ld_scales, s);

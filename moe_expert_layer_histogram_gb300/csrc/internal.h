@@ -121,6 +121,13 @@ cudaError_t launch_pdl(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// The error of a call that failed, taken from the runtime as well: the caller
+// reports it, and the program's next launch check does not find it again.
+inline cudaError_t take_error(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 // Preparation of a kernel that belongs to the device it is done on (its
 // shared-memory limit, say): the first call on each device runs `prepare`, and
 // one that failed is tried again.  Threads that come first together both run

@@ -10,7 +10,7 @@
 #include "internal.h"
 
 namespace {
-int device, failures, launches, attribute_calls;
+int device, failures, bad_launch, launches, attribute_calls;  // bad_launch: 1 is the next one
 cudaError_t last_error;
 std::map<std::pair<int, const void*>, int> limits;
 int last_grid, last_smem, last_stages;
@@ -32,6 +32,7 @@ extern "C" {
 // ---- what a test sets and reads
 void fake_set_device(int d) { device = d; }
 void fake_fail_calls(int n) { failures = n; }  // the next n attribute and launch calls
+void fake_fail_launch(int n) { bad_launch = n + 1; }  // the n-th launch from now, 0 the next
 int fake_launches() { return launches; }
 int fake_attribute_calls() { return attribute_calls; }
 int fake_last_grid() { return last_grid; }
@@ -72,6 +73,7 @@ cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunch
 }
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void** args) {
   if (failures > 0) return --failures, note(cudaErrorUnknown);
+  if (bad_launch > 0 && --bad_launch == 0) return note(cudaErrorUnknown);
   // 48 KB in all without the attribute; a kernel's static part is not known here: 2 KB
   const auto l = limits.find({device, f});
   const size_t limit = l == limits.end() ? 46 << 10 : l->second;

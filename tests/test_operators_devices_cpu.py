@@ -8,7 +8,7 @@ import pytest
 from . import fake_cuda
 
 P = 1 << 20
-OK = 0
+OK, CUDA_ERROR = 0, 4
 
 
 @pytest.fixture(scope="module")
@@ -100,3 +100,23 @@ def test_a_failure_does_not_last(lib, name, failures):
     lib.fake_fail_calls(failures)
     assert CALLS[name](lib) != OK
     assert CALLS[name](lib) == OK
+
+
+@pytest.mark.parametrize("name", ["balance 8 x 64", "balance 4096 x 512",
+                                  "linear (1, 4096, 7168, 0)", "linear (4000, 4096, 1024, 0)",
+                                  "grouped (8, 8, 256, 2048, 0)", "experts (500, 500, 4)",
+                                  "experts (40000, 80000, 4)", "backward", "quantize"])
+def test_a_failed_launch_leaves_no_error_behind(lib, name):
+    # (the next launch check of the program would take it for its own)
+    call = dict(CALLS, backward=lambda L: L.moe_balance_backward(
+        P, 0, 64, 32, 64, 6, 1.0, P, P, P, P, P, P, 64, None),
+        quantize=lambda L: L.moe_blockscale_quantize(P, 256, 8, None, 1, 8, 256, P, 256, P, 8, None)
+    )[name]
+    assert call(lib) == OK
+    start = lib.fake_launches()
+    assert call(lib) == OK
+    for nth in range(lib.fake_launches() - start):      # each of the call's launches in turn
+        lib.fake_fail_launch(nth)
+        assert call(lib) == CUDA_ERROR
+        assert lib.cudaPeekAtLastError() == 0
+    assert call(lib) == OK
