@@ -1155,8 +1155,10 @@ cudaError_t blockscale_clusters(BlockscaleDevice* d) {
 
 bool blockscale_quantizes(int M, int N, int K, const BlockscaleDevice& d) {
   const Plan p = plan_product(M, N, K, 1, false, d);
-  const int64_t smem = p.resident * p.a_rows * 128 + 2 * 128 * 128 + 1024 +
-                       extra_smem<128, false, true, true>(p.a_rows, p.resident) + 16;
+  // (two stages of weights beside the rows)
+  const int extra = p.split > 1 ? extra_smem<128, false, true, true>(p.a_rows, p.resident)
+                                : extra_smem<128, false, false, true>(p.a_rows, p.resident);
+  const int64_t smem = int64_t{p.resident} * p.a_rows * 128 + 2 * 128 * 128 + 1024 + extra + 16;
   return !p.wide && std::min(M, 128) * p.resident <= kBsQuantUnits && smem <= kBsSmemLimit &&
          (p.items * p.split <= d.sms || M <= 16);
 }

@@ -177,3 +177,33 @@ def test_experts_of_tiny_values(M):
     slots = torch.arange(M, dtype=torch.int32, device="cuda")
     y = blockscale_experts(x, slots, off, 1, w13, s13 * (8.5 / H ** 0.5), w2, s2)
     assert bool(torch.isfinite(y).all()) and float(y.abs().max()) < 2.0 ** -90
+
+
+# ---------------------------------------------------------------- sizes
+@pytest.mark.parametrize("M,N,K", [(3, 9856, 11264), (16, 20000, 144)])
+def test_few_rows_into_many_columns(M, N, K):
+    # more tiles than can be split: a row's codes fill most of the shared memory,
+    # and more CTAs than run at a time quantise the same rows
+    from moe_expert_layer_histogram_gb300 import blockscale_linear, blockscale_quantize
+    from .test_gpu_blockscale import assert_product, product_ref
+    x = draw_x(M, K, M + N + K)
+    w, s = draw_w(1, N, K, N)
+    codes, scales = blockscale_quantize(x)
+    assert_product(blockscale_linear(x, w[0], s[0]), *product_ref(codes, scales, w[0], s[0]), K)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_one_weight_row_an_expert(transpose):
+    from moe_expert_layer_histogram_gb300 import blockscale_matmul, blockscale_quantize
+    from .test_gpu_blockscale import assert_product, dequant_rows, dequant_weight, offsets_of
+    counts, cols = [3, 0, 20, 9], 272
+    w, s = draw_w(4, 1, cols, 5)
+    K = 1 if transpose else cols
+    codes, scales = blockscale_quantize(draw_x(32, K, 2))
+    out = blockscale_matmul(codes, scales, w, s, offsets_of(counts), transpose_w=transpose)
+    a, r = dequant_rows(codes, scales).cpu(), 0
+    for e, c in enumerate(counts):
+        b = dequant_weight(w[e], s[e]).cpu()
+        b = b if transpose else b.t()
+        assert_product(out[r:r + c], a[r:r + c] @ b, a[r:r + c].abs() @ b.abs(), K)
+        r += c

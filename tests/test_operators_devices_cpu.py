@@ -120,3 +120,17 @@ def test_a_failed_launch_leaves_no_error_behind(lib, name):
         assert call(lib) == CUDA_ERROR
         assert lib.cudaPeekAtLastError() == 0
     assert call(lib) == OK
+
+
+def test_every_product_has_stages_to_load_ahead(lib):
+    # products that quantise their own rows keep them in shared memory beside the
+    # ring of weight tiles: two stages at least, one to load while one is used
+    seen = 0
+    for M in (1, 2, 5, 16, 17, 32, 48, 64, 65, 128, 333, 1000):
+        for N in (64, 1000, 4096, 9728, 12000, 20000):
+            for K in list(range(128, 13000, 384)) + [10880, 10896, 11008, 11392, 16384, 30000]:
+                own_rows = lib.moe_blockscale_linear_workspace(M, N, K) == 0
+                seen += own_rows
+                assert linear(lib, M, N, K) == OK
+                assert lib.fake_last_stages() >= 2, (M, N, K, own_rows)
+    assert seen > 100
