@@ -207,3 +207,49 @@ def test_one_weight_row_an_expert(transpose):
         b = b if transpose else b.t()
         assert_product(out[r:r + c], a[r:r + c] @ b, a[r:r + c].abs() @ b.abs(), K)
         r += c
+
+
+# ---------------------------------------------------------------- many tokens
+# Sizes for which the experts' call quantises the tokens once and copies their
+# codes to the rows (test_operators_devices_cpu.py holds them to that).
+COPIED = [(2100, 5, 4, 2064, 640), (9000, 5, 2, 1040, 640), (1300, 4, 3, 4400, 1664)]
+
+
+@pytest.mark.parametrize("T,E,topk,H,I", COPIED)
+def test_experts_copy_the_tokens_codes(T, E, topk, H, I):
+    # the same bits as the quantiser's gather and the two products one by one;
+    # slots outside the tokens give zero rows; some rows against 64 bits (as in
+    # test_experts_match_64_bits)
+    import numpy as np
+    from moe_expert_layer_histogram_gb300 import (blockscale_experts, blockscale_matmul,
+                                                  blockscale_quantize, moe_blockscale_swiglu)
+    from .test_gpu_blockscale import dequant_rows, dequant_weight, round_e4m3, swiglu_ref
+    R = T * topk
+    x = draw_x(T, H, T)
+    w13, s13 = draw_w(E, 2 * I, H, 1)
+    w2, s2 = draw_w(E, H, I, 2)
+    s13 = s13 * (8.5 / H ** 0.5)
+    g = torch.Generator().manual_seed(T)
+    ids = torch.rand(T, E, generator=g).topk(topk, 1).indices.reshape(-1)
+    slots = torch.sort(ids, stable=True).indices.to(torch.int32)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = torch.bincount(ids, minlength=E).cumsum(0)
+    out_of = torch.tensor([0, 77, R // 2, R - 1])
+    slots[out_of] = torch.tensor([-1, R, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    slots, off_gpu = slots.cuda(), off.cuda()
+    y = blockscale_experts(x, slots, off_gpu, topk, w13, s13, w2, s2)
+    codes, scales = blockscale_quantize(x, slots, topk)
+    h = torch.empty(R, I, dtype=torch.float8_e4m3fn, device="cuda")
+    hs = torch.empty(I // 128, R, device="cuda")
+    moe_blockscale_swiglu(codes, H, scales, R, w13, H, s13, off_gpu, E, R, I, H, 0.0, h, I, hs, R,
+                          torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(y, blockscale_matmul(h, hs, w2, s2, off_gpu))
+    assert not bool(y[out_of].any()) and bool(y.any(1).sum() == R - 4)
+    for e in range(E):
+        rows = torch.arange(int(off[e]), int(off[e + 1]))[5::131]
+        a = dequant_rows(codes[rows], scales[:, rows]).cpu()
+        hr = swiglu_ref(a, w13[e], s13[e], 0.0).numpy()
+        s = (np.abs(hr.reshape(len(rows), -1, 128)).max(2) / 448).repeat(128, 1)
+        ref = torch.from_numpy(round_e4m3(hr / np.where(s == 0, 1, s)) * s) @ dequant_weight(w2[e], s2[e]).cpu().t()
+        err = float((y[rows].double().cpu() - ref).norm() / ref.norm())
+        assert err <= 1e-2, err

@@ -134,3 +134,16 @@ def test_every_product_has_stages_to_load_ahead(lib):
                 assert linear(lib, M, N, K) == OK
                 assert lib.fake_last_stages() >= 2, (M, N, K, own_rows)
     assert seen > 100
+
+
+def test_experts_of_many_tokens_copy_the_codes(lib):
+    # one launch more: the tokens' quantisation, the copy, two products
+    from .test_gpu_blockscale_edges import COPIED
+    for T, E, topk, H, I in COPIED:
+        before = lib.fake_launches()
+        assert lib.moe_blockscale_experts(P, H, T, P, topk, T * topk, P, E, P, P, P, P, H, I, 0.0, P,
+                                          H, P, 1 << 40, None) == OK
+        assert lib.fake_launches() - before == 4
+    before = lib.fake_launches()
+    assert experts(lib, 64, 128, 4) == OK
+    assert lib.fake_launches() - before == 3
