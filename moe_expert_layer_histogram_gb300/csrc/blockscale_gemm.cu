@@ -1127,8 +1127,10 @@ Plan plan_product(int M, int N, int K, int E, bool swiglu, const BlockscaleDevic
 // row x 7168 into 4096 takes 8.5 us where a quantising kernel and the product
 // take 10.1; 16 rows 10.4 and 10.6; 48 rows x 2048 into 7168 (384 a CTA) 10.4
 // and 9.1; 333 x 2000 into 1001 (512) 11.6 and 8.8; 64 x 7168 into 2048 (640)
-// 13.7 and 10.5.  But the second launch and the workspace make a call 21 us
-// for the host, against 12, so up to 512 the one kernel is the faster call.
+// 13.7 and 10.5; 16 x 4096 into 14592 (512, not split) 17.1 and 15.3, one row of
+// it (32) 13.9 and 15.1.  But the second launch and the workspace make a call
+// 21 us for the host, against 12, so up to 512 the one kernel is the faster
+// call from eager code; replayed from a graph it is up to a third slower.
 constexpr int kBsQuantUnits = 512;
 
 }  // namespace
@@ -1160,7 +1162,7 @@ bool blockscale_quantizes(int M, int N, int K, const BlockscaleDevice& d) {
                                 : extra_smem<128, false, false, true>(p.a_rows, p.resident);
   const int64_t smem = int64_t{p.resident} * p.a_rows * 128 + 2 * 128 * 128 + 1024 + extra + 16;
   return !p.wide && std::min(M, 128) * p.resident <= kBsQuantUnits && smem <= kBsSmemLimit &&
-         (p.items * p.split <= d.sms || M <= 16);
+         p.items * p.split <= d.sms;
 }
 
 cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool swiglu,

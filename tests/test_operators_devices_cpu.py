@@ -147,3 +147,12 @@ def test_experts_of_many_tokens_copy_the_codes(lib):
     before = lib.fake_launches()
     assert experts(lib, 64, 128, 4) == OK
     assert lib.fake_launches() - before == 3
+
+
+def test_rows_are_quantised_in_the_product_only_where_all_ctas_run_at_once(lib):
+    for M in (1, 3, 16, 17, 48, 128, 130, 400, 512):
+        for N in (1, 128, 1000, 4096, 9728, 9729, 19456, 19457, 40000, 128256, 1 << 20):
+            for K in (16, 128, 2000, 4096, 7168, 11008):
+                if lib.moe_blockscale_linear_workspace(M, N, K) == 0:
+                    assert linear(lib, M, (N + 15) // 16 * 16, K) == OK
+                    assert lib.fake_last_grid() <= 152, (M, N, K)
