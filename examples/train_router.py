@@ -18,8 +18,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from moe_expert_layer_histogram_gb300 import (blockscale_experts,  # noqa: E402
-                                              moe_route_permute_static, router_balance,
-                                              router_balance_backward)
+                                              router_balance, router_balance_backward)
 
 
 def quantize_weight(w):
@@ -29,6 +28,17 @@ def quantize_weight(w):
     v = w.float().view(E, N // 128, 128, K // 128, 128)
     s = v.abs().amax(dim=(2, 4)) / 448.0
     return (v / s[:, :, None, :, None]).view(E, N, K).to(torch.float8_e4m3fn), s
+
+
+def expert_order(routing):
+    """The routed slots t * K + k in expert order, as blockscale_experts takes
+    them: slots int32 [T * K], offsets int32 [E + 1].  Slots of tokens that are
+    not live (id -1) come first and belong to no expert."""
+    ids = routing.ids.flatten()
+    slots = torch.sort(ids, stable=True).indices.to(torch.int32)
+    offsets = torch.zeros(routing.counts.numel() + 1, dtype=torch.int32, device=ids.device)
+    torch.cumsum(routing.counts, 0, dtype=torch.int32, out=offsets[1:])
+    return slots, offsets + (ids.numel() - offsets[-1])
 
 
 class FrozenExperts:
@@ -42,18 +52,17 @@ class FrozenExperts:
         self.w2, self.s2 = quantize_weight(
             torch.randn(E, H, I, generator=g, device="cuda") * I ** -0.5)
 
-    def forward(self, x, logits, coef):
-        T = x.shape[0]
-        routing = router_balance(logits, self.K, coef)
-        dev = x.device
-        off = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
-        perm = torch.empty(T * self.K, dtype=torch.int32, device=dev)
-        moe_route_permute_static(logits, T, self.E, self.K, torch.empty_like(routing.ids),
-                                 torch.empty_like(routing.weights), off, perm,
-                                 torch.cuda.current_stream().cuda_stream)
-        y = blockscale_experts(x, perm, off, self.K, self.w13, self.s13, self.w2, self.s2)
-        row_of_slot = torch.empty_like(perm, dtype=torch.int64)
-        row_of_slot[perm.long()] = torch.arange(T * self.K, device=dev)
+    def forward(self, x, logits, coef, mask=None):
+        """Any number of tokens, logits f32 or bf16; mask as router_balance
+        takes it: padding goes through no expert and gives zero rows."""
+        T, dev = x.shape[0], x.device
+        routing = router_balance(logits, self.K, coef, mask=mask)
+        slots, off = expert_order(routing)
+        # (rows of no expert, padding's, are left as they are: zero)
+        y = torch.zeros(T * self.K, x.shape[1], dtype=torch.bfloat16, device=dev)
+        blockscale_experts(x, slots, off, self.K, self.w13, self.s13, self.w2, self.s2, out=y)
+        row_of_slot = torch.empty(T * self.K, dtype=torch.int64, device=dev)
+        row_of_slot[slots.long()] = torch.arange(T * self.K, device=dev)
         rows = y[row_of_slot].view(T, self.K, -1).float()      # each token's expert outputs
         out = (routing.weights.unsqueeze(-1) * rows).sum(1)
         return out, routing, rows

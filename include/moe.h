@@ -474,8 +474,9 @@ moe_status moe_blockscale_linear(const void *x, int64_t ldx, const void *w,
  * slots[r] / top_k of x (bf16 [T, H]) for offsets[e] <= r < offsets[e+1]:
  * quantised, through w13 [E, 2I, H] and SwiGLU (moe_blockscale_swiglu), and
  * through w2 [E, H, I]; both contiguous.  slots int32 [rows] and offsets
- * int32 [E+1] as moe_route_permute_static writes perm and offsets.  H a
- * multiple of 16 and I of 128 (else MOE_ERR_UNSUPPORTED).  workspace: device,
+ * int32 [E+1] as moe_route_permute_static writes perm and offsets (that call
+ * takes up to 4096 tokens of f32 logits and no mask; a stable sort of
+ * moe_balance_forward's ids gives the same for any).  H a multiple of 16 and I of 128 (else MOE_ERR_UNSUPPORTED).  workspace: device,
  * 16-byte aligned, moe_blockscale_experts_workspace(rows, H, I) bytes.
  * rows == 0 is a no-op.  The rest as moe_blockscale_swiglu and moe_blockscale_matmul.   */
 moe_status moe_blockscale_experts(const void *x, int64_t ldx, int T,

@@ -141,7 +141,8 @@ def blockscale_experts(x, slots, offsets, top_k, w13, w13_scales, w2, w2_scales,
                        out=None):
     """The experts' products on routed rows: row r of the result is expert
     e's MLP of x's row slots[r] // top_k, for offsets[e] <= r < offsets[e+1]
-    (slots and offsets as moe_route_permute_static writes perm and offsets).
+    (slots and offsets as moe_route_permute_static writes perm and offsets, or
+    a stable sort of router_balance's ids: examples/train_router.py).
     w13 [E, 2I, H] (gate rows, then up rows), w2 [E, H, I], contiguous -> bf16
     [len(slots), H], in permuted row order; rows of no expert are left as
     they are."""
