@@ -351,8 +351,9 @@ size_t moe_balance_workspace(int T, int E);
  * f_e = counts_e * E / (K * n), the loss whose minimum is an even load; 0
  * when no token is live.  Sums are in fp32 in a fixed order: the same inputs
  * give the same bits.  A NaN logit makes its token's weights and the loss
- * NaN.  T == 0 writes zero counts and loss.  1 <= E <= 512, K <= min(E, 16),
- * T <= 2^31 - 65536 and T * K < 2^31, else MOE_ERR_UNSUPPORTED.  Asynchronous on `stream`;
+ * NaN.  T == 0 writes zero counts and loss.  1 <= K <= E (else
+ * MOE_ERR_INVALID_ARG), E <= 512, K <= 16, T <= 2^31 - 65536 and T * K < 2^31
+ * (else MOE_ERR_UNSUPPORTED).  Asynchronous on `stream`;
  * the workspace must stay until the work is done.  Errors:
  * MOE_ERR_INVALID_ARG (sizes, a NULL or misaligned pointer: logits to their
  * element, the workspace to 16 bytes, the others to 4; workspace_bytes below
@@ -476,9 +477,10 @@ moe_status moe_blockscale_linear(const void *x, int64_t ldx, const void *w,
  * through w2 [E, H, I]; both contiguous.  slots int32 [rows] and offsets
  * int32 [E+1] as moe_route_permute_static writes perm and offsets (that call
  * takes up to 4096 tokens of f32 logits and no mask; a stable sort of
- * moe_balance_forward's ids gives the same for any).  H a multiple of 16 and I of 128 (else MOE_ERR_UNSUPPORTED).  workspace: device,
- * 16-byte aligned, moe_blockscale_experts_workspace(rows, H, I) bytes.
- * rows == 0 is a no-op.  The rest as moe_blockscale_swiglu and moe_blockscale_matmul.   */
+ * moe_balance_forward's ids gives the same for any).  H a multiple of 16 and
+ * I of 128 (else MOE_ERR_UNSUPPORTED).  workspace: device, 16-byte aligned,
+ * moe_blockscale_experts_workspace(rows, H, I) bytes.  rows == 0 is a no-op.
+ * The rest as moe_blockscale_swiglu and moe_blockscale_matmul.            */
 moe_status moe_blockscale_experts(const void *x, int64_t ldx, int T,
                                   const int32_t *slots, int top_k, int rows,
                                   const int32_t *offsets, int E,
