@@ -182,8 +182,9 @@ __device__ __forceinline__ int top_k(const float (&x)[4 * MAXI], int E, int K, i
   return 511 - static_cast<int>(mine & 511u);
 }
 
-// exp of a difference of at most 0, to about two ulp, in one multiply and the
-// hardware's power of two.
+// exp of a difference d of at most 0, in one multiply and the hardware's power
+// of two: off by its two ulp and by |d| 2^-24 of itself, the product's rounding
+// (some ten ulp at d = -20, where the value is 2e-9 of the row's largest).
 __device__ __forceinline__ float exp_diff(float d) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * kLog2e));

@@ -54,10 +54,12 @@
 // through distributed shared memory, in rank order, so the result does not
 // depend on timing.
 //
-// What bounds it: with many rows, the shared memory that feeds the MMAs
-// (8192 x 4096 x 7168: 183 us, 2620 TFLOP/s; a build without the epilogue's
-// sums took 163); with few rows per expert, the weights' bytes (64 tokens over
-// 64 experts of 44 MB: 420 us, 6.7 TB/s).
+// What bounds it: with many rows, the hand-offs between the issuers and the
+// warps that read TMEM (8192 x 4096 x 7168: 183 us, 2620 TFLOP/s; a build
+// without the epilogue's sums took 163).  Nothing is saturated: per active
+// cycle the tensor pipe is busy 57 %, shared memory 72 %, the TMEM ports 62 %
+// (4096 x 4096 x 7168).  With few rows per expert, the weights' bytes (64
+// tokens over 64 experts of 44 MB: 420 us, 6.7 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -398,8 +400,8 @@ __device__ __forceinline__ float clamp_to(float v, float limit) {
 __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
   g = clamp_to(g, clamp);
   u = clamp_to(u, clamp);
-  // e^-g by the hardware's power of two and an approximate quotient, a few ulp:
-  // as near as the sums of the product
+  // e^-g by the hardware's power of two, off by two ulp and |g| 2^-24 of itself,
+  // and an approximate quotient of two ulp: as near as the sums of the product
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
   return __fdividef(g, 1.0f + e) * u;
@@ -1190,7 +1192,8 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs p, bool
   const int grid = std::min(d.sms, items);
   // (pairs for full chunks: one expert of 8192 rows, 4096 x 7168, 183 us
   // against 192; 8 experts of 1024 rows, a whole call, 93 against 100; 64 of
-  // 256 rows, where the second chunk is often short, 195 against 174)
+  // 256 rows, where the second chunk is often short, 195 against 174; averages
+  // between 256 and 1024 and uneven experts were not measured)
   if (wide && p.M / 1024 >= p.E) {
     const int pairs = std::min(d.clusters[2], (items + 1) / 2);
     if (swiglu) return launch_bs<256, true, false, false, true>(maps, p, 2 * pairs, s);
