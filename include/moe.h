@@ -384,6 +384,81 @@ moe_status moe_balance_backward(const void *logits, int dtype, int64_t ld,
                                 const float *d_weights, void *d_logits,
                                 int64_t ld_d, void *stream);
 
+/* ---- the router's gate: scores, groups, a bias for balance ----------------------
+ * How a router scores and chooses (the settings of one gate; the same for a
+ * forward and its backward).                                              */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+typedef struct {
+    int score;         /* moe_score: s of a token's E logits                 */
+    int groups;        /* G: 1..32, a divisor of E; experts e E/G .. are one  */
+    int group_top;     /* groups a token may choose from, 1..G                */
+    int group_score;   /* moe_group_score: of a group's choices, the largest
+                          or the sum of the two largest                      */
+    int normalize;     /* 1: weights divided by their sum                     */
+    float scale;       /* factor of the weights, finite                       */
+} moe_gate_config;
+
+/* Top-K routing by scores, groups and a bias.  logits: device [T, E] of
+ * `dtype` (moe_dtype), row stride ld >= E elements; bias: device f32 [E] or
+ * NULL; mask: device uint8 [T] (0 = padding) or NULL.  A token is live when
+ * its mask is not 0 and at least one of its logits is not -inf.  The choice
+ * goes by c = s + bias, compared as 64-bit arithmetic gives it (without a bias
+ * by the logits, which order the same); ties go to the lower index, a NaN
+ * comes first, experts whose logit is -inf come last (weight 0).  The best
+ * group_top groups stay (ties to the lower group), then the K largest c
+ * within them.  Outputs, device: ids int32 [T, K] by falling c; weights f32
+ * [T, K] = scale * s, over the sum of the chosen s with `normalize` (0 where
+ * that sum is 0); -1 and 0 for tokens that are not live; counts int32 [E]
+ * (live slots per expert: what a rule that moves the bias goes by).  A NaN
+ * logit makes its weight NaN, and with a sum the token's.  T == 0 writes zero
+ * counts.  1 <= K <= group_top * E / G (else MOE_ERR_INVALID_ARG), E <= 512,
+ * K <= 16, T <= 2^31 - 65536 and T * K < 2^31 (else MOE_ERR_UNSUPPORTED).
+ * Asynchronous on `stream`, allocates nothing, no workspace; the same inputs
+ * give the same bits.  Errors: MOE_ERR_INVALID_ARG (sizes, settings, a NULL or
+ * misaligned pointer: logits to their element, the others to 4),
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.  The build's own call, as the other
+ * moe_gate_*, moe_order*, moe_join_* and moe_int8_* ones.                  */
+moe_status moe_gate_forward(const void *logits, int dtype, int64_t ld,
+                            const float *bias, const uint8_t *mask, int T,
+                            int E, int K, const moe_gate_config *cfg,
+                            int32_t *ids, float *weights, int32_t *counts,
+                            void *stream);
+
+/* Gradient of the logits (the bias has none).  ids as moe_gate_forward wrote
+ * them for the same logits and settings; d_weights: device f32 [T, K].
+ * d_logits: device [T, E] of `dtype`, row stride ld_d >= E, rounded once from
+ * fp32.  With u_k = s_k over the sum of the chosen s:
+ *   d s_k = scale / sum * (d_w_k - sum_j u_j d_w_j)  (normalize), or
+ *   d s_k = scale * d_w_k;
+ * d l_e = s_e (1 - s_e) d s_e (sigmoid) or s_e (d s_e - sum_j s_j d s_j)
+ * (softmax); zero for tokens that are not live.  T == 0 is a no-op.  Limits,
+ * alignment and errors as the forward.                                     */
+moe_status moe_gate_backward(const void *logits, int dtype, int64_t ld, int T,
+                             int E, int K, const moe_gate_config *cfg,
+                             const int32_t *ids, const float *d_weights,
+                             void *d_logits, int64_t ld_d, void *stream);
+
+/* Workspace bytes of moe_order (0 for few slots, which need none, and for
+ * sizes it refuses).                                                      */
+size_t moe_order_workspace(int n, int E);
+
+/* Expert order of n routed slots: a stable sort of the ids (device int32 [n],
+ * as moe_gate_forward or moe_balance_forward write them; one outside [0, E) is
+ * of no expert).  Outputs, device: slots int32 [n], the slots expert by expert
+ * and those of no expert last; offsets int32 [E + 1] (rows offsets[e] ..
+ * offsets[e+1] - 1 of that order are expert e's); rows int32 [n] or NULL, the
+ * place of each slot in the order (-1 for a slot of no expert).  These are the
+ * slots and offsets that moe_blockscale_experts and moe_int8_experts take, for
+ * any number of tokens.  workspace: device, 4-byte aligned,
+ * moe_order_workspace(n, E) bytes, no initialisation (may be NULL when that
+ * is 0).  n == 0 writes zero offsets.  E <= 512 (else MOE_ERR_UNSUPPORTED).
+ * Asynchronous on `stream`.  Errors: MOE_ERR_INVALID_ARG,
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.                                      */
+moe_status moe_order(const int32_t *ids, int n, int E, int32_t *slots,
+                     int32_t *offsets, int32_t *rows, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 /* ---- FP8 products with a scale per block of 128 ------------------------------
  * Activations: e4m3 codes [rows, cols] (row stride ld_codes) with one fp32
  * scale per row and 128 columns, stored block-major: scales[b * ld_scales +

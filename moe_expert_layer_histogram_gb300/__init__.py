@@ -33,6 +33,12 @@ class MoEConfig(ctypes.Structure):
                 ("test_fail_alloc_at", ctypes.c_int), ("test_stall_gemm", ctypes.c_int)]
 
 
+class MoEGateConfig(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("groups", ctypes.c_int), ("group_top", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("normalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -47,7 +53,8 @@ EXPORTS = ("moe_create", "moe_prepare_weights", "moe_forward", "moe_forward_batc
            "moe_get_status", "moe_timing_start", "moe_timing_stop", "moe_last_launch_count",
            "moe_gemm_ctas",
            "moe_route_permute_static", "moe_balance_workspace", "moe_balance_forward",
-           "moe_balance_backward", "moe_blockscale_quantize", "moe_blockscale_matmul",
+           "moe_balance_backward", "moe_gate_forward", "moe_gate_backward",
+           "moe_order_workspace", "moe_order", "moe_blockscale_quantize", "moe_blockscale_matmul",
            "moe_blockscale_swiglu", "moe_blockscale_linear_workspace",
            "moe_blockscale_experts_workspace", "moe_blockscale_linear",
            "moe_blockscale_experts", "moe_blockscale_status", "moe_measure_mma_rate", "moe_status_string",
@@ -87,6 +94,11 @@ def lib():
                                       ctypes.c_size_t, vp]
     L.moe_balance_backward.argtypes = [vp, ci, i64, ci, ci, ci, cf, vp, vp, vp, vp, vp, vp, i64,
                                        vp]
+    gate = ctypes.POINTER(MoEGateConfig)
+    L.moe_gate_forward.argtypes = [vp, ci, i64, vp, vp, ci, ci, ci, gate, vp, vp, vp, vp]
+    L.moe_gate_backward.argtypes = [vp, ci, i64, ci, ci, ci, gate, vp, vp, vp, i64, vp]
+    L.moe_order_workspace.argtypes = [ci, ci]
+    L.moe_order.argtypes = [vp, ci, ci, vp, vp, vp, vp, ctypes.c_size_t, vp]
     L.moe_blockscale_quantize.argtypes = [vp, i64, ci, vp, ci, ci, ci, vp, i64, vp, i64, vp]
     L.moe_blockscale_matmul.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp,
                                         i64, vp]
@@ -107,8 +119,8 @@ def lib():
     for name in EXPORTS:
         if name not in ("moe_status_string", "moe_destroy"):
             getattr(L, name).restype = ci
-    for name in ("moe_balance_workspace", "moe_blockscale_linear_workspace",
-                 "moe_blockscale_experts_workspace"):
+    for name in ("moe_balance_workspace", "moe_order_workspace",
+                 "moe_blockscale_linear_workspace", "moe_blockscale_experts_workspace"):
         getattr(L, name).restype = ctypes.c_size_t
     _lib = L
     return L
@@ -253,6 +265,33 @@ def moe_balance_backward(logits, dtype, ld, T, E, K, coef, ids, weights, counts,
     _check(lib().moe_balance_backward(_ptr(logits), dtype, ld, T, E, K, coef, _ptr(ids),
                                       _ptr(weights), _ptr(counts), _ptr(d_loss), _ptr(d_weights),
                                       _ptr(d_logits), ld_d, stream), "moe_balance_backward")
+
+
+MOE_SCORE = {"softmax": 0, "sigmoid": 1}
+MOE_GROUP = {"max": 0, "top2": 1}
+
+
+def moe_gate_forward(logits, dtype, ld, bias, mask, T, E, K, config, ids, weights, counts,
+                     stream=None):
+    _check(lib().moe_gate_forward(_ptr(logits), dtype, ld, _ptr(bias), _ptr(mask), T, E, K, config,
+                                  _ptr(ids), _ptr(weights), _ptr(counts), stream),
+           "moe_gate_forward")
+
+
+def moe_gate_backward(logits, dtype, ld, T, E, K, config, ids, d_weights, d_logits, ld_d,
+                      stream=None):
+    _check(lib().moe_gate_backward(_ptr(logits), dtype, ld, T, E, K, config, _ptr(ids),
+                                   _ptr(d_weights), _ptr(d_logits), ld_d, stream),
+           "moe_gate_backward")
+
+
+def moe_order_workspace(n, E):
+    return lib().moe_order_workspace(n, E)
+
+
+def moe_order(ids, n, E, slots, offsets, rows, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_order(_ptr(ids), n, E, _ptr(slots), _ptr(offsets), _ptr(rows),
+                           _ptr(workspace), workspace_bytes, stream), "moe_order")
 
 
 def moe_blockscale_quantize(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,
@@ -414,7 +453,9 @@ class MoELayer:
 
 # ---- operators on torch tensors (loaded, with torch, when first asked for) ------
 _OPERATORS = {"RouterBalance": "balance", "router_balance": "balance",
-              "router_balance_backward": "balance", "blockscale_quantize": "blockscale",
+              "router_balance_backward": "balance", "RouterGate": "gate", "RouterOrder": "gate",
+              "router_gate": "gate", "router_gate_backward": "gate", "router_order": "gate",
+              "blockscale_quantize": "blockscale",
               "blockscale_matmul": "blockscale", "blockscale_linear": "blockscale",
               "blockscale_linear_dx": "blockscale", "blockscale_experts": "blockscale"}
 
