@@ -459,6 +459,80 @@ moe_status moe_order(const int32_t *ids, int n, int E, int32_t *slots,
                      int32_t *offsets, int32_t *rows, void *workspace,
                      size_t workspace_bytes, void *stream);
 
+/* ---- the end of a block: sum, norms, gate, residual -----------------------------
+ * What a join takes, device pointers; a member that does not apply is NULL.
+ *   y  = sum_k weights_k expert_rows[row_of_slot_k] + sigmoid(gate) * shared
+ *   x' = x + scale * N(y; post_weight)   (without post_weight: + scale * y)
+ *   h  = N(x'; norm_weight),  N(v; w) = w * v / sqrt(mean(v^2) + eps)
+ * x' is stored in x's type and h is the norm of what was stored.  A row_of_slot
+ * outside [0, rows) is no term of its sum (whatever its weight).  With K = 0 and
+ * shared alone this is the end of a dense block (shared: its output); with
+ * neither there is nothing to join and h is the norm of x.                 */
+typedef struct {
+    int T, H, K;               /* tokens, width (1..16384), slots per token
+                                  (0..16)                                   */
+    int x_type;                /* moe_dtype of x, x' and their gradients      */
+    int weight_type;           /* moe_dtype of the norms' weights             */
+    int gate_type;             /* moe_dtype of the gate's logits              */
+    float scale;               /* of the block's output, finite               */
+    float eps;                 /* >= 0                                        */
+    const void *x;             /* [T, H], the residual stream                 */
+    int64_t ld_x;              /* (row strides in elements, >= H)             */
+    const void *expert_rows;   /* bf16 [rows, H], K > 0                       */
+    int64_t ld_rows;
+    int rows;
+    const int32_t *row_of_slot; /* [T, K], as moe_order writes rows           */
+    const float *weights;      /* [T, K]                                      */
+    const void *shared;        /* bf16 [T, H] or NULL                         */
+    int64_t ld_shared;
+    const void *gate;          /* [T] logits of shared's gate, or NULL (1)    */
+    const void *post_weight;   /* [H] or NULL                                 */
+    const void *norm_weight;   /* [H] or NULL (no h)                          */
+} moe_join;
+
+/* x_out: [T, H] of x_type (may be x itself; NULL where nothing is joined);
+ * h: bf16 [T, H] or NULL; codes: int8 [T, H] or NULL, h in 8 bits, with
+ * code_scales f32 [T], as moe_int8_quantize would code the unrounded h;
+ * post_rstd, norm_rstd: f32 [T] or NULL, 1 / sqrt(mean + eps) of the two norms,
+ * which the backward takes.  With norm_weight h or codes (or both) have to be
+ * given, without it neither.  One kernel, asynchronous on `stream`, allocates
+ * nothing; the same inputs give the same bits.  T == 0 is a no-op.  Any
+ * alignment of whole elements; rows on 16 bytes are faster.  Errors:
+ * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (K > 16, H > 16384),
+ * MOE_ERR_CUDA.                                                            */
+moe_status moe_join_forward(const moe_join *join, void *x_out, int64_t ld_out,
+                            void *h, int64_t ld_h, void *codes,
+                            int64_t ld_codes, float *code_scales,
+                            float *post_rstd, float *norm_rstd, void *stream);
+
+/* Workspace bytes of moe_join_backward (0 for sizes out of range); wanted only
+ * with d_post or d_norm.                                                   */
+size_t moe_join_workspace(int T, int H);
+
+/* Gradients of a join (its members as in the forward; x is not read) from
+ * d_x_out [T, H] of x_type, the gradient of x' (NULL: zero), and d_h bf16 [T, H]
+ * (NULL: zero; else x_out and norm_rstd of the forward are wanted; post_rstd with
+ * post_weight).  Outputs, each NULL if it is not wanted: d_x [T, H] of x_type
+ * (may be d_x_out); d_rows bf16 [rows, H], the rows that a slot names (a row is
+ * named by one slot at most, as moe_order's are), and zeros from row *live_rows
+ * on if live_rows (device int32, moe_order's offsets + E) is given; other rows
+ * are left as they are; d_weights f32 [T, K] (0 for a slot without a row);
+ * d_shared bf16 [T, H]; d_gate [T] of gate_type; d_post, d_norm [H] of
+ * weight_type (d_norm: with d_h), sums over the tokens in fp32 in a fixed order,
+ * rounded once; zeros for T == 0.  workspace: device, 16-byte aligned,
+ * moe_join_workspace(T, H) bytes, no initialisation.  Asynchronous on `stream`;
+ * the same inputs give the same bits.  Errors as the forward.              */
+moe_status moe_join_backward(const moe_join *join, const void *x_out,
+                             int64_t ld_out, const float *post_rstd,
+                             const float *norm_rstd, const void *d_x_out,
+                             int64_t ld_dxo, const void *d_h, int64_t ld_dh,
+                             void *d_x, int64_t ld_dx, void *d_rows,
+                             int64_t ld_drows, const int32_t *live_rows,
+                             float *d_weights, void *d_shared,
+                             int64_t ld_dshared, void *d_gate, void *d_post,
+                             void *d_norm, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* ---- FP8 products with a scale per block of 128 ------------------------------
  * Activations: e4m3 codes [rows, cols] (row stride ld_codes) with one fp32
  * scale per row and 128 columns, stored block-major: scales[b * ld_scales +

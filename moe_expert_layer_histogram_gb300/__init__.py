@@ -39,6 +39,18 @@ class MoEGateConfig(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class MoEJoin(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int), ("K", ctypes.c_int),
+                ("x_type", ctypes.c_int), ("weight_type", ctypes.c_int),
+                ("gate_type", ctypes.c_int), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+                ("expert_rows", ctypes.c_void_p), ("ld_rows", ctypes.c_int64),
+                ("rows", ctypes.c_int), ("row_of_slot", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("shared", ctypes.c_void_p),
+                ("ld_shared", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("post_weight", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -54,7 +66,8 @@ EXPORTS = ("moe_create", "moe_prepare_weights", "moe_forward", "moe_forward_batc
            "moe_gemm_ctas",
            "moe_route_permute_static", "moe_balance_workspace", "moe_balance_forward",
            "moe_balance_backward", "moe_gate_forward", "moe_gate_backward",
-           "moe_order_workspace", "moe_order", "moe_blockscale_quantize", "moe_blockscale_matmul",
+           "moe_order_workspace", "moe_order", "moe_join_forward", "moe_join_workspace",
+           "moe_join_backward", "moe_blockscale_quantize", "moe_blockscale_matmul",
            "moe_blockscale_swiglu", "moe_blockscale_linear_workspace",
            "moe_blockscale_experts_workspace", "moe_blockscale_linear",
            "moe_blockscale_experts", "moe_blockscale_status", "moe_measure_mma_rate", "moe_status_string",
@@ -99,6 +112,11 @@ def lib():
     L.moe_gate_backward.argtypes = [vp, ci, i64, ci, ci, ci, gate, vp, vp, vp, i64, vp]
     L.moe_order_workspace.argtypes = [ci, ci]
     L.moe_order.argtypes = [vp, ci, ci, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    join = ctypes.POINTER(MoEJoin)
+    L.moe_join_forward.argtypes = [join, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+    L.moe_join_workspace.argtypes = [ci, ci]
+    L.moe_join_backward.argtypes = [join, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                    vp, vp, i64, vp, vp, vp, vp, ctypes.c_size_t, vp]
     L.moe_blockscale_quantize.argtypes = [vp, i64, ci, vp, ci, ci, ci, vp, i64, vp, i64, vp]
     L.moe_blockscale_matmul.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp,
                                         i64, vp]
@@ -119,7 +137,7 @@ def lib():
     for name in EXPORTS:
         if name not in ("moe_status_string", "moe_destroy"):
             getattr(L, name).restype = ci
-    for name in ("moe_balance_workspace", "moe_order_workspace",
+    for name in ("moe_balance_workspace", "moe_order_workspace", "moe_join_workspace",
                  "moe_blockscale_linear_workspace", "moe_blockscale_experts_workspace"):
         getattr(L, name).restype = ctypes.c_size_t
     _lib = L
@@ -294,6 +312,27 @@ def moe_order(ids, n, E, slots, offsets, rows, workspace, workspace_bytes, strea
                            _ptr(workspace), workspace_bytes, stream), "moe_order")
 
 
+def moe_join_forward(join, x_out, ld_out, h, ld_h, codes, ld_codes, code_scales, post_rstd,
+                     norm_rstd, stream=None):
+    _check(lib().moe_join_forward(join, _ptr(x_out), ld_out, _ptr(h), ld_h, _ptr(codes), ld_codes,
+                                  _ptr(code_scales), _ptr(post_rstd), _ptr(norm_rstd), stream),
+           "moe_join_forward")
+
+
+def moe_join_workspace(T, H):
+    return lib().moe_join_workspace(T, H)
+
+
+def moe_join_backward(join, x_out, ld_out, post_rstd, norm_rstd, d_x_out, ld_dxo, d_h, ld_dh, d_x,
+                      ld_dx, d_rows, ld_drows, live_rows, d_weights, d_shared, ld_dshared, d_gate,
+                      d_post, d_norm, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_join_backward(
+        join, _ptr(x_out), ld_out, _ptr(post_rstd), _ptr(norm_rstd), _ptr(d_x_out), ld_dxo,
+        _ptr(d_h), ld_dh, _ptr(d_x), ld_dx, _ptr(d_rows), ld_drows, _ptr(live_rows),
+        _ptr(d_weights), _ptr(d_shared), ld_dshared, _ptr(d_gate), _ptr(d_post), _ptr(d_norm),
+        _ptr(workspace), workspace_bytes, stream), "moe_join_backward")
+
+
 def moe_blockscale_quantize(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,
                             ld_scales, stream=None):
     _check(lib().moe_blockscale_quantize(_ptr(x), ldx, x_rows, _ptr(slots), top_k, rows, cols,
@@ -455,6 +494,8 @@ class MoELayer:
 _OPERATORS = {"RouterBalance": "balance", "router_balance": "balance",
               "router_balance_backward": "balance", "RouterGate": "gate", "RouterOrder": "gate",
               "router_gate": "gate", "router_gate_backward": "gate", "router_order": "gate",
+              "BlockJoin": "join", "JoinGradients": "join", "block_join": "join",
+              "block_join_backward": "join",
               "blockscale_quantize": "blockscale",
               "blockscale_matmul": "blockscale", "blockscale_linear": "blockscale",
               "blockscale_linear_dx": "blockscale", "blockscale_experts": "blockscale"}

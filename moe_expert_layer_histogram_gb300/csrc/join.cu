@@ -1,0 +1,765 @@
+// join.cu -- the end of a block: its parts added up, a norm after the block, the
+// scaled sum with the residual stream, and the norm before the next block.
+//
+//   y  = sum_k w_k z[row_k] + sigmoid(a) u      (routed rows, shared expert)
+//   x' = x + scale N(y; post)                   (N left out without `post`)
+//   h  = N(x'; norm),   N(v; w) = w v r,  r = 1 / sqrt(mean(v^2) + eps)
+//
+// with h in bf16 or, for the next 8-bit product, as codes with one scale per
+// token.  x' is stored in x's type and h is the norm of what was stored, so the
+// backward pass, which reads x' again, differentiates the same function:
+//
+//   g  = d x' + r2 (v - xh mean(v xh)),   v = norm d h,  xh = x' r2
+//   d x = g;  d n = scale g
+//   d y = r1 (v - yh mean(v yh)),         v = post d n,  yh = y r1
+//   d z[row_k] = w_k d y;  d w_k = <d y, z[row_k]>
+//   d u = sigmoid(a) d y;  d a = <d y, u> s (1 - s)
+//   d norm = sum_t d h xh;  d post = sum_t d n yh
+//
+// Both passes are bound by the rows' bytes.  A block of threads takes a token and
+// keeps the whole row of every sum in registers, so each input is read once (the
+// backward pass with `post` reads z twice, the second time from L2: y has to be
+// complete before d y is known).  The weights' gradients are sums over tokens:
+// each block keeps its columns' sums in registers over its tokens and writes one
+// row of partials, which a second kernel adds in block order; the same inputs
+// give the same bits.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "moe.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr unsigned kAllLanes = 0xFFFFFFFFu;
+constexpr int kSms = 152;
+constexpr int kMaxWidth = 16384;  // H: 512 threads of 4 vectors
+constexpr int kVec = 8;           // columns of a vector
+
+struct JoinArgs {
+  moe_join j;
+  // forward
+  void* x_out;
+  int64_t ld_out;
+  __nv_bfloat16* h;
+  int64_t ld_h;
+  int8_t* codes;
+  int64_t ld_codes;
+  float *code_scales, *post_rstd, *norm_rstd;
+};
+
+struct JoinBackArgs {
+  moe_join j;
+  const void *x_out, *d_x_out, *d_h;
+  int64_t ld_out, ld_dxo, ld_dh;
+  const float *post_rstd, *norm_rstd;
+  void* d_x;
+  int64_t ld_dx;
+  __nv_bfloat16* d_rows;
+  int64_t ld_drows;
+  const int32_t* live_rows;
+  float* d_weights;
+  __nv_bfloat16* d_shared;
+  int64_t ld_dshared;
+  void* d_gate;
+  float *part_post, *part_norm;  // [blocks, H] each, or null
+};
+
+// The columns of a thread's vector i, element c: vectors of eight neighbours, or
+// (rows that do not start on 16 bytes) single columns a block apart, so that
+// either way a warp's accesses are neighbours.
+template <bool VEC>
+__device__ __forceinline__ int column(int i, int c) {
+  const int n = blockDim.x, t = threadIdx.x;
+  return VEC ? (i * n + t) * kVec + c : (i * kVec + c) * n + t;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16* row, int i, int H, float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c0 = column<VEC>(i, 0);
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (c0 < H) q = *reinterpret_cast<const uint4*>(row + c0);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[2 * c] = __uint_as_float(w[c] << 16);
+      v[2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) {
+      const int col = column<VEC>(i, c);
+      v[c] = col < H ? __bfloat162float(row[col]) : 0.0f;
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const float* row, int i, int H, float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c0 = column<VEC>(i, 0);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (c0 < H) {
+      a = *reinterpret_cast<const float4*>(row + c0);
+      b = *reinterpret_cast<const float4*>(row + c0 + 4);
+    }
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) {
+      const int col = column<VEC>(i, c);
+      v[c] = col < H ? row[col] : 0.0f;
+    }
+  }
+}
+// A norm's weights, of either type.
+template <bool VEC>
+__device__ __forceinline__ void load_weights(const void* w, int type, int i, int H,
+                                             float (&v)[kVec]) {
+  if (type == MOE_DTYPE_F32)
+    load8<VEC>(static_cast<const float*>(w), i, H, v);
+  else
+    load8<VEC>(static_cast<const __nv_bfloat16*>(w), i, H, v);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(p);
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int i, int H, const float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c0 = column<VEC>(i, 0);
+    if (c0 < H)
+      *reinterpret_cast<uint4*>(row + c0) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
+                                                       pack2(v[4], v[5]), pack2(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) {
+      const int col = column<VEC>(i, c);
+      if (col < H) row[col] = __float2bfloat16_rn(v[c]);
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float* row, int i, int H, const float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c0 = column<VEC>(i, 0);
+    if (c0 < H) {
+      *reinterpret_cast<float4*>(row + c0) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(row + c0 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) {
+      const int col = column<VEC>(i, c);
+      if (col < H) row[col] = v[c];
+    }
+  }
+}
+
+// What v becomes when it is stored.
+__device__ __forceinline__ float stored(float v, const float*) { return v; }
+__device__ __forceinline__ float stored(float v, const __nv_bfloat16*) {
+  return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kAllLanes, v, off);
+  return v;
+}
+
+// Sum over the block, the same in every thread; `s`: 32 words that no other sum
+// uses between two syncs.
+__device__ __forceinline__ float block_sum(float v, float* s) {
+  v = warp_sum(v);
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < warps ? s[lane] : 0.0f);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
+  v = __reduce_max_sync(kAllLanes, v);
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return __reduce_max_sync(kAllLanes, lane < warps ? s[lane] : 0u);
+}
+
+__device__ __forceinline__ float sigmoid(float a) {
+  return expf(fminf(a, 0.0f)) / (1.0f + expf(-fabsf(a)));
+}
+__device__ __forceinline__ float gate_of(const moe_join& j, int64_t t) {
+  if (!j.gate) return 1.0f;
+  return sigmoid(j.gate_type == MOE_DTYPE_F32
+                     ? static_cast<const float*>(j.gate)[t]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(j.gate)[t]));
+}
+
+// The block's sum y of token t: routed rows (kAtOnce of them on their way
+// together) and the shared expert.
+constexpr int kAtOnce = 4;
+
+template <int NV, bool VEC>
+__device__ __forceinline__ void gather(const moe_join& j, int64_t t, float sg,
+                                       float (&y)[NV][kVec]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) y[i][c] = 0.0f;
+  const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(j.expert_rows);
+  for (int k0 = 0; k0 < j.K; k0 += kAtOnce) {
+    int row[kAtOnce];
+    float w[kAtOnce];
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q) {
+      row[q] = k0 + q < j.K ? j.row_of_slot[t * j.K + k0 + q] : -1;
+      w[q] = k0 + q < j.K ? j.weights[t * j.K + k0 + q] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[kAtOnce][kVec];
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        const bool in = row[q] >= 0 && row[q] < j.rows;
+        load8<VEC>(z + (in ? row[q] : 0) * j.ld_rows, i, in ? j.H : 0, v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        // (a row of no expert is no term: not 0 times whatever its weight is)
+        const float wq = row[q] >= 0 && row[q] < j.rows ? w[q] : 0.0f;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) y[i][c] = fmaf(wq, v[q][c], y[i][c]);
+      }
+    }
+  }
+  if (j.shared) {
+    const __nv_bfloat16* u = static_cast<const __nv_bfloat16*>(j.shared) + t * j.ld_shared;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[kVec];
+      load8<VEC>(u, i, j.H, v);
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) y[i][c] = fmaf(sg, v[c], y[i][c]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- forward
+template <typename X, int NV, bool VEC>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
+    join_forward_kernel(const __grid_constant__ JoinArgs p) {
+  __shared__ float s_post[32], s_norm[32];
+  __shared__ uint32_t s_max[32];
+  const moe_join& j = p.j;
+  const int64_t t = blockIdx.x;
+  const int H = j.H;
+  const X* x = static_cast<const X*>(j.x) + t * j.ld_x;
+  float v[NV][kVec];  // y, then x'
+  if (j.K || j.shared) {
+    gather<NV, VEC>(j, t, j.shared ? gate_of(j, t) : 1.0f, v);
+    float r = 1.0f;
+    if (j.post_weight) {
+      float sq = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) sq = fmaf(v[i][c], v[i][c], sq);
+      r = 1.0f / sqrtf(block_sum(sq, s_post) / H + j.eps);
+      if (p.post_rstd && threadIdx.x == 0) p.post_rstd[t] = r;
+    }
+    X* out = static_cast<X*>(p.x_out) + t * p.ld_out;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float a[kVec];
+      if (j.post_weight) {
+        load_weights<VEC>(j.post_weight, j.weight_type, i, H, a);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) v[i][c] *= r * a[c];
+      }
+      load8<VEC>(x, i, H, a);
+#pragma unroll
+      for (int c = 0; c < kVec; ++c)
+        v[i][c] = stored(fmaf(j.scale, v[i][c], a[c]), static_cast<X*>(nullptr));
+      store8<VEC>(out, i, H, v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load8<VEC>(x, i, H, v[i]);
+    if (p.x_out) {
+      X* out = static_cast<X*>(p.x_out) + t * p.ld_out;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) store8<VEC>(out, i, H, v[i]);
+    }
+  }
+  if (!j.norm_weight) return;
+  float sq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) sq = fmaf(v[i][c], v[i][c], sq);
+  const float r = 1.0f / sqrtf(block_sum(sq, s_norm) / H + j.eps);
+  if (p.norm_rstd && threadIdx.x == 0) p.norm_rstd[t] = r;
+  uint32_t amax = 0u;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float w[kVec];
+    load_weights<VEC>(j.norm_weight, j.weight_type, i, H, w);
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) {
+      v[i][c] *= r * w[c];
+      amax = max(amax, __float_as_uint(v[i][c]) & 0x7FFFFFFFu);
+    }
+    if (p.h) store8<VEC>(p.h + t * p.ld_h, i, H, v[i]);
+  }
+  if (!p.codes) return;
+  // s = amax / 127 (NaN where an infinity or NaN is in the row: the bits of both
+  // are above those of every number); codes round(h / s)
+  amax = block_max(amax, s_max);
+  const float s = amax >= 0x7F800000u ? NAN : __uint_as_float(amax) / 127.0f;
+  if (threadIdx.x == 0) p.code_scales[t] = s;
+  int8_t* codes = p.codes + t * p.ld_codes;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    int q[kVec];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c)
+      q[c] = s > 0.0f ? __float2int_rn(fminf(fmaxf(v[i][c] / s, -127.0f), 127.0f)) : 0;
+    if constexpr (VEC) {
+      const int c0 = column<VEC>(i, 0);
+      uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        lo |= static_cast<uint32_t>(q[c] & 255) << (8 * c);
+        hi |= static_cast<uint32_t>(q[c + 4] & 255) << (8 * c);
+      }
+      if (c0 < H) *reinterpret_cast<uint2*>(codes + c0) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kVec; ++c)
+        if (column<VEC>(i, c) < H) codes[column<VEC>(i, c)] = static_cast<int8_t>(q[c]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+template <typename X, int NV, bool VEC>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
+    join_backward_kernel(const __grid_constant__ JoinBackArgs p) {
+  // by token parity: a warp may write the next token's while another still reads
+  __shared__ float s_norm[2][32], s_post[2][32], s_dot[2][kMaxTopK + 1][32];
+  const moe_join& j = p.j;
+  const int H = j.H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = blockDim.x >> 5;
+  const bool block = j.K || j.shared;
+  float acc_norm[NV][kVec], acc_post[NV][kVec];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) acc_norm[i][c] = acc_post[i][c] = 0.0f;
+  int parity = 0;
+  for (int64_t t = blockIdx.x; t < j.T; t += gridDim.x, parity ^= 1) {
+    // g = d x'
+    float g[NV][kVec];
+    if (p.d_h) {
+      const X* xo = static_cast<const X*>(p.x_out) + t * p.ld_out;
+      const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(p.d_h) + t * p.ld_dh;
+      const float r = p.norm_rstd[t];
+      float xh[NV][kVec], dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float w[kVec];
+        load8<VEC>(xo, i, H, xh[i]);
+        load8<VEC>(dh, i, H, g[i]);
+        load_weights<VEC>(j.norm_weight, j.weight_type, i, H, w);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+          xh[i][c] *= r;
+          acc_norm[i][c] = fmaf(g[i][c], xh[i][c], acc_norm[i][c]);
+          g[i][c] *= w[c];
+          dot = fmaf(g[i][c], xh[i][c], dot);
+        }
+      }
+      const float mean = block_sum(dot, s_norm[parity]) / H;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[i][c] = r * fmaf(-mean, xh[i][c], g[i][c]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[i][c] = 0.0f;
+    }
+    if (p.d_x_out) {
+      const X* dxo = static_cast<const X*>(p.d_x_out) + t * p.ld_dxo;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float a[kVec];
+        load8<VEC>(dxo, i, H, a);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[i][c] += a[c];
+      }
+    }
+    if (p.d_x) {
+      X* dx = static_cast<X*>(p.d_x) + t * p.ld_dx;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) store8<VEC>(dx, i, H, g[i]);
+    }
+    if (!block) continue;
+    const float sg = j.shared ? gate_of(j, t) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) g[i][c] *= j.scale;
+    if (j.post_weight) {
+      float y[NV][kVec], dot = 0.0f;
+      gather<NV, VEC>(j, t, sg, y);
+      const float r = p.post_rstd[t];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float w[kVec];
+        load_weights<VEC>(j.post_weight, j.weight_type, i, H, w);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+          y[i][c] *= r;
+          acc_post[i][c] = fmaf(g[i][c], y[i][c], acc_post[i][c]);
+          g[i][c] *= w[c];
+          dot = fmaf(g[i][c], y[i][c], dot);
+        }
+      }
+      const float mean = block_sum(dot, s_post[parity]) / H;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[i][c] = r * fmaf(-mean, y[i][c], g[i][c]);
+    }
+    // d z, d u and their dot products with d y
+    float(*dots)[32] = s_dot[parity];
+    const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(j.expert_rows);
+    for (int k = 0; k < j.K; ++k) {
+      const int row = j.row_of_slot[t * j.K + k];
+      const bool in = row >= 0 && row < j.rows;
+      const float w = in ? j.weights[t * j.K + k] : 0.0f;
+      float dot = 0.0f;
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float a[kVec];
+          if (p.d_weights) {
+            load8<VEC>(z + row * j.ld_rows, i, H, a);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) dot = fmaf(g[i][c], a[c], dot);
+          }
+          if (p.d_rows) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) a[c] = w * g[i][c];
+            store8<VEC>(p.d_rows + row * p.ld_drows, i, H, a);
+          }
+        }
+      }
+      if (p.d_weights) {
+        dot = warp_sum(dot);
+        if (lane == 0) dots[k][warp] = dot;
+      }
+    }
+    if (j.shared && (p.d_shared || p.d_gate)) {
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float a[kVec];
+        if (p.d_gate) {
+          load8<VEC>(static_cast<const __nv_bfloat16*>(j.shared) + t * j.ld_shared, i, H, a);
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) dot = fmaf(g[i][c], a[c], dot);
+        }
+        if (p.d_shared) {
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) a[c] = sg * g[i][c];
+          store8<VEC>(p.d_shared + t * p.ld_dshared, i, H, a);
+        }
+      }
+      if (p.d_gate) {
+        dot = warp_sum(dot);
+        if (lane == 0) dots[kMaxTopK][warp] = dot;
+      }
+    }
+    if (p.d_weights || p.d_gate) {
+      __syncthreads();
+      if (p.d_weights)
+        for (int k = warp; k < j.K; k += warps) {
+          const float dot = warp_sum(lane < warps ? dots[k][lane] : 0.0f);
+          if (lane == 0) p.d_weights[t * j.K + k] = dot;
+        }
+      if (p.d_gate && warp == warps - 1) {
+        const float d = warp_sum(lane < warps ? dots[kMaxTopK][lane] : 0.0f) * sg * (1.0f - sg);
+        if (lane == 0) {
+          if (j.gate_type == MOE_DTYPE_F32)
+            static_cast<float*>(p.d_gate)[t] = d;
+          else
+            static_cast<__nv_bfloat16*>(p.d_gate)[t] = __float2bfloat16_rn(d);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (p.part_norm)
+      store8<VEC>(p.part_norm + static_cast<int64_t>(blockIdx.x) * H, i, H, acc_norm[i]);
+    if (p.part_post)
+      store8<VEC>(p.part_post + static_cast<int64_t>(blockIdx.x) * H, i, H, acc_post[i]);
+  }
+  // rows of no expert
+  if (p.d_rows && p.live_rows) {
+    float zero[kVec];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) zero[c] = 0.0f;
+    for (int64_t r = max(*p.live_rows, 0) + static_cast<int64_t>(blockIdx.x); r < j.rows;
+         r += gridDim.x)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) store8<VEC>(p.d_rows + r * p.ld_drows, i, H, zero);
+  }
+}
+
+// Column sums of the partials, in block order within each of kFinishRows runs of
+// rows, then run by run.  blockIdx.y: 0 norm, 1 post.
+constexpr int kFinishRows = 16;
+
+struct JoinFinishArgs {
+  const float* part[2];
+  void* out[2];
+  int blocks, H, type;
+};
+
+__global__ void __launch_bounds__(32 * kFinishRows)
+    join_finish_kernel(const __grid_constant__ JoinFinishArgs p) {
+  __shared__ float s[kFinishRows][33];
+  pdl_wait();
+  const float* part = p.part[blockIdx.y];
+  if (!part) return;
+  const int col = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
+  float sum = 0.0f;
+  if (col < p.H)
+#pragma unroll 8
+    for (int b = y; b < p.blocks; b += kFinishRows) sum += part[static_cast<int64_t>(b) * p.H + col];
+  s[y][threadIdx.x] = sum;
+  __syncthreads();
+  if (y != 0 || col >= p.H) return;
+#pragma unroll
+  for (int q = 1; q < kFinishRows; ++q) sum += s[q][threadIdx.x];
+  if (p.type == MOE_DTYPE_F32)
+    static_cast<float*>(p.out[blockIdx.y])[col] = sum;
+  else
+    static_cast<__nv_bfloat16*>(p.out[blockIdx.y])[col] = __float2bfloat16_rn(sum);
+}
+
+// ---------------------------------------------------------------- host
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t size_of(int type) { return type == MOE_DTYPE_F32 ? 4 : 2; }
+bool is_type(int t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE_BF16; }
+
+// Whether rows can be read in vectors.
+bool in_vectors(const void* p, int64_t ld, size_t size) {
+  return !p || (aligned_to(p, 16) && (ld * static_cast<int64_t>(size)) % 16 == 0);
+}
+
+moe_status check_join(const moe_join* j, bool with_x) {
+  if (!j || j->T < 0 || j->H < 1 || j->K < 0 || j->rows < 0) return MOE_ERR_INVALID_ARG;
+  if (!is_type(j->x_type) || !is_type(j->weight_type) || !is_type(j->gate_type))
+    return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(j->scale) || !(j->eps >= 0.0f) || !std::isfinite(j->eps))
+    return MOE_ERR_INVALID_ARG;
+  if (j->K > kMaxTopK || j->H > kMaxWidth) return MOE_ERR_UNSUPPORTED;
+  if ((j->gate && !j->shared) || (j->post_weight && !j->K && !j->shared))
+    return MOE_ERR_INVALID_ARG;
+  if (j->T == 0) return MOE_OK;
+  const size_t xs = size_of(j->x_type);
+  if (with_x && (!j->x || !aligned_to(j->x, xs) || j->ld_x < j->H)) return MOE_ERR_INVALID_ARG;
+  if (j->K && (!j->row_of_slot || !j->weights || !aligned_to(j->row_of_slot, 4) ||
+               !aligned_to(j->weights, 4) || (j->rows > 0 && !j->expert_rows) ||
+               !aligned_to(j->expert_rows, 2) || j->ld_rows < j->H))
+    return MOE_ERR_INVALID_ARG;
+  if (j->shared && (!aligned_to(j->shared, 2) || j->ld_shared < j->H)) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(j->gate, size_of(j->gate_type)) ||
+      !aligned_to(j->post_weight, size_of(j->weight_type)) ||
+      !aligned_to(j->norm_weight, size_of(j->weight_type)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+bool join_vectors(const moe_join& j) {
+  const size_t xs = size_of(j.x_type);
+  return j.H % kVec == 0 && in_vectors(j.x, j.ld_x, xs) && in_vectors(j.expert_rows, j.ld_rows, 2) &&
+         in_vectors(j.shared, j.ld_shared, 2) && in_vectors(j.post_weight, 0, 1) &&
+         in_vectors(j.norm_weight, 0, 1);
+}
+
+// Vectors per thread: as few as 512 threads allow, or (wide) 1024 of one.
+struct Shape {
+  int nv, threads;
+};
+Shape shape_of(int H, bool wide) {
+  const int vectors = (H + kVec - 1) / kVec;
+  int nv = 1;
+  while ((vectors + nv - 1) / nv > (wide && nv == 1 ? 1024 : 512)) nv *= 2;
+  return {nv, ((vectors + nv - 1) / nv + 31) / 32 * 32};
+}
+
+template <typename X, bool VEC>
+cudaError_t run_forward(const JoinArgs& p, cudaStream_t s) {
+  const int T = p.j.T;
+  // Few tokens: as many threads as a block has, each with little to wait for.
+  // Many: blocks that fit twice into an SM, so that one's sums hide behind the
+  // other's loads.
+  const bool few = T <= kSms;
+  const Shape q = shape_of(p.j.H, few);
+  auto go = [&](auto k) { return launch_pdl(false, k, dim3(T), dim3(q.threads), 0, s, p); };
+  if (q.nv == 1) return go(join_forward_kernel<X, 1, VEC>);
+  if (q.nv == 2) return go(join_forward_kernel<X, 2, VEC>);
+  return go(join_forward_kernel<X, 4, VEC>);
+}
+
+constexpr int kBackBlocks = 2 * kSms;
+int back_blocks(int T) { return std::max(1, std::min(T, kBackBlocks)); }
+
+template <typename X, bool VEC>
+cudaError_t run_backward(const JoinBackArgs& p, cudaStream_t s) {
+  const Shape q = shape_of(p.j.H, false);
+  auto go = [&](auto k) {
+    return launch_pdl(false, k, dim3(back_blocks(p.j.T)), dim3(q.threads), 0, s, p);
+  };
+  if (q.nv == 1) return go(join_backward_kernel<X, 1, VEC>);
+  if (q.nv == 2) return go(join_backward_kernel<X, 2, VEC>);
+  return go(join_backward_kernel<X, 4, VEC>);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_join_forward(const moe_join* j, void* x_out, int64_t ld_out, void* h, int64_t ld_h,
+                            void* codes, int64_t ld_codes, float* code_scales, float* post_rstd,
+                            float* norm_rstd, void* stream) {
+  const moe_status st = check_join(j, true);
+  if (st != MOE_OK) return st;
+  if (j->T == 0) return MOE_OK;
+  const bool normed = h || codes;
+  if (normed != (j->norm_weight != nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((x_out && ld_out < j->H) || (h && ld_h < j->H) || (codes && ld_codes < j->H))
+    return MOE_ERR_INVALID_ARG;
+  if ((j->K || j->shared) && !x_out) return MOE_ERR_INVALID_ARG;
+  if (!x_out && !normed) return MOE_ERR_INVALID_ARG;
+  const size_t xs = size_of(j->x_type);
+  if (!aligned_to(x_out, xs) || !aligned_to(h, 2) || (codes && !code_scales) ||
+      !aligned_to(code_scales, 4) || !aligned_to(post_rstd, 4) || !aligned_to(norm_rstd, 4))
+    return MOE_ERR_INVALID_ARG;
+  JoinArgs p{};
+  p.j = *j;
+  p.x_out = x_out, p.ld_out = ld_out;
+  p.h = static_cast<__nv_bfloat16*>(h), p.ld_h = ld_h;
+  p.codes = static_cast<int8_t*>(codes), p.ld_codes = ld_codes;
+  p.code_scales = code_scales, p.post_rstd = post_rstd, p.norm_rstd = norm_rstd;
+  const bool vec = join_vectors(*j) && in_vectors(x_out, ld_out, xs) && in_vectors(h, ld_h, 2) &&
+                   in_vectors(codes, ld_codes, 1);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (j->x_type == MOE_DTYPE_F32)
+    e = vec ? run_forward<float, true>(p, s) : run_forward<float, false>(p, s);
+  else
+    e = vec ? run_forward<__nv_bfloat16, true>(p, s) : run_forward<__nv_bfloat16, false>(p, s);
+  return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+size_t moe_join_workspace(int T, int H) {
+  if (T < 1 || H < 1 || H > kMaxWidth) return 0;
+  return static_cast<size_t>(2) * back_blocks(T) * ((H + 3) / 4 * 4) * 4;
+}
+
+moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_out,
+                             const float* post_rstd, const float* norm_rstd, const void* d_x_out,
+                             int64_t ld_dxo, const void* d_h, int64_t ld_dh, void* d_x,
+                             int64_t ld_dx, void* d_rows, int64_t ld_drows,
+                             const int32_t* live_rows, float* d_weights, void* d_shared,
+                             int64_t ld_dshared, void* d_gate, void* d_post, void* d_norm,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  const moe_status st = check_join(j, false);
+  if (st != MOE_OK) return st;
+  if ((d_h || d_norm) && !j->norm_weight) return MOE_ERR_INVALID_ARG;
+  if ((d_norm && !d_h && j->T > 0) || (d_post && !j->post_weight) || (d_gate && !j->gate) ||
+      (d_shared && !j->shared) || ((d_rows || d_weights) && !j->K))
+    return MOE_ERR_INVALID_ARG;
+  if ((d_x_out && ld_dxo < j->H) || (d_h && (ld_dh < j->H || ld_out < j->H)) ||
+      (d_x && ld_dx < j->H) || (d_rows && ld_drows < j->H) || (d_shared && ld_dshared < j->H))
+    return MOE_ERR_INVALID_ARG;
+  const size_t xs = size_of(j->x_type);
+  if (!aligned_to(d_post, size_of(j->weight_type)) || !aligned_to(d_norm, size_of(j->weight_type)))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  JoinFinishArgs f{{nullptr, nullptr}, {d_norm, d_post}, 0, j->H, j->weight_type};
+  if (j->T > 0) {
+    if ((d_h && (!x_out || !norm_rstd)) || (j->post_weight && !post_rstd) ||
+        !aligned_to(x_out, xs) || !aligned_to(d_x_out, xs) || !aligned_to(d_x, xs) ||
+        !aligned_to(d_h, 2) || !aligned_to(d_rows, 2) || !aligned_to(d_shared, 2) ||
+        !aligned_to(d_gate, size_of(j->gate_type)) || !aligned_to(post_rstd, 4) ||
+        !aligned_to(norm_rstd, 4) || !aligned_to(live_rows, 4) || !aligned_to(d_weights, 4))
+      return MOE_ERR_INVALID_ARG;
+    if ((d_post || d_norm) && (!workspace || !aligned_to(workspace, 16) ||
+                               workspace_bytes < moe_join_workspace(j->T, j->H)))
+      return MOE_ERR_INVALID_ARG;
+    JoinBackArgs p{};
+    p.j = *j;
+    p.x_out = x_out, p.ld_out = ld_out, p.d_x_out = d_x_out, p.ld_dxo = ld_dxo;
+    p.d_h = d_h, p.ld_dh = ld_dh, p.post_rstd = post_rstd, p.norm_rstd = norm_rstd;
+    p.d_x = d_x, p.ld_dx = ld_dx;
+    p.d_rows = static_cast<__nv_bfloat16*>(d_rows), p.ld_drows = ld_drows;
+    p.live_rows = live_rows;
+    p.d_weights = d_weights;
+    p.d_shared = static_cast<__nv_bfloat16*>(d_shared), p.ld_dshared = ld_dshared;
+    p.d_gate = d_gate;
+    f.blocks = back_blocks(j->T);
+    float* ws = static_cast<float*>(workspace);
+    if (d_norm) f.part[0] = p.part_norm = ws;
+    if (d_post)
+      f.part[1] = p.part_post = ws + static_cast<int64_t>(f.blocks) * ((j->H + 3) / 4 * 4);
+    moe_join in = *j;
+    in.x = nullptr;  // (not read)
+    const bool vec = join_vectors(in) && in_vectors(x_out, ld_out, xs) &&
+                     in_vectors(d_x_out, ld_dxo, xs) && in_vectors(d_h, ld_dh, 2) &&
+                     in_vectors(d_x, ld_dx, xs) && in_vectors(d_rows, ld_drows, 2) &&
+                     in_vectors(d_shared, ld_dshared, 2);
+    cudaError_t e;
+    if (j->x_type == MOE_DTYPE_F32)
+      e = vec ? run_backward<float, true>(p, s) : run_backward<float, false>(p, s);
+    else
+      e = vec ? run_backward<__nv_bfloat16, true>(p, s) : run_backward<__nv_bfloat16, false>(p, s);
+    if (take_error(e) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (!d_post && !d_norm) return MOE_OK;
+  if (j->T == 0) {
+    // (sums over no tokens)
+    const size_t bytes = j->H * size_of(j->weight_type);
+    cudaError_t e = cudaSuccess;
+    if (d_norm) e = cudaMemsetAsync(d_norm, 0, bytes, s);
+    if (d_post && e == cudaSuccess) e = cudaMemsetAsync(d_post, 0, bytes, s);
+    return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  const cudaError_t e =
+      launch_pdl(false, join_finish_kernel, dim3((j->H + 31) / 32, d_post ? 2 : 1),
+                 dim3(32, kFinishRows), 0, s, f);
+  return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"
