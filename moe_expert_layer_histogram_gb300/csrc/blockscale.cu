@@ -169,40 +169,6 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The current device, null unless it is an sm_103 one.  What was found out about
-// a device is kept; a look-up that failed is tried again.
-const BlockscaleDevice* current_device() {
-  constexpr int kMaxDevices = 64;
-  struct Entry {
-    std::atomic<bool> known{false};
-    BlockscaleDevice d{};
-  };
-  static Entry entries[kMaxDevices];
-  static std::mutex looking_up;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return nullptr;
-  }
-  Entry& e = entries[dev];
-  if (e.known.load(std::memory_order_acquire)) return &e.d;
-  std::lock_guard<std::mutex> lock(looking_up);
-  if (!e.known.load(std::memory_order_relaxed)) {
-    int major = 0, minor = 0;
-    const bool usable =
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&e.d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
-        major == 10 && minor == 3 && tensor_map_encoder() && blockscale_clusters(&e.d) == cudaSuccess;
-    if (!usable) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    e.known.store(true, std::memory_order_release);
-  }
-  return &e.d;
-}
-
 // early: the product follows the library's own kernel on the stream and may
 // start while it runs (programmatic dependent launch).
 moe_status run_product(const Product& p, bool swiglu, void* out, int64_t ldo, float clamp,
@@ -303,6 +269,40 @@ bool copies_rows(int T, int rows, int H, int I) {
 }
 
 }  // namespace
+
+// See internal.h.  What was found out about a device is kept; a look-up that
+// failed is tried again.
+const BlockscaleDevice* current_device() {
+  constexpr int kMaxDevices = 64;
+  struct Entry {
+    std::atomic<bool> known{false};
+    BlockscaleDevice d{};
+  };
+  static Entry entries[kMaxDevices];
+  static std::mutex looking_up;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  Entry& e = entries[dev];
+  if (e.known.load(std::memory_order_acquire)) return &e.d;
+  std::lock_guard<std::mutex> lock(looking_up);
+  if (!e.known.load(std::memory_order_relaxed)) {
+    int major = 0, minor = 0;
+    const bool usable =
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&e.d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+        major == 10 && minor == 3 && tensor_map_encoder() && blockscale_clusters(&e.d) == cudaSuccess;
+    if (!usable) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    e.known.store(true, std::memory_order_release);
+  }
+  return &e.d;
+}
 
 }  // namespace moe
 

@@ -66,6 +66,7 @@
 #include <type_traits>
 
 #include "blockscale_quant.cuh"
+#include "expert_table.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -143,101 +144,6 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// mbar_wait by a whole warp, with its branches on votes: the lanes stay
-// together without the compiler's reconvergence points, which made a wait on
-// a phase that had completed cost 62 cycles instead of 36 in eight warps (and
-// 176 when one lane waited for the others).
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
-                                               volatile int* abort) {
-  uint32_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    if ((i & 127u) == 0) {
-      // (the low half of the timer: its differences are good for 4 s)
-      uint32_t now;
-      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
-      if (i == 0) t0 = now;
-      if (__any_sync(0xFFFFFFFFu, *abort != 0 || now - t0 > static_cast<uint32_t>(kWaitTimeoutNs))) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
-// One thread of a whole warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
-                                                 uint32_t bar_cluster, int32_t x, int32_t y,
-                                                 int32_t z, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                                 int32_t x, int32_t y, int32_t z,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z),
-      "l"(policy)
-      : "memory");
-}
-
-// 32 consecutive 32-bit columns of the thread's TMEM lane; not valid before
-// tmem_ld_wait() and reg_fence32().
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
-      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19,"
-      " %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile(""
-                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
-                   "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
-}
-
-// Arrive, where `on`, on a barrier at a shared::cluster address (an address
-// of this CTA's own shared memory is one; see also mbar_arrive_cluster): a
-// predicated instruction, no branch.
-__device__ __forceinline__ void mbar_arrive_if(bool on, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
-      "r"(static_cast<uint32_t>(on))
-      : "memory");
-}
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(mapa_shared(saddr, rank))
-               : "memory");
-  return v;
-}
-
 // Rows of scales (one per activation row) for QUANT's resident blocks: the
 // epilogue reads them kBsAhead at a time.
 __host__ __device__ constexpr int scale_rows(int resident) {
@@ -248,23 +154,11 @@ struct BsItem {
   int e, tile, row0, rows;
 };
 
-// Chunk table in shared memory: exclusive counts of the items' chunk groups
-// (`group` chunks of 128 rows each), and the first and last row of every
-// expert.  The offsets are clamped into [0, M] and each is raised to the
-// largest before it, so no row has two experts and the host's bound on the
-// number of items holds whatever the offsets are: the split products have one
-// item per cluster and no more.
-struct BsTable {
-  int* chunk_off;  // [E + 1]
-  int* start;      // [E]
-  int* end;        // [E]
-};
-
 // group: chunks per item (a pair's two; the second may have no rows), rank:
 // the chunk of the item that is wanted.  e: the expert of this or an earlier
 // item, moved up to the item's: a CTA's items come in expert order, so the
 // search is a step or two of the way.
-__device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int tiles, int item, int group,
+__device__ __forceinline__ BsItem map_bs_item(const ExpertTable& t, int tiles, int item, int group,
                                               int rank, int& e) {
   while (t.chunk_off[e + 1] * tiles <= item) ++e;
   const int chunks = t.chunk_off[e + 1] - t.chunk_off[e];
@@ -275,72 +169,6 @@ __device__ __forceinline__ BsItem map_bs_item(const BsTable& t, int tiles, int i
   it.row0 = t.start[e] + (local - it.tile * chunks) * (128 * group) + rank * 128;
   it.rows = min(128, t.end[e] - it.row0);
   return it;
-}
-
-// One warp fills the table, 32 experts at a time; all offsets are on their way
-// before the first is used.
-__device__ __forceinline__ void fill_bs_table(const BlockscaleArgs& p, const BsTable& t, int group,
-                                              int lane) {
-  if (!p.offsets) {
-    if (lane == 0) {
-      t.start[0] = 0;
-      t.end[0] = p.M;
-      t.chunk_off[0] = 0;
-      t.chunk_off[1] = (p.M + 128 * group - 1) / (128 * group);
-    }
-    return;
-  }
-  constexpr int kPer = kMaxExperts / 32;
-  const int per_item = 128 * group;
-  int first[kPer], last[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = 32 * i + lane;
-    first[i] = e < p.E ? p.offsets[e] : 0;
-    last[i] = e < p.E ? p.offsets[e + 1] : 0;
-  }
-  bool falls = false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) falls |= last[i] < first[i];
-  if (__any_sync(0xFFFFFFFFu, falls)) {
-    int top = 0;
-    for (int i = 0; i < kPer && 32 * i < p.E; ++i) {
-      const int e = 32 * i + lane;
-      int m = max(e < p.E ? p.offsets[e] : 0, top);
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, m, off);
-        if (lane >= off) m = max(m, o);
-      }
-      if (e < p.E) t.start[e] = m;
-      top = __shfl_sync(0xFFFFFFFFu, m, 31);
-    }
-    // (every lane reads back what it wrote itself)
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (32 * i + lane < p.E) first[i] = t.start[32 * i + lane];
-  }
-  int run = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (32 * i >= p.E) break;
-    const int e = 32 * i + lane;
-    const int r0 = min(max(first[i], 0), p.M), r1 = min(max(last[i], r0), p.M);
-    const int chunks = e < p.E ? (r1 - r0 + per_item - 1) / per_item : 0;
-    int inc = chunks;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    if (e < p.E) {
-      t.start[e] = r0;
-      t.end[e] = r1;
-      t.chunk_off[e] = run + inc - chunks;
-    }
-    run += __shfl_sync(0xFFFFFFFFu, inc, 31);
-  }
-  if (lane == 0) t.chunk_off[p.E] = run;
 }
 
 // acc += s v for 32 columns.
@@ -450,7 +278,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_tab = reinterpret_cast<int*>(tmem_holder + 2);
-  const BsTable tab{s_tab, s_tab + p.E + 1, s_tab + 2 * p.E + 1};
+  const ExpertTable tab{s_tab, s_tab + p.E + 1, s_tab + 2 * p.E + 1};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // (not early: below)
@@ -493,7 +321,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       tmem_relinquish();
     }
   }
-  if (warp == 2) fill_bs_table(p, tab, kGroup, lane);
+  if (warp == 2) fill_expert_table(p, tab, 128 * kGroup, lane);
   tc_fence_before();
   __syncthreads();
   // both CTAs' barriers are initialised before either arrives on the other's

@@ -254,6 +254,8 @@ struct BlockscaleDevice {
   int clusters[kBsMaxSplit + 1];
 };
 cudaError_t blockscale_clusters(BlockscaleDevice* d);  // the current device's
+// The current device (blockscale.cu), null unless it is an sm_103 one.
+const BlockscaleDevice* current_device();
 // Whether a product of one matrix is small enough to quantise its activations
 // itself (args.x): a CTA's share of them stays in its shared memory.
 bool blockscale_quantizes(int M, int N, int K, const BlockscaleDevice& d);
