@@ -644,6 +644,81 @@ moe_status moe_blockscale_experts(const void *x, int64_t ldx, int T,
  * gave up a bounded wait, else MOE_OK; MOE_ERR_CUDA on a CUDA error.      */
 moe_status moe_blockscale_status(void);
 
+/* ---- 8-bit integer products with a scale per token and per output channel -------
+ * Activations: int8 codes [rows, cols] (row stride ld_codes) with one fp32 scale
+ * per row.  Weights: int8 codes [E, N, K], rows of ldw codes, with one fp32 scale
+ * per row (output channel), w_scales [E, N].
+ *
+ * Quantise bf16 rows: s = amax / 127 and codes round(x / s) to even within
+ * +-127, both quotients rounded to nearest in fp32; a zero row gets s = 0 and
+ * zero codes, one with an infinity or NaN s = NaN and zero codes (its products
+ * are NaN).  x: device bf16 [x_rows, cols], row stride ldx; slots: device int32
+ * [rows] or NULL; row r reads row slots[r] / top_k of x, or row r; a slot outside
+ * x gives a zero row.  Any alignment of whole elements.  rows == 0 is a no-op.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (more than 2^31 - 65792
+ * columns), MOE_ERR_CUDA.                                                  */
+moe_status moe_int8_quantize(const void *x, int64_t ldx, int x_rows,
+                             const int32_t *slots, int top_k, int rows,
+                             int cols, void *codes, int64_t ld_codes,
+                             float *scales, void *stream);
+
+/* Workspace bytes of the products (0 for sizes out of range).  The contents need
+ * no initialisation and mean nothing after the call; a call's workspace is in
+ * use until its work is done.                                              */
+size_t moe_int8_matmul_workspace(int M, int K);
+size_t moe_int8_linear_workspace(int M, int N, int K);
+size_t moe_int8_experts_workspace(int rows, int H, int I);
+
+/* out[m, n] = a_scales[m] w_scales[e, n] sum_k a[m, k] w_e[n, k] for the rows m of
+ * each expert e, one rounding to bf16; products are exact, sums in fp32 (exact
+ * up to 2^24).  a: int8 [M, K], row stride lda, any alignment; offsets: device
+ * int32 [E + 1], rows offsets[e] .. offsets[e+1] - 1 belong to expert e, or NULL
+ * for one expert of all M rows (E = 1).  w: 16-byte aligned, ldw >= K a
+ * multiple of 16.  out: bf16 [M, N], row stride ldo.  Rows of no expert are not
+ * written; offsets are clamped into [0, M], and one that is below an earlier
+ * offset counts as that one.  The order of a row's sums depends on E, M, N, K and
+ * the device alone.  N, K, M of any size up to 2^31 - 65792, E <= 512.  M == 0
+ * is a no-op.  workspace: device, 16-byte aligned.  Asynchronous on `stream`,
+ * allocates nothing.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.  A kernel that gives up a bounded wait leaves
+ * its output incomplete and records it for moe_int8_status.                */
+moe_status moe_int8_matmul(const void *a, int64_t lda, const float *a_scales,
+                           const void *w, int64_t ldw, const float *w_scales,
+                           const int32_t *offsets, int E, int M, int N, int K,
+                           void *out, int64_t ldo, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* moe_int8_quantize of the bf16 rows x [M, K] (any alignment of whole elements)
+ * and the product with one matrix w [N, K] in one call.  The rest as
+ * moe_int8_matmul.                                                         */
+moe_status moe_int8_linear(const void *x, int64_t ldx, const void *w,
+                           int64_t ldw, const float *w_scales, int M, int N,
+                           int K, void *out, int64_t ldo, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* The experts' products of one layer on routed rows, as moe_blockscale_experts:
+ * row r of out (bf16 [rows, H], row stride ldo) is expert e's MLP of row
+ * slots[r] / top_k of x (bf16 [T, H]) for offsets[e] <= r < offsets[e+1]:
+ * quantised, through w13 [E, 2I, H] (gate rows, then up rows) and h = silu(gate)
+ * * up in fp32 (gate and up clamped to [-clamp_limit, clamp_limit] first when
+ * that is > 0 and finite; a NaN stays one), h quantised without an intermediate
+ * rounding, and through w2 [E, H, I]; w13 and w2 contiguous, w13_scales [E, 2I],
+ * w2_scales [E, H].  slots and offsets as moe_order writes them.  H and I
+ * multiples of 16 (else MOE_ERR_UNSUPPORTED).  rows == 0 is a no-op.  The rest
+ * as moe_int8_matmul.                                                      */
+moe_status moe_int8_experts(const void *x, int64_t ldx, int T,
+                            const int32_t *slots, int top_k, int rows,
+                            const int32_t *offsets, int E, const void *w13,
+                            const float *w13_scales, const void *w2,
+                            const float *w2_scales, int H, int I,
+                            float clamp_limit, void *out, int64_t ldo,
+                            void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Synchronises the device and returns (and clears) what the moe_int8_* kernels
+ * recorded on it since the last call, as moe_blockscale_status.            */
+moe_status moe_int8_status(void);
+
 /* Tensor-pipe rate of one MMA kind on this GPU (measurement, not part of the
  * layer): one CTA per SM issues `iters` groups of four back-to-back
  * tcgen05.mma (M = 128, N = n_cols in {128, 256}) on zero operands resident

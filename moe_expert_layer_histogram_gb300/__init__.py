@@ -70,7 +70,10 @@ EXPORTS = ("moe_create", "moe_prepare_weights", "moe_forward", "moe_forward_batc
            "moe_join_backward", "moe_blockscale_quantize", "moe_blockscale_matmul",
            "moe_blockscale_swiglu", "moe_blockscale_linear_workspace",
            "moe_blockscale_experts_workspace", "moe_blockscale_linear",
-           "moe_blockscale_experts", "moe_blockscale_status", "moe_measure_mma_rate", "moe_status_string",
+           "moe_blockscale_experts", "moe_blockscale_status", "moe_int8_quantize",
+           "moe_int8_matmul_workspace", "moe_int8_linear_workspace", "moe_int8_experts_workspace",
+           "moe_int8_matmul", "moe_int8_linear", "moe_int8_experts", "moe_int8_status",
+           "moe_measure_mma_rate", "moe_status_string",
            "moe_destroy")
 
 _lib = None
@@ -129,6 +132,17 @@ def lib():
     L.moe_blockscale_experts.argtypes = [vp, i64, ci, vp, ci, ci, vp, ci, vp, vp, vp, vp, ci, ci,
                                          cf, vp, i64, vp, ctypes.c_size_t, vp]
     L.moe_blockscale_status.argtypes = []
+    L.moe_int8_quantize.argtypes = [vp, i64, ci, vp, ci, ci, ci, vp, i64, vp, vp]
+    L.moe_int8_matmul_workspace.argtypes = [ci, ci]
+    L.moe_int8_linear_workspace.argtypes = [ci, ci, ci]
+    L.moe_int8_experts_workspace.argtypes = [ci, ci, ci]
+    L.moe_int8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, vp, ci, ci, ci, ci, vp, i64, vp,
+                                  ctypes.c_size_t, vp]
+    L.moe_int8_linear.argtypes = [vp, i64, vp, i64, vp, ci, ci, ci, vp, i64, vp, ctypes.c_size_t,
+                                  vp]
+    L.moe_int8_experts.argtypes = [vp, i64, ci, vp, ci, ci, vp, ci, vp, vp, vp, vp, ci, ci, cf, vp,
+                                   i64, vp, ctypes.c_size_t, vp]
+    L.moe_int8_status.argtypes = []
     L.moe_measure_mma_rate.argtypes = [ci, ci, ci, ci, ctypes.POINTER(ctypes.c_double), vp]
     L.moe_status_string.argtypes = [ci]
     L.moe_status_string.restype = ctypes.c_char_p
@@ -138,7 +152,9 @@ def lib():
         if name not in ("moe_status_string", "moe_destroy"):
             getattr(L, name).restype = ci
     for name in ("moe_balance_workspace", "moe_order_workspace", "moe_join_workspace",
-                 "moe_blockscale_linear_workspace", "moe_blockscale_experts_workspace"):
+                 "moe_blockscale_linear_workspace", "moe_blockscale_experts_workspace",
+                 "moe_int8_matmul_workspace", "moe_int8_linear_workspace",
+                 "moe_int8_experts_workspace"):
         getattr(L, name).restype = ctypes.c_size_t
     _lib = L
     return L
@@ -383,6 +399,50 @@ def moe_blockscale_status():
     return lib().moe_blockscale_status()
 
 
+def moe_int8_quantize(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,
+                      stream=None):
+    _check(lib().moe_int8_quantize(_ptr(x), ldx, x_rows, _ptr(slots), top_k, rows, cols,
+                                   _ptr(codes), ld_codes, _ptr(scales), stream),
+           "moe_int8_quantize")
+
+
+def moe_int8_matmul_workspace(M, K):
+    return lib().moe_int8_matmul_workspace(M, K)
+
+
+def moe_int8_linear_workspace(M, N, K):
+    return lib().moe_int8_linear_workspace(M, N, K)
+
+
+def moe_int8_experts_workspace(rows, H, I):
+    return lib().moe_int8_experts_workspace(rows, H, I)
+
+
+def moe_int8_matmul(a, lda, a_scales, w, ldw, w_scales, offsets, E, M, N, K, out, ldo, workspace,
+                    workspace_bytes, stream=None):
+    _check(lib().moe_int8_matmul(_ptr(a), lda, _ptr(a_scales), _ptr(w), ldw, _ptr(w_scales),
+                                 _ptr(offsets), E, M, N, K, _ptr(out), ldo, _ptr(workspace),
+                                 workspace_bytes, stream), "moe_int8_matmul")
+
+
+def moe_int8_linear(x, ldx, w, ldw, w_scales, M, N, K, out, ldo, workspace, workspace_bytes,
+                    stream=None):
+    _check(lib().moe_int8_linear(_ptr(x), ldx, _ptr(w), ldw, _ptr(w_scales), M, N, K, _ptr(out),
+                                 ldo, _ptr(workspace), workspace_bytes, stream), "moe_int8_linear")
+
+
+def moe_int8_experts(x, ldx, T, slots, top_k, rows, offsets, E, w13, w13_scales, w2, w2_scales, H,
+                     I, clamp_limit, out, ldo, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_int8_experts(_ptr(x), ldx, T, _ptr(slots), top_k, rows, _ptr(offsets), E,
+                                  _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales), H, I,
+                                  clamp_limit, _ptr(out), ldo, _ptr(workspace), workspace_bytes,
+                                  stream), "moe_int8_experts")
+
+
+def moe_int8_status():
+    return lib().moe_int8_status()
+
+
 def moe_measure_mma_rate(fmt, n_cols=128, copy_scales=False, iters=20000, stream=None):
     """Dense TFLOP/s of the layer's MMA kind for `fmt` on the current GPU
     (tcgen05.mma on shared-memory-resident operands, one CTA per SM)."""
@@ -498,7 +558,9 @@ _OPERATORS = {"RouterBalance": "balance", "router_balance": "balance",
               "block_join_backward": "join",
               "blockscale_quantize": "blockscale",
               "blockscale_matmul": "blockscale", "blockscale_linear": "blockscale",
-              "blockscale_linear_dx": "blockscale", "blockscale_experts": "blockscale"}
+              "blockscale_linear_dx": "blockscale", "blockscale_experts": "blockscale",
+              "int8_quantize": "int8", "int8_matmul": "int8", "int8_linear": "int8",
+              "int8_experts": "int8"}
 
 
 def __getattr__(name):

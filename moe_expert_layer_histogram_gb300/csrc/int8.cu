@@ -1,0 +1,459 @@
+// int8.cu -- products of 8-bit integer matrices with a scale per token and a scale
+// per output channel: the quantiser of the activations, and the entry points with
+// their checks.  The products run in int8_gemm.cu.
+//
+// Quantisation of a row: s = amax / 127, codes round(x / s) to even within +-127,
+// both quotients rounded to nearest in fp32.  The products take the codes as f16
+// (exact), so the calls that quantise for themselves write them so at once.
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "internal.h"
+#include "moe.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+// Largest M, N and K of a product: rounding one up to a tile, or to a block's
+// stride over a row, stays in 32 bits.
+constexpr int kMaxExtent = INT32_MAX - 65791;
+
+// Scale of a row from the bits of its largest magnitude, and its codes.
+__device__ __forceinline__ float scale_of(uint32_t amax) {
+  return amax >= 0x7F800000u ? NAN : __uint_as_float(amax) / 127.0f;
+}
+__device__ __forceinline__ int code_of(float v, float s) {
+  return s > 0.0f ? __float2int_rn(fminf(fmaxf(v / s, -127.0f), 127.0f)) : 0;
+}
+__device__ __forceinline__ uint32_t f16_bits(int code) {
+  // 1152 + code has the bits 0x6480 + code
+  uint32_t b = static_cast<uint32_t>(0x6480 + code);
+  asm("{\n\t.reg .b16 h, o;\n\tcvt.u16.u32 h, %0;\n\tmov.b16 o, 0x6480;\n\t"
+      "sub.f16 h, h, o;\n\tcvt.u32.u16 %0, h;\n\t}"
+      : "+r"(b));
+  return b;
+}
+
+// Eight codes to memory: bytes, or f16.
+template <bool F16>
+__device__ __forceinline__ void store_codes(void* row, int c0, int cols, bool vec,
+                                            const int (&q)[8]) {
+  if constexpr (F16) {
+    uint16_t* d = static_cast<uint16_t*>(row) + c0;
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = f16_bits(q[i]);
+    if (vec && c0 + 8 <= cols) {
+      *reinterpret_cast<uint4*>(d) = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16,
+                                                h[4] | h[5] << 16, h[6] | h[7] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + i < cols) d[i] = static_cast<uint16_t>(h[i]);
+    }
+  } else {
+    int8_t* d = static_cast<int8_t*>(row) + c0;
+    if (vec && c0 + 8 <= cols) {
+      uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo |= static_cast<uint32_t>(q[i] & 255) << (8 * i);
+        hi |= static_cast<uint32_t>(q[i + 4] & 255) << (8 * i);
+      }
+      *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + i < cols) d[i] = static_cast<int8_t>(q[i]);
+    }
+  }
+}
+
+// A block takes a row.  Its first kKept vectors of eight per thread stay in
+// registers between the maximum and the codes; what a longer row has beyond is
+// read again.  amax (or null): a word per row that is set to zero for a later
+// kernel.
+constexpr int kKept = 4;
+
+template <bool F16>
+__global__ void __launch_bounds__(256)
+    int8_quantize_kernel(const __nv_bfloat16* x, int64_t ldx, int x_rows, const int32_t* slots,
+                         int top_k, int cols, void* codes, int64_t ld_codes, float* scales,
+                         uint32_t* amax, int vec) {
+  // (a product that follows may set itself up and load weights meanwhile)
+  pdl_launch_dependents();
+  __shared__ uint32_t s_max[8];
+  const int64_t r = blockIdx.x;
+  const int slot = slots ? slots[r] : 0;
+  const int64_t src = slots ? slot / top_k : r;
+  const bool in = slot >= 0 && src < x_rows;
+  const __nv_bfloat16* row = x + (in ? src : 0) * ldx;
+  const int stride = blockDim.x * 8;
+  auto load = [&](int c0, uint32_t (&v)[4]) {
+    if (!in || c0 >= cols) {
+      v[0] = v[1] = v[2] = v[3] = 0u;
+    } else if (vec && c0 + 8 <= cols) {
+      const uint4 q = *reinterpret_cast<const uint4*>(row + c0);
+      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+      const uint16_t* s = reinterpret_cast<const uint16_t*>(row) + c0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = c0 + 2 * i < cols ? s[2 * i] : 0u;
+        const uint32_t hi = c0 + 2 * i + 1 < cols ? s[2 * i + 1] : 0u;
+        v[i] = lo | hi << 16;
+      }
+    }
+  };
+  auto largest = [](const uint32_t (&v)[4], uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max((v[i] << 16) & 0x7FFFFFFFu, v[i] & 0x7FFF0000u));
+    return m;
+  };
+  uint32_t kept[kKept][4], m = 0u;
+  const int first = threadIdx.x * 8;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) load(first + i * stride, kept[i]);
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) m = largest(kept[i], m);
+  for (int c0 = first + kKept * stride; c0 < cols; c0 += stride) {
+    uint32_t v[4];
+    load(c0, v);
+    m = largest(v, m);
+  }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) m = max(m, s_max[w]);
+  const float s = scale_of(m);
+  if (threadIdx.x == 0) {
+    scales[r] = s;
+    if (amax) amax[r] = 0u;
+  }
+  void* out = F16 ? static_cast<void*>(static_cast<uint16_t*>(codes) + r * ld_codes)
+                  : static_cast<void*>(static_cast<int8_t*>(codes) + r * ld_codes);
+  auto put = [&](int c0, const uint32_t (&v)[4]) {
+    if (c0 >= cols) return;
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[2 * i] = code_of(__uint_as_float(v[i] << 16), s);
+      q[2 * i + 1] = code_of(__uint_as_float(v[i] & 0xFFFF0000u), s);
+    }
+    store_codes<F16>(out, c0, cols, vec, q);
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) put(first + i * stride, kept[i]);
+  for (int c0 = first + kKept * stride; c0 < cols; c0 += stride) {
+    uint32_t v[4];
+    load(c0, v);
+    put(c0, v);
+  }
+}
+
+// int8 codes to f16 ones, eight at a time.
+__global__ void __launch_bounds__(256)
+    int8_widen_kernel(const int8_t* codes, int64_t ld, int rows, int cols, uint16_t* out,
+                      int64_t ld_out, int vec) {
+  pdl_launch_dependents();
+  const int per = (cols + 7) / 8;
+  const int64_t n = static_cast<int64_t>(rows) * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / per;
+    const int c0 = static_cast<int>(i - r * per) * 8;
+    const int8_t* src = codes + r * ld + c0;
+    int q[8];
+    if (vec && c0 + 8 <= cols) {
+      const uint2 w = *reinterpret_cast<const uint2*>(src);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        q[b] = static_cast<int8_t>(w.x >> (8 * b));
+        q[b + 4] = static_cast<int8_t>(w.y >> (8 * b));
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) q[b] = c0 + b < cols ? src[b] : 0;
+    }
+    store_codes<true>(out + r * ld_out, c0, cols, true, q);
+  }
+}
+
+// fp32 rows to f16 codes, by the rows' largest magnitudes.
+__global__ void __launch_bounds__(256)
+    int8_requantize_kernel(const float* h, const uint32_t* amax, int64_t rows, int cols,
+                           uint16_t* out, int64_t ld_out, float* scales) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per = (cols + 7) / 8;
+  const int64_t n = rows * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / per;
+    const int c0 = static_cast<int>(i - r * per) * 8;
+    const float s = scale_of(amax[r]);
+    if (c0 == 0) scales[r] = s;
+    const float* src = h + r * cols + c0;
+    int q[8];
+    if (c0 + 8 <= cols && cols % 4 == 0) {
+      const float4 a = *reinterpret_cast<const float4*>(src),
+                   b = *reinterpret_cast<const float4*>(src + 4);
+      q[0] = code_of(a.x, s), q[1] = code_of(a.y, s), q[2] = code_of(a.z, s), q[3] = code_of(a.w, s);
+      q[4] = code_of(b.x, s), q[5] = code_of(b.y, s), q[6] = code_of(b.z, s), q[7] = code_of(b.w, s);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) q[b] = c0 + b < cols ? code_of(src[b], s) : 0;
+    }
+    store_codes<true>(out + r * ld_out, c0, cols, true, q);
+  }
+}
+
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// ---------------------------------------------------------------- arguments
+struct Product {
+  const void* w;
+  int64_t ldw;
+  const float* w_scales;
+  const int32_t* offsets;
+  int E, M, N, K;
+};
+
+// TMA wants 16-byte aligned bases and row strides; scales and offsets are read as
+// 32-bit words.
+moe_status check_weights(const Product& p) {
+  if (p.M < 0 || p.N < 1 || p.K < 1 || p.E < 1 || (!p.offsets && p.E != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (p.E > kMaxExperts || p.M > kMaxExtent || p.N > kMaxExtent || p.K > kMaxExtent)
+    return MOE_ERR_UNSUPPORTED;
+  if (p.ldw < p.K) return MOE_ERR_INVALID_ARG;
+  if (p.M == 0) return MOE_OK;
+  if (!p.w || !p.w_scales || !aligned_to(p.w, 16) || p.ldw % 16 || !aligned_to(p.w_scales, 4) ||
+      !aligned_to(p.offsets, 4))
+    return MOE_ERR_INVALID_ARG;
+  // strides of the tensor maps and the item count stay in range
+  if (p.ldw >= (int64_t{1} << 39) / p.N ||
+      (static_cast<int64_t>(p.E) + p.M / 128 + 1) * ((p.N + 127) / 128) > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Workspaces: f16 codes in rows of a multiple of eight, then the scales.
+int64_t padded(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+struct Coded {
+  uint16_t* codes;
+  int64_t ld;
+  float* scales;
+  static int64_t code_bytes(int64_t rows, int64_t cols) {
+    return padded(rows * padded(cols, 8) * 2, 256);
+  }
+  static int64_t bytes(int64_t rows, int64_t cols) {
+    return code_bytes(rows, cols) + padded(rows * 4, 256);
+  }
+  Coded(void* ws, int64_t rows, int64_t cols)
+      : codes(static_cast<uint16_t*>(ws)), ld(padded(cols, 8)),
+        scales(reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + code_bytes(rows, cols))) {}
+};
+
+// The product of f16 codes x [M, K] with their scales.
+moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const float* scales,
+                       bool swiglu, void* out, int64_t ldo, float clamp, uint32_t* amax,
+                       cudaStream_t s) {
+  const BlockscaleDevice* d = current_device();
+  if (!d) return MOE_ERR_NO_DEVICE;
+  auto encode = [&](CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
+                    const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t one[3] = {1, 1, 1};
+    return tensor_map_encoder()(m, type, rank, const_cast<void*>(base), dims, strides, box, one,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  Int8Maps maps;
+  // (one expert: all chunks take the largest box)
+  const int boxes = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 3 : 4;
+  const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M)};
+  const cuuint64_t xstr[1] = {static_cast<cuuint64_t>(ld) * 2};
+  for (int i = p.E == 1 ? boxes - 1 : 0; i < boxes; ++i) {
+    const cuuint32_t box[2] = {64, 16u << i};
+    if (!encode(&maps.x[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, 2, xdims, xstr, box))
+      return MOE_ERR_CUDA;
+  }
+  const cuuint64_t wdims[3] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.N),
+                               static_cast<cuuint64_t>(p.E)};
+  const cuuint64_t wstr[2] = {static_cast<cuuint64_t>(p.ldw), static_cast<cuuint64_t>(p.ldw) * p.N};
+  const cuuint32_t wbox[3] = {128, 128, 1};
+  if (!encode(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, 3, wdims, wstr, wbox)) return MOE_ERR_CUDA;
+  Int8Args a{};
+  a.a_scales = scales;
+  a.w_scales = p.w_scales;
+  a.offsets = p.offsets;
+  a.E = p.E, a.M = p.M, a.N = p.N, a.K = p.K;
+  a.out = out;
+  a.ldo = ldo;
+  a.out_pairs = aligned_to(out, 4) && ldo % 2 == 0;
+  a.clamp = clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY;
+  a.amax = amax;
+  return take_error(launch_int8(maps, a, swiglu, *d, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <bool F16>
+moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* slots, int top_k,
+                        int rows, int cols, void* codes, int64_t ld_codes, float* scales,
+                        uint32_t* amax, cudaStream_t s) {
+  const bool vec = aligned_to(x, 16) && ldx % 8 == 0 && aligned_to(codes, F16 ? 16 : 8) &&
+                   ld_codes % 8 == 0;
+  const int threads =
+      static_cast<int>(std::min<int64_t>(256, padded((static_cast<int64_t>(cols) + 7) / 8, 32)));
+  const cudaError_t e =
+      launch_pdl(false, int8_quantize_kernel<F16>, dim3(rows), dim3(threads), 0, s,
+                 static_cast<const __nv_bfloat16*>(x), ldx, x_rows, slots, top_k, cols, codes,
+                 ld_codes, scales, amax, static_cast<int>(vec));
+  return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Blocks of an elementwise kernel of 256 threads over n vectors.
+int vector_blocks(int64_t n) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 152 * 8 * 4)));
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_int8_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* slots,
+                             int top_k, int rows, int cols, void* codes, int64_t ld_codes,
+                             float* scales, void* stream) {
+  if (rows < 0 || cols < 1 || x_rows < 0 || ldx < cols || ld_codes < cols)
+    return MOE_ERR_INVALID_ARG;
+  if (slots ? top_k < 1 : x_rows < rows) return MOE_ERR_INVALID_ARG;
+  if (cols > kMaxExtent) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if ((!x && x_rows > 0) || !codes || !scales || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
+      !aligned_to(scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  return run_quantize<false>(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,
+                             nullptr, static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_int8_matmul_workspace(int M, int K) {
+  if (M < 1 || K < 1 || M > kMaxExtent || K > kMaxExtent) return 0;
+  return static_cast<size_t>(Coded::bytes(M, K));
+}
+
+moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, const void* w,
+                           int64_t ldw, const float* w_scales, const int32_t* offsets, int E,
+                           int M, int N, int K, void* out, int64_t ldo, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const Product p{w, ldw, w_scales, offsets, E, M, N, K};
+  const moe_status st = check_weights(p);
+  if (st != MOE_OK) return st;
+  if (lda < K || ldo < N) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!a || !a_scales || !out || !aligned_to(a_scales, 4) || !aligned_to(out, 2) || !workspace ||
+      !aligned_to(workspace, 16) || workspace_bytes < moe_int8_matmul_workspace(M, K))
+    return MOE_ERR_INVALID_ARG;
+  if (!current_device()) return MOE_ERR_NO_DEVICE;
+  const Coded c(workspace, M, K);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t vectors = static_cast<int64_t>(M) * ((K + 7) / 8);
+  const cudaError_t e = launch_pdl(false, int8_widen_kernel, dim3(vector_blocks(vectors)),
+                                   dim3(256), 0, s, static_cast<const int8_t*>(a), lda, M, K,
+                                   c.codes, c.ld, static_cast<int>(aligned_to(a, 8) && lda % 8 == 0));
+  if (take_error(e) != cudaSuccess) return MOE_ERR_CUDA;
+  return run_product(p, c.codes, c.ld, a_scales, false, out, ldo, 0.0f, nullptr, s);
+}
+
+size_t moe_int8_linear_workspace(int M, int N, int K) {
+  return N < 1 || N > kMaxExtent ? 0 : moe_int8_matmul_workspace(M, K);
+}
+
+moe_status moe_int8_linear(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                           const float* w_scales, int M, int N, int K, void* out, int64_t ldo,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  const Product p{w, ldw, w_scales, nullptr, 1, M, N, K};
+  const moe_status st = check_weights(p);
+  if (st != MOE_OK) return st;
+  if (ldx < K || ldo < N) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x || !out || !aligned_to(x, 2) || !aligned_to(out, 2) || !workspace ||
+      !aligned_to(workspace, 16) || workspace_bytes < moe_int8_linear_workspace(M, N, K))
+    return MOE_ERR_INVALID_ARG;
+  if (!current_device()) return MOE_ERR_NO_DEVICE;
+  const Coded c(workspace, M, K);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const moe_status sq =
+      run_quantize<true>(x, ldx, M, nullptr, 1, M, K, c.codes, c.ld, c.scales, nullptr, s);
+  if (sq != MOE_OK) return sq;
+  return run_product(p, c.codes, c.ld, c.scales, false, out, ldo, 0.0f, nullptr, s);
+}
+
+size_t moe_int8_experts_workspace(int rows, int H, int I) {
+  if (rows < 1 || H < 1 || I < 1 || rows > kMaxExtent || H > kMaxExtent || I > kMaxExtent / 2)
+    return 0;
+  // the rows' codes, h in fp32 and its rows' maxima, its codes
+  return static_cast<size_t>(Coded::bytes(rows, H) +
+                             padded(static_cast<int64_t>(rows) * I * 4, 256) +
+                             padded(static_cast<int64_t>(rows) * 4, 256) + Coded::bytes(rows, I));
+}
+
+moe_status moe_int8_experts(const void* x, int64_t ldx, int T, const int32_t* slots, int top_k,
+                            int rows, const int32_t* offsets, int E, const void* w13,
+                            const float* w13_scales, const void* w2, const float* w2_scales, int H,
+                            int I, float clamp_limit, void* out, int64_t ldo, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (I < 1 || H < 1 || T < 0 || top_k < 1 || !offsets) return MOE_ERR_INVALID_ARG;
+  if (I % 16 || H % 16 || I > kMaxExtent / 2) return MOE_ERR_UNSUPPORTED;
+  const Product p1{w13, H, w13_scales, offsets, E, rows, 2 * I, H};
+  const Product p2{w2, I, w2_scales, offsets, E, rows, H, I};
+  moe_status st = check_weights(p1);
+  if (st == MOE_OK) st = check_weights(p2);
+  if (st != MOE_OK) return st;
+  if (ldx < H || ldo < H) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if ((!x && T > 0) || !slots || !out || !workspace || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
+      !aligned_to(out, 2) || !aligned_to(workspace, 16) ||
+      workspace_bytes < moe_int8_experts_workspace(rows, H, I))
+    return MOE_ERR_INVALID_ARG;
+  if (!current_device()) return MOE_ERR_NO_DEVICE;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  const Coded c(at, rows, H);
+  at += Coded::bytes(rows, H);
+  float* h = reinterpret_cast<float*>(at);
+  at += padded(static_cast<int64_t>(rows) * I * 4, 256);
+  uint32_t* amax = reinterpret_cast<uint32_t*>(at);
+  at += padded(static_cast<int64_t>(rows) * 4, 256);
+  const Coded hc(at, rows, I);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = run_quantize<true>(x, ldx, T, slots, top_k, rows, H, c.codes, c.ld, c.scales, amax, s);
+  if (st == MOE_OK)
+    st = run_product(p1, c.codes, c.ld, c.scales, true, h, I, clamp_limit, amax, s);
+  if (st != MOE_OK) return st;
+  const int64_t vectors = static_cast<int64_t>(rows) * ((I + 7) / 8);
+  if (take_error(launch_pdl(true, int8_requantize_kernel, dim3(vector_blocks(vectors)), dim3(256),
+                            0, s, h, amax, rows, I, hc.codes, hc.ld, hc.scales)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return run_product(p2, hc.codes, hc.ld, hc.scales, false, out, ldo, 0.0f, nullptr, s);
+}
+
+moe_status moe_int8_status(void) {
+  int v = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess || int8_status(&v) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return v ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
+}
+
+}  // extern "C"

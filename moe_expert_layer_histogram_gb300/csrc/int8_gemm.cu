@@ -1,0 +1,595 @@
+// int8_gemm.cu -- products of 8-bit integer matrices with a scale per token and a
+// scale per output channel, on the sm_103a tensor cores.
+//
+//   y[m][n] = sx[m] sw[n] sum_k cx[m][k] cw[n][k]
+//
+// sm_103a's tensor cores have no fast integer kind, but an 8-bit code is exact in
+// f16 and so is the product of two in the fp32 accumulator (|sum| <= 2^24, that
+// is 1024 products of largest codes, is exact; a longer sum rounds as fp32 sums
+// do).  So the codes run as kind::f16, and the weights stay 8 bits wide in HBM,
+// in L2 and in shared memory: they are the A operand, which the tensor cores can
+// read from TMEM, and are widened on the way from shared memory into it.  A code
+// c becomes the f16 with the bits 0x6400 + (c + 128), which is 1152 + c, and a
+// subtraction takes the 1152 away: five instructions for four codes.  The tokens
+// are the B operand, as f16 codes in shared memory.
+//
+// So D[channel][token]: a tile is 256 channels (two halves of 128 TMEM lanes) by
+// up to 128 tokens.  Structure: one persistent CTA per SM walks the items (expert,
+// tile, chunk of at most 128 rows).  Warp 0 (one thread) fills a ring of stages by
+// TMA: 128 columns of the reduction, as 8-bit weights (32 KB) and f16 codes of the
+// chunk's rows (box height 16 / 32 / 64 / 128).  Warps 4-11 widen: warp w takes
+// the TMEM lanes 32 (w % 4).. of half (w - 4) / 4 and writes its rows' f16 into
+// one of two TMEM buffers.  Warp 1 issues the MMAs.  The widening warps also read
+// the results out: after the first two blocks of the next item have been widened,
+// so the tensor cores go on as soon as the results are in registers, and the
+// scaling and the stores run beside them.
+//
+// Few rows leave most SMs without an item; there a cluster of two to eight CTAs
+// splits the reduction of each item and joins its fp32 partial sums through
+// distributed shared memory, in rank order, so the result does not depend on
+// timing.
+//
+// With SWIGLU the halves are 128 gate channels and the 128 up channels that go
+// with them; h = silu(gate) up is stored in fp32, and the largest |h| of each row
+// kept by an atomic maximum (of bits: the order of the updates does not matter),
+// from which the kernel after this one takes the rows' scales.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "expert_table.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kI8Threads = 384;
+constexpr int kI8WideWarp0 = 4;     // warps 4-11 widen the weights and read the results
+constexpr int kI8WideWarps = 8;
+constexpr int kI8Tile = 256;        // channels of an item
+constexpr int kI8MaxStages = 6;
+constexpr int kI8WBytes = kI8Tile * 128;
+constexpr int kI8SmemLimit = 232448;
+constexpr int kI8Buffers = 2;       // TMEM buffers of widened weights, 128 columns each
+constexpr uint32_t kI8Results = 0;  // TMEM columns: results (2 x 128), then the buffers
+constexpr uint32_t kI8Weights = 256;
+constexpr int kI8PartLd = kI8Tile + 4;
+
+__device__ int g_int8_status;
+
+// kind::f16 with f16 inputs, f32 accumulator, both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// A from TMEM (lane = row, a column holds two neighbouring k), B from shared
+// memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                           uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+// Four codes in a word to two words of two f16 each.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;  // c + 128
+  lo = __byte_perm(w, 0x64646464u, 0x4140);
+  hi = __byte_perm(w, 0x64646464u, 0x4342);
+  asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));  // 1152
+  asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+}
+
+__device__ __forceinline__ float clamp_to(float v, float limit) {
+  // (a NaN stays one; fminf and fmaxf would drop it)
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-limit));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(limit));
+  return v;
+}
+
+__device__ __forceinline__ float swiglu(float g, float u, float clamp) {
+  g = clamp_to(g, clamp);
+  u = clamp_to(u, clamp);
+  // e^-g by the hardware's power of two, off by two ulp and |g| 2^-24 of itself,
+  // and an approximate quotient of two ulp
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  return __fdividef(g, 1.0f + e) * u;
+}
+
+struct I8Item {
+  int e, tile, row0, rows;
+};
+
+// Items of an expert: groups of up to `group` chunks, tile by tile within a group,
+// chunk by chunk within a tile, so that CTAs that run together share both weights
+// and tokens in L2.  e: the expert of this or an earlier item, moved up.
+__device__ __forceinline__ I8Item map_i8_item(const ExpertTable& t, int tiles, int group, int item,
+                                              int& e) {
+  while (t.chunk_off[e + 1] * tiles <= item) ++e;
+  const int chunks = t.chunk_off[e + 1] - t.chunk_off[e];
+  const int local = item - t.chunk_off[e] * tiles;
+  const int g = local / (group * tiles), in = local - g * group * tiles;
+  const int size = min(group, chunks - g * group);
+  I8Item it;
+  it.e = e;
+  it.tile = in / size;
+  it.row0 = t.start[e] + (g * group + in - it.tile * size) * 128;
+  it.rows = min(128, t.end[e] - it.row0);
+  return it;
+}
+
+template <bool SWIGLU, bool SPLIT>
+__global__ void __launch_bounds__(kI8Threads, 1)
+    int8_gemm_kernel(const __grid_constant__ Int8Maps maps, const __grid_constant__ Int8Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int x_bytes = p.a_rows * 256, stage_bytes = kI8WBytes + x_bytes, stages = p.stages;
+  // per widening warp: the scales of a chunk's rows
+  float* s_scale = reinterpret_cast<float*>(smem + stages * stage_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + kI8WideWarps * 128);
+  uint64_t* empty = full + kI8MaxStages;
+  uint64_t* afull = empty + kI8MaxStages;
+  uint64_t* aempty = afull + kI8Buffers;
+  uint64_t* dfull = aempty + kI8Buffers;
+  uint64_t* dempty = dfull + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dempty + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* s_tab = reinterpret_cast<int*>(tmem_holder + 2);
+  const ExpertTable tab{s_tab, s_tab + p.E + 1, s_tab + 2 * p.E + 1};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < kI8Buffers; ++b) {
+      mbar_init(&afull[b], kI8WideWarps);
+      mbar_init(&aempty[b], 1);
+    }
+    mbar_init(dfull, 1);
+    mbar_init(dempty, kI8WideWarps);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // The kernel before this one is the library's own: it writes the codes and their
+  // scales, neither offsets nor weights, and has let this one start only when all
+  // before it was over.
+  pdl_launch_dependents();
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (warp == 2) fill_expert_table(p, tab, 128, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int kb_all = (p.K + 127) / 128;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int kb0 = SPLIT ? kb_all * rank / p.split : 0;
+  const int kb1 = SPLIT ? kb_all * (rank + 1) / p.split : kb_all;
+  const int first = SPLIT ? blockIdx.x / p.split : blockIdx.x;
+  const int step = SPLIT ? gridDim.x / p.split : gridDim.x;
+  const int total = tab.chunk_off[p.E] * p.tiles;
+  int expert = 0;  // of the role's latest item
+  auto map_item = [&](int item) {
+    return map_i8_item(tab, p.tiles, p.chunk_group, item, expert);
+  };
+  // (one expert: the box that all its chunks take, the last one short)
+  auto box_of = [&](int rows) {
+    rows = p.E == 1 ? p.a_rows : rows;
+    return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------- TMA producer
+      const uint64_t once = l2_policy_evict_first(), reused = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto load_w = [&](const I8Item& it, int st, int kb) {
+        // weights of an expert with one chunk are read once
+        const uint64_t policy = tab.chunk_off[it.e + 1] - tab.chunk_off[it.e] > 1 ? reused : once;
+        mbar_arrive_expect_tx(&full[st], kI8WBytes + (16u << box_of(it.rows)) * 256u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n0 = SWIGLU ? it.tile * 128 + h * (p.N / 2) : it.tile * kI8Tile + h * 128;
+          tma_load_3d_hint(smem + st * stage_bytes + h * (kI8WBytes / 2), &maps.w, &full[st],
+                           kb * 128, n0, it.e, policy);
+        }
+      };
+      int ahead = 0;  // stages of the first item whose weights are on their way
+      if (first < total) {
+        const I8Item it = map_item(first);
+        for (; ahead < min(stages, kb1 - kb0); ++ahead) load_w(it, ahead, kb0 + ahead);
+      }
+      pdl_wait();
+      fence_proxy_async_global();
+      for (int item = first; ok && item < total; item += step) {
+        const I8Item it = map_item(item);
+        const int box = box_of(it.rows);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (ahead > 0) {
+            --ahead;
+          } else {
+            ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
+            if (!ok) break;
+            load_w(it, stage, kb);
+          }
+          uint8_t* sx = smem + stage * stage_bytes + kI8WBytes;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d_hint(sx + h * (16 << box) * 128, &maps.x[box], &full[stage],
+                             kb * 128 + h * 64, it.row0, reused);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) report_status(&g_int8_status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------- MMA issuer
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, aphase = 0, dphase = 0;
+    bool ok = true;
+    for (int item = first; ok && item < total; item += step) {
+      const I8Item it = map_item(item);
+      const int box = box_of(it.rows), n = 16 << box;
+      const uint32_t idesc = idesc_f16(128, n);
+      ok = mbar_wait_warp(dempty, dphase ^ 1, abort_flag);
+      dphase ^= 1;
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
+        ok = mbar_wait_warp(&full[stage], phase, abort_flag) &&
+             mbar_wait_warp(&afull[buf], aphase, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t sx = smem_u32(smem + stage * stage_bytes + kI8WBytes);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // 16 of the 128 columns: 32 bytes further in a row of 64 f16
+            const uint64_t b = desc_sw128(sx + (k >> 2) * n * 128 + (k & 3) * 32);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_f16_ts(tmem + kI8Results + h * 128, tmem + kI8Weights + buf * 128 + h * 64 + k * 8,
+                         b, idesc, kb > kb0 || k > 0);
+          }
+          tc_commit(&empty[stage]);
+          tc_commit(&aempty[buf]);
+          if (kb + 1 == kb1) tc_commit(dfull);
+        }
+        __syncwarp();
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (++buf == kI8Buffers) {
+          buf = 0;
+          aphase ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
+  } else if (warp >= kI8WideWarp0) {
+    // ---------------------------------------------------- widen, and results
+    const int quarter = warp & 3, half = (warp - kI8WideWarp0) >> 2;
+    const int row = quarter * 32 + lane;  // of the half: the thread's TMEM lane
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* scales = s_scale + (warp - kI8WideWarp0) * 128;
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, aphase = 0, dphase = 0;
+    bool ok = true, waited = false;
+
+    auto widen = [&]() {
+      if (!mbar_wait_warp(&full[stage], phase, abort_flag)) return false;
+      const uint8_t* src = smem + stage * stage_bytes + half * (kI8WBytes / 2) + row * 128;
+      uint4 v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        v[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+      if (!mbar_wait_warp(&aempty[buf], aphase ^ 1, abort_flag)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          widen4(v[4 * q + c].x, w[8 * c], w[8 * c + 1]);
+          widen4(v[4 * q + c].y, w[8 * c + 2], w[8 * c + 3]);
+          widen4(v[4 * q + c].z, w[8 * c + 4], w[8 * c + 5]);
+          widen4(v[4 * q + c].w, w[8 * c + 6], w[8 * c + 7]);
+        }
+        tmem_st32(lanes + kI8Weights + buf * 128 + half * 64 + q * 32, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive_if(lane == 0, smem_u32(&afull[buf]));
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (++buf == kI8Buffers) {
+        buf = 0;
+        aphase ^= 1;
+      }
+      return true;
+    };
+
+    // Results of 32 columns (tokens) from `col` on.
+    auto read32 = [&](uint32_t col, uint32_t (&v)[32]) { tmem_ld32(lanes + kI8Results + col, v); };
+
+    auto results = [&](const I8Item& it) {
+      if (!waited) {
+        // (the scales are the kernel's before this one)
+        pdl_wait();
+        waited = true;
+      }
+      const float* sx = p.a_scales + it.row0;
+      const float* sw = p.w_scales + static_cast<int64_t>(it.e) * p.N;
+      float sr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sr[i] = 32 * i + lane < it.rows ? sx[32 * i + lane] : 0.0f;
+      if (!mbar_wait_warp(dfull, dphase, abort_flag)) return false;
+      dphase ^= 1;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) scales[32 * i + lane] = sr[i];
+      __syncwarp();
+      if constexpr (SPLIT) {
+        // fp32 sums to [token][channel] in what was the ring of stages
+        float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          if (c >= it.rows) break;
+          uint32_t v[32];
+          read32(half * 128 + c, v);
+          tmem_ld_wait();
+          reg_fence32(v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < it.rows)
+              part[(c + i) * kI8PartLd + half * 128 + row] = __uint_as_float(v[i]);
+        }
+        tc_fence_before();
+      } else if constexpr (SWIGLU) {
+        // all channels of one half of the tokens: gate and up of each
+        uint32_t g[2][32], u[2][32];
+        const int c0 = half * 64;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (c0 + 32 * i >= it.rows) break;
+          read32(c0 + 32 * i, g[i]);
+          read32(128 + c0 + 32 * i, u[i]);
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          reg_fence32(g[i]);
+          reg_fence32(u[i]);
+        }
+        tc_fence_before();
+        mbar_arrive_if(lane == 0, smem_u32(dempty));
+        const int I = p.N / 2, n = it.tile * 128 + row;
+        const float sg = n < I ? sw[n] : 0.0f, su = n < I ? sw[I + n] : 0.0f;
+        float* out = static_cast<float*>(p.out) + static_cast<int64_t>(it.row0) * p.ldo + n;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (c0 + 32 * i >= it.rows) break;
+          uint32_t mine = 0u;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int token = c0 + 32 * i + c;
+            const float s = scales[token];
+            const float h = swiglu(__uint_as_float(g[i][c]) * (s * sg),
+                                   __uint_as_float(u[i][c]) * (s * su), p.clamp);
+            const bool in = token < it.rows && n < I;
+            if (in) out[token * p.ldo] = h;
+            const uint32_t m =
+                __reduce_max_sync(0xFFFFFFFFu, in ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
+            if (lane == c) mine = m;
+          }
+          if (mine) atomicMax(&p.amax[it.row0 + c0 + 32 * i + lane], mine);
+        }
+        return true;
+      } else {
+        uint32_t v[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (32 * i < it.rows) read32(half * 128 + 32 * i, v[i]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reg_fence32(v[i]);
+        tc_fence_before();
+        mbar_arrive_if(lane == 0, smem_u32(dempty));
+        const int n = it.tile * kI8Tile + half * 128 + row;
+        const float s = n < p.N ? sw[n] : 0.0f;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(it.row0) * p.ldo;
+        const bool odd = lane & 1;
+        // Two tokens at a time: a lane packs its channel's values of both, an
+        // even lane takes the first token's pair of channels from it and its
+        // neighbour, the odd one the second's.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (32 * i >= it.rows) break;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const int token = 32 * i + c;
+            const __nv_bfloat162 b =
+                __floats2bfloat162_rn(__uint_as_float(v[i][c]) * (scales[token] * s),
+                                      __uint_as_float(v[i][c + 1]) * (scales[token + 1] * s));
+            const uint32_t w = reinterpret_cast<const uint32_t&>(b);
+            if (p.out_pairs) {
+              const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+              const uint32_t r = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+              const int t = token + (odd ? 1 : 0), m = n & ~1;
+              uint16_t* d = out + t * p.ldo + m;
+              if (t < it.rows) {
+                if (m + 1 < p.N)
+                  *reinterpret_cast<uint32_t*>(d) = r;
+                else if (m < p.N)
+                  *d = static_cast<uint16_t>(r);
+              }
+            } else if (n < p.N) {
+              if (token < it.rows) out[token * p.ldo + n] = static_cast<uint16_t>(w);
+              if (token + 1 < it.rows)
+                out[(token + 1) * p.ldo + n] = static_cast<uint16_t>(w >> 16);
+            }
+          }
+        }
+      }
+      return true;
+    };
+
+    I8Item before{};
+    bool pending = false;
+    for (int item = first; ok && item < total; item += step) {
+      const I8Item it = map_item(item);
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
+        if (pending && kb == kb0 + kI8Buffers) {
+          ok = results(before);
+          pending = false;
+          if (!ok) break;
+        }
+        ok = widen();
+      }
+      if (ok && pending) ok = results(before);
+      before = it;
+      pending = true;
+    }
+    if (ok && pending) ok = results(before);
+    if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
+  }
+
+  if constexpr (SPLIT) {
+    // Join: the ranks' partial sums in rank order, rank r taking every split-th
+    // token.
+    __syncwarp();
+    cluster_sync();
+    if (first < total && warp >= kI8WideWarp0) {
+      const I8Item it = map_item(first);
+      const float* sw = p.w_scales + static_cast<int64_t>(it.e) * p.N;
+      const int c = (warp - kI8WideWarp0) * 32 + lane;
+      const float* part = reinterpret_cast<const float*>(smem);
+      pdl_wait();
+      if constexpr (SWIGLU) {
+        // 128 channels: the warps take two tokens at a time
+        const int I = p.N / 2, ch = c & 127, n = it.tile * 128 + ch;
+        const float sg = n < I ? sw[n] : 0.0f, su = n < I ? sw[I + n] : 0.0f;
+        for (int t = 2 * rank + (c >> 7); t < it.rows; t += 2 * p.split) {
+          float g = 0.0f, u = 0.0f;
+          for (int k = 0; k < p.split; ++k) {
+            g += ld_cluster_f32(smem_u32(part + t * kI8PartLd + ch), k);
+            u += ld_cluster_f32(smem_u32(part + t * kI8PartLd + 128 + ch), k);
+          }
+          const float s = p.a_scales[it.row0 + t];
+          const float h = swiglu(g * (s * sg), u * (s * su), p.clamp);
+          if (n < I) static_cast<float*>(p.out)[(it.row0 + t) * p.ldo + n] = h;
+          const uint32_t m =
+              __reduce_max_sync(0xFFFFFFFFu, n < I ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
+          if (lane == 0 && m) atomicMax(&p.amax[it.row0 + t], m);
+        }
+      } else {
+        const int n = it.tile * kI8Tile + c;
+        const float s = n < p.N ? sw[n] : 0.0f;
+        for (int t = rank; t < it.rows; t += p.split) {
+          float sum = 0.0f;
+          for (int k = 0; k < p.split; ++k)
+            sum += ld_cluster_f32(smem_u32(part + t * kI8PartLd + c), k);
+          if (n < p.N)
+            static_cast<__nv_bfloat16*>(p.out)[(it.row0 + t) * p.ldo + n] =
+                __float2bfloat16_rn(sum * (p.a_scales[it.row0 + t] * s));
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the other ranks' shared memory stays until it has been read
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- host
+int extra_smem(int E) {
+  return kI8WideWarps * 128 * 4 + (2 * kI8MaxStages + 2 * kI8Buffers + 2) * 8 + 8 +
+         (3 * E + 1) * 4;
+}
+
+template <bool SWIGLU, bool SPLIT>
+cudaError_t launch_i8(const Int8Maps& maps, Int8Args p, int grid, cudaStream_t s) {
+  auto k = int8_gemm_kernel<SWIGLU, SPLIT>;
+  static OncePerDevice prepared;
+  const cudaError_t ready = prepared([&] {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8SmemLimit);
+  });
+  if (ready != cudaSuccess) return ready;
+  const int stage = kI8WBytes + p.a_rows * 256, fixed = 1024 + extra_smem(p.E);
+  // (three stages of 64 KB to six of 36: one CTA to an SM, so no CTA waits for
+  // TMEM that another holds)
+  p.stages = std::min(kI8MaxStages, (kI8SmemLimit - fixed) / stage);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  if (SPLIT) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = p.split;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  return cudaLaunchKernelEx(&cfg, k, maps, p);
+}
+
+}  // namespace
+
+// See internal.h.  Fewer items than half the SMs: the reduction is split over
+// clusters of as many CTAs (up to eight) as still run all at once.  Several
+// experts only with a token's rows or two in all, so that with more a row's sums
+// keep their order whatever the other experts' number.
+cudaError_t launch_int8(const Int8Maps& maps, Int8Args p, bool swiglu, const BlockscaleDevice& d,
+                        cudaStream_t s) {
+  const int64_t chunks = p.E == 1 ? (p.M + 127) / 128 : std::min<int64_t>(p.E, p.M) + p.M / 128;
+  const int kb = (p.K + 127) / 128;
+  p.tiles = swiglu ? (p.N / 2 + 127) / 128 : (p.N + kI8Tile - 1) / kI8Tile;
+  p.a_rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  p.chunk_group = 8;
+  const int64_t items = chunks * p.tiles;
+  if (items > INT32_MAX) return cudaErrorInvalidValue;
+  p.split = 1;
+  if (p.E == 1 || p.M <= 16)
+    for (int n = 2; n <= std::min(kBsMaxSplit, kb); ++n)
+      if (items <= d.clusters[n] && (kb + n - 1) / n < (kb + p.split - 1) / p.split) p.split = n;
+  if (p.split > 1) {
+    const int grid = static_cast<int>(items) * p.split;
+    return swiglu ? launch_i8<true, true>(maps, p, grid, s) : launch_i8<false, true>(maps, p, grid, s);
+  }
+  const int grid = static_cast<int>(std::min<int64_t>(d.sms, items));
+  return swiglu ? launch_i8<true, false>(maps, p, grid, s) : launch_i8<false, false>(maps, p, grid, s);
+}
+
+cudaError_t int8_status(int* code) {
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_int8_status, sizeof(int));
+  if (e == cudaSuccess && *code) e = cudaMemcpyToSymbol(g_int8_status, &zero, sizeof(int));
+  return e;
+}
+
+}  // namespace moe

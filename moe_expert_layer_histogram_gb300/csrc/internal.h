@@ -266,6 +266,31 @@ cudaError_t launch_blockscale(const BlockscaleMaps& maps, BlockscaleArgs args, b
 // last call (0: none).
 cudaError_t blockscale_status(int* code);
 
+// 8-bit integer products (int8_gemm.cu).
+struct Int8Maps {
+  CUtensorMap x[4];  // f16 codes [M, K], boxes of 16/32/64/128 rows x 64 columns
+  CUtensorMap w;     // int8 codes [E, N, K], boxes of 128 x 128
+};
+
+struct Int8Args {
+  const float* a_scales;   // [M]
+  const float* w_scales;   // [E, N]
+  const int32_t* offsets;  // [E+1] or null (one expert of all M rows)
+  int E, M, N, K;
+  void* out;               // bf16 [M, ldo], or (SwiGLU) h in f32 [M, ldo]
+  int64_t ldo;
+  int out_pairs;           // bf16 rows start on 4-byte boundaries
+  float clamp;             // SwiGLU (+inf: none)
+  uint32_t* amax;          // SwiGLU [M]: bits of each row's largest |h| (zero before)
+  // set by launch_int8
+  int a_rows, tiles, stages, split, chunk_group;
+};
+// swiglu: N = 2 I, gate and up rows.  The kernel before it on the stream is the
+// library's own and lets it start early.
+cudaError_t launch_int8(const Int8Maps& maps, Int8Args args, bool swiglu,
+                        const BlockscaleDevice& d, cudaStream_t s);
+cudaError_t int8_status(int* code);
+
 // Routing, permutation + activation quantisation, combine.
 cudaError_t launch_route(const float* logits, int T, int E, int K, int32_t* ids, float* w,
                          int32_t* blockhist, cudaStream_t s);

@@ -1,0 +1,157 @@
+"""Products of 8-bit integers with a scale per token and a scale per output
+channel, on torch tensors.
+
+Weights are int8 codes [N, K] (or [E, N, K]) with fp32 scales [N] ([E, N]);
+activations come in bf16 and are quantised per token on the way in, or as int8
+codes with one fp32 scale per row (int8_quantize, or block_join's).  Thin wrappers
+of the ``moe_int8_*`` calls (``include/moe.h`` states the formulas); work goes on
+torch's current stream, and the workspaces live in torch's allocator for the
+length of the call.
+"""
+import torch
+
+from . import MoEError, lib
+from ._tensors import check, fits, row_stride, stream_on
+
+_F32, _BF16, _I8, _I32 = torch.float32, torch.bfloat16, torch.int8, torch.int32
+
+
+def _weights(w, w_scales):
+    """(E, N, K, row stride) of [N, K] or [E, N, K] weights; checks the scales."""
+    if w.dtype is not _I8 or not w.is_cuda:
+        raise ValueError("w: CUDA int8 codes")
+    shape, strides = w.shape, w.stride()
+    if len(shape) == 2:
+        E, (N, K), (ldw, one) = 1, shape, strides
+        scales = (N,)
+    elif len(shape) == 3:
+        (E, N, K), (ld_e, ldw, one) = shape, strides
+        scales = (E, N)
+        if E > 1:
+            if N == 1:  # (the stride of a single row says nothing)
+                ldw = ld_e
+            if ld_e != N * ldw or ldw < K:
+                raise ValueError("w: experts at a stride of N rows of at least K codes")
+    else:
+        raise ValueError("w: [N, K] or [E, N, K]")
+    if one != 1 and K > 1:
+        raise ValueError("w: contiguous rows")
+    fits(max(E, N, K), "w")
+    if N == 1 and ldw < K:  # (one expert)
+        ldw = K
+    check(w_scales, _F32, scales, w.device, "w_scales")
+    return E, N, K, ldw
+
+
+def _result(out, M, N, device):
+    """(bf16 [M, N], its row stride): the caller's or a new one."""
+    if out is None:
+        return torch.empty(M, N, dtype=_BF16, device=device), N
+    ldo = row_stride(out, _BF16, "out")
+    if out.shape != (M, N) or out.device != device:
+        raise ValueError("out: [%d, %d] on %s" % (M, N, device))
+    return out, ldo
+
+
+def int8_quantize(x, slots=None, top_k=1):
+    """bf16 rows -> (codes int8 [R, C], scales f32 [R]).  With int32 `slots` [R],
+    row r is x's row slots[r] // top_k (zero where that is outside x).  The codes'
+    rows are 16-byte aligned."""
+    ldx = row_stride(x, _BF16, "x")
+    (T, C), dev = x.shape, x.device
+    stream = stream_on(dev)
+    R = T
+    fits(top_k, "top_k")
+    if slots is not None:
+        R = slots.numel()
+        check(slots, _I32, (R,), dev, "slots")
+    ld = (C + 15) // 16 * 16
+    codes = torch.empty(R, ld, dtype=_I8, device=dev)
+    scales = torch.empty(R, dtype=_F32, device=dev)
+    code = lib().moe_int8_quantize(x.data_ptr(), ldx, T, None if slots is None else slots.data_ptr(),
+                                   top_k, R, C, codes.data_ptr(), ld, scales.data_ptr(), stream)
+    if code:
+        raise MoEError(code, "moe_int8_quantize")
+    return (codes if ld == C else codes[:, :C]), scales
+
+
+def int8_matmul(codes, scales, w, w_scales, offsets=None, out=None):
+    """Codes int8 [M, K] with scales f32 [M] times w^T -> bf16 [M, N].  offsets
+    int32 [E+1]: the rows of each expert of w [E, N, K]; rows of no expert are
+    left as they are."""
+    lda = row_stride(codes, _I8, "codes")
+    E, N, K, ldw = _weights(w, w_scales)
+    M, dev = codes.shape[0], w.device
+    stream = stream_on(dev)
+    if codes.shape[1] != K or codes.device != dev:
+        raise ValueError("codes: [M, %d] on %s" % (K, dev))
+    check(scales, _F32, (M,), dev, "scales")
+    if offsets is not None:
+        check(offsets, _I32, (E + 1,), dev, "offsets")
+    elif E != 1:
+        raise ValueError("offsets: wanted for weights of several experts")
+    out, ldo = _result(out, M, N, dev)
+    L = lib()
+    nbytes = L.moe_int8_matmul_workspace(M, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    code = L.moe_int8_matmul(codes.data_ptr(), lda, scales.data_ptr(), w.data_ptr(), ldw,
+                             w_scales.data_ptr(), None if offsets is None else offsets.data_ptr(), E,
+                             M, N, K, out.data_ptr(), ldo, ws.data_ptr(), nbytes, stream)
+    if code:
+        raise MoEError(code, "moe_int8_matmul")
+    return out
+
+
+def int8_linear(x, w, w_scales, out=None):
+    """y = x w^T for bf16 x [M, K] and weights [N, K] -> bf16 [M, N]."""
+    ldx = row_stride(x, _BF16, "x")
+    if w.dim() != 2:
+        raise ValueError("w: one weight matrix")
+    _, N, K, ldw = _weights(w, w_scales)
+    M, dev = x.shape[0], w.device
+    stream = stream_on(dev)
+    if x.shape[1] != K or x.device != dev:
+        raise ValueError("x: [M, %d] on %s" % (K, dev))
+    out, ldo = _result(out, M, N, dev)
+    L = lib()
+    nbytes = L.moe_int8_linear_workspace(M, N, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    code = L.moe_int8_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, w_scales.data_ptr(), M, N, K,
+                             out.data_ptr(), ldo, ws.data_ptr(), nbytes, stream)
+    if code:
+        raise MoEError(code, "moe_int8_linear")
+    return out
+
+
+def int8_experts(x, slots, offsets, top_k, w13, w13_scales, w2, w2_scales, clamp=0.0, out=None):
+    """The experts' products on routed rows: row r of the result is expert e's MLP
+    of x's row slots[r] // top_k, for offsets[e] <= r < offsets[e+1] (router_order
+    gives slots and offsets).  w13 [E, 2I, H] (gate rows, then up rows), w2
+    [E, H, I], contiguous -> bf16 [len(slots), H], in that order; rows of no
+    expert are left as they are."""
+    ldx = row_stride(x, _BF16, "x")
+    E, I2, H, _ = _weights(w13, w13_scales)
+    I = I2 // 2
+    _weights(w2, w2_scales)
+    if (w13.dim() != 3 or w2.shape != (E, H, I) or I2 % 32 or not w13.is_contiguous()
+            or not w2.is_contiguous()):
+        raise ValueError("contiguous w13 [E, 2I, H] and w2 [E, H, I] with I a multiple of 16")
+    T, dev = x.shape[0], w13.device
+    stream = stream_on(dev)
+    if x.shape[1] != H or x.device != dev or w2.device != dev:
+        raise ValueError("x: [T, %d], all on %s" % (H, dev))
+    R = slots.numel()
+    fits(top_k, "top_k")
+    check(slots, _I32, (R,), dev, "slots")
+    check(offsets, _I32, (E + 1,), dev, "offsets")
+    out, ldo = _result(out, R, H, dev)
+    L = lib()
+    nbytes = L.moe_int8_experts_workspace(R, H, I)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    code = L.moe_int8_experts(
+        x.data_ptr(), ldx, T, slots.data_ptr(), top_k, R, offsets.data_ptr(), E, w13.data_ptr(),
+        w13_scales.data_ptr(), w2.data_ptr(), w2_scales.data_ptr(), H, I, clamp, out.data_ptr(),
+        ldo, ws.data_ptr(), nbytes, stream)
+    if code:
+        raise MoEError(code, "moe_int8_experts")
+    return out

@@ -1,0 +1,349 @@
+"""8-bit integer products with a scale per token and per output channel: codes
+against the format's definition, products and the experts' MLPs against plain
+implementations in 64 bits.
+
+Tolerances.  u = 2^-24.  Products of codes are exact and a sum of K of them is off
+by at most K u of the sum of their magnitudes; the two scales add 2 u, the store
+2^-8 of the result.  h = silu(gate) up is off by 3 times the gate's and up's
+errors and 8 u; its codes may each differ by one step where the quotient lies
+within that of a half, so an expert's output is off by at most the steps of the
+codes that lie so near (none, a few or, for the test, those that a 64-bit
+quotient puts within 1e-4 of a half).
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF16 = 2.0 ** -8
+
+
+@pytest.fixture(autouse=True)
+def no_wait_gave_up():
+    yield
+    from moe_expert_layer_histogram_gb300 import moe_int8_status
+    assert moe_int8_status() == 0
+
+
+def randn(*shape, seed=0, dtype=torch.bfloat16, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def codes_of(*shape, seed=0, low=-127):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(low, 128, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+def scales_of(*shape, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 100)
+    return torch.rand(*shape, generator=g, device="cuda") * 0.01 + 1e-4
+
+
+def quantized(x):
+    """Codes and scales of rows, by the definition (IEEE quotients in fp32)."""
+    v = x.float()
+    amax = v.abs().amax(1)
+    s = torch.where(torch.isfinite(amax), amax / torch.full_like(amax, 127.0), float("nan"))
+    q = v / torch.where(s > 0, s, 1.0)[:, None]
+    q = torch.where((s > 0)[:, None], torch.round(q).clamp(-127, 127), 0.0)
+    return q, s
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (5, 8), (2, 255), (70, 2001), (33, 7168),
+                                       (4, 8192), (3, 8200), (2, 30001)])
+def test_quantize(rows, cols):
+    from moe_expert_layer_histogram_gb300 import int8_quantize
+    x = randn(rows, cols, seed=cols)
+    codes, s = int8_quantize(x)
+    want, ws = quantized(x)
+    assert torch.equal(s, ws) and torch.equal(codes.float(), want)
+    assert codes.stride(0) % 16 == 0 or rows == 1
+
+
+def test_quantize_every_half():
+    # quotients that lie on halves and next to them: all pairs of significands
+    from moe_expert_layer_histogram_gb300 import int8_quantize
+    sig = torch.arange(128, 256, device="cuda", dtype=torch.float32)
+    x = torch.cat([sig[:, None], sig[None].repeat(128, 1) / 2, -sig[None].repeat(128, 1) / 4,
+                   sig[None].repeat(128, 1) / 64], 1).bfloat16()
+    for scale in (1.0, 2.0 ** -100, 2.0 ** 100):
+        codes, s = int8_quantize((x.float() * scale).bfloat16())
+        want, ws = quantized((x.float() * scale).bfloat16())
+        assert torch.equal(s, ws) and torch.equal(codes.float(), want)
+
+
+def test_quantize_special_rows():
+    from moe_expert_layer_histogram_gb300 import int8_quantize
+    x = randn(6, 300)
+    x[1] = 0
+    x[2, 7] = float("inf")
+    x[3, 9] = float("nan")
+    x[4] = 2.0 ** -133                      # the smallest bf16 numbers
+    codes, s = int8_quantize(x)
+    want, ws = quantized(x)
+    assert float(s[1]) == 0 and bool(torch.isnan(s[2:4]).all())
+    assert bool((codes[1:4] == 0).all())
+    keep = [0, 4, 5]
+    assert torch.equal(s[keep], ws[keep]) and torch.equal(codes[keep].float(), want[keep])
+
+
+def test_quantize_by_slots_and_strides():
+    from moe_expert_layer_histogram_gb300 import int8_quantize
+    big = randn(20, 100)
+    slots = torch.tensor([3, 0, 59, 7, 60, -1, 2 ** 31 - 1, 31], dtype=torch.int32, device="cuda")
+    for x in (big[:, :96], big[:, 1:98], big[:, 4:68]):
+        codes, s = int8_quantize(x, slots, 3)
+        for r, slot in enumerate(slots.tolist()):
+            if 0 <= slot < 60:
+                want, ws = quantized(x[slot // 3:slot // 3 + 1])
+                assert torch.equal(codes[r].float(), want[0]) and float(s[r]) == float(ws[0])
+            else:
+                assert bool((codes[r] == 0).all()) and float(s[r]) == 0
+
+
+def matmul_reference(a, s, w, ws, offsets=None):
+    """(result, the magnitudes of its terms) in 64 bits."""
+    if offsets is None:
+        scale = s.double()[:, None] * ws.double()
+        return (a.double() @ w.double().t()) * scale, (a.double().abs() @ w.double().abs().t()) * scale
+    M, N = a.shape[0], w.shape[1]
+    out = torch.full((M, N), float("nan"), dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(out)
+    last = 0
+    for e in range(w.shape[0]):
+        r0 = min(max(offsets[e], last, 0), M)
+        last = max(last, offsets[e])
+        r1 = min(max(offsets[e + 1], r0), M)
+        if r1 > r0:
+            out[r0:r1], mag[r0:r1] = matmul_reference(a[r0:r1], s[r0:r1], w[e], ws[e])
+    return out, mag
+
+
+def close(got, want, mag, K):
+    tol = (K + 4) * U * mag
+    tol = tol + BF16 * (want.abs() + tol)
+    err = (got.double() - want).abs()
+    assert bool((err <= tol + 1e-30).all()), float((err - tol).max())
+
+
+SHAPES = [(1, 1, 16), (1, 4096, 7168), (2, 256, 128), (3, 300, 48), (16, 257, 130), (17, 1001, 2000),
+          (33, 512, 1024), (64, 640, 4096), (65, 255, 144), (128, 256, 512), (129, 1000, 272),
+          (333, 1001, 2000), (500, 3000, 64), (1300, 2100, 1040), (2048, 4096, 256), (40, 20000, 32)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_matmul(M, N, K):
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    ld = (K + 15) // 16 * 16
+    a, w = codes_of(M, K, seed=1), codes_of(N, ld, seed=2)[:, :K]
+    s, ws = scales_of(M), scales_of(N, seed=1)
+    out = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = int8_matmul(a, s, w, ws, out=out[1:M + 1])
+    assert torch.equal(out[0], out[-1]) and bool((out[0] == 7).all())
+    close(got, *matmul_reference(a, s, w, ws), K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1008), (100, 300, 1008), (400, 300, 1008)])
+def test_sums_that_fp32_holds_are_exact(M, N, K):
+    # scales 1 and at most 1008 products of up to 127 x 128: whole numbers below 2^24,
+    # so the result is the exact sum rounded to bf16
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    a, w = codes_of(M, K, seed=3), codes_of(N, K, seed=4, low=-128)
+    got = int8_matmul(a, torch.ones(M, device="cuda"), w, torch.ones(N, device="cuda"))
+    want = a.double() @ w.double().t()
+    assert torch.equal(got, want.float().bfloat16())
+
+
+@pytest.mark.parametrize("offset,ldo", [(0, 301), (1, 302), (2, 304), (0, 320)])
+def test_results_of_any_alignment(offset, ldo):
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    for M in (5, 200, 700):
+        N, K = 301, 256
+        a, w = codes_of(M, K, seed=5), codes_of(N, K, seed=6)
+        s, ws = scales_of(M), scales_of(N, seed=1)
+        flat = torch.full((M * ldo + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = torch.as_strided(flat, (M, N), (ldo, 1), offset)
+        keep = torch.ones_like(flat, dtype=torch.bool)
+        torch.as_strided(keep, (M, N), (ldo, 1), offset).fill_(False)
+        int8_matmul(a, s, w, ws, out=out)
+        close(out, *matmul_reference(a, s, w, ws), K)
+        assert bool((flat[keep] == 7).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 7168), (7, 100, 130), (333, 1001, 2000), (1000, 512, 512)])
+@pytest.mark.parametrize("lead", [0, 1])
+def test_linear(M, N, K, lead):
+    from moe_expert_layer_histogram_gb300 import int8_linear, int8_matmul, int8_quantize
+    ld = (K + 15) // 16 * 16
+    x, w, ws = randn(M, K + lead)[:, lead:], codes_of(N, ld, seed=2)[:, :K], scales_of(N)
+    got = int8_linear(x, w, ws)
+    q, s = quantized(x)
+    close(got, *matmul_reference(q, s, w, ws), K)
+    assert torch.equal(got, int8_matmul(*int8_quantize(x), w, ws))
+
+
+GROUPS = [
+    ([0, 5, 5, 130, 131, 400, 400, 433, 433], 433),
+    ([0, 1, 1, 2, 2, 3, 3, 3, 3], 3),                 # a token: split
+    ([0, 0, 0, 0, 0, 0, 0, 0, 0], 6),                 # rows of no expert only
+    ([10, 20, 300, 300, 300, 310, 310, 320, 325], 330),
+    ([-5, 20, 15, 60, 2 ** 31 - 1, 7, 80, 90, 100], 64),   # not a table: clamped
+    ([0, 1200, 1200, 2500, 2500, 2500, 2600, 2601, 2700], 2700),
+]
+
+
+@pytest.mark.parametrize("offsets,M", GROUPS)
+@pytest.mark.parametrize("N,K", [(256, 512), (333, 144)])
+def test_experts_rows(offsets, M, N, K):
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    E = len(offsets) - 1
+    a, w = codes_of(M, K, seed=7), codes_of(E, N, K, seed=8)
+    s, ws = scales_of(M), scales_of(E, N, seed=1)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    int8_matmul(a, s, w, ws, offsets=off, out=out)
+    want, mag = matmul_reference(a, s, w, ws, offsets)
+    mine = ~torch.isnan(want[:, 0])
+    close(out[mine], want[mine], mag[mine], K)
+    assert bool((out[~mine] == 7).all())
+
+
+def route(T, E, k, seed=0, masked=0.0):
+    from moe_expert_layer_histogram_gb300 import router_gate, router_order
+    mask = None
+    if masked:
+        mask = torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(seed + 9),
+                          device="cuda") >= masked
+    r = router_gate(randn(T, E, seed=seed, dtype=torch.float32), k, mask=mask)
+    return r, router_order(r.ids, E)
+
+
+@pytest.mark.parametrize("T,E,k,H,I,clamp,masked", [
+    (1, 8, 2, 256, 128, 0.0, 0.0), (2, 64, 6, 2048, 1024, 7.0, 0.0), (40, 16, 3, 272, 144, 0.0, 0.2),
+    (64, 64, 8, 1024, 512, 0.0, 0.0), (700, 8, 2, 512, 256, 0.5, 0.1), (300, 4, 4, 144, 16, 0.0, 0.0),
+    (1500, 8, 4, 256, 400, 7.0, 0.0)])
+def test_experts(T, E, k, H, I, clamp, masked):
+    from moe_expert_layer_histogram_gb300 import int8_experts
+    x = randn(T, H)
+    w13, w2 = codes_of(E, 2 * I, H, seed=1), codes_of(E, H, I, seed=2)
+    s13, s2 = scales_of(E, 2 * I) * 0.02, scales_of(E, H, seed=1)
+    _, o = route(T, E, k, masked=masked)
+    out = torch.full((T * k, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    int8_experts(x, o.slots, o.offsets, k, w13, s13, w2, s2, clamp=clamp, out=out)
+    q, s = quantized(x)
+    off = o.offsets.tolist()
+    rows = o.slots.long() // k
+    for e in range(E):
+        r = rows[off[e]:off[e + 1]]
+        if not len(r):
+            continue
+        gu, _ = matmul_reference(q[r], s[r], w13[e], s13[e])
+        gate, up = gu[:, :I], gu[:, I:]
+        if clamp:
+            gate, up = gate.clamp(-clamp, clamp), up.clamp(-clamp, clamp)
+        h = gate * torch.sigmoid(gate) * up
+        sh = h.abs().amax(1) / 127
+        quot = h / torch.where(sh > 0, sh, 1.0)[:, None]
+        c = torch.round(quot).clamp(-127, 127)
+        near = ((quot - torch.floor(quot)) - 0.5).abs() < 1e-4
+        want, mag = matmul_reference(c, sh, w2[e], s2[e])
+        # (a scale that is off by 1e-5 of itself, and the codes next to a half)
+        step = (near.double() @ w2[e].double().abs().t()) * sh[:, None] * s2[e].double()
+        got = out[off[e]:off[e + 1]].double()
+        tol = step + 1e-5 * mag + (I + 4) * U * mag
+        tol = tol + BF16 * (want.abs() + tol)
+        err = (got - want).abs()
+        assert bool((err <= tol + 1e-30).all()), float((err - tol).max())
+    assert bool((out[off[E]:] == 7).all())
+
+
+def test_rows_with_nan_keep_to_themselves():
+    from moe_expert_layer_histogram_gb300 import int8_experts, int8_linear
+    x = randn(200, 256)
+    w, ws = codes_of(300, 256), scales_of(300)
+    good = int8_linear(x, w, ws)
+    bad = x.clone()
+    bad[3, 5], bad[150, 0] = float("nan"), float("inf")
+    got = int8_linear(bad, w, ws)
+    other = [t for t in range(200) if t not in (3, 150)]
+    assert bool(torch.isnan(got[[3, 150]]).all()) and torch.equal(got[other], good[other])
+    w13, w2 = codes_of(2, 256, 256, seed=1), codes_of(2, 256, 128, seed=2)
+    s13, s2 = scales_of(2, 256) * 0.02, scales_of(2, 256)
+    slots = torch.arange(200, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 120, 200], dtype=torch.int32, device="cuda")
+    a = int8_experts(x, slots, off, 1, w13, s13, w2, s2)
+    b = int8_experts(bad, slots, off, 1, w13, s13, w2, s2)
+    assert bool(torch.isnan(b[[3, 150]]).all()) and torch.equal(a[other], b[other])
+
+
+def test_same_bits_every_time_on_streams_and_in_graphs():
+    from moe_expert_layer_histogram_gb300 import int8_experts, int8_linear
+    x = randn(300, 512)
+    w, ws = codes_of(1000, 512), scales_of(1000)
+    w13, w2 = codes_of(8, 512, 512, seed=1), codes_of(8, 512, 256, seed=2)
+    s13, s2 = scales_of(8, 512) * 0.02, scales_of(8, 512)
+    _, o = route(300, 8, 2)
+
+    def once():
+        return (int8_linear(x, w, ws), int8_linear(x[:4], w, ws),
+                int8_experts(x, o.slots, o.offsets, 2, w13, s13, w2, s2))
+    want = once()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(once())
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g in got for p, q in zip(g, want))
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = once()
+        graphs.append((g, held))
+    for _ in range(3):
+        for g, _ in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for _, held in graphs for p, q in zip(held, want))
+
+
+def test_no_rows():
+    from moe_expert_layer_histogram_gb300 import int8_experts, int8_linear, int8_matmul, int8_quantize
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    w, ws = codes_of(32, 64), scales_of(32)
+    assert int8_linear(x, w, ws).shape == (0, 32)
+    assert int8_matmul(*int8_quantize(x), w, ws).shape == (0, 32)
+    slots = torch.empty(0, dtype=torch.int32, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = int8_experts(x, slots, off, 2, codes_of(2, 64, 64), scales_of(2, 64), codes_of(2, 64, 32),
+                       scales_of(2, 64))
+    assert out.shape == (0, 64)
+
+
+def test_refusals():
+    from moe_expert_layer_histogram_gb300 import (MoEError, int8_experts, int8_linear, int8_matmul,
+                                                  int8_quantize)
+    x, w, ws = randn(8, 64), codes_of(32, 64), scales_of(32)
+    with pytest.raises(MoEError):
+        int8_linear(x[:, :40].contiguous(), codes_of(32, 40), ws)     # (rows off 16 bytes)
+    for bad in (lambda: int8_linear(x, w, ws[:31]), lambda: int8_linear(x.float(), w, ws),
+                lambda: int8_linear(x[:, :48], w, ws), lambda: int8_linear(x, w.float(), ws),
+                lambda: int8_linear(x, codes_of(2, 32, 64), scales_of(2, 32)),
+                lambda: int8_matmul(x, ws, w, ws), lambda: int8_quantize(x.float()),
+                lambda: int8_matmul(codes_of(8, 64), scales_of(7), w, ws),
+                lambda: int8_matmul(codes_of(8, 64), scales_of(8), codes_of(2, 32, 64),
+                                    scales_of(2, 32)),
+                lambda: int8_linear(x, w, ws, out=torch.empty(8, 31, dtype=torch.bfloat16,
+                                                              device="cuda")),
+                lambda: int8_experts(x, torch.zeros(8, dtype=torch.int32, device="cuda"),
+                                     torch.zeros(3, dtype=torch.int32, device="cuda"), 1,
+                                     codes_of(2, 48, 64), scales_of(2, 48), codes_of(2, 64, 24),
+                                     scales_of(2, 64))):
+        with pytest.raises(ValueError):
+            bad()
