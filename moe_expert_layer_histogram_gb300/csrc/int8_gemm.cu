@@ -76,6 +76,25 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// mbar_wait by a whole warp, without a look at the timer before the wait has
+// lasted for many tries: reading it takes longer than most waits here.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  uint32_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 127u) == 127u) {
+      // (the low half of the timer: its differences are good for 4 s)
+      uint32_t now;
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+      if (i == 127u) t0 = now;
+      if (__any_sync(0xFFFFFFFFu, *abort != 0 || now - t0 > static_cast<uint32_t>(kWaitTimeoutNs))) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // Four codes in a word to two words of two f16 each.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   w ^= 0x80808080u;  // c + 128
@@ -247,11 +266,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       const I8Item it = map_item(item);
       const int box = box_of(it.rows), n = 16 << box;
       const uint32_t idesc = idesc_f16(128, n);
-      ok = mbar_wait_warp(dempty, dphase ^ 1, abort_flag);
+      ok = wait_warp(dempty, dphase ^ 1, abort_flag);
       dphase ^= 1;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
-        ok = mbar_wait_warp(&full[stage], phase, abort_flag) &&
-             mbar_wait_warp(&afull[buf], aphase, abort_flag);
+        ok = wait_warp(&full[stage], phase, abort_flag) &&
+             wait_warp(&afull[buf], aphase, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -292,13 +311,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     bool ok = true, waited = false;
 
     auto widen = [&]() {
-      if (!mbar_wait_warp(&full[stage], phase, abort_flag)) return false;
+      if (!wait_warp(&full[stage], phase, abort_flag)) return false;
       const uint8_t* src = smem + stage * stage_bytes + half * (kI8WBytes / 2) + row * 128;
       uint4 v[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         v[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
-      if (!mbar_wait_warp(&aempty[buf], aphase ^ 1, abort_flag)) return false;
+      if (!wait_warp(&aempty[buf], aphase ^ 1, abort_flag)) return false;
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -340,7 +359,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       float sr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) sr[i] = 32 * i + lane < it.rows ? sx[32 * i + lane] : 0.0f;
-      if (!mbar_wait_warp(dfull, dphase, abort_flag)) return false;
+      if (!wait_warp(dfull, dphase, abort_flag)) return false;
       dphase ^= 1;
       tc_fence_after();
 #pragma unroll
@@ -368,7 +387,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const int c0 = half * 64;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (c0 + 32 * i >= it.rows) break;
           read32(c0 + 32 * i, g[i]);
           read32(128 + c0 + 32 * i, u[i]);
         }
@@ -405,8 +423,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       } else {
         uint32_t v[4][32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (32 * i < it.rows) read32(half * 128 + 32 * i, v[i]);
+        for (int i = 0; i < 4; ++i) read32(half * 128 + 32 * i, v[i]);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 4; ++i) reg_fence32(v[i]);
@@ -451,23 +468,24 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       return true;
     };
 
+    // (one place in the code for each: copies of `results` cost registers)
     I8Item before{};
     bool pending = false;
-    for (int item = first; ok && item < total; item += step) {
-      const I8Item it = map_item(item);
-      for (int kb = kb0; ok && kb < kb1; ++kb) {
-        if (pending && kb == kb0 + kI8Buffers) {
+    for (int item = first; ok; item += step) {
+      const bool more = item < total;
+      const int blocks = more ? kb1 - kb0 : 0, ahead = min(kI8Buffers, blocks);
+      for (int kb = 0;; ++kb) {
+        if (pending && kb == ahead) {
           ok = results(before);
           pending = false;
-          if (!ok) break;
         }
+        if (!ok || kb == blocks) break;
         ok = widen();
       }
-      if (ok && pending) ok = results(before);
-      before = it;
+      if (!more) break;
+      before = map_item(item);
       pending = true;
     }
-    if (ok && pending) ok = results(before);
     if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
   }
 
