@@ -13,6 +13,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "int8_quant.cuh"
 #include "internal.h"
 #include "moe.h"
 #include "ptx.cuh"
@@ -25,53 +26,30 @@ namespace {
 // stride over a row, stays in 32 bits.
 constexpr int kMaxExtent = INT32_MAX - 65791;
 
-// Scale of a row from the bits of its largest magnitude, and its codes.
-__device__ __forceinline__ float scale_of(uint32_t amax) {
-  return amax >= 0x7F800000u ? NAN : __uint_as_float(amax) / 127.0f;
-}
-__device__ __forceinline__ int code_of(float v, float s) {
-  return s > 0.0f ? __float2int_rn(fminf(fmaxf(v / s, -127.0f), 127.0f)) : 0;
-}
-__device__ __forceinline__ uint32_t f16_bits(int code) {
-  // 1152 + code has the bits 0x6480 + code
-  uint32_t b = static_cast<uint32_t>(0x6480 + code);
-  asm("{\n\t.reg .b16 h, o;\n\tcvt.u16.u32 h, %0;\n\tmov.b16 o, 0x6480;\n\t"
-      "sub.f16 h, h, o;\n\tcvt.u32.u16 %0, h;\n\t}"
-      : "+r"(b));
-  return b;
-}
-
 // Eight codes to memory: bytes, or f16.
 template <bool F16>
 __device__ __forceinline__ void store_codes(void* row, int c0, int cols, bool vec,
-                                            const int (&q)[8]) {
+                                            const I8Coder& coder, const float (&v)[8]) {
   if constexpr (F16) {
     uint16_t* d = static_cast<uint16_t*>(row) + c0;
-    uint32_t h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = f16_bits(q[i]);
+    const uint4 w = coder.f16(v);
     if (vec && c0 + 8 <= cols) {
-      *reinterpret_cast<uint4*>(d) = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16,
-                                                h[4] | h[5] << 16, h[6] | h[7] << 16);
+      *reinterpret_cast<uint4*>(d) = w;
     } else {
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c0 + i < cols) d[i] = static_cast<uint16_t>(h[i]);
+        if (c0 + i < cols) d[i] = static_cast<uint16_t>(h[i >> 1] >> (16 * (i & 1)));
     }
   } else {
     int8_t* d = static_cast<int8_t*>(row) + c0;
+    const uint2 w = coder.bytes(v);
     if (vec && c0 + 8 <= cols) {
-      uint32_t lo = 0u, hi = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo |= static_cast<uint32_t>(q[i] & 255) << (8 * i);
-        hi |= static_cast<uint32_t>(q[i + 4] & 255) << (8 * i);
-      }
-      *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+      *reinterpret_cast<uint2*>(d) = w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c0 + i < cols) d[i] = static_cast<int8_t>(q[i]);
+        if (c0 + i < cols) d[i] = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
     }
   }
 }
@@ -132,7 +110,8 @@ __global__ void __launch_bounds__(256)
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
   for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) m = max(m, s_max[w]);
-  const float s = scale_of(m);
+  const float s = i8_scale(m);
+  const I8Coder coder(s);
   if (threadIdx.x == 0) {
     scales[r] = s;
     if (amax) amax[r] = 0u;
@@ -141,13 +120,13 @@ __global__ void __launch_bounds__(256)
                   : static_cast<void*>(static_cast<int8_t*>(codes) + r * ld_codes);
   auto put = [&](int c0, const uint32_t (&v)[4]) {
     if (c0 >= cols) return;
-    int q[8];
+    float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      q[2 * i] = code_of(__uint_as_float(v[i] << 16), s);
-      q[2 * i + 1] = code_of(__uint_as_float(v[i] & 0xFFFF0000u), s);
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
     }
-    store_codes<F16>(out, c0, cols, vec, q);
+    store_codes<F16>(out, c0, cols, vec, coder, f);
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) put(first + i * stride, kept[i]);
@@ -158,7 +137,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// int8 codes to f16 ones, eight at a time.
+// int8 codes to f16 ones, eight at a time; out: rows of a multiple of eight.
 __global__ void __launch_bounds__(256)
     int8_widen_kernel(const int8_t* codes, int64_t ld, int rows, int cols, uint16_t* out,
                       int64_t ld_out, int vec) {
@@ -170,19 +149,21 @@ __global__ void __launch_bounds__(256)
     const int64_t r = i / per;
     const int c0 = static_cast<int>(i - r * per) * 8;
     const int8_t* src = codes + r * ld + c0;
-    int q[8];
+    uint32_t q[2] = {0u, 0u};  // four codes each
     if (vec && c0 + 8 <= cols) {
       const uint2 w = *reinterpret_cast<const uint2*>(src);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        q[b] = static_cast<int8_t>(w.x >> (8 * b));
-        q[b + 4] = static_cast<int8_t>(w.y >> (8 * b));
-      }
+      q[0] = w.x, q[1] = w.y;
     } else {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) q[b] = c0 + b < cols ? src[b] : 0;
+      for (int b = 0; b < 8; ++b)
+        if (c0 + b < cols)
+          q[b >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[b])) << (8 * (b & 3));
     }
-    store_codes<true>(out + r * ld_out, c0, cols, true, q);
+    uint4 f;
+    i8_widen4(q[0], f.x, f.y);
+    i8_widen4(q[1], f.z, f.w);
+    // (rows of a multiple of eight codes: the last ones' padding is theirs)
+    *reinterpret_cast<uint4*>(out + r * ld_out + c0) = f;
   }
 }
 
@@ -198,20 +179,14 @@ __global__ void __launch_bounds__(256)
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t r = i / per;
     const int c0 = static_cast<int>(i - r * per) * 8;
-    const float s = scale_of(amax[r]);
+    const float s = i8_scale(amax[r]);
     if (c0 == 0) scales[r] = s;
     const float* src = h + r * cols + c0;
-    int q[8];
-    if (c0 + 8 <= cols && cols % 4 == 0) {
-      const float4 a = *reinterpret_cast<const float4*>(src),
-                   b = *reinterpret_cast<const float4*>(src + 4);
-      q[0] = code_of(a.x, s), q[1] = code_of(a.y, s), q[2] = code_of(a.z, s), q[3] = code_of(a.w, s);
-      q[4] = code_of(b.x, s), q[5] = code_of(b.y, s), q[6] = code_of(b.z, s), q[7] = code_of(b.w, s);
-    } else {
-#pragma unroll
-      for (int b = 0; b < 8; ++b) q[b] = c0 + b < cols ? code_of(src[b], s) : 0;
-    }
-    store_codes<true>(out + r * ld_out, c0, cols, true, q);
+    // (cols is a multiple of 16)
+    const float4 a = *reinterpret_cast<const float4*>(src),
+                 b = *reinterpret_cast<const float4*>(src + 4);
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    *reinterpret_cast<uint4*>(out + r * ld_out + c0) = I8Coder(s).f16(v);
   }
 }
 

@@ -38,6 +38,7 @@
 #include <algorithm>
 
 #include "expert_table.cuh"
+#include "int8_quant.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -93,15 +94,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
       }
     }
   }
-}
-
-// Four codes in a word to two words of two f16 each.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  w ^= 0x80808080u;  // c + 128
-  lo = __byte_perm(w, 0x64646464u, 0x4140);
-  hi = __byte_perm(w, 0x64646464u, 0x4342);
-  asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));  // 1152
-  asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
 
 __device__ __forceinline__ float clamp_to(float v, float limit) {
@@ -324,10 +316,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          widen4(v[4 * q + c].x, w[8 * c], w[8 * c + 1]);
-          widen4(v[4 * q + c].y, w[8 * c + 2], w[8 * c + 3]);
-          widen4(v[4 * q + c].z, w[8 * c + 4], w[8 * c + 5]);
-          widen4(v[4 * q + c].w, w[8 * c + 6], w[8 * c + 7]);
+          i8_widen4(v[4 * q + c].x, w[8 * c], w[8 * c + 1]);
+          i8_widen4(v[4 * q + c].y, w[8 * c + 2], w[8 * c + 3]);
+          i8_widen4(v[4 * q + c].z, w[8 * c + 4], w[8 * c + 5]);
+          i8_widen4(v[4 * q + c].w, w[8 * c + 6], w[8 * c + 7]);
         }
         tmem_st32(lanes + kI8Weights + buf * 128 + half * 64 + q * 32, w);
       }

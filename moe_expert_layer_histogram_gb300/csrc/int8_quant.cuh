@@ -1,0 +1,82 @@
+// int8_quant.cuh -- 8-bit codes of a row: s = amax / 127 and round(x / s) to even
+// within +-127, both quotients rounded to nearest in fp32.
+//
+// A division an element would cost more than the row's bytes take, so the codes
+// come from x r with r = 1 / s, rounded by the fused multiply-add that adds a
+// number of 1.5 2^23's size: its sum's last bits are the code.  x r is within 127
+// 2^-24 of the quotient (r's rounding; the product is not rounded), and the fp32
+// quotient within 2^-18 of it, together below 1.2e-5: only where x r is nearer than
+// that to a half may the code be another, and there, and for scales whose
+// reciprocal is not a number's (below 2^-100), the division is done.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+namespace moe {
+
+// Four codes in a word to two words of two f16 each: a code with 128 added under the
+// f16 1024's bits is 1152 + code.
+__device__ __forceinline__ void i8_widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  lo = __byte_perm(w, 0x64646464u, 0x4140);
+  hi = __byte_perm(w, 0x64646464u, 0x4342);
+  asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+  asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+}
+
+// The scale of a row from the bits of its largest magnitude (NaN where an infinity
+// or NaN is in the row: their bits are above those of every number).
+__device__ __forceinline__ float i8_scale(uint32_t amax) {
+  return amax >= 0x7F800000u ? NAN : __fdiv_rn(__uint_as_float(amax), 127.0f);
+}
+
+struct I8Coder {
+  // Low half of the sum's bits: 0x6480 + code, which as f16 is 1152 + code.
+  static constexpr float kMagic = 12582912.0f + 25728.0f;
+  float s, r;
+  __device__ explicit I8Coder(float scale) : s(scale), r(scale >= 0x1p-100f ? 1.0f / scale : 0.0f) {}
+
+  __device__ static uint32_t divided(float v, float s) {
+    const float q = s > 0.0f ? fminf(fmaxf(__fdiv_rn(v, s), -127.0f), 127.0f) : 0.0f;
+    return static_cast<uint32_t>(0x6480 + __float2int_rn(q));
+  }
+
+  // 0x6480 + code of eight values, two to a word.
+  __device__ __forceinline__ void biased(const float (&v)[8], uint32_t (&w)[4]) const {
+    float far = r > 0.0f ? 0.0f : 1.0f;
+    uint32_t t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float sum = fmaf(v[i], r, kMagic);
+      far = fmaxf(far, fabsf(fmaf(v[i], r, kMagic - sum)));
+      t[i] = __float_as_uint(sum);
+    }
+    if (far > 0.49998f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = divided(v[i], s);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __byte_perm(t[2 * i], t[2 * i + 1], 0x5410);
+  }
+
+  // The codes as f16.
+  __device__ __forceinline__ uint4 f16(const float (&v)[8]) const {
+    uint32_t w[4];
+    biased(v, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("sub.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(0x64806480u));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+
+  // The codes as bytes.
+  __device__ __forceinline__ uint2 bytes(const float (&v)[8]) const {
+    uint32_t w[4];
+    biased(v, w);
+    // (the low byte of 0x6480 + code is code + 128)
+    return make_uint2(__byte_perm(w[0], w[1], 0x6420) ^ 0x80808080u,
+                      __byte_perm(w[2], w[3], 0x6420) ^ 0x80808080u);
+  }
+};
+
+}  // namespace moe

@@ -29,6 +29,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "int8_quant.cuh"
 #include "internal.h"
 #include "moe.h"
 #include "ptx.cuh"
@@ -322,31 +323,22 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
     if (p.h) store8<VEC>(p.h + t * p.ld_h, i, H, v[i]);
   }
   if (!p.codes) return;
-  // s = amax / 127 (NaN where an infinity or NaN is in the row: the bits of both
-  // are above those of every number); codes round(h / s)
   amax = block_max(amax, s_max);
-  const float s = amax >= 0x7F800000u ? NAN : __uint_as_float(amax) / 127.0f;
+  const float s = i8_scale(amax);
   if (threadIdx.x == 0) p.code_scales[t] = s;
+  const I8Coder coder(s);
   int8_t* codes = p.codes + t * p.ld_codes;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    int q[kVec];
-#pragma unroll
-    for (int c = 0; c < kVec; ++c)
-      q[c] = s > 0.0f ? __float2int_rn(fminf(fmaxf(v[i][c] / s, -127.0f), 127.0f)) : 0;
+    const uint2 w = coder.bytes(v[i]);
     if constexpr (VEC) {
       const int c0 = column<VEC>(i, 0);
-      uint32_t lo = 0u, hi = 0u;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        lo |= static_cast<uint32_t>(q[c] & 255) << (8 * c);
-        hi |= static_cast<uint32_t>(q[c + 4] & 255) << (8 * c);
-      }
-      if (c0 < H) *reinterpret_cast<uint2*>(codes + c0) = make_uint2(lo, hi);
+      if (c0 < H) *reinterpret_cast<uint2*>(codes + c0) = w;
     } else {
 #pragma unroll
       for (int c = 0; c < kVec; ++c)
-        if (column<VEC>(i, c) < H) codes[column<VEC>(i, c)] = static_cast<int8_t>(q[c]);
+        if (column<VEC>(i, c) < H)
+          codes[column<VEC>(i, c)] = static_cast<int8_t>((c < 4 ? w.x : w.y) >> (8 * (c & 3)));
     }
   }
 }
