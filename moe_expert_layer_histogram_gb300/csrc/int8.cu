@@ -54,28 +54,33 @@ __device__ __forceinline__ void store_codes(void* row, int c0, int cols, bool ve
   }
 }
 
-// A block takes a row.  Its first kKept vectors of eight per thread stay in
-// registers between the maximum and the codes; what a longer row has beyond is
-// read again.  amax (or null): a word per row that is set to zero for a later
-// kernel.
+// `warps` warps of a block (a power of two) take a row, the block 8 / warps of
+// them.  A thread's first kKept vectors of eight stay in registers between the
+// maximum and the codes; what a longer row has beyond is read again.  amax (or
+// null): a word per row that is set to zero for a later kernel.  Bound by the
+// bytes where there are many rows (8192 x 7168: 37 us, 6.3 TB/s; with a block to
+// a row and one vector at a time 24576 x 2048 took 81 us, now 34).
 constexpr int kKept = 4;
 
 template <bool F16>
 __global__ void __launch_bounds__(256)
     int8_quantize_kernel(const __nv_bfloat16* x, int64_t ldx, int x_rows, const int32_t* slots,
-                         int top_k, int cols, void* codes, int64_t ld_codes, float* scales,
-                         uint32_t* amax, int vec) {
+                         int top_k, int rows, int cols, void* codes, int64_t ld_codes,
+                         float* scales, uint32_t* amax, int vec, int warps) {
   // (a product that follows may set itself up and load weights meanwhile)
   pdl_launch_dependents();
   __shared__ uint32_t s_max[8];
-  const int64_t r = blockIdx.x;
-  const int slot = slots ? slots[r] : 0;
+  const int warp = threadIdx.x >> 5, sub = warp & (warps - 1);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (8 / warps) + warp / warps;
+  const bool real = r < rows;
+  const int slot = real && slots ? slots[r] : 0;
   const int64_t src = slots ? slot / top_k : r;
-  const bool in = slot >= 0 && src < x_rows;
+  const bool in = real && slot >= 0 && src < x_rows;
   const __nv_bfloat16* row = x + (in ? src : 0) * ldx;
-  const int stride = blockDim.x * 8;
+  const int stride = warps * 256;  // columns of one vector of every thread of the row
+  const int first = (sub * 32 + (threadIdx.x & 31)) * 8, end = in ? cols : 0;
   auto load = [&](int c0, uint32_t (&v)[4]) {
-    if (!in || c0 >= cols) {
+    if (c0 >= end) {
       v[0] = v[1] = v[2] = v[3] = 0u;
     } else if (vec && c0 + 8 <= cols) {
       const uint4 q = *reinterpret_cast<const uint4*>(row + c0);
@@ -96,23 +101,25 @@ __global__ void __launch_bounds__(256)
     return m;
   };
   uint32_t kept[kKept][4], m = 0u;
-  const int first = threadIdx.x * 8;
 #pragma unroll
   for (int i = 0; i < kKept; ++i) load(first + i * stride, kept[i]);
 #pragma unroll
   for (int i = 0; i < kKept; ++i) m = largest(kept[i], m);
-  for (int c0 = first + kKept * stride; c0 < cols; c0 += stride) {
+  for (int c0 = first + kKept * stride; c0 < end; c0 += stride) {
     uint32_t v[4];
     load(c0, v);
     m = largest(v, m);
   }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
-  __syncthreads();
-  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) m = max(m, s_max[w]);
+  if (warps > 1) {
+    if ((threadIdx.x & 31) == 0) s_max[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < warps; ++w) m = max(m, s_max[warp - sub + w]);
+  }
+  if (!real) return;
   const float s = i8_scale(m);
   const I8Coder coder(s);
-  if (threadIdx.x == 0) {
+  if (first == 0) {
     scales[r] = s;
     if (amax) amax[r] = 0u;
   }
@@ -215,7 +222,7 @@ moe_status check_weights(const Product& p) {
     return MOE_ERR_INVALID_ARG;
   // strides of the tensor maps and the item count stay in range
   if (p.ldw >= (int64_t{1} << 39) / p.N ||
-      (static_cast<int64_t>(p.E) + p.M / 128 + 1) * ((p.N + 127) / 128) > INT32_MAX)
+      (static_cast<int64_t>(p.E) + p.M / 16 + 1) * ((p.N + 127) / 128) > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -253,7 +260,8 @@ moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const fl
   };
   Int8Maps maps;
   // (one expert: all chunks take the largest box)
-  const int boxes = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 3 : 4;
+  const int most = int8_chunk_rows(p.M, p.E);
+  const int boxes = most <= 16 ? 1 : most <= 32 ? 2 : most <= 64 ? 3 : 4;
   const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M)};
   const cuuint64_t xstr[1] = {static_cast<cuuint64_t>(ld) * 2};
   for (int i = p.E == 1 ? boxes - 1 : 0; i < boxes; ++i) {
@@ -285,12 +293,17 @@ moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* s
                         uint32_t* amax, cudaStream_t s) {
   const bool vec = aligned_to(x, 16) && ldx % 8 == 0 && aligned_to(codes, F16 ? 16 : 8) &&
                    ld_codes % 8 == 0;
-  const int threads =
-      static_cast<int>(std::min<int64_t>(256, padded((static_cast<int64_t>(cols) + 7) / 8, 32)));
+  // Warps of a row: as many as keep it in registers, and more where the rows alone
+  // would leave SMs without a block.
+  int warps = 1;
+  while (warps < 8 && (cols > warps * 256 * kKept ||
+                       (static_cast<int64_t>(rows) * warps < 152 * 8 && cols > warps * 256)))
+    warps *= 2;
+  const int64_t blocks = (static_cast<int64_t>(rows) * warps + 7) / 8;
   const cudaError_t e =
-      launch_pdl(false, int8_quantize_kernel<F16>, dim3(rows), dim3(threads), 0, s,
-                 static_cast<const __nv_bfloat16*>(x), ldx, x_rows, slots, top_k, cols, codes,
-                 ld_codes, scales, amax, static_cast<int>(vec));
+      launch_pdl(false, int8_quantize_kernel<F16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                 s, static_cast<const __nv_bfloat16*>(x), ldx, x_rows, slots, top_k, rows, cols,
+                 codes, ld_codes, scales, amax, static_cast<int>(vec), warps);
   return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

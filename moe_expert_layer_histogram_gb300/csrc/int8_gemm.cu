@@ -117,11 +117,11 @@ struct I8Item {
   int e, tile, row0, rows;
 };
 
-// Items of an expert: groups of up to `group` chunks, tile by tile within a group,
+// Items of an expert: groups of up to `group` chunks of `rows` rows, tile by tile within a group,
 // chunk by chunk within a tile, so that CTAs that run together share both weights
 // and tokens in L2.  e: the expert of this or an earlier item, moved up.
-__device__ __forceinline__ I8Item map_i8_item(const ExpertTable& t, int tiles, int group, int item,
-                                              int& e) {
+__device__ __forceinline__ I8Item map_i8_item(const ExpertTable& t, int tiles, int group, int rows,
+                                              int item, int& e) {
   while (t.chunk_off[e + 1] * tiles <= item) ++e;
   const int chunks = t.chunk_off[e + 1] - t.chunk_off[e];
   const int local = item - t.chunk_off[e] * tiles;
@@ -130,8 +130,8 @@ __device__ __forceinline__ I8Item map_i8_item(const ExpertTable& t, int tiles, i
   I8Item it;
   it.e = e;
   it.tile = in / size;
-  it.row0 = t.start[e] + (g * group + in - it.tile * size) * 128;
-  it.rows = min(128, t.end[e] - it.row0);
+  it.row0 = t.start[e] + (g * group + in - it.tile * size) * rows;
+  it.rows = min(rows, t.end[e] - it.row0);
   return it;
 }
 
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
-  if (warp == 2) fill_expert_table(p, tab, 128, lane);
+  if (warp == 2) fill_expert_table(p, tab, p.a_rows, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int total = tab.chunk_off[p.E] * p.tiles;
   int expert = 0;  // of the role's latest item
   auto map_item = [&](int item) {
-    return map_i8_item(tab, p.tiles, p.chunk_group, item, expert);
+    return map_i8_item(tab, p.tiles, p.chunk_group, p.a_rows, item, expert);
   };
   // (one expert: the box that all its chunks take, the last one short)
   auto box_of = [&](int rows) {
@@ -570,16 +570,27 @@ cudaError_t launch_i8(const Int8Maps& maps, Int8Args p, int grid, cudaStream_t s
 
 }  // namespace
 
-// See internal.h.  Fewer items than half the SMs: the reduction is split over
-// clusters of as many CTAs (up to eight) as still run all at once.  Several
-// experts only with a token's rows or two in all, so that with more a row's sums
-// keep their order whatever the other experts' number.
+int int8_chunk_rows(int M, int E) {
+  const int64_t most = E == 1 ? M : std::min<int64_t>(M, std::max<int64_t>(32, 2 * (static_cast<int64_t>(M) / E)));
+  return most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
+}
+
+// See internal.h.  Chunks: of all rows where there are few, else 128; with several
+// experts of few rows each on average, twice that average at least, since a lower
+// chunk leaves room for more stages of weights (64 experts, 512 rows, 7168 x 2048:
+// chunks of 128 rows and three stages 319 + 171 us, of 32 rows and five 294 + 151),
+// and an expert with more rows reads its weights again from L2.  Fewer items than
+// half the SMs: the reduction is split over clusters of as many CTAs (up to eight)
+// as still run all at once.  Several experts only with a token's rows or two in
+// all, so that with more a row's sums keep their order whatever the other experts'
+// number.
 cudaError_t launch_int8(const Int8Maps& maps, Int8Args p, bool swiglu, const BlockscaleDevice& d,
                         cudaStream_t s) {
-  const int64_t chunks = p.E == 1 ? (p.M + 127) / 128 : std::min<int64_t>(p.E, p.M) + p.M / 128;
+  p.a_rows = int8_chunk_rows(p.M, p.E);
   const int kb = (p.K + 127) / 128;
+  const int64_t chunks = p.E == 1 ? (p.M + p.a_rows - 1) / p.a_rows
+                                  : std::min<int64_t>(p.E, p.M) + p.M / p.a_rows;
   p.tiles = swiglu ? (p.N / 2 + 127) / 128 : (p.N + kI8Tile - 1) / kI8Tile;
-  p.a_rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   p.chunk_group = 8;
   const int64_t items = chunks * p.tiles;
   if (items > INT32_MAX) return cudaErrorInvalidValue;

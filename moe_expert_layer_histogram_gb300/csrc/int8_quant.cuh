@@ -1,13 +1,12 @@
 // int8_quant.cuh -- 8-bit codes of a row: s = amax / 127 and round(x / s) to even
 // within +-127, both quotients rounded to nearest in fp32.
 //
-// A division an element would cost more than the row's bytes take, so the codes
-// come from x r with r = 1 / s, rounded by the fused multiply-add that adds a
-// number of 1.5 2^23's size: its sum's last bits are the code.  x r is within 127
-// 2^-24 of the quotient (r's rounding; the product is not rounded), and the fp32
-// quotient within 2^-18 of it, together below 1.2e-5: only where x r is nearer than
-// that to a half may the code be another, and there, and for scales whose
-// reciprocal is not a number's (below 2^-100), the division is done.
+// With r = 1 / s rounded to nearest, q = x r, e = x - q s and q' = q + e r, each
+// rounded once, q' is the correctly rounded quotient x / s (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990): one reciprocal a row and three operations an element.  Adding a number of
+// 1.5 2^23's size rounds q' to a whole number, to even, whose code is in the sum's
+// last bits.  Scales below 2^-100, whose remainders could underflow, divide.
 #pragma once
 
 #include <cmath>
@@ -44,15 +43,13 @@ struct I8Coder {
 
   // 0x6480 + code of eight values, two to a word.
   __device__ __forceinline__ void biased(const float (&v)[8], uint32_t (&w)[4]) const {
-    float far = r > 0.0f ? 0.0f : 1.0f;
     uint32_t t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float sum = fmaf(v[i], r, kMagic);
-      far = fmaxf(far, fabsf(fmaf(v[i], r, kMagic - sum)));
-      t[i] = __float_as_uint(sum);
+      const float q = __fmul_rn(v[i], r), e = __fmaf_rn(-q, s, v[i]);
+      t[i] = __float_as_uint(__fadd_rn(__fmaf_rn(e, r, q), kMagic));
     }
-    if (far > 0.49998f) {
+    if (!(r > 0.0f)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = divided(v[i], s);
     }

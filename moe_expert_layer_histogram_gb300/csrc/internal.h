@@ -289,6 +289,8 @@ struct Int8Args {
 // library's own and lets it start early.
 cudaError_t launch_int8(const Int8Maps& maps, Int8Args args, bool swiglu,
                         const BlockscaleDevice& d, cudaStream_t s);
+// Most rows of a chunk of its products, and of the boxes of the codes' maps.
+int int8_chunk_rows(int M, int E);
 cudaError_t int8_status(int* code);
 
 // Routing, permutation + activation quantisation, combine.
