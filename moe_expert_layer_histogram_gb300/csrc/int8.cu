@@ -56,18 +56,19 @@ __device__ __forceinline__ void store_codes(void* row, int c0, int cols, bool ve
 
 // `warps` warps of a block (a power of two) take a row, the block 8 / warps of
 // them.  A thread's first kKept vectors of eight stay in registers between the
-// maximum and the codes; what a longer row has beyond is read again.  amax (or
-// null): a word per row that is set to zero for a later kernel.  Bound by the
-// bytes where there are many rows (8192 x 7168: 37 us, 6.3 TB/s; with a block to
-// a row and one vector at a time 24576 x 2048 took 81 us, now 34).
+// maximum and the codes; what a longer row has beyond is read again.  With many rows
+// 8192 x 7168 take 43 us (5.4 TB/s), 24576 gathered ones x 2048 34 us (81 with a
+// block to a row).
 constexpr int kKept = 4;
 
-template <bool F16>
+template <typename X, bool F16>
 __global__ void __launch_bounds__(256)
-    int8_quantize_kernel(const __nv_bfloat16* x, int64_t ldx, int x_rows, const int32_t* slots,
-                         int top_k, int rows, int cols, void* codes, int64_t ld_codes,
-                         float* scales, uint32_t* amax, int vec, int warps) {
-  // (a product that follows may set itself up and load weights meanwhile)
+    int8_quantize_kernel(const X* x, int64_t ldx, int x_rows, const int32_t* slots, int top_k,
+                         int rows, int cols, void* codes, int64_t ld_codes, float* scales, int vec,
+                         int warps) {
+  // A product that follows may set itself up and load weights meanwhile.  (fp32 rows
+  // are those of the product before, which may not be over.)
+  if (sizeof(X) == 4) pdl_wait();
   pdl_launch_dependents();
   __shared__ uint32_t s_max[8];
   const int warp = threadIdx.x >> 5, sub = warp & (warps - 1);
@@ -76,37 +77,50 @@ __global__ void __launch_bounds__(256)
   const int slot = real && slots ? slots[r] : 0;
   const int64_t src = slots ? slot / top_k : r;
   const bool in = real && slot >= 0 && src < x_rows;
-  const __nv_bfloat16* row = x + (in ? src : 0) * ldx;
+  const X* row = x + (in ? src : 0) * ldx;
   const int stride = warps * 256;  // columns of one vector of every thread of the row
   const int first = (sub * 32 + (threadIdx.x & 31)) * 8, end = in ? cols : 0;
-  auto load = [&](int c0, uint32_t (&v)[4]) {
+  // eight values: bf16 in pairs, or fp32
+  constexpr int kWords = sizeof(X) == 2 ? 4 : 8;
+  auto load = [&](int c0, uint32_t (&v)[kWords]) {
     if (c0 >= end) {
-      v[0] = v[1] = v[2] = v[3] = 0u;
-    } else if (vec && c0 + 8 <= cols) {
-      const uint4 q = *reinterpret_cast<const uint4*>(row + c0);
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    } else {
-      const uint16_t* s = reinterpret_cast<const uint16_t*>(row) + c0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = c0 + 2 * i < cols ? s[2 * i] : 0u;
-        const uint32_t hi = c0 + 2 * i + 1 < cols ? s[2 * i + 1] : 0u;
-        v[i] = lo | hi << 16;
+      for (int i = 0; i < kWords; ++i) v[i] = 0u;
+    } else if (vec && c0 + 8 <= cols) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 q = reinterpret_cast<const uint4*>(row + c0)[i / 4];
+        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(X) == 2) {
+          const uint16_t* s = reinterpret_cast<const uint16_t*>(row) + c0;
+          const uint32_t lo = c0 + 2 * i < cols ? s[2 * i] : 0u;
+          const uint32_t hi = c0 + 2 * i + 1 < cols ? s[2 * i + 1] : 0u;
+          v[i] = lo | hi << 16;
+        } else {
+          v[i] = c0 + i < cols ? __float_as_uint(row[c0 + i]) : 0u;
+        }
       }
     }
   };
-  auto largest = [](const uint32_t (&v)[4], uint32_t m) {
+  auto largest = [](const uint32_t (&v)[kWords], uint32_t m) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((v[i] << 16) & 0x7FFFFFFFu, v[i] & 0x7FFF0000u));
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(X) == 2) m = max(m, (v[i] << 16) & 0x7FFFFFFFu);
+      m = max(m, v[i] & (sizeof(X) == 2 ? 0x7FFF0000u : 0x7FFFFFFFu));
+    }
     return m;
   };
-  uint32_t kept[kKept][4], m = 0u;
+  uint32_t kept[kKept][kWords], m = 0u;
 #pragma unroll
   for (int i = 0; i < kKept; ++i) load(first + i * stride, kept[i]);
 #pragma unroll
   for (int i = 0; i < kKept; ++i) m = largest(kept[i], m);
   for (int c0 = first + kKept * stride; c0 < end; c0 += stride) {
-    uint32_t v[4];
+    uint32_t v[kWords];
     load(c0, v);
     m = largest(v, m);
   }
@@ -119,26 +133,27 @@ __global__ void __launch_bounds__(256)
   if (!real) return;
   const float s = i8_scale(m);
   const I8Coder coder(s);
-  if (first == 0) {
-    scales[r] = s;
-    if (amax) amax[r] = 0u;
-  }
+  if (first == 0) scales[r] = s;
   void* out = F16 ? static_cast<void*>(static_cast<uint16_t*>(codes) + r * ld_codes)
                   : static_cast<void*>(static_cast<int8_t*>(codes) + r * ld_codes);
-  auto put = [&](int c0, const uint32_t (&v)[4]) {
+  auto put = [&](int c0, const uint32_t (&v)[kWords]) {
     if (c0 >= cols) return;
     float f[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(v[i] << 16);
-      f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(X) == 2) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+      } else {
+        f[i] = __uint_as_float(v[i]);
+      }
     }
     store_codes<F16>(out, c0, cols, vec, coder, f);
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) put(first + i * stride, kept[i]);
   for (int c0 = first + kKept * stride; c0 < cols; c0 += stride) {
-    uint32_t v[4];
+    uint32_t v[kWords];
     load(c0, v);
     put(c0, v);
   }
@@ -171,29 +186,6 @@ __global__ void __launch_bounds__(256)
     i8_widen4(q[1], f.z, f.w);
     // (rows of a multiple of eight codes: the last ones' padding is theirs)
     *reinterpret_cast<uint4*>(out + r * ld_out + c0) = f;
-  }
-}
-
-// fp32 rows to f16 codes, by the rows' largest magnitudes.
-__global__ void __launch_bounds__(256)
-    int8_requantize_kernel(const float* h, const uint32_t* amax, int64_t rows, int cols,
-                           uint16_t* out, int64_t ld_out, float* scales) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int per = (cols + 7) / 8;
-  const int64_t n = rows * per;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / per;
-    const int c0 = static_cast<int>(i - r * per) * 8;
-    const float s = i8_scale(amax[r]);
-    if (c0 == 0) scales[r] = s;
-    const float* src = h + r * cols + c0;
-    // (cols is a multiple of 16)
-    const float4 a = *reinterpret_cast<const float4*>(src),
-                 b = *reinterpret_cast<const float4*>(src + 4);
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    *reinterpret_cast<uint4*>(out + r * ld_out + c0) = I8Coder(s).f16(v);
   }
 }
 
@@ -246,8 +238,7 @@ struct Coded {
 
 // The product of f16 codes x [M, K] with their scales.
 moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const float* scales,
-                       bool swiglu, void* out, int64_t ldo, float clamp, uint32_t* amax,
-                       cudaStream_t s) {
+                       bool swiglu, void* out, int64_t ldo, float clamp, cudaStream_t s) {
   const BlockscaleDevice* d = current_device();
   if (!d) return MOE_ERR_NO_DEVICE;
   auto encode = [&](CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
@@ -283,14 +274,13 @@ moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const fl
   a.ldo = ldo;
   a.out_pairs = aligned_to(out, 4) && ldo % 2 == 0;
   a.clamp = clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY;
-  a.amax = amax;
   return take_error(launch_int8(maps, a, swiglu, *d, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-template <bool F16>
-moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* slots, int top_k,
+template <bool F16, typename X>
+moe_status run_quantize(const X* x, int64_t ldx, int x_rows, const int32_t* slots, int top_k,
                         int rows, int cols, void* codes, int64_t ld_codes, float* scales,
-                        uint32_t* amax, cudaStream_t s) {
+                        cudaStream_t s) {
   const bool vec = aligned_to(x, 16) && ldx % 8 == 0 && aligned_to(codes, F16 ? 16 : 8) &&
                    ld_codes % 8 == 0;
   // Warps of a row: as many as keep it in registers, and more where the rows alone
@@ -301,9 +291,9 @@ moe_status run_quantize(const void* x, int64_t ldx, int x_rows, const int32_t* s
     warps *= 2;
   const int64_t blocks = (static_cast<int64_t>(rows) * warps + 7) / 8;
   const cudaError_t e =
-      launch_pdl(false, int8_quantize_kernel<F16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                 s, static_cast<const __nv_bfloat16*>(x), ldx, x_rows, slots, top_k, rows, cols,
-                 codes, ld_codes, scales, amax, static_cast<int>(vec), warps);
+      launch_pdl(sizeof(X) == 4, int8_quantize_kernel<X, F16>, dim3(static_cast<unsigned>(blocks)),
+                 dim3(256), 0, s, x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,
+                 static_cast<int>(vec), warps);
   return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -331,8 +321,8 @@ moe_status moe_int8_quantize(const void* x, int64_t ldx, int x_rows, const int32
   if ((!x && x_rows > 0) || !codes || !scales || !aligned_to(x, 2) || !aligned_to(slots, 4) ||
       !aligned_to(scales, 4))
     return MOE_ERR_INVALID_ARG;
-  return run_quantize<false>(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,
-                             nullptr, static_cast<cudaStream_t>(stream));
+  return run_quantize<false>(static_cast<const __nv_bfloat16*>(x), ldx, x_rows, slots, top_k, rows,
+                             cols, codes, ld_codes, scales, static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_int8_matmul_workspace(int M, int K) {
@@ -360,7 +350,7 @@ moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, co
                                    dim3(256), 0, s, static_cast<const int8_t*>(a), lda, M, K,
                                    c.codes, c.ld, static_cast<int>(aligned_to(a, 8) && lda % 8 == 0));
   if (take_error(e) != cudaSuccess) return MOE_ERR_CUDA;
-  return run_product(p, c.codes, c.ld, a_scales, false, out, ldo, 0.0f, nullptr, s);
+  return run_product(p, c.codes, c.ld, a_scales, false, out, ldo, 0.0f, s);
 }
 
 size_t moe_int8_linear_workspace(int M, int N, int K) {
@@ -381,19 +371,19 @@ moe_status moe_int8_linear(const void* x, int64_t ldx, const void* w, int64_t ld
   if (!current_device()) return MOE_ERR_NO_DEVICE;
   const Coded c(workspace, M, K);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const moe_status sq =
-      run_quantize<true>(x, ldx, M, nullptr, 1, M, K, c.codes, c.ld, c.scales, nullptr, s);
+  const moe_status sq = run_quantize<true>(static_cast<const __nv_bfloat16*>(x), ldx, M, nullptr, 1,
+                                           M, K, c.codes, c.ld, c.scales, s);
   if (sq != MOE_OK) return sq;
-  return run_product(p, c.codes, c.ld, c.scales, false, out, ldo, 0.0f, nullptr, s);
+  return run_product(p, c.codes, c.ld, c.scales, false, out, ldo, 0.0f, s);
 }
 
 size_t moe_int8_experts_workspace(int rows, int H, int I) {
   if (rows < 1 || H < 1 || I < 1 || rows > kMaxExtent || H > kMaxExtent || I > kMaxExtent / 2)
     return 0;
-  // the rows' codes, h in fp32 and its rows' maxima, its codes
+  // the rows' codes, h in fp32, its codes
   return static_cast<size_t>(Coded::bytes(rows, H) +
                              padded(static_cast<int64_t>(rows) * I * 4, 256) +
-                             padded(static_cast<int64_t>(rows) * 4, 256) + Coded::bytes(rows, I));
+                             Coded::bytes(rows, I));
 }
 
 moe_status moe_int8_experts(const void* x, int64_t ldx, int T, const int32_t* slots, int top_k,
@@ -420,19 +410,15 @@ moe_status moe_int8_experts(const void* x, int64_t ldx, int T, const int32_t* sl
   at += Coded::bytes(rows, H);
   float* h = reinterpret_cast<float*>(at);
   at += padded(static_cast<int64_t>(rows) * I * 4, 256);
-  uint32_t* amax = reinterpret_cast<uint32_t*>(at);
-  at += padded(static_cast<int64_t>(rows) * 4, 256);
   const Coded hc(at, rows, I);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = run_quantize<true>(x, ldx, T, slots, top_k, rows, H, c.codes, c.ld, c.scales, amax, s);
+  st = run_quantize<true>(static_cast<const __nv_bfloat16*>(x), ldx, T, slots, top_k, rows, H,
+                          c.codes, c.ld, c.scales, s);
+  if (st == MOE_OK) st = run_product(p1, c.codes, c.ld, c.scales, true, h, I, clamp_limit, s);
   if (st == MOE_OK)
-    st = run_product(p1, c.codes, c.ld, c.scales, true, h, I, clamp_limit, amax, s);
-  if (st != MOE_OK) return st;
-  const int64_t vectors = static_cast<int64_t>(rows) * ((I + 7) / 8);
-  if (take_error(launch_pdl(true, int8_requantize_kernel, dim3(vector_blocks(vectors)), dim3(256),
-                            0, s, h, amax, rows, I, hc.codes, hc.ld, hc.scales)) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  return run_product(p2, hc.codes, hc.ld, hc.scales, false, out, ldo, 0.0f, nullptr, s);
+    st = run_quantize<true>(h, I, rows, nullptr, 1, rows, I, hc.codes, hc.ld, hc.scales, s);
+  if (st == MOE_OK) st = run_product(p2, hc.codes, hc.ld, hc.scales, false, out, ldo, 0.0f, s);
+  return st;
 }
 
 moe_status moe_int8_status(void) {

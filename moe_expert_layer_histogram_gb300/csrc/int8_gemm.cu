@@ -30,9 +30,8 @@
 // timing.
 //
 // With SWIGLU the halves are 128 gate channels and the 128 up channels that go
-// with them; h = silu(gate) up is stored in fp32, and the largest |h| of each row
-// kept by an atomic maximum (of bits: the order of the updates does not matter),
-// from which the kernel after this one takes the rows' scales.
+// with them; h = silu(gate) up is stored in fp32, for a row's scale is known only
+// when all of its tiles are.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -396,20 +395,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (c0 + 32 * i >= it.rows) break;
-          uint32_t mine = 0u;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int token = c0 + 32 * i + c;
             const float s = scales[token];
             const float h = swiglu(__uint_as_float(g[i][c]) * (s * sg),
                                    __uint_as_float(u[i][c]) * (s * su), p.clamp);
-            const bool in = token < it.rows && n < I;
-            if (in) out[token * p.ldo] = h;
-            const uint32_t m =
-                __reduce_max_sync(0xFFFFFFFFu, in ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
-            if (lane == c) mine = m;
+            if (token < it.rows && n < I) out[token * p.ldo] = h;
           }
-          if (mine) atomicMax(&p.amax[it.row0 + c0 + 32 * i + lane], mine);
         }
         return true;
       } else {
@@ -505,9 +498,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           const float s = p.a_scales[it.row0 + t];
           const float h = swiglu(g * (s * sg), u * (s * su), p.clamp);
           if (n < I) static_cast<float*>(p.out)[(it.row0 + t) * p.ldo + n] = h;
-          const uint32_t m =
-              __reduce_max_sync(0xFFFFFFFFu, n < I ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
-          if (lane == 0 && m) atomicMax(&p.amax[it.row0 + t], m);
         }
       } else {
         const int n = it.tile * kI8Tile + c;
@@ -578,7 +568,7 @@ int int8_chunk_rows(int M, int E) {
 // See internal.h.  Chunks: of all rows where there are few, else 128; with several
 // experts of few rows each on average, twice that average at least, since a lower
 // chunk leaves room for more stages of weights (64 experts, 512 rows, 7168 x 2048:
-// chunks of 128 rows and three stages 319 + 171 us, of 32 rows and five 294 + 151),
+// chunks of 128 rows and three stages 319 + 171 us, of 32 rows and five 301 + 160),
 // and an expert with more rows reads its weights again from L2.  Fewer items than
 // half the SMs: the reduction is split over clusters of as many CTAs (up to eight)
 // as still run all at once.  Several experts only with a token's rows or two in

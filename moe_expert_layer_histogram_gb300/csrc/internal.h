@@ -281,7 +281,6 @@ struct Int8Args {
   int64_t ldo;
   int out_pairs;           // bf16 rows start on 4-byte boundaries
   float clamp;             // SwiGLU (+inf: none)
-  uint32_t* amax;          // SwiGLU [M]: bits of each row's largest |h| (zero before)
   // set by launch_int8
   int a_rows, tiles, stages, split, chunk_group;
 };
