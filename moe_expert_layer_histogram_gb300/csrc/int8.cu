@@ -251,11 +251,12 @@ moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const fl
   };
   Int8Maps maps;
   // (one expert: all chunks take the largest box)
-  const int most = int8_chunk_rows(p.M, p.E);
+  const bool pairs = int8_in_pairs(p.M, p.N, p.E);
+  const int most = pairs ? 128 : int8_chunk_rows(p.M, p.N, p.E);
   const int boxes = most <= 16 ? 1 : most <= 32 ? 2 : most <= 64 ? 3 : 4;
   const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M)};
   const cuuint64_t xstr[1] = {static_cast<cuuint64_t>(ld) * 2};
-  for (int i = p.E == 1 ? boxes - 1 : 0; i < boxes; ++i) {
+  for (int i = p.E == 1 && !pairs ? boxes - 1 : 0; i < boxes; ++i) {
     const cuuint32_t box[2] = {64, 16u << i};
     if (!encode(&maps.x[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, 2, xdims, xstr, box))
       return MOE_ERR_CUDA;
@@ -263,7 +264,7 @@ moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const fl
   const cuuint64_t wdims[3] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.N),
                                static_cast<cuuint64_t>(p.E)};
   const cuuint64_t wstr[2] = {static_cast<cuuint64_t>(p.ldw), static_cast<cuuint64_t>(p.ldw) * p.N};
-  const cuuint32_t wbox[3] = {128, 128, 1};
+  const cuuint32_t wbox[3] = {128, pairs && swiglu ? 64u : 128u, 1};
   if (!encode(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, 3, wdims, wstr, wbox)) return MOE_ERR_CUDA;
   Int8Args a{};
   a.a_scales = scales;

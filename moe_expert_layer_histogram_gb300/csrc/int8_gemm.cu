@@ -134,6 +134,44 @@ __device__ __forceinline__ I8Item map_i8_item(const ExpertTable& t, int tiles, i
   return it;
 }
 
+// bf16 results of 128 tokens (columns) and the warp's 32 channels (lane = channel):
+// v times the tokens' scales and the channel's, n the lane's channel of N, out the
+// first token's row, rows how many are real.  Two tokens at a time: a lane packs its
+// channel's values of both, an even lane takes the first token's pair of channels
+// from it and its neighbour, the odd one the second's.
+__device__ __forceinline__ void store_tokens(const uint32_t (&v)[4][32], const float* scales,
+                                             float s, uint16_t* out, int64_t ldo, int n, int N,
+                                             int rows, bool pairs, int lane) {
+  const bool odd = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (32 * i >= rows) break;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      const int token = 32 * i + c;
+      const __nv_bfloat162 b =
+          __floats2bfloat162_rn(__uint_as_float(v[i][c]) * (scales[token] * s),
+                                __uint_as_float(v[i][c + 1]) * (scales[token + 1] * s));
+      const uint32_t w = reinterpret_cast<const uint32_t&>(b);
+      if (pairs) {
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+        const uint32_t r = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+        const int t = token + (odd ? 1 : 0), m = n & ~1;
+        uint16_t* d = out + t * ldo + m;
+        if (t < rows) {
+          if (m + 1 < N)
+            *reinterpret_cast<uint32_t*>(d) = r;
+          else if (m < N)
+            *d = static_cast<uint16_t>(r);
+        }
+      } else if (n < N) {
+        if (token < rows) out[token * ldo + n] = static_cast<uint16_t>(w);
+        if (token + 1 < rows) out[(token + 1) * ldo + n] = static_cast<uint16_t>(w >> 16);
+      }
+    }
+  }
+}
+
 template <bool SWIGLU, bool SPLIT>
 __global__ void __launch_bounds__(kI8Threads, 1)
     int8_gemm_kernel(const __grid_constant__ Int8Maps maps, const __grid_constant__ Int8Args p) {
@@ -417,38 +455,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const int n = it.tile * kI8Tile + half * 128 + row;
         const float s = n < p.N ? sw[n] : 0.0f;
         uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(it.row0) * p.ldo;
-        const bool odd = lane & 1;
-        // Two tokens at a time: a lane packs its channel's values of both, an
-        // even lane takes the first token's pair of channels from it and its
-        // neighbour, the odd one the second's.
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (32 * i >= it.rows) break;
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const int token = 32 * i + c;
-            const __nv_bfloat162 b =
-                __floats2bfloat162_rn(__uint_as_float(v[i][c]) * (scales[token] * s),
-                                      __uint_as_float(v[i][c + 1]) * (scales[token + 1] * s));
-            const uint32_t w = reinterpret_cast<const uint32_t&>(b);
-            if (p.out_pairs) {
-              const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-              const uint32_t r = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
-              const int t = token + (odd ? 1 : 0), m = n & ~1;
-              uint16_t* d = out + t * p.ldo + m;
-              if (t < it.rows) {
-                if (m + 1 < p.N)
-                  *reinterpret_cast<uint32_t*>(d) = r;
-                else if (m < p.N)
-                  *d = static_cast<uint16_t>(r);
-              }
-            } else if (n < p.N) {
-              if (token < it.rows) out[token * p.ldo + n] = static_cast<uint16_t>(w);
-              if (token + 1 < it.rows)
-                out[(token + 1) * p.ldo + n] = static_cast<uint16_t>(w >> 16);
-            }
-          }
-        }
+        store_tokens(v, scales, s, out, p.ldo, n, p.N, it.rows, p.out_pairs, lane);
       }
       return true;
     };
@@ -522,6 +529,340 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// ---------------------------------------------------------------- CTA pairs
+// Many rows.  A single CTA's 256 x 128 block of 128 columns moves 64 KB into shared
+// memory, 32 KB out of it for the widening and 64 KB for the MMAs (the tokens once
+// for each half), and 64 KB into TMEM, which takes the same path: 1800 cycles of it
+// against 1024 of MMA.  In a pair (cta_group::2) two CTAs share 256 channels x up
+// to 256 tokens: each widens its own 128 channels and loads half of the tokens: 48
+// KB in, 16 and 32 KB out, 32 KB into TMEM, 1024 cycles.
+//
+// Rank 0 issues; each CTA's results are its own 128 channels (TMEM lanes) of all
+// tokens.  An item's tokens are cut in two halves of a multiple of 16, and an
+// expert's rows evenly into items, so that short and odd ones share the work.  The widening warps take every other
+// block of 128 columns: four on one, four on the next.  With SWIGLU the CTA's
+// channels are 64 gate and the 64 up channels that go with them, 16 of each to a
+// warp's 32 lanes, so that a gate and its up meet by a shuffle.
+constexpr int kP8MaxStages = 4;
+constexpr int kP8WBytes = 128 * 128;
+constexpr int kP8Buffers = 4;      // TMEM buffers of widened weights, 64 columns each
+constexpr uint32_t kP8Weights = 256;
+constexpr int kP8Tokens = 256;     // most tokens of an item
+
+__device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                                uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kI8Threads, 1)
+    int8_pair_kernel(const __grid_constant__ Int8Maps maps, const __grid_constant__ Int8Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int stage_bytes = kP8WBytes + p.a_rows / 2 * 256, stages = p.stages;
+  // per widening warp: the scales of its 128 tokens
+  float* s_scale = reinterpret_cast<float*>(smem + stages * stage_bytes);
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(s_scale + kI8WideWarps * 128);
+  uint64_t* xfull = wfull + kP8MaxStages;  // (rank 0's: both CTAs' tokens)
+  uint64_t* empty = xfull + kP8MaxStages;
+  uint64_t* afull = empty + kP8MaxStages;  // (rank 0's: both CTAs' weights)
+  uint64_t* aempty = afull + kP8Buffers;
+  uint64_t* dfull = aempty + kP8Buffers;
+  uint64_t* dempty = dfull + 1;            // (rank 0's)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dempty + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* s_tab = reinterpret_cast<int*>(tmem_holder + 2);
+  const ExpertTable tab{s_tab, s_tab + p.E + 1, s_tab + 2 * p.E + 1};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&xfull[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < kP8Buffers; ++b) {
+      mbar_init(&afull[b], 8);  // four warps of each CTA
+      mbar_init(&aempty[b], 1);
+    }
+    mbar_init(dfull, 1);
+    mbar_init(dempty, 2 * kI8WideWarps);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 2) fill_expert_table(p, tab, p.a_rows, lane);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers, before either arrives on the other's
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int blocks = (p.K + 127) / 128;
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int total = tab.chunk_off[p.E] * p.tiles;
+  int expert = 0;  // of the role's latest item
+  // row0, rows: of the item, cut evenly among its expert's chunks
+  auto map_item = [&](int item) {
+    while (tab.chunk_off[expert + 1] * p.tiles <= item) ++expert;
+    const int chunks = tab.chunk_off[expert + 1] - tab.chunk_off[expert];
+    const int local = item - tab.chunk_off[expert] * p.tiles;
+    const int g = local / (p.chunk_group * p.tiles), in = local - g * p.chunk_group * p.tiles;
+    const int size = min(p.chunk_group, chunks - g * p.chunk_group);
+    const int r0 = tab.start[expert], rows = tab.end[expert] - r0;
+    I8Item it;
+    it.e = expert;
+    it.tile = in / size;
+    const int c = g * p.chunk_group + in - it.tile * size;
+    const int each = ((rows + chunks - 1) / chunks + 31) & ~31;  // at most a_rows
+    it.row0 = r0 + c * each;
+    it.rows = max(min(each, r0 + rows - it.row0), 0);
+    return it;
+  };
+  // rows of either CTA's part of an item (the MMA's N, both parts, is a multiple of
+  // 32), and their box
+  auto part_of = [](const I8Item& it) { return max((it.rows + 31) / 32 * 16, 16); };
+  auto box_of = [](int part) { return part <= 16 ? 0 : part <= 32 ? 1 : part <= 64 ? 2 : 3; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------- TMA producer
+      const uint64_t reused = l2_policy_evict_normal();
+      const uint32_t xfull0 = mapa_shared(smem_u32(xfull), 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto load_w = [&](const I8Item& it, int st, int kb) {
+        mbar_arrive_expect_tx(&wfull[st], kP8WBytes);
+        if constexpr (SWIGLU) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d_hint(smem + st * stage_bytes + h * (kP8WBytes / 2), &maps.w, &wfull[st],
+                             kb * 128, it.tile * 128 + rank * 64 + h * (p.N / 2), it.e, reused);
+        } else {
+          tma_load_3d_hint(smem + st * stage_bytes, &maps.w, &wfull[st], kb * 128,
+                           it.tile * kI8Tile + rank * 128, it.e, reused);
+        }
+      };
+      int ahead = 0;  // stages of the first item whose weights are on their way
+      if (first < total) {
+        const I8Item it = map_item(first);
+        for (; ahead < min(stages, blocks); ++ahead) load_w(it, ahead, ahead);
+      }
+      pdl_wait();
+      fence_proxy_async_global();
+      for (int item = first; ok && item < total; item += step) {
+        const I8Item it = map_item(item);
+        const int part = part_of(it), box = box_of(part);
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (ahead > 0) {
+            --ahead;
+          } else {
+            ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
+            if (!ok) break;
+            load_w(it, stage, kb);
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&xfull[stage], 2u * (16u << box) * 256u);
+          uint8_t* sx = smem + stage * stage_bytes + kP8WBytes;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d_pair(sx + h * (16 << box) * 128, &maps.x[box], xfull0 + stage * 8,
+                             kb * 128 + h * 64, it.row0 + rank * part, reused);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // every stage's last release has arrived here before this CTA may leave
+      for (int s = 0; ok && s < stages; ++s) {
+        ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) report_status(&g_int8_status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------- MMA issuer
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, aphase = 0, dphase = 0;
+    bool ok = true;
+    for (int item = first; ok && item < total; item += step) {
+      const I8Item it = map_item(item);
+      const int part = part_of(it), n = 16 << box_of(part);
+      const uint32_t idesc = idesc_f16(256, 2 * part);
+      ok = wait_warp(dempty, dphase ^ 1, abort_flag);
+      dphase ^= 1;
+      for (int kb = 0; ok && kb < blocks; ++kb) {
+        ok = wait_warp(&xfull[stage], phase, abort_flag) &&
+             wait_warp(&afull[buf], aphase, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t sx = smem_u32(smem + stage * stage_bytes + kP8WBytes);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_ts_pair(tmem, tmem + kP8Weights + buf * 64 + k * 8,
+                            desc_sw128(sx + (k >> 2) * n * 128 + (k & 3) * 32), idesc,
+                            kb > 0 || k > 0);
+          tc_commit_pair(&empty[stage], 3);
+          tc_commit_pair(&aempty[buf], 3);
+          if (kb + 1 == blocks) tc_commit_pair(dfull, 3);
+        }
+        __syncwarp();
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (++buf == kP8Buffers) {
+          buf = 0;
+          aphase ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
+  } else if (warp >= kI8WideWarp0) {
+    // ---------------------------------------------------- widen, and results
+    const int quarter = warp & 3, group = (warp - kI8WideWarp0) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    // the row of the tile that becomes this thread's TMEM lane
+    const int row = SWIGLU ? (lane >> 4) * 64 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
+    float* scales = s_scale + (warp - kI8WideWarp0) * 128;
+    const uint32_t afull0 = mapa_shared(smem_u32(afull), 0);
+    const uint32_t dempty0 = mapa_shared(smem_u32(dempty), 0);
+    int count = 0;  // blocks so far, of both groups
+    uint32_t dphase = 0;
+    bool ok = true, waited = false;
+
+    // Every other block: this group's turn.
+    auto widen = [&](int block) {
+      const int stage = block % stages, buf = block % kP8Buffers;
+      if (!wait_warp(&wfull[stage], (block / stages) & 1, abort_flag)) return false;
+      const uint8_t* src = smem + stage * stage_bytes + row * 128;
+      uint4 v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        v[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+      if (!wait_warp(&aempty[buf], ((block / kP8Buffers) & 1) ^ 1, abort_flag)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          i8_widen4(v[4 * q + c].x, w[8 * c], w[8 * c + 1]);
+          i8_widen4(v[4 * q + c].y, w[8 * c + 2], w[8 * c + 3]);
+          i8_widen4(v[4 * q + c].z, w[8 * c + 4], w[8 * c + 5]);
+          i8_widen4(v[4 * q + c].w, w[8 * c + 6], w[8 * c + 7]);
+        }
+        tmem_st32(lanes + kP8Weights + buf * 64 + q * 32, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive_if(lane == 0, afull0 + buf * 8);
+      return true;
+    };
+
+    auto results = [&](const I8Item& it) {
+      if (!waited) {
+        // (the scales are the kernel's before this one)
+        pdl_wait();
+        waited = true;
+      }
+      const int c0 = group * 128, left = it.rows - c0;  // this group's tokens
+      const float* sx = p.a_scales + it.row0 + c0;
+      const float* sw = p.w_scales + static_cast<int64_t>(it.e) * p.N;
+      float sr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sr[i] = 32 * i + lane < left ? sx[32 * i + lane] : 0.0f;
+      if (!wait_warp(dfull, dphase, abort_flag)) return false;
+      dphase ^= 1;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) scales[32 * i + lane] = sr[i];
+      __syncwarp();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(lanes + c0 + 32 * i, v[i]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reg_fence32(v[i]);
+      tc_fence_before();
+      mbar_arrive_if(lane == 0, dempty0);
+      if constexpr (SWIGLU) {
+        // lanes below 16 take the first of two tokens, the others the second
+        const int I = p.N / 2, n = it.tile * 128 + rank * 64 + quarter * 16 + (lane & 15);
+        const bool high = lane & 16;
+        const float sg = n < I ? sw[n] : 0.0f, su = n < I ? sw[I + n] : 0.0f;
+        float* out = static_cast<float*>(p.out) + static_cast<int64_t>(it.row0 + c0) * p.ldo + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (32 * i >= left) break;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, high ? v[i][c] : v[i][c + 1], 16);
+            const float g = __uint_as_float(high ? o : v[i][c]);
+            const float u = __uint_as_float(high ? v[i][c + 1] : o);
+            const int t = 32 * i + c + (high ? 1 : 0);
+            const float s = scales[t];
+            const float h = swiglu(g * (s * sg), u * (s * su), p.clamp);
+            if (t < left && n < I) out[t * p.ldo] = h;
+          }
+        }
+      } else {
+        const int n = it.tile * kI8Tile + rank * 128 + quarter * 32 + lane;
+        const float s = n < p.N ? sw[n] : 0.0f;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(it.row0 + c0) * p.ldo;
+        store_tokens(v, scales, s, out, p.ldo, n, p.N, left, p.out_pairs, lane);
+      }
+      return true;
+    };
+
+    I8Item before{};
+    bool pending = false;
+    for (int item = first; ok; item += step) {
+      const bool more = item < total;
+      const int n = more ? blocks : 0, ahead = min(kP8Buffers, n);
+      for (int kb = 0;; ++kb) {
+        if (pending && kb == ahead) {
+          ok = results(before);
+          pending = false;
+        }
+        if (!ok || kb == n) break;
+        if ((count & 1) == group) ok = widen(count);
+        ++count;
+      }
+      if (!more) break;
+      before = map_item(item);
+      pending = true;
+    }
+    // the last releases of the buffers, before this CTA may leave
+    for (int b = 0; ok && b < kP8Buffers; ++b)
+      if (count - 1 - b >= 0)
+        ok = wait_warp(&aempty[(count - 1 - b) % kP8Buffers],
+                       ((count - 1 - b) / kP8Buffers) & 1, abort_flag);
+    if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 // ---------------------------------------------------------------- host
 int extra_smem(int E) {
   return kI8WideWarps * 128 * 4 + (2 * kI8MaxStages + 2 * kI8Buffers + 2) * 8 + 8 +
@@ -558,9 +899,43 @@ cudaError_t launch_i8(const Int8Maps& maps, Int8Args p, int grid, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, k, maps, p);
 }
 
+template <bool SWIGLU>
+cudaError_t launch_i8_pair(const Int8Maps& maps, Int8Args p, int pairs, cudaStream_t s) {
+  auto k = int8_pair_kernel<SWIGLU>;
+  static OncePerDevice prepared;
+  const cudaError_t ready = prepared([&] {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8SmemLimit);
+  });
+  if (ready != cudaSuccess) return ready;
+  const int stage = kP8WBytes + p.a_rows / 2 * 256;
+  const int fixed = 1024 + kI8WideWarps * 128 * 4 +
+                    (3 * kP8MaxStages + 2 * kP8Buffers + 2) * 8 + 8 + (3 * p.E + 1) * 4;
+  p.stages = std::min(kP8MaxStages, (kI8SmemLimit - fixed) / stage);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  return cudaLaunchKernelEx(&cfg, k, maps, p);
+}
+
 }  // namespace
 
-int int8_chunk_rows(int M, int E) {
+// Pairs where every pair of SMs has an item and the experts' rows fill most of one.
+bool int8_in_pairs(int M, int N, int E) {
+  return M / 192 >= E && static_cast<int64_t>(M / kP8Tokens) * ((N + kI8Tile - 1) / kI8Tile) >= 76;
+}
+
+int int8_chunk_rows(int M, int N, int E) {
+  if (int8_in_pairs(M, N, E)) return kP8Tokens;
   const int64_t most = E == 1 ? M : std::min<int64_t>(M, std::max<int64_t>(32, 2 * (static_cast<int64_t>(M) / E)));
   return most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
 }
@@ -576,7 +951,7 @@ int int8_chunk_rows(int M, int E) {
 // number.
 cudaError_t launch_int8(const Int8Maps& maps, Int8Args p, bool swiglu, const BlockscaleDevice& d,
                         cudaStream_t s) {
-  p.a_rows = int8_chunk_rows(p.M, p.E);
+  p.a_rows = int8_chunk_rows(p.M, p.N, p.E);
   const int kb = (p.K + 127) / 128;
   const int64_t chunks = p.E == 1 ? (p.M + p.a_rows - 1) / p.a_rows
                                   : std::min<int64_t>(p.E, p.M) + p.M / p.a_rows;
@@ -584,6 +959,10 @@ cudaError_t launch_int8(const Int8Maps& maps, Int8Args p, bool swiglu, const Blo
   p.chunk_group = 8;
   const int64_t items = chunks * p.tiles;
   if (items > INT32_MAX) return cudaErrorInvalidValue;
+  if (int8_in_pairs(p.M, p.N, p.E)) {
+    const int pairs = static_cast<int>(std::min<int64_t>(d.clusters[2], items));
+    return swiglu ? launch_i8_pair<true>(maps, p, pairs, s) : launch_i8_pair<false>(maps, p, pairs, s);
+  }
   p.split = 1;
   if (p.E == 1 || p.M <= 16)
     for (int n = 2; n <= std::min(kBsMaxSplit, kb); ++n)

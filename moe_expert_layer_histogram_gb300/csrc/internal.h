@@ -269,7 +269,7 @@ cudaError_t blockscale_status(int* code);
 // 8-bit integer products (int8_gemm.cu).
 struct Int8Maps {
   CUtensorMap x[4];  // f16 codes [M, K], boxes of 16/32/64/128 rows x 64 columns
-  CUtensorMap w;     // int8 codes [E, N, K], boxes of 128 x 128
+  CUtensorMap w;     // int8 codes [E, N, K], boxes of 128 (or 64) rows x 128
 };
 
 struct Int8Args {
@@ -288,8 +288,10 @@ struct Int8Args {
 // library's own and lets it start early.
 cudaError_t launch_int8(const Int8Maps& maps, Int8Args args, bool swiglu,
                         const BlockscaleDevice& d, cudaStream_t s);
-// Most rows of a chunk of its products, and of the boxes of the codes' maps.
-int int8_chunk_rows(int M, int E);
+// Whether a product runs on CTA pairs (its weights' boxes are 64 rows high with
+// swiglu), and the most rows of a chunk of its items.
+bool int8_in_pairs(int M, int N, int E);
+int int8_chunk_rows(int M, int N, int E);
 cudaError_t int8_status(int* code);
 
 // Routing, permutation + activation quantisation, combine.

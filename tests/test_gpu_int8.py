@@ -146,7 +146,14 @@ def test_matmul(M, N, K):
     close(got, *matmul_reference(a, s, w, ws), K)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 300, 1008), (100, 300, 1008), (400, 300, 1008)])
+@pytest.mark.parametrize("M,N,K", [(4864, 1024, 400), (5000, 1025, 130), (9728, 500, 64),
+                                   (2049, 9800, 1000), (20000, 256, 16)])
+def test_matmul_of_many_rows(M, N, K):
+    test_matmul(M, N, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1008), (100, 300, 1008), (400, 300, 1008),
+                                   (5000, 1000, 1008)])
 def test_sums_that_fp32_holds_are_exact(M, N, K):
     # scales 1 and at most 1008 products of up to 127 x 128: whole numbers below 2^24,
     # so the result is the exact sum rounded to bf16
@@ -192,11 +199,12 @@ GROUPS = [
     ([10, 20, 300, 300, 300, 310, 310, 320, 325], 330),
     ([-5, 20, 15, 60, 2 ** 31 - 1, 7, 80, 90, 100], 64),   # not a table: clamped
     ([0, 1200, 1200, 2500, 2500, 2500, 2600, 2601, 2700], 2700),
+    ([0, 257, 257, 258, 513, 4000, 12001, 19990, 20001], 20010),
 ]
 
 
 @pytest.mark.parametrize("offsets,M", GROUPS)
-@pytest.mark.parametrize("N,K", [(256, 512), (333, 144)])
+@pytest.mark.parametrize("N,K", [(256, 512), (333, 144), (1300, 272)])
 def test_experts_rows(offsets, M, N, K):
     from moe_expert_layer_histogram_gb300 import int8_matmul
     E = len(offsets) - 1
@@ -224,7 +232,8 @@ def route(T, E, k, seed=0, masked=0.0):
 @pytest.mark.parametrize("T,E,k,H,I,clamp,masked", [
     (1, 8, 2, 256, 128, 0.0, 0.0), (2, 64, 6, 2048, 1024, 7.0, 0.0), (40, 16, 3, 272, 144, 0.0, 0.2),
     (64, 64, 8, 1024, 512, 0.0, 0.0), (700, 8, 2, 512, 256, 0.5, 0.1), (300, 4, 4, 144, 16, 0.0, 0.0),
-    (1500, 8, 4, 256, 400, 7.0, 0.0)])
+    (1500, 8, 4, 256, 400, 7.0, 0.0), (4000, 4, 2, 1024, 720, 0.0, 0.0),
+    (6000, 8, 4, 528, 256, 1.0, 0.1)])
 def test_experts(T, E, k, H, I, clamp, masked):
     from moe_expert_layer_histogram_gb300 import int8_experts
     x = randn(T, H)
