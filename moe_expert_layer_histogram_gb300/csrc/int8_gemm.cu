@@ -134,41 +134,68 @@ __device__ __forceinline__ I8Item map_i8_item(const ExpertTable& t, int tiles, i
   return it;
 }
 
+__device__ __forceinline__ void st_if_b32(bool on, void* p, uint32_t v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(p),
+               "r"(v), "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
+__device__ __forceinline__ void st_if_b16(bool on, void* p, uint32_t v) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b16 h;\n\tsetp.ne.u32 p, %2, 0;\n\tcvt.u16.u32 h, %1;\n\t"
+      "@p st.global.b16 [%0], h;\n\t}" ::"l"(p),
+      "r"(v), "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
+
 // bf16 results of 128 tokens (columns) and the warp's 32 channels (lane = channel):
 // v times the tokens' scales and the channel's, n the lane's channel of N, out the
 // first token's row, rows how many are real.  Two tokens at a time: a lane packs its
 // channel's values of both, an even lane takes the first token's pair of channels
-// from it and its neighbour, the odd one the second's.
+// from it and its neighbour, the odd one the second's.  No branches within 32
+// tokens: with them the steps of one pair waited for those of the one before, 9000
+// cycles for the 128 tokens.
 __device__ __forceinline__ void store_tokens(const uint32_t (&v)[4][32], const float* scales,
                                              float s, uint16_t* out, int64_t ldo, int n, int N,
                                              int rows, bool pairs, int lane) {
   const bool odd = lane & 1;
+  // (the last channel of an odd N has no partner; its pair's even lane stores it)
+  const bool both = (n | 1) < N, one = (n & ~1) < N && !both;
+  uint16_t* d = pairs ? out + (n & ~1) + (odd ? ldo : 0) : out + n;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (32 * i >= rows) break;
+    uint32_t w[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const int token = 32 * i + c;
-      const __nv_bfloat162 b =
-          __floats2bfloat162_rn(__uint_as_float(v[i][c]) * (scales[token] * s),
-                                __uint_as_float(v[i][c + 1]) * (scales[token + 1] * s));
-      const uint32_t w = reinterpret_cast<const uint32_t&>(b);
-      if (pairs) {
-        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-        const uint32_t r = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
-        const int t = token + (odd ? 1 : 0), m = n & ~1;
-        uint16_t* d = out + t * ldo + m;
-        if (t < rows) {
-          if (m + 1 < N)
-            *reinterpret_cast<uint32_t*>(d) = r;
-          else if (m < N)
-            *d = static_cast<uint16_t>(r);
-        }
-      } else if (n < N) {
-        if (token < rows) out[token * ldo + n] = static_cast<uint16_t>(w);
-        if (token + 1 < rows) out[(token + 1) * ldo + n] = static_cast<uint16_t>(w >> 16);
+    for (int c = 0; c < 32; c += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(scales + 32 * i + c);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(v[i][c]) * (f.x * s),
+                                                      __uint_as_float(v[i][c + 1]) * (f.y * s));
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(v[i][c + 2]) * (f.z * s),
+                                                      __uint_as_float(v[i][c + 3]) * (f.w * s));
+      w[c / 2] = reinterpret_cast<const uint32_t&>(lo);
+      w[c / 2 + 1] = reinterpret_cast<const uint32_t&>(hi);
+    }
+    const int left = rows - 32 * i;
+    if (pairs) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w[c], 1);
+        w[c] = odd ? __byte_perm(o, w[c], 0x7632) : __byte_perm(w[c], o, 0x5410);
+      }
+      const int first = left - (odd ? 1 : 0);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) st_if_b32(both && 2 * c < first, d + 2 * c * ldo, w[c]);
+      if (__any_sync(0xFFFFFFFFu, one))
+#pragma unroll
+        for (int c = 0; c < 16; ++c) st_if_b16(one && 2 * c < first, d + 2 * c * ldo, w[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        st_if_b16(n < N && 2 * c < left, d + 2 * c * ldo, w[c]);
+        st_if_b16(n < N && 2 * c + 1 < left, d + (2 * c + 1) * ldo, w[c] >> 16);
       }
     }
+    d += 32 * ldo;
   }
 }
 
@@ -434,13 +461,19 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         for (int i = 0; i < 2; ++i) {
           if (c0 + 32 * i >= it.rows) break;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int token = c0 + 32 * i + c;
-            const float s = scales[token];
-            const float h = swiglu(__uint_as_float(g[i][c]) * (s * sg),
-                                   __uint_as_float(u[i][c]) * (s * su), p.clamp);
-            if (token < it.rows && n < I) out[token * p.ldo] = h;
+          for (int c = 0; c < 32; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(scales + c0 + 32 * i + c);
+            const float sc[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              g[i][c + k] = __float_as_uint(swiglu(__uint_as_float(g[i][c + k]) * (sc[k] * sg),
+                                                   __uint_as_float(u[i][c + k]) * (sc[k] * su),
+                                                   p.clamp));
           }
+          const int rest = it.rows - c0 - 32 * i;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            st_if_b32(c < rest && n < I, out + (c0 + 32 * i + c) * p.ldo, g[i][c]);
         }
         return true;
       } else {
@@ -806,20 +839,29 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const int I = p.N / 2, n = it.tile * 128 + rank * 64 + quarter * 16 + (lane & 15);
         const bool high = lane & 16;
         const float sg = n < I ? sw[n] : 0.0f, su = n < I ? sw[I + n] : 0.0f;
-        float* out = static_cast<float*>(p.out) + static_cast<int64_t>(it.row0 + c0) * p.ldo + n;
+        float* out = static_cast<float*>(p.out) +
+                     static_cast<int64_t>(it.row0 + c0 + (high ? 1 : 0)) * p.ldo + n;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (32 * i >= left) break;
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, high ? v[i][c] : v[i][c + 1], 16);
-            const float g = __uint_as_float(high ? o : v[i][c]);
-            const float u = __uint_as_float(high ? v[i][c + 1] : o);
-            const int t = 32 * i + c + (high ? 1 : 0);
-            const float s = scales[t];
-            const float h = swiglu(g * (s * sg), u * (s * su), p.clamp);
-            if (t < left && n < I) out[t * p.ldo] = h;
+          for (int c = 0; c < 32; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(scales + 32 * i + c);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const uint32_t x = v[i][c + k], y = v[i][c + k + 1];
+              const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, high ? x : y, 16);
+              const float sc = k ? (high ? f.w : f.z) : (high ? f.y : f.x);
+              v[i][c + k] = __float_as_uint(swiglu(__uint_as_float(high ? o : x) * (sc * sg),
+                                                   __uint_as_float(high ? y : o) * (sc * su),
+                                                   p.clamp));
+            }
           }
+          // (the stores after all 32 tokens' sums: no load or step waits for one)
+          const int rest = left - 32 * i - (high ? 1 : 0);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) st_if_b32(c < rest && n < I, out + c * p.ldo, v[i][c]);
+          out += 32 * p.ldo;
         }
       } else {
         const int n = it.tile * kI8Tile + rank * 128 + quarter * 32 + lane;
@@ -834,7 +876,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     bool pending = false;
     for (int item = first; ok; item += step) {
       const bool more = item < total;
-      const int n = more ? blocks : 0, ahead = min(kP8Buffers, n);
+      const int n = more ? blocks : 0, ahead = min(kP8Buffers - 1, n);
       for (int kb = 0;; ++kb) {
         if (pending && kb == ahead) {
           ok = results(before);
