@@ -15,12 +15,22 @@
 // the sum is 0, so there too only the chosen experts' logits have a gradient).
 //
 // Sigmoid and softmax rise with the logit, so without a bias the choice goes by
-// the logits themselves.  With one, two choices may be nearer to each other than
-// fp32 tells apart (9 gaps of about 0.01 at K = 8 and E = 384, and scores off by
-// up to 4e-7: one token in a thousand); such a token is decided again in 64 bits.
+// the logits themselves.
+//
+// A warp takes a token; a lane holds a run of neighbouring experts of one group.
+// Each choice becomes a 32-bit word that orders as it does: the float's bits (made
+// positive) but the last four, which hold 15 - j for the lane's j-th expert.  So
+// one redux.sync finds a round's winner and, with a vote for the lane, its index,
+// and a lane's two largest words, which are all that a group's score needs too,
+// take three operations an expert.  (Keys and indices apart took 1880 instructions
+// a token, this 400.)  The words are coarser than fp32, and fp32 scores are off by
+// a few 2^-24: where the order of neighbours, or the border, could be another, the
+// token is decided again in 64 bits, its near choices only (at E = 384 and K = 8
+// nine gaps of about 0.008 against 5e-6: one token in two hundred).
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -94,15 +104,19 @@ __device__ __forceinline__ uint64_t order_key(double v) {
   return b >> 63 ? ~b : b | (uint64_t{1} << 63);
 }
 
-// How far apart two choices that were worked out in fp32 have to be for their
-// order to be certain; s the larger score, c the larger choice.  Sigmoid: the
-// power is off by (2 + 1.5 |l|) 2^-24 of itself, which moves s by s (1 - s) of
-// that (|l| s (1 - s) <= 0.23), sum and quotient by 2^-23 s: below 3 2^-23 in
-// all, twice for two.  Softmax: sum and powers are off by at most 50 2^-24 of
-// themselves beside |d| e^d <= 0.37.  Adding the bias: 2^-24 |c|.
-__device__ __forceinline__ float doubt(bool softmax, float s, float c) {
-  const float of_sum = 0x1p-22f * fabsf(c);
-  return softmax ? 0x1p-17f * fabsf(s) + 0x1p-22f + of_sum : 0x1p-20f + of_sum;
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// How far apart two scores that were worked out in fp32, s the larger at most, have
+// to be for their order to be certain.  Sigmoid: the power is off by (2 + 1.5 |l|)
+// 2^-24 of itself, which moves s by s (1 - s) of that (|l| s (1 - s) <= 0.23), sum
+// and reciprocal by 2^-23 s: below 3 2^-23 in all, twice for two.  Softmax: sum and
+// powers are off by at most 50 2^-24 of themselves beside |d| e^d <= 0.37.
+__device__ __forceinline__ float doubt(bool softmax, float s) {
+  return softmax ? 0x1p-17f * s + 0x1p-22f : 0x1p-20f;
 }
 
 // The lane's share of a row: `per` experts of its group from `base` on, n real.
@@ -142,38 +156,74 @@ __device__ __forceinline__ void load_share(const T* __restrict__ row, const Shar
 }
 
 // ---------------------------------------------------------------- 64 bits
-// The choice of one token in 64 bits, by the whole warp: lane k < K receives the
-// k-th expert.  Rare, so it reads the row again and keeps its values in local
-// memory.
+// Scores of one token in 64 bits.
 template <typename T>
-__device__ __noinline__ int choose_exact(const T* __restrict__ row, const GateArgs& p) {
+struct ExactScore {
+  bool softmax, by_choice;
+  double top = 0.0, inv = 1.0;
+  // The whole warp; sum: whether a softmax's sum is wanted.
+  __device__ ExactScore(const T* row, const GateArgs& p, const Share& sh, bool sum_wanted)
+      : softmax(p.softmax != 0), by_choice(p.bias != nullptr) {
+    if (!softmax || !sum_wanted) return;
+    float m = -INFINITY;
+    for (int j = 0; j < sh.n; ++j) {
+      const float l = to_f32(row[sh.base + j]);
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(l));
+    }
+    top = static_cast<double>(warp_max(m));
+    double sum = 0.0;
+    for (int j = 0; j < sh.n; ++j) sum += exp(static_cast<double>(to_f32(row[sh.base + j])) - top);
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, off);
+    inv = 1.0 / sum;
+  }
+  __device__ double score(float l) const {
+    const double d = static_cast<double>(l);
+    return softmax ? exp(d - top) * inv : 1.0 / (1.0 + exp(-d));
+  }
+  // What an expert is chosen by: -inf if it is disabled.
+  __device__ double choice(float l, const float* bias) const {
+    if (l == -INFINITY) return -INFINITY;
+    return by_choice ? score(l) + static_cast<double>(*bias) : static_cast<double>(l);
+  }
+};
+
+// The experts marked in the lanes' masks (bit j: the lane's j-th), one to a lane in
+// order of their indices; returns how many there are, at most 33.
+__device__ __forceinline__ int collect(uint32_t mask, const Share& sh, int lane, int& e, int& from) {
+  int m = 0;
+  for (;;) {
+    const unsigned left = __ballot_sync(kAllLanes, mask != 0u);
+    if (!left || m == 33) return m;
+    const int owner = __ffs(left) - 1;
+    const int found = __shfl_sync(kAllLanes, sh.base + __ffs(mask) - 1, owner);
+    if (lane == m) {
+      e = found;
+      from = owner;
+    }
+    if (lane == owner) mask &= mask - 1;
+    ++m;
+  }
+}
+
+// The choice of one token in 64 bits, by the whole warp: lane k < K receives the
+// k-th expert.  all: groups and every expert; else only the experts `among` (a bit
+// each).  For tokens with a NaN or masses of ties, so it keeps its values in local
+// memory and takes its time.
+template <typename T>
+__device__ __noinline__ int choose_slowly(const T* __restrict__ row, const GateArgs& p, bool all,
+                                          uint32_t among) {
   constexpr int kMost = 32;
   const int lane = threadIdx.x & 31;
   const Share sh(p, lane);
-  double m = 0.0, r = 1.0;
-  if (p.softmax) {
-    float top = -INFINITY;
-    for (int j = 0; j < sh.n; ++j) top = fmaxf(top, to_f32(row[sh.base + j]));
-    m = static_cast<double>(warp_max(top));
-    double sum = 0.0;
-    for (int j = 0; j < sh.n; ++j) sum += exp(static_cast<double>(to_f32(row[sh.base + j])) - m);
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, off);
-    r = 1.0 / sum;
-  }
-  auto score = [&](float l) {
-    const double d = static_cast<double>(l);
-    return p.softmax ? exp(d - m) * r : 1.0 / (1.0 + exp(-d));
-  };
+  const uint32_t wanted = !all ? among : sh.n >= 32 ? 0xFFFFFFFFu : (1u << sh.n) - 1u;
+  const ExactScore<T> x(row, p, sh, true);
   double c[kMost];
   for (int j = 0; j < kMost; ++j) {
     c[j] = -INFINITY;
-    if (j >= sh.n) continue;
-    const float l = to_f32(row[sh.base + j]);
-    if (l == -INFINITY) continue;
-    c[j] = p.bias ? score(l) + static_cast<double>(p.bias[sh.base + j]) : static_cast<double>(l);
+    if (wanted >> j & 1u) c[j] = x.choice(to_f32(row[sh.base + j]), p.bias + sh.base + j);
   }
   bool kept = sh.in;
-  if (p.group_top < p.groups) {
+  if (all && p.group_top < p.groups) {
     double a = -INFINITY, b = -INFINITY;  // the group's two largest
     auto put = [&](double v) {
       if (order_key(v) > order_key(a)) {
@@ -194,8 +244,8 @@ __device__ __noinline__ int choose_exact(const T* __restrict__ row, const GateAr
       if (p.bias)
         v = a + b;
       else
-        v = (a == -INFINITY ? a : score(static_cast<float>(a))) +
-            (b == -INFINITY ? b : score(static_cast<float>(b)));
+        v = (a == -INFINITY ? a : x.score(static_cast<float>(a))) +
+            (b == -INFINITY ? b : x.score(static_cast<float>(b)));
     }
     const uint64_t mine = order_key(v);
     int rank = 0;
@@ -205,8 +255,7 @@ __device__ __noinline__ int choose_exact(const T* __restrict__ row, const GateAr
     }
     kept = kept && rank < p.group_top;
   }
-  uint32_t open = 0u;  // the lane's experts that are still to be chosen
-  if (kept) open = sh.n >= 32 ? 0xFFFFFFFFu : (1u << sh.n) - 1u;
+  uint32_t open = kept ? wanted : 0u;  // the lane's experts that are still to be chosen
   int id = 0;
   for (int k = 0; k < p.K; ++k) {
     uint64_t best = 0;
@@ -229,6 +278,68 @@ __device__ __noinline__ int choose_exact(const T* __restrict__ row, const GateAr
   return id;
 }
 
+// The same among a few experts, which are scored at once, one to a lane.
+template <typename T>
+__device__ __noinline__ int choose_exact(const T* __restrict__ row, const GateArgs& p,
+                                         uint32_t among) {
+  const int lane = threadIdx.x & 31;
+  const Share sh(p, lane);
+  int e = 0, from = 0;
+  const int m = collect(among, sh, lane, e, from);
+  if (m > 32) return choose_slowly(row, p, false, among);
+  const ExactScore<T> x(row, p, sh, p.bias != nullptr);
+  const double c = lane < m ? x.choice(to_f32(row[e]), p.bias + e) : -INFINITY;
+  int rank = 0;
+  for (int i = 0; i < m; ++i) {
+    const double o = __shfl_sync(kAllLanes, c, i);
+    rank += o > c || (o == c && i < lane);  // (the lanes' experts rise)
+  }
+  int id = 0;
+  for (int i = 0; i < m; ++i) {
+    const int r = __shfl_sync(kAllLanes, rank, i), found = __shfl_sync(kAllLanes, e, i);
+    if (lane == r) id = found;
+  }
+  return id;
+}
+
+// Whether this lane's group is among the group_top best, in 64 bits.  sure: it
+// certainly is; open: it may be, and `among` are the lane's experts that may be its
+// two largest.  2: too many to tell this way.
+template <typename T>
+__device__ __noinline__ int groups_exact(const T* __restrict__ row, const GateArgs& p, bool sure,
+                                         bool open, uint32_t among) {
+  const int lane = threadIdx.x & 31;
+  const Share sh(p, lane);
+  int e = 0, from = 0;
+  const int m = collect(open ? among : 0u, sh, lane, e, from);
+  if (m > 32) return 2;
+  const bool pair = p.top2 && p.size > 1;
+  const ExactScore<T> x(row, p, sh, p.bias != nullptr || pair);
+  const float l = lane < m ? to_f32(row[e]) : -INFINITY;
+  double c = lane < m ? x.choice(l, p.bias + e) : -INFINITY;
+  // (the logits order as their scores, and the sum is of scores)
+  if (pair && !p.bias && lane < m && l != -INFINITY) c = x.score(l);
+  const int of = from / p.lanes;
+  double a = -INFINITY, b = -INFINITY;
+  for (int i = 0; i < m; ++i) {
+    const double o = __shfl_sync(kAllLanes, c, i);
+    const int group = __shfl_sync(kAllLanes, of, i);
+    if (group == sh.group) {
+      b = o > a ? a : o > b ? o : b;
+      a = o > a ? o : a;
+    }
+  }
+  const double v = pair ? a + b : a;
+  int left = p.group_top, rank = 0;
+  for (int g = 0; g < p.groups; ++g) {
+    const double o = __shfl_sync(kAllLanes, v, g * p.lanes);
+    left -= __shfl_sync(kAllLanes, static_cast<int>(sure), g * p.lanes);
+    const int other = __shfl_sync(kAllLanes, static_cast<int>(open), g * p.lanes);
+    rank += other && (o > v || (o == v && g < sh.group));
+  }
+  return sure || (open && rank < left);
+}
+
 // ---------------------------------------------------------------- forward
 // Unnormalised weight of a chosen logit; top: the largest chosen logit.  Stable
 // for any logits: sigmoid(l) = e^min(l, 0) / (1 + e^-|l|), and the ratios of
@@ -242,188 +353,212 @@ __device__ __forceinline__ float sigmoid_exactly(float l) {
   return expf(fminf(l, 0.0f)) / (1.0f + expf(-fabsf(l)));
 }
 
-// One token by a warp.  bias: this lane's share (0 where there is none).
-// Returns whether the token is live; lane k < K receives the k-th expert and its
-// weight.
-template <int NL, typename T>
+// How the words are made: from choices with a bias (less the least bias, plus 1/16,
+// so positive), from fp32 logits, or from bf16 logits, whose 16-bit keys leave room
+// for the expert's own index: those words are exact.
+enum { kByChoice, kByLogit, kByShortLogit };
+
+// One token by a warp.  bias: this lane's share, less the least bias, plus 1/16.
+// exact: decide in 64 bits from the start.  Returns whether the token is live; lane
+// k < K receives the k-th expert and its weight.
+template <int NL, int MODE, typename T>
 __device__ __forceinline__ bool gate_token(const T* __restrict__ row, const GateArgs& p,
-                                           const Share& sh, const float (&bias)[NL], int lane,
-                                           int* id_out, float* w_out) {
+                                           const Share& sh, const float (&bias)[NL], bool exact,
+                                           int lane, int* id_out, float* w_out) {
+  // last bits of a word: kLow - j for the lane's j-th expert
+  constexpr uint32_t kLow = NL > 16 ? 31u : 15u;
+  constexpr float kCut = (kLow + 1) * 0x1p-23f;  // what they are of the value, at most
   const bool softmax = p.softmax != 0;
-  float x[NL];
-  load_share<NL>(row, sh, p.vec != 0, x);
-  float top = -INFINITY;
+  uint32_t word[NL], first = 0u, second = 0u;
+  float top = 0.0f, inv = 1.0f;
+  bool all = exact;  // decide everything slowly, in 64 bits
+  {
+    float x[NL];
+    load_share<NL>(row, sh, p.vec != 0, x);
+    float odd = 0.0f;
 #pragma unroll
-  for (int j = 0; j < NL; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(x[j]));
-  top = warp_max(top);
-  if (top == -INFINITY) return false;
-  // the softmax's sum, where scores are wanted: with a bias, for sums of two, or
-  // for weights that are not normalised
-  float inv = 1.0f;
-  if (softmax && (p.bias || p.top2 || !p.normalize)) {
-    float sum = 0.0f;
+    for (int j = 0; j < NL; ++j) odd = fmaf(j < sh.n ? x[j] : 0.0f, 0.0f, odd);
+    bool off = false;  // whether some expert's logit is -inf
+    if (__any_sync(kAllLanes, odd != 0.0f)) {  // (an infinity or NaN times 0)
+      bool live = false, nan = false;
 #pragma unroll
-    for (int j = 0; j < NL; ++j) sum += exp_fast(x[j] - top);
-    inv = 1.0f / warp_sum(sum);
-  }
-  auto score = [&](float l) {
-    return softmax ? exp_fast(l - top) * inv : __fdividef(1.0f, 1.0f + exp_fast(-l));
-  };
-  // the choices; without a bias the logits, which order the same
-  float c[NL];
+      for (int j = 0; j < NL; ++j) {
+        live |= j < sh.n && x[j] != -INFINITY;
+        nan |= x[j] != x[j];
+        off |= j < sh.n && x[j] == -INFINITY;
+      }
+      if (!__any_sync(kAllLanes, live)) return false;
+      all |= __any_sync(kAllLanes, nan);
+      off = __any_sync(kAllLanes, off);
+    }
+    if (softmax && (MODE == kByChoice || p.top2)) {
+      top = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < NL; ++j)
-    c[j] = p.bias && x[j] != -INFINITY ? score(x[j]) + bias[j] : x[j];
-  bool unsure = false, kept = sh.in;
-  if (p.group_top < p.groups) {
-    float a = -INFINITY, b = -INFINITY;  // the group's two largest
+      for (int j = 0; j < NL; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(x[j]));
+      top = warp_max(top);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NL; ++j) sum += exp_fast(x[j] - top);
+      inv = 1.0f / warp_sum(sum);
+      all |= inv != inv;
+    }
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
-      float low = a;
-      asm("min.NaN.f32 %0, %0, %1;" : "+f"(low) : "f"(c[j]));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(c[j]));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(low));
+      if constexpr (MODE == kByChoice) {
+        const float s = softmax ? exp_fast(x[j] - top) * inv : rcp_fast(1.0f + exp_fast(-x[j]));
+        word[j] = (__float_as_uint(s + bias[j]) & ~kLow) | (kLow - j);
+      } else {
+        const uint32_t key = logit_key(x[j]);
+        word[j] = MODE == kByLogit ? (key & ~kLow) | (kLow - j)
+                                   : (key & 0xFFFF0000u) | static_cast<uint32_t>(0xFFFF - sh.base - j);
+      }
+      if (j >= sh.n) word[j] = 0u;
     }
-    for (int off = 1; off < p.lanes; off <<= 1) {
-      const float oa = __shfl_xor_sync(kAllLanes, a, off), ob = __shfl_xor_sync(kAllLanes, b, off);
-      float low = a;
-      asm("min.NaN.f32 %0, %0, %1;" : "+f"(low) : "f"(oa));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(oa));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(low));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(ob));
-    }
-    float v = a;
-    const bool pair = p.top2 && p.size > 1;
-    if (pair) {
-      if (p.bias)
-        v = a + b;
-      else
-        v = (a == -INFINITY ? a : score(a)) + (b == -INFINITY ? b : score(b));
-    }
-    // (a NaN anywhere in the sums above: the exact choice orders it)
-    const uint32_t mine = order_key(v);
-    int rank = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const uint32_t o = __shfl_sync(kAllLanes, mine, g * p.lanes);
-      rank += o > mine || (o == mine && g < sh.group);
-    }
-    kept = kept && rank < p.group_top;
-    unsure = v != v;
-    if (p.bias || pair) {
-      const uint32_t last = __reduce_min_sync(kAllLanes, kept ? mine : 0xFFFFFFFFu);
-      const uint32_t next = __reduce_max_sync(kAllLanes, sh.in && !kept ? mine : 0u);
-      const float vl = key_logit(last), vn = key_logit(next);
-      // (two choices, so twice the doubt; their scores are at most 1 each)
-      unsure |= vl - vn <= 2.0f * doubt(softmax, 1.0f, fmaxf(fabsf(vl), fabsf(a) + fabsf(b)));
-    }
-  }
-  // K rounds: the largest key, the lowest lane that has it, the lane's lowest
-  // expert.  A lane keeps its two largest; one that wins a second time looks
-  // through its share for the next.
-  uint32_t first = 0u, second = 0u;
-  int at1 = 0, at2 = 0;
-  uint32_t key[NL];
+    if (MODE == kByChoice && off) {
+      // (the last of all, their order left to 64 bits)
 #pragma unroll
-  for (int j = 0; j < NL; ++j) {
-    key[j] = kept && j < sh.n ? order_key(c[j]) : 0u;
-    if (key[j] > first) {
-      second = first;
-      at2 = at1;
-      first = key[j];
-      at1 = j;
-    } else if (key[j] > second) {
-      second = key[j];
-      at2 = j;
+      for (int j = 0; j < NL; ++j)
+        if (j < sh.n && x[j] == -INFINITY) word[j] = (kLow + 1) | (kLow - j);
+    }
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+      second = max(second, min(first, word[j]));
+      first = max(first, word[j]);
     }
   }
-  int id = 0;
-  uint32_t chosen = 0u;
+  auto score = [&](float l) {
+    return softmax ? exp_fast(l - top) * inv : rcp_fast(1.0f + exp_fast(-l));
+  };
+  // how near two choices, the larger of them c, may be for their order to be in doubt
+  auto margin = [&](float c) {
+    return doubt(softmax, fmaxf(c - 0.0625f, 0.0f)) + c * (0x1p-21f + kCut);
+  };
+  // whether the expert of `lo` could belong before that of `hi`
+  auto near = [&](uint32_t hi, uint32_t lo) {
+    if constexpr (MODE == kByShortLogit) return false;
+    if constexpr (MODE == kByLogit) return ((hi ^ lo) & ~kLow) == 0u;
+    const float c = __uint_as_float(hi & ~kLow);
+    return c - __uint_as_float(lo & ~kLow) <= margin(c);
+  };
+  bool kept = sh.in;
+  if (p.group_top < p.groups) {
+    uint32_t a = first, b = second;  // the group's two largest
+    for (int o = 1; o < p.lanes; o <<= 1) {
+      const uint32_t oa = __shfl_xor_sync(kAllLanes, a, o), ob = __shfl_xor_sync(kAllLanes, b, o);
+      b = max(max(b, ob), min(a, oa));
+      a = max(a, oa);
+    }
+    const bool pair = p.top2 && p.size > 1;
+    int rank = 0;
+    if (MODE == kByShortLogit && !pair) {
+      // (the words of different groups differ, and order by index where logits tie)
+      for (int g = 0; g < p.groups; ++g) rank += __shfl_sync(kAllLanes, a, g * p.lanes) > a;
+      kept = kept && rank < p.group_top;
+    } else {
+      float v, d;
+      if constexpr (MODE == kByChoice) {
+        // (a disabled expert's word stands for a choice of -inf)
+        const float va = a <= 2 * kLow + 1 ? -INFINITY : __uint_as_float(a & ~kLow);
+        const float vb = b <= 2 * kLow + 1 ? -INFINITY : __uint_as_float(b & ~kLow);
+        v = pair ? va + vb : va;
+        d = pair ? 2.0f * margin(fmaxf(va, 0.0f)) + 0x1p-22f * fmaxf(v, 0.0f) : margin(fmaxf(va, 0.0f));
+      } else {
+        auto logit = [&](uint32_t w) {
+          if (MODE == kByLogit) return key_logit(w & ~kLow);
+          return key_logit(w >> 31 ? w & 0xFFFF0000u : w | 0xFFFFu);
+        };
+        const float la = logit(a), lb = logit(b);
+        v = pair ? score(la) + score(lb) : la;
+        d = pair ? 2.0f * doubt(softmax, 1.0f) + 0x1p-21f + 2.0f * kCut * (fabsf(la) + fabsf(lb)) : 0.0f;
+        // (a group with fewer than two enabled experts)
+        if (pair && !(lb > -FLT_MAX)) v = NAN;
+      }
+      for (int g = 0; g < p.groups; ++g) rank += __shfl_sync(kAllLanes, v, g * p.lanes) > v;
+      kept = kept && rank < p.group_top;
+      // the border: the least of the kept, and the largest of the others
+      const uint32_t mine = order_key(v);
+      const float vl = key_logit(__reduce_min_sync(kAllLanes, kept ? mine : 0xFF800000u));
+      const float vn = key_logit(__reduce_max_sync(kAllLanes, sh.in && !kept ? mine : 0x007FFFFFu));
+      const int groups = __popc(__ballot_sync(kAllLanes, kept && lane % p.lanes == 0));
+      // (equal ones, and NaN: more than group_top may have been kept)
+      if (__any_sync(kAllLanes, v != v || !(vl - vn > d) || groups != p.group_top)) {
+        // the largest doubt of any group decides which are open
+        const float most = warp_max(sh.in ? d : 0.0f);
+        const bool sure = kept && v > vn + most && v > vl + most, open = sh.in && !sure && v >= vl - most;
+        uint32_t among = 0u;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+          // (what may be its group's second largest, or largest)
+          const uint32_t least = pair ? b : a;
+          among |= static_cast<uint32_t>(j < sh.n && (word[j] >= least || near(least, word[j]))) << j;
+        }
+        const bool odd = __any_sync(kAllLanes, v != v || !(most < INFINITY));
+        const int in = odd ? 2 : groups_exact(row, p, sure, open, among);
+        all |= in == 2;
+        kept = in == 1;
+      }
+    }
+    if (!kept) first = second = 0u;
+  }
+  // K rounds: the largest word and the lowest lane that has it.  A lane that has won
+  // twice looks through its share for the next.
+  uint32_t mine = 0u;
+  int from = 0;
   for (int k = 0; k < p.K; ++k) {
     const uint32_t w = __reduce_max_sync(kAllLanes, first);
     const int winner = __ffs(__ballot_sync(kAllLanes, first == w)) - 1;
-    const int e = __shfl_sync(kAllLanes, sh.base + at1, winner);
     if (lane == k) {
-      id = e;
-      chosen = w;
+      mine = w;
+      from = winner;
     }
-    bool search = false;
-    uint32_t won = 0u;
-    int won_at = 0;
-    if (lane == winner) {
-      search = second == 0u;
-      won = first;
-      won_at = at1;
-      first = second;
-      at1 = at2;
-      second = 0u;
-    }
-    if (__any_sync(kAllLanes, search)) {
-      uint32_t f = 0u;
-      int fa = 0;
+    const bool won = lane == winner;
+    first = won ? second : first;
+    second = won ? 0u : second;
+    if (__any_sync(kAllLanes, won && first == 0u)) {
+      uint32_t next = 0u;
 #pragma unroll
-      for (int j = 0; j < NL; ++j)
-        if ((key[j] < won || (key[j] == won && j > won_at)) && key[j] > f) {
-          f = key[j];
-          fa = j;
-        }
-      if (search) {
-        first = f;
-        at1 = fa;
-      }
+      for (int j = 0; j < NL; ++j) next = max(next, word[j] < w ? word[j] : 0u);
+      if (won) first = next;
     }
   }
-  // (fp32 keys of choices with a bias: the order of neighbours, and that nothing
-  // that was left out belongs before the last)
-  const float l = lane < p.K ? to_f32(row[id]) : -INFINITY;
-  if (p.bias) {
-    const float mine = lane < p.K ? key_logit(chosen) : 0.0f;
-    const float b = lane < p.K ? p.bias[id] : 0.0f;
-    const float next = __shfl_down_sync(kAllLanes, mine, 1);
-    const float nl = __shfl_down_sync(kAllLanes, l, 1), nb = __shfl_down_sync(kAllLanes, b, 1);
-    if (lane + 1 < p.K)
-      unsure |= mine - next <= doubt(softmax, fmaxf(fabsf(mine - b), fabsf(next - nb)),
-                                     fmaxf(fabsf(mine), fabsf(next))) &&
-                !(l == nl && b == nb);
-    const float last = __shfl_sync(kAllLanes, mine, p.K - 1);
-    const float ll = __shfl_sync(kAllLanes, l, p.K - 1), lb = __shfl_sync(kAllLanes, b, p.K - 1);
-    const int last_id = __shfl_sync(kAllLanes, id, p.K - 1);
-    const uint32_t last_key = order_key(last);
-    const float least = last - doubt(softmax, last - lb, last), own = softmax ? 0x1p-17f : 0.0f;
-    bool near = false;
+  int id = 0;
+  bool unsure = all;
+  const uint32_t last = __shfl_sync(kAllLanes, mine, p.K - 1);
+  if constexpr (MODE == kByShortLogit) {
+    id = 0xFFFF - static_cast<int>(mine & 0xFFFFu);
+  } else {
+    id = from / p.lanes * p.size + from % p.lanes * p.per + static_cast<int>(kLow - (mine & kLow));
+    const uint32_t after = __shfl_down_sync(kAllLanes, mine, 1);
+    unsure |= (lane + 1 < p.K && near(mine, after)) || (first != 0u && near(last, first));
+  }
+  if (__any_sync(kAllLanes, unsure)) {
+    uint32_t among = 0u;
 #pragma unroll
     for (int j = 0; j < NL; ++j)
-      near |= key[j] != 0u && fmaf(own, fabsf(c[j] - bias[j]), c[j]) >= least;
-    if (__any_sync(kAllLanes, near)) {
-      // (the chosen ones are near too: those come before the last by key and index)
-#pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        const bool after = key[j] < last_key || (key[j] == last_key && sh.base + j > last_id);
-        unsure |= key[j] != 0u && fmaf(own, fabsf(c[j] - bias[j]), c[j]) >= least && after &&
-                  !(x[j] == ll && bias[j] == lb);
-      }
-    }
-  }
-  float mine_l = l;
-  if (__any_sync(kAllLanes, unsure)) {
-    id = choose_exact(row, p);
-    mine_l = lane < p.K ? to_f32(row[id]) : -INFINITY;
+      among |= static_cast<uint32_t>(j < sh.n && kept && (word[j] >= last || near(last, word[j]))) << j;
+    id = all ? choose_slowly(row, p, true, 0u) : choose_exact(row, p, among);
   }
   const bool used = lane < p.K;
+  const float l = used ? to_f32(row[id]) : -INFINITY;
   float w;
   if (p.normalize) {
-    const float m = warp_max(used ? mine_l : -INFINITY);
-    const float t = used ? ratio_term(softmax, mine_l, m) : 0.0f;
+    const float m = warp_max(l);
+    const float t = used ? ratio_term(softmax, l, m) : 0.0f;
     const float sum = warp_sum(t);
     w = sum == 0.0f ? 0.0f : t / sum;
   } else if (softmax) {
-    // (the sum of powers above, once more with the exact ones)
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NL; ++j) sum += j < sh.n ? expf(x[j] - top) : 0.0f;
+    // (the whole row once more, with expf)
+    float m = -INFINITY, sum = 0.0f;
+    for (int e = lane; e < p.E; e += 32) {
+      const float v = to_f32(row[e]);
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v));
+    }
+    m = warp_max(m);
+    for (int e = lane; e < p.E; e += 32) sum += expf(to_f32(row[e]) - m);
     sum = warp_sum(sum);
-    w = used ? expf(mine_l - top) / sum : 0.0f;
+    w = used ? expf(l - m) / sum : 0.0f;
   } else {
-    w = used ? sigmoid_exactly(mine_l) : 0.0f;
+    w = used ? sigmoid_exactly(l) : 0.0f;
   }
   *id_out = id;
   *w_out = p.scale * w;
@@ -435,10 +570,10 @@ constexpr int kGateWarps = 16;
 // itself (16 tokens of 64 experts: one launch instead of two).
 constexpr int kGateSmall = 32;
 
-// SMALL: one block.  Else the counts are zero already (once the kernel before
-// this one is over) and the blocks add theirs: whole numbers, so the order does
-// not matter.
-template <int NL, bool SMALL, typename T>
+// SMALL: one block.  Else the counts are zero already (once the kernel before this
+// one is over) and the blocks add theirs: whole numbers, so the order does not
+// matter.
+template <int NL, int MODE, bool SMALL, typename T>
 __global__ void __launch_bounds__(SMALL ? 1024 : 32 * kGateWarps, SMALL ? 1 : NL > 16 ? 1 : 2)
     gate_forward_kernel(const T* __restrict__ logits, const __grid_constant__ GateArgs p) {
   __shared__ int s_count[kMaxExperts];
@@ -448,14 +583,26 @@ __global__ void __launch_bounds__(SMALL ? 1024 : 32 * kGateWarps, SMALL ? 1 : NL
   __syncthreads();
   const Share sh(p, lane);
   float bias[NL];
+  bool exact = false;  // a bias that is no number
+  if constexpr (MODE == kByChoice) {
+    float least = INFINITY, odd = 0.0f;
 #pragma unroll
-  for (int j = 0; j < NL; ++j) bias[j] = p.bias && j < sh.n ? p.bias[sh.base + j] : 0.0f;
+    for (int j = 0; j < NL; ++j) {
+      bias[j] = j < sh.n ? p.bias[sh.base + j] : INFINITY;
+      least = fminf(least, bias[j]);
+      if (j < sh.n) odd = fmaf(bias[j], 0.0f, odd);
+    }
+    least = -warp_max(-least);
+    exact = __any_sync(kAllLanes, odd != 0.0f);
+#pragma unroll
+    for (int j = 0; j < NL; ++j) bias[j] = j < sh.n ? bias[j] - least + 0.0625f : 0.0625f;
+  }
   for (int t = blockIdx.x + gridDim.x * warp; t < p.T; t += gridDim.x * warps) {
     int id = -1;
     float w = 0.0f;
-    const bool live =
-        (!p.mask || p.mask[t]) &&
-        gate_token<NL>(logits + static_cast<int64_t>(t) * p.ld, p, sh, bias, lane, &id, &w);
+    const bool live = (!p.mask || p.mask[t]) &&
+                      gate_token<NL, MODE>(logits + static_cast<int64_t>(t) * p.ld, p, sh, bias,
+                                           exact, lane, &id, &w);
     if (lane < p.K) {
       p.ids[static_cast<int64_t>(t) * p.K + lane] = live ? id : -1;
       p.weights[static_cast<int64_t>(t) * p.K + lane] = live ? w : 0.0f;
@@ -724,18 +871,22 @@ cudaError_t run_forward(const T* logits, GateArgs p, cudaStream_t s) {
   p.per = (p.size + p.lanes - 1) / p.lanes;
   p.vec = aligned_to(logits, 4 * sizeof(T)) && p.ld % 4 == 0 && p.size % 4 == 0;
   if (p.vec) p.per = (p.per + 3) / 4 * 4;
-  return by_share(p.per, [&](auto nl) {
-    constexpr int kN = decltype(nl)::value;
+  auto with = [&](auto nl, auto mode) {
+    constexpr int kN = decltype(nl)::value, kMode = decltype(mode)::value;
     if (p.T <= kGateSmall)
-      return launch_pdl(false, gate_forward_kernel<kN, true, T>, dim3(1),
+      return launch_pdl(false, gate_forward_kernel<kN, kMode, true, T>, dim3(1),
                         dim3(32 * std::max(p.T, 1)), 0, s, logits, p);
     cudaError_t e =
         launch_pdl(false, gate_zero_kernel, dim3(1), dim3(kMaxExperts), 0, s, p.counts, p.E);
     if (e == cudaSuccess)
-      e = launch_pdl(true, gate_forward_kernel<kN, false, T>,
+      e = launch_pdl(true, gate_forward_kernel<kN, kMode, false, T>,
                      dim3(std::min((kN > 16 ? 1 : 2) * kSms, (p.T + kGateWarps - 1) / kGateWarps)),
                      dim3(32 * kGateWarps), 0, s, logits, p);
     return e;
+  };
+  return by_share(p.per, [&](auto nl) {
+    if (p.bias) return with(nl, std::integral_constant<int, kByChoice>{});
+    return with(nl, std::integral_constant<int, sizeof(T) == 4 ? kByLogit : kByShortLogit>{});
   });
 }
 
