@@ -438,30 +438,45 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
     // d z, d u and their dot products with d y
     float(*dots)[32] = s_dot[parity];
     const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(j.expert_rows);
-    for (int k = 0; k < j.K; ++k) {
-      const int row = j.row_of_slot[t * j.K + k];
-      const bool in = row >= 0 && row < j.rows;
-      const float w = in ? j.weights[t * j.K + k] : 0.0f;
-      float dot = 0.0f;
-      if (in) {
+    for (int k0 = 0; k0 < j.K; k0 += kAtOnce) {
+      int row[kAtOnce];
+      float dot[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          float a[kVec];
-          if (p.d_weights) {
-            load8<VEC>(z + row * j.ld_rows, i, H, a);
+      for (int q = 0; q < kAtOnce; ++q) {
+        const int r = k0 + q < j.K ? j.row_of_slot[t * j.K + k0 + q] : -1;
+        row[q] = r < j.rows ? r : -1;
+        dot[q] = 0.0f;
+      }
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) dot = fmaf(g[i][c], a[c], dot);
-          }
-          if (p.d_rows) {
+      for (int i = 0; i < NV; ++i) {
+        if (p.d_weights) {
+          float a[kAtOnce][kVec];
+#pragma unroll
+          for (int q = 0; q < kAtOnce; ++q)
+            load8<VEC>(z + max(row[q], 0) * j.ld_rows, i, row[q] < 0 ? 0 : H, a[q]);
+#pragma unroll
+          for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) dot[q] = fmaf(g[i][c], a[q][c], dot[q]);
+        }
+        if (p.d_rows) {
+#pragma unroll
+          for (int q = 0; q < kAtOnce; ++q) {
+            if (row[q] < 0) continue;
+            const float w = j.weights[t * j.K + k0 + q];
+            float a[kVec];
 #pragma unroll
             for (int c = 0; c < kVec; ++c) a[c] = w * g[i][c];
-            store8<VEC>(p.d_rows + row * p.ld_drows, i, H, a);
+            store8<VEC>(p.d_rows + row[q] * p.ld_drows, i, H, a);
           }
         }
       }
       if (p.d_weights) {
-        dot = warp_sum(dot);
-        if (lane == 0) dots[k][warp] = dot;
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+          const float sum = warp_sum(dot[q]);
+          if (lane == 0 && k0 + q < j.K) dots[k0 + q][warp] = row[q] < 0 ? 0.0f : sum;
+        }
       }
     }
     if (j.shared && (p.d_shared || p.d_gate)) {
@@ -595,39 +610,41 @@ bool join_vectors(const moe_join& j) {
          in_vectors(j.norm_weight, 0, 1);
 }
 
-// Vectors per thread: as few as 512 threads allow, or (wide) 1024 of one.
+// Vectors per thread: one up to 1024 threads, else as few as 512 threads allow.
+// (More threads with little to keep beat fewer with more: 4096 x 7168 in two vectors
+// of 448 threads took 150 us forward and 470 backward.)
 struct Shape {
   int nv, threads;
 };
-Shape shape_of(int H, bool wide) {
+Shape shape_of(int H) {
   const int vectors = (H + kVec - 1) / kVec;
   int nv = 1;
-  while ((vectors + nv - 1) / nv > (wide && nv == 1 ? 1024 : 512)) nv *= 2;
+  while ((vectors + nv - 1) / nv > (nv == 1 ? 1024 : 512)) nv *= 2;
   return {nv, ((vectors + nv - 1) / nv + 31) / 32 * 32};
 }
 
 template <typename X, bool VEC>
 cudaError_t run_forward(const JoinArgs& p, cudaStream_t s) {
   const int T = p.j.T;
-  // Few tokens: as many threads as a block has, each with little to wait for.
-  // Many: blocks that fit twice into an SM, so that one's sums hide behind the
-  // other's loads.
-  const bool few = T <= kSms;
-  const Shape q = shape_of(p.j.H, few);
+  const Shape q = shape_of(p.j.H);
   auto go = [&](auto k) { return launch_pdl(false, k, dim3(T), dim3(q.threads), 0, s, p); };
   if (q.nv == 1) return go(join_forward_kernel<X, 1, VEC>);
   if (q.nv == 2) return go(join_forward_kernel<X, 2, VEC>);
   return go(join_forward_kernel<X, 4, VEC>);
 }
 
-constexpr int kBackBlocks = 2 * kSms;
-int back_blocks(int T) { return std::max(1, std::min(T, kBackBlocks)); }
+// Blocks of the backward pass: as many as run at a time.
+int back_blocks(int T, int H) {
+  const Shape q = shape_of(H);
+  const int resident = std::max(1, std::min(8, 65536 / ((q.nv == 1 ? 64 : 128) * q.threads)));
+  return std::max(1, std::min(T, resident * kSms));
+}
 
 template <typename X, bool VEC>
 cudaError_t run_backward(const JoinBackArgs& p, cudaStream_t s) {
-  const Shape q = shape_of(p.j.H, false);
+  const Shape q = shape_of(p.j.H);
   auto go = [&](auto k) {
-    return launch_pdl(false, k, dim3(back_blocks(p.j.T)), dim3(q.threads), 0, s, p);
+    return launch_pdl(false, k, dim3(back_blocks(p.j.T, p.j.H)), dim3(q.threads), 0, s, p);
   };
   if (q.nv == 1) return go(join_backward_kernel<X, 1, VEC>);
   if (q.nv == 2) return go(join_backward_kernel<X, 2, VEC>);
@@ -677,7 +694,7 @@ moe_status moe_join_forward(const moe_join* j, void* x_out, int64_t ld_out, void
 
 size_t moe_join_workspace(int T, int H) {
   if (T < 1 || H < 1 || H > kMaxWidth) return 0;
-  return static_cast<size_t>(2) * back_blocks(T) * ((H + 3) / 4 * 4) * 4;
+  return static_cast<size_t>(2) * back_blocks(T, H) * ((H + 3) / 4 * 4) * 4;
 }
 
 moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_out,
@@ -721,7 +738,7 @@ moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_ou
     p.d_weights = d_weights;
     p.d_shared = static_cast<__nv_bfloat16*>(d_shared), p.ld_dshared = ld_dshared;
     p.d_gate = d_gate;
-    f.blocks = back_blocks(j->T);
+    f.blocks = back_blocks(j->T, j->H);
     float* ws = static_cast<float*>(workspace);
     if (d_norm) f.part[0] = p.part_norm = ws;
     if (d_post)
