@@ -533,6 +533,12 @@ moe_status moe_join_backward(const moe_join *join, const void *x_out,
                              void *d_norm, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* Synchronises the device and returns (and clears) what the moe_join_* kernels
+ * recorded on it since the last call: MOE_ERR_DEVICE_TIMEOUT if one gave up a
+ * bounded wait (its outputs are incomplete), else MOE_OK; MOE_ERR_CUDA on a CUDA
+ * error.                                                                   */
+moe_status moe_join_status(void);
+
 /* ---- FP8 products with a scale per block of 128 ------------------------------
  * Activations: e4m3 codes [rows, cols] (row stride ld_codes) with one fp32
  * scale per row and 128 columns, stored block-major: scales[b * ld_scales +

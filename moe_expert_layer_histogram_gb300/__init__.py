@@ -67,7 +67,7 @@ EXPORTS = ("moe_create", "moe_prepare_weights", "moe_forward", "moe_forward_batc
            "moe_route_permute_static", "moe_balance_workspace", "moe_balance_forward",
            "moe_balance_backward", "moe_gate_forward", "moe_gate_backward",
            "moe_order_workspace", "moe_order", "moe_join_forward", "moe_join_workspace",
-           "moe_join_backward", "moe_blockscale_quantize", "moe_blockscale_matmul",
+           "moe_join_backward", "moe_join_status", "moe_blockscale_quantize", "moe_blockscale_matmul",
            "moe_blockscale_swiglu", "moe_blockscale_linear_workspace",
            "moe_blockscale_experts_workspace", "moe_blockscale_linear",
            "moe_blockscale_experts", "moe_blockscale_status", "moe_int8_quantize",
@@ -120,6 +120,7 @@ def lib():
     L.moe_join_workspace.argtypes = [ci, ci]
     L.moe_join_backward.argtypes = [join, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp,
                                     vp, vp, i64, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.moe_join_status.argtypes = []
     L.moe_blockscale_quantize.argtypes = [vp, i64, ci, vp, ci, ci, ci, vp, i64, vp, i64, vp]
     L.moe_blockscale_matmul.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp,
                                         i64, vp]
@@ -347,6 +348,10 @@ def moe_join_backward(join, x_out, ld_out, post_rstd, norm_rstd, d_x_out, ld_dxo
         _ptr(d_h), ld_dh, _ptr(d_x), ld_dx, _ptr(d_rows), ld_drows, _ptr(live_rows),
         _ptr(d_weights), _ptr(d_shared), ld_dshared, _ptr(d_gate), _ptr(d_post), _ptr(d_norm),
         _ptr(workspace), workspace_bytes, stream), "moe_join_backward")
+
+
+def moe_join_status():
+    return lib().moe_join_status()
 
 
 def moe_blockscale_quantize(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes, scales,

@@ -23,6 +23,14 @@
 // each block keeps its columns' sums in registers over its tokens and writes one
 // row of partials, which a second kernel adds in block order; the same inputs
 // give the same bits.
+//
+// Rows come by bulk copies: a warp of the block's own walks through its tokens' rows
+// ahead of the others and fills a ring of stages in shared memory, one row each, so
+// that a token's dozen rows, which depend on its indices and on one another's sums,
+// are all on their way at once and the next token's behind them.  Rows that do not
+// start on 16 bytes, or are wider than the threads of a block, are loaded by the
+// threads that use them (kernels below): 4096 x 7168, top-8, took 143 us forward and
+// 318 backward that way.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -43,6 +51,8 @@ constexpr int kSms = 152;
 constexpr int kMaxWidth = 16384;  // H: 512 threads of 4 vectors
 constexpr int kVec = 8;           // columns of a vector
 
+__device__ int g_join_status;
+
 struct JoinArgs {
   moe_join j;
   // forward
@@ -53,6 +63,7 @@ struct JoinArgs {
   int8_t* codes;
   int64_t ld_codes;
   float *code_scales, *post_rstd, *norm_rstd;
+  int stages;  // of the ring
 };
 
 struct JoinBackArgs {
@@ -70,6 +81,7 @@ struct JoinBackArgs {
   int64_t ld_dshared;
   void* d_gate;
   float *part_post, *part_norm;  // [blocks, H] each, or null
+  int stages;                    // of the ring
 };
 
 // The columns of a thread's vector i, element c: vectors of eight neighbours, or
@@ -359,6 +371,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
 #pragma unroll
     for (int c = 0; c < kVec; ++c) acc_norm[i][c] = acc_post[i][c] = 0.0f;
   int parity = 0;
+  pdl_launch_dependents();
   for (int64_t t = blockIdx.x; t < j.T; t += gridDim.x, parity ^= 1) {
     // g = d x'
     float g[NV][kVec];
@@ -537,6 +550,412 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
   }
 }
 
+// ---------------------------------------------------------------- by bulk copies
+// The ring's bookkeeping: the consumers (all warps but the last) and the warp that
+// fills it walk through the same rows in the same order.  A token's slots' rows and
+// weights travel beside it; a token has a row at least, so no more tokens than
+// stages are on their way.
+constexpr int kMaxStages = 30;
+constexpr int kInfos = 32;
+static_assert(kInfos > kMaxStages);
+
+struct TokenInfo {
+  int row[kMaxTopK];  // -1: none
+  float w[kMaxTopK];
+  float gate, norm_rstd, post_rstd, unused;
+};
+
+struct Ring {
+  uint8_t* data;
+  TokenInfo* info;
+  uint64_t *full, *empty;
+  volatile int* abort;
+  int stages, bytes;
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+
+  __device__ Ring(uint8_t* smem, int stages, int bytes) : stages(stages), bytes(bytes) {
+    data = smem;
+    info = reinterpret_cast<TokenInfo*>(smem + stages * bytes);
+    full = reinterpret_cast<uint64_t*>(info + kInfos);
+    empty = full + kMaxStages;
+    abort = reinterpret_cast<volatile int*>(empty + kMaxStages);
+  }
+  __device__ void init(int consumers) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], consumers);
+    }
+    *abort = 0;
+    fence_mbar_init();
+  }
+  __device__ void next() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  // The filling warp: a row of n bytes.
+  __device__ void put(const void* row, int n, int lane) {
+    if (!ok) return;
+    ok = wait_warp(&empty[stage], phase ^ 1, abort);
+    if (!ok) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[stage], n);
+      bulk_load(data + stage * bytes, row, n, &full[stage]);
+    }
+    next();
+  }
+  // A consumer's vector of the next row.
+  template <typename T>
+  __device__ void get(int H, float (&v)[kVec]) {
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) v[c] = 0.0f;
+    if (!ok) return;
+    ok = wait_warp(&full[stage], phase, abort);
+    if (!ok) return;
+    const int c0 = threadIdx.x * kVec;
+    const uint8_t* row = data + stage * bytes;
+    if (c0 < H) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 a = reinterpret_cast<const float4*>(row)[2 * threadIdx.x],
+                     b = reinterpret_cast<const float4*>(row)[2 * threadIdx.x + 1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      } else {
+        const uint4 q = reinterpret_cast<const uint4*>(row)[threadIdx.x];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[2 * c] = __uint_as_float(w[c] << 16);
+          v[2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
+        }
+      }
+    }
+    __syncwarp();
+    mbar_arrive_if((threadIdx.x & 31) == 0, smem_u32(&empty[stage]));
+    next();
+  }
+};
+
+// Sums over the consumers (a named barrier: the filling warp takes no part).
+__device__ __forceinline__ void sync_consumers(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+__device__ __forceinline__ float consumer_sum(float v, float* s, int threads) {
+  v = warp_sum(v);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) s[threadIdx.x >> 5] = v;
+  sync_consumers(threads);
+  return warp_sum(lane < threads >> 5 ? s[lane] : 0.0f);
+}
+
+// y of a token from the ring: its rows, then the shared expert's.
+__device__ __forceinline__ void gather_ring(const moe_join& j, Ring& ring, const TokenInfo& info,
+                                            float (&y)[kVec]) {
+  float v[kVec];
+#pragma unroll
+  for (int c = 0; c < kVec; ++c) y[c] = 0.0f;
+  for (int k = 0; k < j.K; ++k) {
+    if (info.row[k] < 0) continue;
+    ring.get<__nv_bfloat16>(j.H, v);
+    const float w = info.w[k];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) y[c] = fmaf(w, v[c], y[c]);
+  }
+  if (j.shared) {
+    const float sg = info.gate;
+    ring.get<__nv_bfloat16>(j.H, v);
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) y[c] = fmaf(sg, v[c], y[c]);
+  }
+}
+
+// The filling warp's part of the same: the rows `row` (a lane each, -1: none).
+__device__ __forceinline__ void put_rows(const moe_join& j, Ring& ring, int64_t t, int row, int lane,
+                                         bool rows, bool shared) {
+  const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(j.expert_rows);
+  for (int k = 0; rows && k < j.K; ++k) {
+    const int r = __shfl_sync(kAllLanes, row, k);
+    if (r >= 0) ring.put(z + r * j.ld_rows, j.H * 2, lane);
+  }
+  if (shared && j.shared)
+    ring.put(static_cast<const __nv_bfloat16*>(j.shared) + t * j.ld_shared, j.H * 2, lane);
+}
+
+// What a token's threads want to know of it, a lane a word: loaded a token ahead, and
+// left in the ring.
+struct TokenWords {
+  int row = -1;
+  float w = 0.0f;
+  __device__ void load(const moe_join& j, const float* norm_rstd, const float* post_rstd, int64_t t,
+                       int lane) {
+    row = -1;
+    w = 0.0f;
+    if (t >= j.T) return;
+    if (lane < j.K) {
+      row = j.row_of_slot[t * j.K + lane];
+      w = j.weights[t * j.K + lane];
+      if (row >= j.rows || row < 0) row = -1;
+    } else if (lane == kMaxTopK) {
+      w = j.shared ? gate_of(j, t) : 1.0f;
+    } else if (lane == kMaxTopK + 1 && norm_rstd) {
+      w = norm_rstd[t];
+    } else if (lane == kMaxTopK + 2 && post_rstd) {
+      w = post_rstd[t];
+    }
+  }
+  __device__ void leave(TokenInfo& info, int lane) const {
+    if (lane < kMaxTopK) {
+      info.row[lane] = row;
+      info.w[lane] = w;
+    }
+    if (lane == kMaxTopK) info.gate = w;
+    if (lane == kMaxTopK + 1) info.norm_rstd = w;
+    if (lane == kMaxTopK + 2) info.post_rstd = w;
+    __syncwarp();
+  }
+};
+
+template <typename X>
+__global__ void __launch_bounds__(1024, 1)
+    join_forward_ring_kernel(const __grid_constant__ JoinArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_post[2][32], s_norm[2][32];
+  __shared__ uint32_t s_max[2][32];
+  const moe_join& j = p.j;
+  const int H = j.H, consumers = blockDim.x - 32, lane = threadIdx.x & 31;
+  Ring ring(smem, p.stages, H * static_cast<int>(sizeof(X)));
+  if (threadIdx.x == 0) ring.init(consumers >> 5);
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) >= consumers) {
+    TokenWords words, next;
+    words.load(j, nullptr, nullptr, blockIdx.x, lane);
+    int n = 0;
+    for (int64_t t = blockIdx.x; ring.ok && t < j.T; t += gridDim.x, ++n) {
+      next.load(j, nullptr, nullptr, t + gridDim.x, lane);
+      words.leave(ring.info[n % kInfos], lane);
+      ring.put(static_cast<const X*>(j.x) + t * j.ld_x, H * sizeof(X), lane);
+      put_rows(j, ring, t, words.row, lane, true, true);
+      words = next;
+    }
+    if (!ring.ok && lane == 0) report_status(&g_join_status, kStatusTimeout);
+    return;
+  }
+  const bool block = j.K || j.shared;
+  int parity = 0, n = 0;
+  // (a wait that gave up ends no loop here: the others count on this warp's arrivals)
+  for (int64_t t = blockIdx.x; t < j.T; t += gridDim.x, parity ^= 1, ++n) {
+    const TokenInfo& info = ring.info[n % kInfos];
+    float x[kVec], v[kVec], a[kVec];
+    ring.get<X>(H, x);
+    if (block) {
+      gather_ring(j, ring, info, v);
+      if (j.post_weight) {
+        load_weights<true>(j.post_weight, j.weight_type, 0, H, a);
+        float sq = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) sq = fmaf(v[c], v[c], sq);
+        const float r = 1.0f / sqrtf(consumer_sum(sq, s_post[parity], consumers) / H + j.eps);
+        if (p.post_rstd && threadIdx.x == 0) p.post_rstd[t] = r;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) v[c] *= r * a[c];
+      }
+#pragma unroll
+      for (int c = 0; c < kVec; ++c)
+        v[c] = stored(fmaf(j.scale, v[c], x[c]), static_cast<X*>(nullptr));
+    } else {
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) v[c] = x[c];
+    }
+    if (p.x_out) store8<true>(static_cast<X*>(p.x_out) + t * p.ld_out, 0, H, v);
+    if (!j.norm_weight) continue;
+    load_weights<true>(j.norm_weight, j.weight_type, 0, H, a);
+    float sq = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) sq = fmaf(v[c], v[c], sq);
+    const float r = 1.0f / sqrtf(consumer_sum(sq, s_norm[parity], consumers) / H + j.eps);
+    if (p.norm_rstd && threadIdx.x == 0) p.norm_rstd[t] = r;
+    uint32_t amax = 0u;
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) {
+      v[c] *= r * a[c];
+      amax = max(amax, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+    }
+    if (p.h) store8<true>(p.h + t * p.ld_h, 0, H, v);
+    if (!p.codes) continue;
+    amax = __reduce_max_sync(kAllLanes, amax);
+    if (lane == 0) s_max[parity][threadIdx.x >> 5] = amax;
+    sync_consumers(consumers);
+    amax = __reduce_max_sync(kAllLanes, lane < consumers >> 5 ? s_max[parity][lane] : 0u);
+    const float s = i8_scale(amax);
+    if (threadIdx.x == 0) p.code_scales[t] = s;
+    const uint2 w = I8Coder(s).bytes(v);
+    const int c0 = threadIdx.x * kVec;
+    if (c0 < H) *reinterpret_cast<uint2*>(p.codes + t * p.ld_codes + c0) = w;
+  }
+}
+
+template <typename X, bool POST>
+__global__ void __launch_bounds__(1024, 1)
+    join_backward_ring_kernel(const __grid_constant__ JoinBackArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_norm[2][32], s_post[2][32], s_dot[2][kMaxTopK + 1][32];
+  const moe_join& j = p.j;
+  const int H = j.H, consumers = blockDim.x - 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = consumers >> 5;
+  Ring ring(smem, p.stages, H * static_cast<int>(sizeof(X)));
+  if (threadIdx.x == 0) ring.init(warps);
+  pdl_launch_dependents();
+  __syncthreads();
+  const bool block = j.K || j.shared;
+  if (warp == warps) {
+    TokenWords words, next;
+    words.load(j, p.norm_rstd, p.post_rstd, blockIdx.x, lane);
+    int n = 0;
+    for (int64_t t = blockIdx.x; ring.ok && t < j.T; t += gridDim.x, ++n) {
+      next.load(j, p.norm_rstd, p.post_rstd, t + gridDim.x, lane);
+      words.leave(ring.info[n % kInfos], lane);
+      // (x' at any rate: a token has a row at least)
+      ring.put(static_cast<const X*>(p.x_out) + t * p.ld_out, H * sizeof(X), lane);
+      if (p.d_h) ring.put(static_cast<const __nv_bfloat16*>(p.d_h) + t * p.ld_dh, H * 2, lane);
+      if (p.d_x_out)
+        ring.put(static_cast<const X*>(p.d_x_out) + t * p.ld_dxo, H * sizeof(X), lane);
+      if (POST) put_rows(j, ring, t, words.row, lane, true, true);
+      if (block) put_rows(j, ring, t, words.row, lane, p.d_weights != nullptr, p.d_gate != nullptr);
+      words = next;
+    }
+    if (!ring.ok && lane == 0) report_status(&g_join_status, kStatusTimeout);
+  } else {
+    float acc_norm[kVec], acc_post[POST ? kVec : 1];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) acc_norm[c] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < (POST ? kVec : 1); ++c) acc_post[c] = 0.0f;
+    int parity = 0, n = 0;
+    for (int64_t t = blockIdx.x; t < j.T; t += gridDim.x, parity ^= 1, ++n) {
+      const TokenInfo& info = ring.info[n % kInfos];
+      float g[kVec], a[kVec], xh[kVec];
+      ring.get<X>(H, xh);
+      if (p.d_h) {
+        const float r = info.norm_rstd;
+        float dot = 0.0f;
+        load_weights<true>(j.norm_weight, j.weight_type, 0, H, a);
+        ring.get<__nv_bfloat16>(H, g);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+          xh[c] *= r;
+          acc_norm[c] = fmaf(g[c], xh[c], acc_norm[c]);
+          g[c] *= a[c];
+          dot = fmaf(g[c], xh[c], dot);
+        }
+        const float mean = consumer_sum(dot, s_norm[parity], consumers) / H;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[c] = r * fmaf(-mean, xh[c], g[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[c] = 0.0f;
+      }
+      if (p.d_x_out) {
+        ring.get<X>(H, a);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[c] += a[c];
+      }
+      if (p.d_x) store8<true>(static_cast<X*>(p.d_x) + t * p.ld_dx, 0, H, g);
+      if (!block) continue;
+      const float sg = info.gate;
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) g[c] *= j.scale;
+      if constexpr (POST) {
+        float y[kVec], dot = 0.0f;
+        gather_ring(j, ring, info, y);
+        const float r = info.post_rstd;
+        load_weights<true>(j.post_weight, j.weight_type, 0, H, a);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+          y[c] *= r;
+          acc_post[c] = fmaf(g[c], y[c], acc_post[c]);
+          g[c] *= a[c];
+          dot = fmaf(g[c], y[c], dot);
+        }
+        const float mean = consumer_sum(dot, s_post[parity], consumers) / H;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) g[c] = r * fmaf(-mean, y[c], g[c]);
+      }
+      // d z, d u and their dot products with d y
+      float(*dots)[32] = s_dot[parity];
+      for (int k = 0; k < j.K; ++k) {
+        const int row = info.row[k];
+        float dot = 0.0f;
+        if (row >= 0) {
+          if (p.d_weights) {
+            ring.get<__nv_bfloat16>(H, a);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) dot = fmaf(g[c], a[c], dot);
+          }
+          if (p.d_rows && ring.ok) {
+            const float w = info.w[k];
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) a[c] = w * g[c];
+            store8<true>(p.d_rows + row * p.ld_drows, 0, H, a);
+          }
+        }
+        if (p.d_weights) {
+          dot = warp_sum(dot);
+          if (lane == 0) dots[k][warp] = dot;
+        }
+      }
+      if (j.shared) {
+        if (p.d_gate) {
+          float dot = 0.0f;
+          ring.get<__nv_bfloat16>(H, a);
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) dot = fmaf(g[c], a[c], dot);
+          dot = warp_sum(dot);
+          if (lane == 0) dots[kMaxTopK][warp] = dot;
+        }
+        if (p.d_shared) {
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) a[c] = sg * g[c];
+          store8<true>(p.d_shared + t * p.ld_dshared, 0, H, a);
+        }
+      }
+      if (p.d_weights || p.d_gate) {
+        sync_consumers(consumers);
+        if (p.d_weights)
+          for (int k = warp; k < j.K; k += warps) {
+            const float dot = warp_sum(lane < warps ? dots[k][lane] : 0.0f);
+            if (lane == 0) p.d_weights[t * j.K + k] = dot;
+          }
+        if (p.d_gate && warp == warps - 1) {
+          const float d = warp_sum(lane < warps ? dots[kMaxTopK][lane] : 0.0f) * sg * (1.0f - sg);
+          if (lane == 0) {
+            if (j.gate_type == MOE_DTYPE_F32)
+              static_cast<float*>(p.d_gate)[t] = d;
+            else
+              static_cast<__nv_bfloat16*>(p.d_gate)[t] = __float2bfloat16_rn(d);
+          }
+        }
+      }
+    }
+    if (p.part_norm)
+      store8<true>(p.part_norm + static_cast<int64_t>(blockIdx.x) * H, 0, H, acc_norm);
+    if constexpr (POST)
+      if (p.part_post)
+        store8<true>(p.part_post + static_cast<int64_t>(blockIdx.x) * H, 0, H, acc_post);
+    // rows of no expert
+    if (p.d_rows && p.live_rows) {
+      float zero[kVec];
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) zero[c] = 0.0f;
+      for (int64_t r = max(*p.live_rows, 0) + static_cast<int64_t>(blockIdx.x); r < j.rows;
+           r += gridDim.x)
+        store8<true>(p.d_rows + r * p.ld_drows, 0, H, zero);
+    }
+  }
+}
+
 // Column sums of the partials, in block order within each of kFinishRows runs of
 // rows, then run by run.  blockIdx.y: 0 norm, 1 post.
 constexpr int kFinishRows = 16;
@@ -623,9 +1042,48 @@ Shape shape_of(int H) {
   return {nv, ((vectors + nv - 1) / nv + 31) / 32 * 32};
 }
 
+// The ring's shape: blocks of an SM, and stages of each.
+struct RingShape {
+  int threads, blocks, stages, smem;
+};
+constexpr int kRingMost = 1024 - 32;  // consumers
+constexpr int kSmSmem = 233472;       // of which each block has 1 KB more than it asks for
+constexpr int kRingStatic = 5120;     // static shared memory, at most
+constexpr int kRingDynamic = 232448 - kRingStatic;
+bool ring_fits(int H) { return (H + kVec - 1) / kVec <= kRingMost; }
+RingShape ring_shape(int H, int size) {
+  constexpr int kFixed = kInfos * sizeof(TokenInfo) + 2 * kMaxStages * 8 + 16;
+  const int bytes = H * size;
+  RingShape r;
+  r.threads = ((H + kVec - 1) / kVec + 31) / 32 * 32 + 32;
+  // (64 registers a thread; several blocks, whose sums hide behind each other's
+  // copies, with a dozen rows' stages each)
+  r.blocks = std::max(1, std::min({16, 1024 / r.threads,
+                                   kSmSmem / (12 * bytes + kFixed + kRingStatic + 1024)}));
+  r.stages = std::min(kMaxStages, (kSmSmem / r.blocks - 1024 - kRingStatic - kFixed) / bytes);
+  r.smem = r.stages * bytes + kFixed;
+  return r;
+}
+
+template <typename K, typename Args>
+cudaError_t launch_ring(K kernel, OncePerDevice& prepared, const RingShape& r, int T, Args p,
+                        cudaStream_t s) {
+  const cudaError_t ready = prepared([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingDynamic);
+  });
+  if (ready != cudaSuccess) return ready;
+  p.stages = r.stages;
+  return launch_pdl(false, kernel, dim3(std::min(T, r.blocks * kSms)), dim3(r.threads), r.smem, s, p);
+}
+
 template <typename X, bool VEC>
 cudaError_t run_forward(const JoinArgs& p, cudaStream_t s) {
   const int T = p.j.T;
+  if constexpr (VEC)
+    if (ring_fits(p.j.H)) {
+      static OncePerDevice prepared;
+      return launch_ring(join_forward_ring_kernel<X>, prepared, ring_shape(p.j.H, sizeof(X)), T, p, s);
+    }
   const Shape q = shape_of(p.j.H);
   auto go = [&](auto k) { return launch_pdl(false, k, dim3(T), dim3(q.threads), 0, s, p); };
   if (q.nv == 1) return go(join_forward_kernel<X, 1, VEC>);
@@ -633,18 +1091,30 @@ cudaError_t run_forward(const JoinArgs& p, cudaStream_t s) {
   return go(join_forward_kernel<X, 4, VEC>);
 }
 
-// Blocks of the backward pass: as many as run at a time.
-int back_blocks(int T, int H) {
+// Blocks of the backward pass: as many as run at a time (ring: 0, or the size of x's
+// elements).
+int back_blocks(int T, int H, int ring) {
   const Shape q = shape_of(H);
-  const int resident = std::max(1, std::min(8, 65536 / ((q.nv == 1 ? 64 : 128) * q.threads)));
+  const int resident = ring ? ring_shape(H, ring).blocks
+                            : std::max(1, std::min(8, 65536 / ((q.nv == 1 ? 64 : 128) * q.threads)));
   return std::max(1, std::min(T, resident * kSms));
 }
 
+bool back_by_ring(const JoinBackArgs& p, int) { return p.x_out && ring_fits(p.j.H); }
+
 template <typename X, bool VEC>
 cudaError_t run_backward(const JoinBackArgs& p, cudaStream_t s) {
+  if constexpr (VEC)
+    if (back_by_ring(p, sizeof(X))) {
+      static OncePerDevice plain, post;
+      const RingShape r = ring_shape(p.j.H, sizeof(X));
+      return p.j.post_weight
+                 ? launch_ring(join_backward_ring_kernel<X, true>, post, r, p.j.T, p, s)
+                 : launch_ring(join_backward_ring_kernel<X, false>, plain, r, p.j.T, p, s);
+    }
   const Shape q = shape_of(p.j.H);
   auto go = [&](auto k) {
-    return launch_pdl(false, k, dim3(back_blocks(p.j.T, p.j.H)), dim3(q.threads), 0, s, p);
+    return launch_pdl(false, k, dim3(back_blocks(p.j.T, p.j.H, 0)), dim3(q.threads), 0, s, p);
   };
   if (q.nv == 1) return go(join_backward_kernel<X, 1, VEC>);
   if (q.nv == 2) return go(join_backward_kernel<X, 2, VEC>);
@@ -694,7 +1164,10 @@ moe_status moe_join_forward(const moe_join* j, void* x_out, int64_t ld_out, void
 
 size_t moe_join_workspace(int T, int H) {
   if (T < 1 || H < 1 || H > kMaxWidth) return 0;
-  return static_cast<size_t>(2) * back_blocks(T, H) * ((H + 3) / 4 * 4) * 4;
+  const int blocks =
+      std::max({back_blocks(T, H, 0), ring_fits(H) ? back_blocks(T, H, 2) : 0,
+                ring_fits(H) ? back_blocks(T, H, 4) : 0});
+  return static_cast<size_t>(2) * blocks * ((H + 3) / 4 * 4) * 4;
 }
 
 moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_out,
@@ -738,17 +1211,18 @@ moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_ou
     p.d_weights = d_weights;
     p.d_shared = static_cast<__nv_bfloat16*>(d_shared), p.ld_dshared = ld_dshared;
     p.d_gate = d_gate;
-    f.blocks = back_blocks(j->T, j->H);
-    float* ws = static_cast<float*>(workspace);
-    if (d_norm) f.part[0] = p.part_norm = ws;
-    if (d_post)
-      f.part[1] = p.part_post = ws + static_cast<int64_t>(f.blocks) * ((j->H + 3) / 4 * 4);
     moe_join in = *j;
     in.x = nullptr;  // (not read)
     const bool vec = join_vectors(in) && in_vectors(x_out, ld_out, xs) &&
                      in_vectors(d_x_out, ld_dxo, xs) && in_vectors(d_h, ld_dh, 2) &&
                      in_vectors(d_x, ld_dx, xs) && in_vectors(d_rows, ld_drows, 2) &&
                      in_vectors(d_shared, ld_dshared, 2);
+    f.blocks = back_blocks(j->T, j->H,
+                           vec && back_by_ring(p, 0) ? static_cast<int>(size_of(j->x_type)) : 0);
+    float* ws = static_cast<float*>(workspace);
+    if (d_norm) f.part[0] = p.part_norm = ws;
+    if (d_post)
+      f.part[1] = p.part_post = ws + static_cast<int64_t>(f.blocks) * ((j->H + 3) / 4 * 4);
     cudaError_t e;
     if (j->x_type == MOE_DTYPE_F32)
       e = vec ? run_backward<float, true>(p, s) : run_backward<float, false>(p, s);
@@ -766,9 +1240,19 @@ moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_ou
     return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   const cudaError_t e =
-      launch_pdl(false, join_finish_kernel, dim3((j->H + 31) / 32, d_post ? 2 : 1),
+      launch_pdl(true, join_finish_kernel, dim3((j->H + 31) / 32, d_post ? 2 : 1),
                  dim3(32, kFinishRows), 0, s, f);
   return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_join_status(void) {
+  int v = 0;
+  const int zero = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_join_status, sizeof(int));
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_join_status, &zero, sizeof(int));
+  if (take_error(e) != cudaSuccess) return MOE_ERR_CUDA;
+  return v ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
 
 }  // extern "C"

@@ -583,4 +583,23 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
+// mbar_wait by a whole warp, without a look at the timer before the wait has
+// lasted for many tries: reading it takes longer than most waits here.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  uint32_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 127u) == 127u) {
+      // (the low half of the timer: its differences are good for 4 s)
+      uint32_t now;
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+      if (i == 127u) t0 = now;
+      if (__any_sync(0xFFFFFFFFu, *abort != 0 || now - t0 > static_cast<uint32_t>(kWaitTimeoutNs))) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 }  // namespace moe

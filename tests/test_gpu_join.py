@@ -389,3 +389,17 @@ def test_refusals():
     with pytest.raises(ValueError):
         block_join_backward(block_join(**dict(a, norm_weight=None)),
                             d_h=torch.zeros(6, 32, dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.fixture(autouse=True)
+def no_wait_gave_up():
+    yield
+    from moe_expert_layer_histogram_gb300 import moe_join_status
+    assert moe_join_status() == 0
+
+
+@pytest.mark.parametrize("T,H,K", [(5000, 64, 2), (3000, 1032, 3), (1000, 4096, 16), (700, 7936, 4),
+                                   (400, 7944, 4), (2500, 8, 1)])
+@pytest.mark.parametrize("x_type", [torch.float32, torch.bfloat16])
+def test_many_tokens_for_each_block(T, H, K, x_type):
+    check(make(T, H, K, x_type=x_type, w_type=x_type, post=K % 2 == 0))
