@@ -27,10 +27,11 @@
 // Rows come by bulk copies: a warp of the block's own walks through its tokens' rows
 // ahead of the others and fills a ring of stages in shared memory, one row each, so
 // that a token's dozen rows, which depend on its indices and on one another's sums,
-// are all on their way at once and the next token's behind them.  Rows that do not
-// start on 16 bytes, or are wider than the threads of a block, are loaded by the
-// threads that use them (kernels below): 4096 x 7168, top-8, took 143 us forward and
-// 318 backward that way.
+// are all on their way at once and the next token's behind them (4096 x 7168, top-8:
+// 127 us forward and 203 backward, 6.4 TB/s; with rows loaded by the threads that use
+// them 143 and 318).  With few tokens to a block there is little to run ahead of, and
+// narrow rows have more blocks to an SM; those, and rows that do not start on 16
+// bytes, are loaded by their threads (use_ring).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1065,6 +1066,18 @@ RingShape ring_shape(int H, int size) {
   return r;
 }
 
+// Where the ring is the faster way.  Forward pass, 7168 columns: 512 tokens 20 us
+// against 15 of loads, 1024 38 and 42, 2048 70 and 75; 2048 columns: 4096 tokens 41
+// and 38.  Backward pass, 7168: 304 tokens 23 and 27, 512 42 and 58, 2048 112 and
+// 176; 2048 with a norm after the block: 1024 tokens 33 and 29, 4096 97 and 97; 512:
+// 8192 tokens 40 and 53.
+bool use_ring(int T, int H, int size, bool backward) {
+  if (!ring_fits(H)) return false;
+  const bool wide = H > 4096;
+  if (!backward && !wide) return false;
+  return T >= (backward && wide ? 2 : 5) * ring_shape(H, size).blocks * kSms;
+}
+
 template <typename K, typename Args>
 cudaError_t launch_ring(K kernel, OncePerDevice& prepared, const RingShape& r, int T, Args p,
                         cudaStream_t s) {
@@ -1080,7 +1093,7 @@ template <typename X, bool VEC>
 cudaError_t run_forward(const JoinArgs& p, cudaStream_t s) {
   const int T = p.j.T;
   if constexpr (VEC)
-    if (ring_fits(p.j.H)) {
+    if (use_ring(T, p.j.H, sizeof(X), false)) {
       static OncePerDevice prepared;
       return launch_ring(join_forward_ring_kernel<X>, prepared, ring_shape(p.j.H, sizeof(X)), T, p, s);
     }
@@ -1100,7 +1113,9 @@ int back_blocks(int T, int H, int ring) {
   return std::max(1, std::min(T, resident * kSms));
 }
 
-bool back_by_ring(const JoinBackArgs& p, int) { return p.x_out && ring_fits(p.j.H); }
+bool back_by_ring(const JoinBackArgs& p, int size) {
+  return p.x_out && use_ring(p.j.T, p.j.H, size, true);
+}
 
 template <typename X, bool VEC>
 cudaError_t run_backward(const JoinBackArgs& p, cudaStream_t s) {
@@ -1217,8 +1232,8 @@ moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_ou
                      in_vectors(d_x_out, ld_dxo, xs) && in_vectors(d_h, ld_dh, 2) &&
                      in_vectors(d_x, ld_dx, xs) && in_vectors(d_rows, ld_drows, 2) &&
                      in_vectors(d_shared, ld_dshared, 2);
-    f.blocks = back_blocks(j->T, j->H,
-                           vec && back_by_ring(p, 0) ? static_cast<int>(size_of(j->x_type)) : 0);
+    const int size = static_cast<int>(xs);
+    f.blocks = back_blocks(j->T, j->H, vec && back_by_ring(p, size) ? size : 0);
     float* ws = static_cast<float*>(workspace);
     if (d_norm) f.part[0] = p.part_norm = ws;
     if (d_post)

@@ -398,7 +398,7 @@ def no_wait_gave_up():
     assert moe_join_status() == 0
 
 
-@pytest.mark.parametrize("T,H,K", [(5000, 64, 2), (3000, 1032, 3), (1000, 4096, 16), (700, 7936, 4),
+@pytest.mark.parametrize("T,H,K", [(12500, 64, 2), (4000, 1032, 3), (1000, 4096, 16), (1000, 7936, 4),
                                    (400, 7944, 4), (2500, 8, 1)])
 @pytest.mark.parametrize("x_type", [torch.float32, torch.bfloat16])
 def test_many_tokens_for_each_block(T, H, K, x_type):
