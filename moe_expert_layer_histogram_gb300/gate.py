@@ -4,6 +4,8 @@ balance, the gradient of the logits, and the routed slots in expert order.
 Thin wrappers of ``moe_gate_forward``, ``moe_gate_backward`` and ``moe_order``
 (``include/moe.h`` states the formulas); work goes on torch's current stream.
 """
+import functools
+
 import torch
 
 from . import MOE_GROUP, MOE_SCORE, MoEError, MoEGateConfig, lib
@@ -32,6 +34,15 @@ class RouterOrder:
         self.slots, self.offsets, self.rows = slots, offsets, rows
 
 
+@functools.lru_cache(maxsize=64)
+def _config(score, groups, group_top, group_score, normalize, scale):
+    if score not in MOE_SCORE or group_score not in MOE_GROUP:
+        raise ValueError("score: one of %s, group_score: one of %s"
+                         % (sorted(MOE_SCORE), sorted(MOE_GROUP)))
+    return MoEGateConfig(MOE_SCORE[score], groups, groups if group_top is None else group_top,
+                         MOE_GROUP[group_score], 1 if normalize else 0, scale)
+
+
 def _logits(t, name):
     """(element type code, row stride) of logits or their gradient."""
     if t.dtype is _F32:
@@ -57,13 +68,9 @@ def router_gate(logits, top_k, score="softmax", bias=None, groups=1, group_top=N
         check(bias, _F32, (E,), dev, "bias")
     if mask is not None:
         check(mask, torch.bool if mask.dtype is torch.bool else torch.uint8, (T,), dev, "mask")
-    for n, name in ((top_k, "top_k"), (groups, "groups")):
-        fits(n, name)
-    if score not in MOE_SCORE or group_score not in MOE_GROUP:
-        raise ValueError("score: one of %s, group_score: one of %s"
-                         % (sorted(MOE_SCORE), sorted(MOE_GROUP)))
-    config = MoEGateConfig(MOE_SCORE[score], groups, groups if group_top is None else group_top,
-                           MOE_GROUP[group_score], 1 if normalize else 0, scale)
+    fits(top_k, "top_k")
+    fits(max(groups, group_top or 0), "groups")
+    config = _config(score, groups, group_top, group_score, normalize, scale)
     k = max(top_k, 0)
     ids = torch.empty(T, k, dtype=_I32, device=dev)
     weights = torch.empty(T, k, dtype=_F32, device=dev)
@@ -114,8 +121,7 @@ def router_order(ids, num_experts):
         raise ValueError("ids: contiguous int32")
     L = lib()
     nbytes = L.moe_order_workspace(n, num_experts)
-    slots = torch.empty(n, dtype=_I32, device=dev)
-    rows = torch.empty(n, dtype=_I32, device=dev)
+    slots, rows = torch.empty(n, dtype=_I32, device=dev), torch.empty(n, dtype=_I32, device=dev)
     offsets = torch.empty(max(num_experts, 0) + 1, dtype=_I32, device=dev)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     code = L.moe_order(ids.data_ptr(), n, num_experts, slots.data_ptr(), offsets.data_ptr(),

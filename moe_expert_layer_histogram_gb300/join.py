@@ -6,10 +6,13 @@ gradients.
 Thin wrappers of ``moe_join_forward`` and ``moe_join_backward``
 (``include/moe.h`` states the formulas); work goes on torch's current stream.
 """
+import struct
+
 import torch
 
 from . import MoEError, MoEJoin, lib
 from ._tensors import check, row_stride, stream_on
+from .gate import RouterOrder
 
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 _TYPE = {_F32: 0, _BF16: 1}
@@ -19,12 +22,12 @@ class BlockJoin:
     """What the join gave: x [T, H] (x's type; x itself where nothing was
     joined), h bf16 [T, H] or None, or in 8 bits codes int8 [T, H] and code_scales
     f32 [T]; and what its backward pass takes."""
-    __slots__ = ("x", "h", "codes", "code_scales", "_join", "_inputs", "_post_rstd", "_norm_rstd")
+    __slots__ = ("x", "h", "codes", "code_scales", "_join", "_ld_x", "_stats", "_live", "_inputs")
 
-    def __init__(self, x, h, codes, code_scales, join, inputs, post_rstd, norm_rstd):
+    def __init__(self, x, h, codes, code_scales, join, ld_x, stats, live, inputs):
         self.x, self.h, self.codes, self.code_scales = x, h, codes, code_scales
-        self._join, self._inputs = join, inputs
-        self._post_rstd, self._norm_rstd = post_rstd, norm_rstd
+        self._join, self._ld_x, self._stats = join, ld_x, stats
+        self._live, self._inputs = live, inputs
 
 
 class JoinGradients:
@@ -36,6 +39,11 @@ class JoinGradients:
         self.x, self.expert_rows, self.weights = x, expert_rows, weights
         self.shared, self.gate = shared, gate
         self.post_weight, self.norm_weight = post_weight, norm_weight
+
+
+# moe_join's members, in order
+_pack = struct.Struct("6i2fQqQqi4xQQQqQQQ").pack
+_empty = torch.empty
 
 
 def _type(t, name):
@@ -52,8 +60,11 @@ def _rows(t, dtype, shape, device, name):
     return ld
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _vector(t, dtype, n, device, name):
+    """Address of a contiguous vector of n elements."""
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s: contiguous %s [%d] on %s" % (name, dtype, n, device))
+    return t.data_ptr()
 
 
 def block_join(x, expert_rows=None, order=None, weights=None, shared=None, gate=None,
@@ -65,82 +76,89 @@ def block_join(x, expert_rows=None, order=None, weights=None, shared=None, gate=
     bf16 -> BlockJoin.  h comes in 8 bits if `quantize`; out: where the new x
     goes (x itself, say)."""
     x_type = _type(x, "x")
-    ld_x = row_stride(x, x.dtype, "x")
+    dtype = x.dtype
+    ld_x = row_stride(x, dtype, "x")
     T, H = shape = x.shape
     dev = x.device
     stream = stream_on(dev)
-    join = MoEJoin(T=T, H=H, x_type=x_type, scale=scale, eps=eps, x=x.data_ptr(), ld_x=ld_x)
+    K = ld_rows = rows = rows_ptr = slots_ptr = weights_ptr = 0
     row_of_slot = live = None
     if expert_rows is not None:
         if order is None or weights is None or weights.dim() != 2:
             raise ValueError("expert_rows: wanted with order and weights [T, K]")
-        K = join.K = weights.shape[1]
-        row_of_slot = getattr(order, "rows", order)
-        if row_of_slot is not order:
-            live = order.offsets[-1:]
+        K = weights.shape[1]
+        row_of_slot = order
+        if isinstance(order, RouterOrder):
+            row_of_slot, live = order.rows, order.offsets
         check(weights, _F32, (T, K), dev, "weights")
         if (row_of_slot.dtype is not _I32 or row_of_slot.numel() != T * K
                 or row_of_slot.device != dev or not row_of_slot.is_contiguous()):
             raise ValueError("order: int32 rows of %d slots on %s" % (T * K, dev))
-        join.ld_rows = row_stride(expert_rows, _BF16, "expert_rows")
-        join.rows = expert_rows.shape[0]
-        if expert_rows.shape[1] != H or expert_rows.device != dev:
+        ld_rows = row_stride(expert_rows, _BF16, "expert_rows")
+        rows, width = expert_rows.shape
+        if width != H or expert_rows.device != dev:
             raise ValueError("expert_rows: [R, %d] on %s" % (H, dev))
-        join.expert_rows, join.row_of_slot = expert_rows.data_ptr(), row_of_slot.data_ptr()
-        join.weights = weights.data_ptr()
+        if live is not None and (live.dtype is not _I32 or live.dim() != 1 or live.device != dev
+                                 or not live.numel() or not live.is_contiguous()):
+            raise ValueError("order: contiguous int32 offsets on %s" % dev)
+        rows_ptr, slots_ptr = expert_rows.data_ptr(), row_of_slot.data_ptr()
+        weights_ptr = weights.data_ptr()
     elif order is not None or weights is not None:
         raise ValueError("order and weights: wanted with expert_rows")
+    ld_shared = shared_ptr = gate_ptr = gate_type = 0
     if shared is not None:
-        join.ld_shared = _rows(shared, _BF16, shape, dev, "shared")
-        join.shared = shared.data_ptr()
+        ld_shared = _rows(shared, _BF16, shape, dev, "shared")
+        shared_ptr = shared.data_ptr()
     if gate is not None:
-        join.gate_type = _type(gate, "gate")
-        check(gate, gate.dtype, (T,), dev, "gate")
+        gate_type = _type(gate, "gate")
         if shared is None:
             raise ValueError("gate: wanted with shared")
-        join.gate = gate.data_ptr()
-    norms = [w for w in (post_weight, norm_weight) if w is not None]
-    for w, name in ((post_weight, "post_weight"), (norm_weight, "norm_weight")):
-        if w is not None:
-            join.weight_type = _type(w, name)
-            check(w, norms[0].dtype, (H,), dev, name)
-    join.post_weight, join.norm_weight = _ptr(post_weight), _ptr(norm_weight)
-    joined = join.K > 0 or shared is not None
+        gate_ptr = _vector(gate, gate.dtype, T, dev, "gate")
+    post_ptr = norm_ptr = weight_type = 0
+    if post_weight is not None:
+        weight_type = _type(post_weight, "post_weight")
+        post_ptr = _vector(post_weight, post_weight.dtype, H, dev, "post_weight")
+    if norm_weight is not None:
+        weight_type = _type(norm_weight, "norm_weight")
+        norm_ptr = _vector(norm_weight, norm_weight.dtype if post_weight is None
+                           else post_weight.dtype, H, dev, "norm_weight")
+    elif quantize:
+        raise ValueError("quantize: wanted with norm_weight")
+    joined = K > 0 or shared is not None
     if not joined and norm_weight is None:
         raise ValueError("nothing to join and no norm_weight")
-    if quantize and norm_weight is None:
-        raise ValueError("quantize: wanted with norm_weight")
-    ld_out, x_out = H, None
-    if joined:
-        x_out = torch.empty(T, H, dtype=x.dtype, device=dev) if out is None else out
+    ld_out, x_out, out_ptr = H, x, None
+    if not joined:
         if out is not None:
-            ld_out = _rows(out, x.dtype, shape, dev, "out")
-    elif out is not None:
-        raise ValueError("out: there is nothing to join")
-    h = codes = code_scales = norm_rstd = post_rstd = None
+            raise ValueError("out: there is nothing to join")
+    elif out is None:
+        x_out = _empty(shape, dtype=dtype, device=dev)
+        out_ptr = x_out.data_ptr()
+    else:
+        ld_out, x_out = _rows(out, dtype, shape, dev, "out"), out
+        out_ptr = out.data_ptr()
+    # (the norms' statistics and the codes' scales: a row each)
+    stats = _empty((3, T), dtype=_F32, device=dev)
+    base = stats.data_ptr()
+    h = codes = code_scales = h_ptr = codes_ptr = scales_ptr = None
     ld_codes = (H + 15) // 16 * 16
-    # (one allocation for the norms' statistics and the codes' scales)
-    stats = torch.empty(3, T, dtype=_F32, device=dev)
-    if norm_weight is not None:
-        norm_rstd = stats[0]
-        if quantize:
-            codes = torch.empty(T, ld_codes, dtype=torch.int8, device=dev)
-            code_scales = stats[2]
-        else:
-            h = torch.empty(T, H, dtype=_BF16, device=dev)
-    if post_weight is not None:
-        post_rstd = stats[1]
-    code = lib().moe_join_forward(join, _ptr(x_out), ld_out, _ptr(h), H, _ptr(codes), ld_codes,
-                                  _ptr(code_scales), _ptr(post_rstd), _ptr(norm_rstd), stream)
+    if norm_ptr and quantize:
+        codes = _empty((T, ld_codes), dtype=torch.int8, device=dev)
+        codes_ptr, scales_ptr, code_scales = codes.data_ptr(), base + 8 * T, stats[2]
+    elif norm_weight is not None:
+        h = _empty(shape, dtype=_BF16, device=dev)
+        h_ptr = h.data_ptr()
+    join = MoEJoin.from_buffer_copy(_pack(
+        T, H, K, x_type, weight_type, gate_type, scale, eps, x.data_ptr(), ld_x, rows_ptr, ld_rows,
+        rows, slots_ptr, weights_ptr, shared_ptr, ld_shared, gate_ptr, post_ptr, norm_ptr))
+    code = lib().moe_join_forward(join, out_ptr, ld_out, h_ptr, H, codes_ptr, ld_codes, scales_ptr,
+                                  base + 4 * T, base, stream)
     if code:
         raise MoEError(code, "moe_join_forward")
     if codes is not None and ld_codes != H:
         codes = codes[:, :H]
-    if x_out is None:
-        x_out, ld_out = x, ld_x
-    return BlockJoin(x_out, h, codes, code_scales, join,
-                     (ld_out, row_of_slot, live, expert_rows, weights, shared, gate, post_weight,
-                      norm_weight), post_rstd, norm_rstd)
+    return BlockJoin(x_out, h, codes, code_scales, join, ld_out if joined else ld_x, stats, live,
+                     (expert_rows, row_of_slot, weights, shared, gate, post_weight, norm_weight))
 
 
 def block_join_backward(fwd, d_x=None, d_h=None):
@@ -150,40 +168,54 @@ def block_join_backward(fwd, d_x=None, d_h=None):
     were.  The gradient of expert_rows is zero for rows of no expert, where fwd
     was given a RouterOrder; with plain rows it has whatever was in memory in
     rows that no slot names."""
-    join, x = fwd._join, fwd.x
-    (ld_out, row_of_slot, live, expert_rows, weights, shared, gate, post_weight,
-     norm_weight) = fwd._inputs
+    x = fwd.x
+    expert_rows, _, weights, shared, gate, post_weight, norm_weight = fwd._inputs
+    live = fwd._live
     T, H = shape = x.shape
     dev = x.device
     stream = stream_on(dev)
-    ld_dxo = H if d_x is None else _rows(d_x, x.dtype, shape, dev, "d_x")
-    ld_dh = H
+    ld_dxo = ld_dh = H
+    dx_ptr = dh_ptr = rows_ptr = live_ptr = weights_ptr = shared_ptr = gate_ptr = None
+    post_ptr = norm_ptr = None
+    if d_x is not None:
+        ld_dxo = _rows(d_x, x.dtype, shape, dev, "d_x")
+        dx_ptr = d_x.data_ptr()
     if d_h is not None:
         if norm_weight is None:
             raise ValueError("d_h: the join had no norm_weight")
         ld_dh = _rows(d_h, _BF16, shape, dev, "d_h")
-    out_x = torch.empty(T, H, dtype=x.dtype, device=dev)
+        dh_ptr = d_h.data_ptr()
+    out_x = _empty(shape, dtype=x.dtype, device=dev)
     d_rows = d_weights = d_shared = d_gate = d_post = d_norm = None
-    if row_of_slot is not None:
-        d_rows = torch.empty(expert_rows.shape[0], H, dtype=_BF16, device=dev)
+    if expert_rows is not None:
+        d_rows = _empty((expert_rows.shape[0], H), dtype=_BF16, device=dev)
         d_weights = torch.empty_like(weights)
+        rows_ptr, weights_ptr = d_rows.data_ptr(), d_weights.data_ptr()
+        if live is not None:
+            live_ptr = live.data_ptr() + 4 * (live.numel() - 1)
     if shared is not None:
-        d_shared = torch.empty(T, H, dtype=_BF16, device=dev)
+        d_shared = _empty(shape, dtype=_BF16, device=dev)
+        shared_ptr = d_shared.data_ptr()
     if gate is not None:
         d_gate = torch.empty_like(gate)
+        gate_ptr = d_gate.data_ptr()
     if post_weight is not None:
         d_post = torch.empty_like(post_weight)
+        post_ptr = d_post.data_ptr()
     if d_h is not None:
         d_norm = torch.empty_like(norm_weight)
+        norm_ptr = d_norm.data_ptr()
     L = lib()
-    nbytes, ws = 0, None
-    if d_post is not None or d_norm is not None:
+    nbytes, ws_ptr = 0, None
+    if post_ptr or norm_ptr:
         nbytes = L.moe_join_workspace(T, H)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = _empty(nbytes, dtype=torch.uint8, device=dev)
+        ws_ptr = ws.data_ptr()
+    base = fwd._stats.data_ptr()
     code = L.moe_join_backward(
-        join, x.data_ptr(), ld_out, _ptr(fwd._post_rstd), _ptr(fwd._norm_rstd), _ptr(d_x), ld_dxo,
-        _ptr(d_h), ld_dh, out_x.data_ptr(), H, _ptr(d_rows), H, _ptr(live), _ptr(d_weights),
-        _ptr(d_shared), H, _ptr(d_gate), _ptr(d_post), _ptr(d_norm), _ptr(ws), nbytes, stream)
+        fwd._join, x.data_ptr(), fwd._ld_x, base + 4 * T, base, dx_ptr, ld_dxo, dh_ptr, ld_dh,
+        out_x.data_ptr(), H, rows_ptr, H, live_ptr, weights_ptr, shared_ptr, H, gate_ptr, post_ptr,
+        norm_ptr, ws_ptr, nbytes, stream)
     if code:
         raise MoEError(code, "moe_join_backward")
     return JoinGradients(out_x, d_rows, d_weights, d_shared, d_gate, d_post, d_norm)
