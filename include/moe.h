@@ -668,8 +668,8 @@ moe_status moe_int8_quantize(const void *x, int64_t ldx, int x_rows,
                              int cols, void *codes, int64_t ld_codes,
                              float *scales, void *stream);
 
-/* Workspace bytes of the products (0 for sizes out of range).  The contents need
- * no initialisation and mean nothing after the call; a call's workspace is in
+/* Workspace bytes of the products (0 for sizes out of range, and for a linear
+ * product of a row or two, which needs none).  The contents need no initialisation and mean nothing after the call; a call's workspace is in
  * use until its work is done.                                              */
 size_t moe_int8_matmul_workspace(int M, int K);
 size_t moe_int8_linear_workspace(int M, int N, int K);

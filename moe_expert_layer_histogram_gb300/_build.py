@@ -16,7 +16,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_gb300.so")
 SOURCES = ["gemm.cu", "gemm_pair.cu", "decode.cu", "route.cu", "prep.cu", "api.cu",
            "route_static.cu", "peak.cu", "balance.cu", "gate.cu", "join.cu", "blockscale.cu",
-           "blockscale_gemm.cu", "int8.cu", "int8_gemm.cu"]
+           "blockscale_gemm.cu", "int8.cu", "int8_gemm.cu", "int8_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -298,6 +298,19 @@ moe_status run_quantize(const X* x, int64_t ldx, int x_rows, const int32_t* slot
   return take_error(e) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The product of a few rows: x in bf16, or codes a with their scales.
+moe_status run_rows(const Product& p, const void* x, int64_t ldx, const int8_t* a, int64_t lda,
+                    const float* scales, bool early, void* out, int64_t ldo, cudaStream_t s) {
+  Int8RowsArgs r{};
+  r.w = static_cast<const int8_t*>(p.w), r.ldw = p.ldw, r.w_scales = p.w_scales;
+  r.x = static_cast<const __nv_bfloat16*>(x), r.ldx = ldx;
+  r.x_vec = aligned_to(x, 16) && ldx % 8 == 0;
+  r.a = a, r.lda = lda, r.a_vec = aligned_to(a, 16) && lda % 16 == 0, r.a_scales = scales;
+  r.M = p.M, r.N = p.N, r.K = p.K;
+  r.out = static_cast<__nv_bfloat16*>(out), r.ldo = ldo;
+  return take_error(launch_int8_rows(r, early, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // Blocks of an elementwise kernel of 256 threads over n vectors.
 int vector_blocks(int64_t n) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 152 * 8 * 4)));
@@ -344,8 +357,10 @@ moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, co
       !aligned_to(workspace, 16) || workspace_bytes < moe_int8_matmul_workspace(M, K))
     return MOE_ERR_INVALID_ARG;
   if (!current_device()) return MOE_ERR_NO_DEVICE;
-  const Coded c(workspace, M, K);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (int8_by_rows(M, K, E) && !offsets)
+    return run_rows(p, nullptr, 0, static_cast<const int8_t*>(a), lda, a_scales, false, out, ldo, s);
+  const Coded c(workspace, M, K);
   const int64_t vectors = static_cast<int64_t>(M) * ((K + 7) / 8);
   const cudaError_t e = launch_pdl(false, int8_widen_kernel, dim3(vector_blocks(vectors)),
                                    dim3(256), 0, s, static_cast<const int8_t*>(a), lda, M, K,
@@ -355,7 +370,7 @@ moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, co
 }
 
 size_t moe_int8_linear_workspace(int M, int N, int K) {
-  return N < 1 || N > kMaxExtent ? 0 : moe_int8_matmul_workspace(M, K);
+  return N < 1 || N > kMaxExtent || int8_rows_quantize(M, K, 1) ? 0 : moe_int8_matmul_workspace(M, K);
 }
 
 moe_status moe_int8_linear(const void* x, int64_t ldx, const void* w, int64_t ldw,
@@ -366,12 +381,23 @@ moe_status moe_int8_linear(const void* x, int64_t ldx, const void* w, int64_t ld
   if (st != MOE_OK) return st;
   if (ldx < K || ldo < N) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  if (!x || !out || !aligned_to(x, 2) || !aligned_to(out, 2) || !workspace ||
-      !aligned_to(workspace, 16) || workspace_bytes < moe_int8_linear_workspace(M, N, K))
+  const size_t need = moe_int8_linear_workspace(M, N, K);
+  if (!x || !out || !aligned_to(x, 2) || !aligned_to(out, 2) || workspace_bytes < need ||
+      (need && (!workspace || !aligned_to(workspace, 16))))
     return MOE_ERR_INVALID_ARG;
   if (!current_device()) return MOE_ERR_NO_DEVICE;
-  const Coded c(workspace, M, K);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!need) return run_rows(p, x, ldx, nullptr, 0, nullptr, false, out, ldo, s);
+  const Coded c(workspace, M, K);
+  if (int8_by_rows(M, K, 1)) {
+    // (codes of 8 bits where those of 16 would be)
+    int8_t* codes = reinterpret_cast<int8_t*>(c.codes);
+    const int64_t ld = padded(K, 16);
+    const moe_status sq = run_quantize<false>(static_cast<const __nv_bfloat16*>(x), ldx, M, nullptr,
+                                              1, M, K, codes, ld, c.scales, s);
+    if (sq != MOE_OK) return sq;
+    return run_rows(p, nullptr, 0, codes, ld, c.scales, true, out, ldo, s);
+  }
   const moe_status sq = run_quantize<true>(static_cast<const __nv_bfloat16*>(x), ldx, M, nullptr, 1,
                                            M, K, c.codes, c.ld, c.scales, s);
   if (sq != MOE_OK) return sq;

@@ -1,0 +1,218 @@
+// int8_rows.cu -- 8-bit integer products of a few rows: y[m][n] = sx[m] sw[n]
+// sum_k cx[m][k] cw[n][k] for up to eight m.
+//
+// Such a product is as fast as its weights come out of HBM, and a row's dot products
+// of four codes (dp4a, int32 sums: exact) keep up with that without the tensor
+// cores' staging.  A warp takes four channels and a slice of the reduction, 16 codes
+// a lane and channel at a time; it has its first loads under way before anything
+// else: one or two rows are quantised by every block for itself meanwhile (QUANT),
+// more by a kernel that this one overlaps.  4096 x 7168: one row 8.4 us a call of
+// one kernel (29 MB: 4.3 us of HBM), through the tensor cores 17.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "int8_quant.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsChannels = 4;  // of a warp
+constexpr int kRowsAhead = 2;     // blocks of 512 codes that are loaded together
+constexpr int kRowsOwn = 32768;   // codes that a block quantises for itself, at most
+constexpr unsigned kAllLanes = 0xFFFFFFFFu;
+
+// Sixteen codes from column k on; past K: zeros.
+__device__ __forceinline__ uint4 load16(const int8_t* row, int k, int K, bool aligned) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (aligned && k + 16 <= K) {
+    v = *reinterpret_cast<const uint4*>(row + k);
+  } else if (k < K) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (k + i < K) w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+__device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
+  acc = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), acc);
+  acc = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), acc);
+  acc = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), acc);
+  return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), acc);
+}
+
+// M: rows (some may be past p.M).  QUANT: p.x in bf16, else codes p.a and scales.
+// p.slices warps of a block share four channels' reduction.
+template <int M, bool QUANT>
+__global__ void __launch_bounds__(kRowsThreads, M <= 4 ? 3 : 2)
+    int8_rows_kernel(const __grid_constant__ Int8RowsArgs p) {
+  extern __shared__ uint8_t s_codes[];  // QUANT: [M][K rounded up to 16]
+  __shared__ uint32_t s_max[8][M];
+  __shared__ int s_sum[8][kRowsChannels * M];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slice = warp % p.slices, group = warp / p.slices, groups = 8 / p.slices;
+  const int n0 = (blockIdx.x * groups + group) * kRowsChannels;
+  const int step = p.slices * 512;
+  uint4 w[kRowsAhead][kRowsChannels];
+  auto load_w = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < kRowsAhead; ++i)
+#pragma unroll
+      for (int c = 0; c < kRowsChannels; ++c) {
+        const int k = k0 + i * step;
+        w[i][c] = n0 + c < p.N ? load16(p.w + static_cast<int64_t>(n0 + c) * p.ldw, k, p.K, true)
+                               : make_uint4(0u, 0u, 0u, 0u);
+      }
+  };
+  int k0 = (slice * 32 + lane) * 16;
+  if (!QUANT) pdl_launch_dependents();
+  load_w(k0);
+  const int ld = (p.K + 15) / 16 * 16;
+  float scale[QUANT ? M : 1];
+  if constexpr (QUANT) {
+    const int vectors = (p.K + 7) / 8;
+    auto load_x = [&](int m, int v, float (&f)[8]) {
+      const uint16_t* src =
+          reinterpret_cast<const uint16_t*>(p.x) + static_cast<int64_t>(m) * p.ldx + v * 8;
+      if (p.x_vec && v * 8 + 8 <= p.K) {
+        const uint4 q = *reinterpret_cast<const uint4*>(src);
+        const uint32_t b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = __uint_as_float(b[i] << 16);
+          f[2 * i + 1] = __uint_as_float(b[i] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          f[i] = v * 8 + i < p.K ? __uint_as_float(static_cast<uint32_t>(src[i]) << 16) : 0.0f;
+      }
+    };
+    uint32_t most[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      most[m] = 0u;
+      if (m < p.M)
+        for (int v = threadIdx.x; v < vectors; v += kRowsThreads) {
+          float f[8];
+          load_x(m, v, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) most[m] = max(most[m], __float_as_uint(f[i]) & 0x7FFFFFFFu);
+        }
+      most[m] = __reduce_max_sync(kAllLanes, most[m]);
+      if (lane == 0) s_max[warp][m] = most[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most[m] = max(most[m], s_max[i][m]);
+      scale[m] = i8_scale(most[m]);
+      const I8Coder coder(scale[m]);
+      for (int v = threadIdx.x; v * 8 < ld; v += kRowsThreads) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (m < p.M && v < vectors) load_x(m, v, f);
+        *reinterpret_cast<uint2*>(s_codes + m * ld + v * 8) = coder.bytes(f);
+      }
+    }
+    __syncthreads();
+  } else {
+    pdl_wait();
+  }
+  int acc[kRowsChannels][M];
+#pragma unroll
+  for (int c = 0; c < kRowsChannels; ++c)
+#pragma unroll
+    for (int m = 0; m < M; ++m) acc[c][m] = 0;
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < kRowsAhead; ++i) {
+      const int k = k0 + i * step;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (QUANT) {
+          if (k < p.K) x = *reinterpret_cast<const uint4*>(s_codes + m * ld + k);
+        } else if (m < p.M) {
+          x = load16(p.a + static_cast<int64_t>(m) * p.lda, k, p.K, p.a_vec != 0);
+        }
+#pragma unroll
+        for (int c = 0; c < kRowsChannels; ++c) acc[c][m] = dot16(w[i][c], x, acc[c][m]);
+      }
+    }
+    k0 += kRowsAhead * step;
+    if (k0 - (slice * 32 + lane) * 16 >= p.K) break;  // (the same for all lanes)
+    load_w(k0);
+  }
+#pragma unroll
+  for (int c = 0; c < kRowsChannels; ++c)
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int sum = __reduce_add_sync(kAllLanes, acc[c][m]);
+      if (lane == 0) s_sum[warp][c * M + m] = sum;
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < groups * kRowsChannels * M; i += kRowsThreads) {
+    const int g = i / (kRowsChannels * M), c = i / M % kRowsChannels, m = i % M;
+    const int n = (blockIdx.x * groups + g) * kRowsChannels + c;
+    if (n >= p.N || m >= p.M) continue;
+    int sum = 0;
+    for (int s = 0; s < p.slices; ++s) sum += s_sum[g * p.slices + s][c * M + m];
+    float sx;
+    if constexpr (QUANT) {
+      sx = scale[0];
+#pragma unroll
+      for (int q = 1; q < M; ++q) sx = m == q ? scale[q] : sx;
+    } else {
+      sx = p.a_scales[m];
+    }
+    p.out[m * p.ldo + n] = __float2bfloat16_rn(static_cast<float>(sum) * (sx * p.w_scales[n]));
+  }
+}
+
+template <int M, bool QUANT>
+cudaError_t launch(const Int8RowsArgs& p, bool early, cudaStream_t s) {
+  const int groups = 8 / p.slices;
+  const int64_t blocks = (static_cast<int64_t>(p.N) + groups * kRowsChannels - 1) / (groups * kRowsChannels);
+  const int smem = QUANT ? M * ((p.K + 15) / 16 * 16) : 0;
+  static OncePerDevice prepared;
+  if (QUANT) {
+    const cudaError_t e = prepared([&] {
+      return cudaFuncSetAttribute(int8_rows_kernel<M, QUANT>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsOwn + 64);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(early, int8_rows_kernel<M, QUANT>, dim3(static_cast<unsigned>(blocks)),
+                    dim3(kRowsThreads), smem, s, p);
+}
+
+}  // namespace
+
+// See internal.h.  Int32 sums hold K products of up to 127 x 128.
+bool int8_by_rows(int M, int K, int E) { return E == 1 && M <= 8 && K <= 131072; }
+bool int8_rows_quantize(int M, int K, int E) {
+  return int8_by_rows(M, K, E) && M <= 2 && M * static_cast<int64_t>(K) <= kRowsOwn;
+}
+
+cudaError_t launch_int8_rows(Int8RowsArgs p, bool early, cudaStream_t s) {
+  // Warps to a reduction: as many as leave each the blocks that it loads at once.
+  const int blocks = (p.K + 511) / 512;
+  p.slices = 1;
+  while (p.slices < 8 && p.slices * kRowsAhead < blocks) p.slices *= 2;
+  if (p.x) return p.M == 1 ? launch<1, true>(p, false, s) : launch<2, true>(p, false, s);
+  if (p.M == 1) return launch<1, false>(p, early, s);
+  if (p.M == 2) return launch<2, false>(p, early, s);
+  if (p.M <= 4) return launch<4, false>(p, early, s);
+  return launch<8, false>(p, early, s);
+}
+
+}  // namespace moe

@@ -288,6 +288,29 @@ struct Int8Args {
 // library's own and lets it start early.
 cudaError_t launch_int8(const Int8Maps& maps, Int8Args args, bool swiglu,
                         const BlockscaleDevice& d, cudaStream_t s);
+// Products of a few rows without the tensor cores (int8_rows.cu).
+struct Int8RowsArgs {
+  const int8_t* w;         // [N, K]
+  int64_t ldw;
+  const float* w_scales;   // [N]
+  const __nv_bfloat16* x;  // rows that the kernel quantises itself, or null:
+  int64_t ldx;
+  int x_vec;               // (rows on 16 bytes)
+  const int8_t* a;         // their codes,
+  int64_t lda;
+  int a_vec;
+  const float* a_scales;   // and scales
+  int M, N, K;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  int slices;              // set by launch_int8_rows
+};
+bool int8_by_rows(int M, int K, int E);
+bool int8_rows_quantize(int M, int K, int E);  // ... and quantises its rows
+// early: the kernel before it is the library's own, writes codes and scales, and lets
+// it start early.
+cudaError_t launch_int8_rows(Int8RowsArgs p, bool early, cudaStream_t s);
+
 // Whether a product runs on CTA pairs (its weights' boxes are 64 rows high with
 // swiglu), and the most rows of a chunk of its items.
 bool int8_in_pairs(int M, int N, int E);

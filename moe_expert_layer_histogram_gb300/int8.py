@@ -115,9 +115,9 @@ def int8_linear(x, w, w_scales, out=None):
     out, ldo = _result(out, M, N, dev)
     L = lib()
     nbytes = L.moe_int8_linear_workspace(M, N, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     code = L.moe_int8_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, w_scales.data_ptr(), M, N, K,
-                             out.data_ptr(), ldo, ws.data_ptr(), nbytes, stream)
+                             out.data_ptr(), ldo, ws.data_ptr() if nbytes else None, nbytes, stream)
     if code:
         raise MoEError(code, "moe_int8_linear")
     return out

@@ -146,6 +146,37 @@ def test_matmul(M, N, K):
     close(got, *matmul_reference(a, s, w, ws), K)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 16), (7, 33), (130, 512), (257, 1000), (1001, 2500),
+                                 (64, 20000), (300, 4113)])
+def test_few_rows(M, N, K):
+    from moe_expert_layer_histogram_gb300 import int8_linear, int8_matmul, int8_quantize
+    ld = (K + 15) // 16 * 16
+    flat = codes_of((N - 1) * ld + K, seed=2)               # (nothing behind the last row)
+    w, ws = torch.as_strided(flat, (N, K), (ld, 1)), scales_of(N)
+    if N == 1:
+        w = flat.view(1, K)
+    for lead in (0, 3):
+        a, s = codes_of(M, K + 5 + lead, seed=1)[:, lead:lead + K], scales_of(M)
+        got = int8_matmul(a, s, w, ws)
+        want, mag = matmul_reference(a, s, w, ws)
+        close(got, want, mag, K)
+        x = randn(M, K + 8 + lead)[:, lead:lead + K]
+        assert torch.equal(int8_linear(x, w, ws), int8_matmul(*int8_quantize(x), w, ws))
+
+
+def test_few_rows_of_the_largest_codes():
+    # 131072 products of 127 x -128: int32 sums at their limit, then fp32 ones
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    for K in (131072, 131088):
+        for M in (1, 8):
+            a = torch.full((M, K), 127, dtype=torch.int8, device="cuda")
+            w = torch.full((5, K), -128, dtype=torch.int8, device="cuda")
+            got = int8_matmul(a, torch.ones(M, device="cuda"), w, torch.ones(5, device="cuda"))
+            want = torch.full((M, 5), -127.0 * 128 * K, dtype=torch.float64, device="cuda")
+            close(got, want, -want, K)
+
+
 @pytest.mark.parametrize("M,N,K", [(4864, 1024, 400), (5000, 1025, 130), (9728, 500, 64),
                                    (2049, 9800, 1000), (20000, 256, 16)])
 def test_matmul_of_many_rows(M, N, K):
