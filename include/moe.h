@@ -668,10 +668,11 @@ moe_status moe_int8_quantize(const void *x, int64_t ldx, int x_rows,
                              int cols, void *codes, int64_t ld_codes,
                              float *scales, void *stream);
 
-/* Workspace bytes of the products (0 for sizes out of range, and for a linear
- * product of a row or two, which needs none).  The contents need no initialisation and mean nothing after the call; a call's workspace is in
+/* Workspace bytes of the products (0 for sizes out of range, and for products of a
+ * few rows, which need none; grouped: whether offsets will be given).  The contents
+ * need no initialisation and mean nothing after the call; a call's workspace is in
  * use until its work is done.                                              */
-size_t moe_int8_matmul_workspace(int M, int K);
+size_t moe_int8_matmul_workspace(int M, int K, int grouped);
 size_t moe_int8_linear_workspace(int M, int N, int K);
 size_t moe_int8_experts_workspace(int rows, int H, int I);
 
@@ -684,7 +685,8 @@ size_t moe_int8_experts_workspace(int rows, int H, int I);
  * written; offsets are clamped into [0, M], and one that is below an earlier
  * offset counts as that one.  The order of a row's sums depends on E, M, N, K and
  * the device alone.  N, K, M of any size up to 2^31 - 65792, E <= 512.  M == 0
- * is a no-op.  workspace: device, 16-byte aligned.  Asynchronous on `stream`,
+ * is a no-op.  workspace: device, 16-byte aligned (may be NULL when none is needed).
+ * Asynchronous on `stream`,
  * allocates nothing.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
  * MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.  A kernel that gives up a bounded wait leaves
  * its output incomplete and records it for moe_int8_status.                */

@@ -134,7 +134,7 @@ def lib():
                                          cf, vp, i64, vp, ctypes.c_size_t, vp]
     L.moe_blockscale_status.argtypes = []
     L.moe_int8_quantize.argtypes = [vp, i64, ci, vp, ci, ci, ci, vp, i64, vp, vp]
-    L.moe_int8_matmul_workspace.argtypes = [ci, ci]
+    L.moe_int8_matmul_workspace.argtypes = [ci, ci, ci]
     L.moe_int8_linear_workspace.argtypes = [ci, ci, ci]
     L.moe_int8_experts_workspace.argtypes = [ci, ci, ci]
     L.moe_int8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, vp, ci, ci, ci, ci, vp, i64, vp,
@@ -411,8 +411,8 @@ def moe_int8_quantize(x, ldx, x_rows, slots, top_k, rows, cols, codes, ld_codes,
            "moe_int8_quantize")
 
 
-def moe_int8_matmul_workspace(M, K):
-    return lib().moe_int8_matmul_workspace(M, K)
+def moe_int8_matmul_workspace(M, K, grouped=False):
+    return lib().moe_int8_matmul_workspace(M, K, int(bool(grouped)))
 
 
 def moe_int8_linear_workspace(M, N, K):

@@ -274,6 +274,7 @@ moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const fl
   a.out = out;
   a.ldo = ldo;
   a.out_pairs = aligned_to(out, 4) && ldo % 2 == 0;
+  a.out_fours = aligned_to(out, 8) && ldo % 4 == 0;
   a.clamp = clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY;
   return take_error(launch_int8(maps, a, swiglu, *d, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -339,9 +340,9 @@ moe_status moe_int8_quantize(const void* x, int64_t ldx, int x_rows, const int32
                              cols, codes, ld_codes, scales, static_cast<cudaStream_t>(stream));
 }
 
-size_t moe_int8_matmul_workspace(int M, int K) {
+size_t moe_int8_matmul_workspace(int M, int K, int grouped) {
   if (M < 1 || K < 1 || M > kMaxExtent || K > kMaxExtent) return 0;
-  return static_cast<size_t>(Coded::bytes(M, K));
+  return !grouped && int8_by_rows(M, K, 1) ? 0 : static_cast<size_t>(Coded::bytes(M, K));
 }
 
 moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, const void* w,
@@ -353,12 +354,13 @@ moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, co
   if (st != MOE_OK) return st;
   if (lda < K || ldo < N) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  if (!a || !a_scales || !out || !aligned_to(a_scales, 4) || !aligned_to(out, 2) || !workspace ||
-      !aligned_to(workspace, 16) || workspace_bytes < moe_int8_matmul_workspace(M, K))
+  const size_t need = moe_int8_matmul_workspace(M, K, offsets != nullptr);
+  if (!a || !a_scales || !out || !aligned_to(a_scales, 4) || !aligned_to(out, 2) ||
+      workspace_bytes < need || (need && (!workspace || !aligned_to(workspace, 16))))
     return MOE_ERR_INVALID_ARG;
   if (!current_device()) return MOE_ERR_NO_DEVICE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (int8_by_rows(M, K, E) && !offsets)
+  if (!need)
     return run_rows(p, nullptr, 0, static_cast<const int8_t*>(a), lda, a_scales, false, out, ldo, s);
   const Coded c(workspace, M, K);
   const int64_t vectors = static_cast<int64_t>(M) * ((K + 7) / 8);
@@ -370,7 +372,8 @@ moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, co
 }
 
 size_t moe_int8_linear_workspace(int M, int N, int K) {
-  return N < 1 || N > kMaxExtent || int8_rows_quantize(M, K, 1) ? 0 : moe_int8_matmul_workspace(M, K);
+  return N < 1 || N > kMaxExtent || int8_rows_quantize(M, K, 1) ? 0
+                                                                : moe_int8_matmul_workspace(M, K, 1);
 }
 
 moe_status moe_int8_linear(const void* x, int64_t ldx, const void* w, int64_t ldw,

@@ -1,13 +1,15 @@
 // int8_rows.cu -- 8-bit integer products of a few rows: y[m][n] = sx[m] sw[n]
-// sum_k cx[m][k] cw[n][k] for up to eight m.
+// sum_k cx[m][k] cw[n][k] for up to four m.
 //
 // Such a product is as fast as its weights come out of HBM, and a row's dot products
 // of four codes (dp4a, int32 sums: exact) keep up with that without the tensor
 // cores' staging.  A warp takes four channels and a slice of the reduction, 16 codes
 // a lane and channel at a time; it has its first loads under way before anything
 // else: one or two rows are quantised by every block for itself meanwhile (QUANT),
-// more by a kernel that this one overlaps.  4096 x 7168: one row 8.4 us a call of
-// one kernel (29 MB: 4.3 us of HBM), through the tensor cores 17.
+// more by a kernel that this one overlaps.  On the GPU, 7168 -> 4096: one row 7.1
+// us, three 9.3, four 10.0, eight 18.6 (the dot products take the time by then);
+// through the tensor cores nine rows 12.4.  4096 -> 14592 (60 MB, 8.8 us of HBM): one
+// row 8.7, four 14.0, nine 15.9.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -24,6 +26,7 @@ namespace {
 constexpr int kRowsThreads = 256;
 constexpr int kRowsChannels = 4;  // of a warp
 constexpr int kRowsAhead = 2;     // blocks of 512 codes that are loaded together
+constexpr int kRowsSms = 152, kRowsResident = 3;  // blocks of an SM at a time
 constexpr int kRowsOwn = 32768;   // codes that a block quantises for itself, at most
 constexpr unsigned kAllLanes = 0xFFFFFFFFu;
 
@@ -52,14 +55,16 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
 // M: rows (some may be past p.M).  QUANT: p.x in bf16, else codes p.a and scales.
 // p.slices warps of a block share four channels' reduction.
 template <int M, bool QUANT>
-__global__ void __launch_bounds__(kRowsThreads, M <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kRowsThreads, kRowsResident)
     int8_rows_kernel(const __grid_constant__ Int8RowsArgs p) {
   extern __shared__ uint8_t s_codes[];  // QUANT: [M][K rounded up to 16]
   __shared__ uint32_t s_max[8][M];
-  __shared__ int s_sum[8][kRowsChannels * M];
+  __shared__ int s_sum[2][8][kRowsChannels * M];  // by turns
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slice = warp % p.slices, group = warp / p.slices, groups = 8 / p.slices;
-  const int n0 = (blockIdx.x * groups + group) * kRowsChannels;
+  // this block's units (groups * kRowsChannels channels), and the warp's channels
+  const int units = (p.N + groups * kRowsChannels - 1) / (groups * kRowsChannels);
+  int unit = blockIdx.x, n0 = (unit * groups + group) * kRowsChannels;
   const int step = p.slices * 512;
   uint4 w[kRowsAhead][kRowsChannels];
   auto load_w = [&](int k0) {
@@ -127,61 +132,73 @@ __global__ void __launch_bounds__(kRowsThreads, M <= 4 ? 3 : 2)
   } else {
     pdl_wait();
   }
-  int acc[kRowsChannels][M];
+  for (int turn = 0;; turn ^= 1) {
+    int acc[kRowsChannels][M];
 #pragma unroll
-  for (int c = 0; c < kRowsChannels; ++c)
+    for (int c = 0; c < kRowsChannels; ++c)
 #pragma unroll
-    for (int m = 0; m < M; ++m) acc[c][m] = 0;
-  for (;;) {
+      for (int m = 0; m < M; ++m) acc[c][m] = 0;
+    for (;;) {
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i) {
-      const int k = k0 + i * step;
+      for (int i = 0; i < kRowsAhead; ++i) {
+        const int k = k0 + i * step;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (QUANT) {
+            if (k < p.K) x = *reinterpret_cast<const uint4*>(s_codes + m * ld + k);
+          } else if (m < p.M) {
+            x = load16(p.a + static_cast<int64_t>(m) * p.lda, k, p.K, p.a_vec != 0);
+          }
+#pragma unroll
+          for (int c = 0; c < kRowsChannels; ++c) acc[c][m] = dot16(w[i][c], x, acc[c][m]);
+        }
+      }
+      k0 += kRowsAhead * step;
+      if (k0 - (slice * 32 + lane) * 16 >= p.K) break;  // (the same for all lanes)
+      load_w(k0);
+    }
+    // the next unit's weights are on their way while this one's sums are joined
+    const int done = unit;
+    unit += gridDim.x;
+    k0 = (slice * 32 + lane) * 16;
+    if (unit < units) {
+      n0 = (unit * groups + group) * kRowsChannels;
+      load_w(k0);
+    }
+#pragma unroll
+    for (int c = 0; c < kRowsChannels; ++c)
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (QUANT) {
-          if (k < p.K) x = *reinterpret_cast<const uint4*>(s_codes + m * ld + k);
-        } else if (m < p.M) {
-          x = load16(p.a + static_cast<int64_t>(m) * p.lda, k, p.K, p.a_vec != 0);
-        }
-#pragma unroll
-        for (int c = 0; c < kRowsChannels; ++c) acc[c][m] = dot16(w[i][c], x, acc[c][m]);
+        const int sum = __reduce_add_sync(kAllLanes, acc[c][m]);
+        if (lane == 0) s_sum[turn][warp][c * M + m] = sum;
       }
-    }
-    k0 += kRowsAhead * step;
-    if (k0 - (slice * 32 + lane) * 16 >= p.K) break;  // (the same for all lanes)
-    load_w(k0);
-  }
+    __syncthreads();
+    for (int i = threadIdx.x; i < groups * kRowsChannels * M; i += kRowsThreads) {
+      const int g = i / (kRowsChannels * M), c = i / M % kRowsChannels, m = i % M;
+      const int n = (done * groups + g) * kRowsChannels + c;
+      if (n >= p.N || m >= p.M) continue;
+      int sum = 0;
+      for (int s = 0; s < p.slices; ++s) sum += s_sum[turn][g * p.slices + s][c * M + m];
+      float sx;
+      if constexpr (QUANT) {
+        sx = scale[0];
 #pragma unroll
-  for (int c = 0; c < kRowsChannels; ++c)
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const int sum = __reduce_add_sync(kAllLanes, acc[c][m]);
-      if (lane == 0) s_sum[warp][c * M + m] = sum;
+        for (int q = 1; q < M; ++q) sx = m == q ? scale[q] : sx;
+      } else {
+        sx = p.a_scales[m];
+      }
+      p.out[m * p.ldo + n] = __float2bfloat16_rn(static_cast<float>(sum) * (sx * p.w_scales[n]));
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < groups * kRowsChannels * M; i += kRowsThreads) {
-    const int g = i / (kRowsChannels * M), c = i / M % kRowsChannels, m = i % M;
-    const int n = (blockIdx.x * groups + g) * kRowsChannels + c;
-    if (n >= p.N || m >= p.M) continue;
-    int sum = 0;
-    for (int s = 0; s < p.slices; ++s) sum += s_sum[g * p.slices + s][c * M + m];
-    float sx;
-    if constexpr (QUANT) {
-      sx = scale[0];
-#pragma unroll
-      for (int q = 1; q < M; ++q) sx = m == q ? scale[q] : sx;
-    } else {
-      sx = p.a_scales[m];
-    }
-    p.out[m * p.ldo + n] = __float2bfloat16_rn(static_cast<float>(sum) * (sx * p.w_scales[n]));
+    if (unit >= units) break;
   }
 }
 
 template <int M, bool QUANT>
 cudaError_t launch(const Int8RowsArgs& p, bool early, cudaStream_t s) {
   const int groups = 8 / p.slices;
-  const int64_t blocks = (static_cast<int64_t>(p.N) + groups * kRowsChannels - 1) / (groups * kRowsChannels);
+  const int units = (p.N - 1) / (groups * kRowsChannels) + 1;
+  const int blocks = std::min(units, kRowsResident * kRowsSms);
   const int smem = QUANT ? M * ((p.K + 15) / 16 * 16) : 0;
   static OncePerDevice prepared;
   if (QUANT) {
@@ -191,14 +208,14 @@ cudaError_t launch(const Int8RowsArgs& p, bool early, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(early, int8_rows_kernel<M, QUANT>, dim3(static_cast<unsigned>(blocks)),
+  return launch_pdl(early, int8_rows_kernel<M, QUANT>, dim3(blocks),
                     dim3(kRowsThreads), smem, s, p);
 }
 
 }  // namespace
 
 // See internal.h.  Int32 sums hold K products of up to 127 x 128.
-bool int8_by_rows(int M, int K, int E) { return E == 1 && M <= 8 && K <= 131072; }
+bool int8_by_rows(int M, int K, int E) { return E == 1 && M <= 4 && K <= 131072; }
 bool int8_rows_quantize(int M, int K, int E) {
   return int8_by_rows(M, K, E) && M <= 2 && M * static_cast<int64_t>(K) <= kRowsOwn;
 }
@@ -211,8 +228,7 @@ cudaError_t launch_int8_rows(Int8RowsArgs p, bool early, cudaStream_t s) {
   if (p.x) return p.M == 1 ? launch<1, true>(p, false, s) : launch<2, true>(p, false, s);
   if (p.M == 1) return launch<1, false>(p, early, s);
   if (p.M == 2) return launch<2, false>(p, early, s);
-  if (p.M <= 4) return launch<4, false>(p, early, s);
-  return launch<8, false>(p, early, s);
+  return launch<4, false>(p, early, s);
 }
 
 }  // namespace moe

@@ -280,6 +280,7 @@ struct Int8Args {
   void* out;               // bf16 [M, ldo], or (SwiGLU) h in f32 [M, ldo]
   int64_t ldo;
   int out_pairs;           // bf16 rows start on 4-byte boundaries
+  int out_fours;           // ... on 8-byte ones
   float clamp;             // SwiGLU (+inf: none)
   // set by launch_int8
   int a_rows, tiles, stages, split, chunk_group;

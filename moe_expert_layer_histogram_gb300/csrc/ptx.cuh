@@ -574,15 +574,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];"
-               : "=f"(v)
-               : "r"(mapa_shared(saddr, rank))
-               : "memory");
-  return v;
-}
-
 // mbar_wait by a whole warp, without a look at the timer before the wait has
 // lasted for many tries: reading it takes longer than most waits here.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {

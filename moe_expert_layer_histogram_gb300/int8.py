@@ -92,11 +92,12 @@ def int8_matmul(codes, scales, w, w_scales, offsets=None, out=None):
         raise ValueError("offsets: wanted for weights of several experts")
     out, ldo = _result(out, M, N, dev)
     L = lib()
-    nbytes = L.moe_int8_matmul_workspace(M, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    nbytes = L.moe_int8_matmul_workspace(M, K, 0 if offsets is None else 1)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     code = L.moe_int8_matmul(codes.data_ptr(), lda, scales.data_ptr(), w.data_ptr(), ldw,
                              w_scales.data_ptr(), None if offsets is None else offsets.data_ptr(), E,
-                             M, N, K, out.data_ptr(), ldo, ws.data_ptr(), nbytes, stream)
+                             M, N, K, out.data_ptr(), ldo, ws.data_ptr() if nbytes else None, nbytes,
+                             stream)
     if code:
         raise MoEError(code, "moe_int8_matmul")
     return out
