@@ -432,8 +432,9 @@ moe_status moe_gate_forward(const void *logits, int dtype, int64_t ld,
  *   d s_k = scale / sum * (d_w_k - sum_j u_j d_w_j)  (normalize), or
  *   d s_k = scale * d_w_k;
  * d l_e = s_e (1 - s_e) d s_e (sigmoid) or s_e (d s_e - sum_j s_j d s_j)
- * (softmax); zero for tokens that are not live.  T == 0 is a no-op.  Limits,
- * alignment and errors as the forward.                                     */
+ * (softmax); zero for tokens that are not live; d_logits may be logits
+ * itself, with ld_d = ld.  T == 0 is a no-op.  Limits, alignment and errors as the
+ * forward.                                                                 */
 moe_status moe_gate_backward(const void *logits, int dtype, int64_t ld, int T,
                              int E, int K, const moe_gate_config *cfg,
                              const int32_t *ids, const float *d_weights,

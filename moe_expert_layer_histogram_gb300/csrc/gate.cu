@@ -22,11 +22,12 @@
 // positive) but the last four, which hold 15 - j for the lane's j-th expert.  So
 // one redux.sync finds a round's winner and, with a vote for the lane, its index,
 // and a lane's two largest words, which are all that a group's score needs too,
-// take three operations an expert.  (Keys and indices apart took 1880 instructions
-// a token, this 400.)  The words are coarser than fp32, and fp32 scores are off by
-// a few 2^-24: where the order of neighbours, or the border, could be another, the
-// token is decided again in 64 bits, its near choices only (at E = 384 and K = 8
-// nine gaps of about 0.008 against 5e-6: one token in two hundred).
+// take three operations an expert.  (32768 x 384 in 8 groups: keys and indices apart
+// took 124 us, this 39, of which the logits' bytes are 8: instructions bound it.)
+// The words are coarser than fp32, and fp32 scores are off by a few 2^-24: where the
+// order of neighbours, or the border, could be another, the token is decided again
+// in 64 bits, its near choices only (at E = 384 and K = 8 nine gaps of about 0.008
+// against 5e-6: one token in two hundred).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -440,7 +441,7 @@ __device__ __forceinline__ bool gate_token(const T* __restrict__ row, const Gate
     if constexpr (MODE == kByShortLogit) return false;
     if constexpr (MODE == kByLogit) return ((hi ^ lo) & ~kLow) == 0u;
     const float c = __uint_as_float(hi & ~kLow);
-    return c - __uint_as_float(lo & ~kLow) <= margin(c);
+    return !(c - __uint_as_float(lo & ~kLow) > margin(c));  // (two infinities: near)
   };
   bool kept = sh.in;
   if (p.group_top < p.groups) {
@@ -569,14 +570,16 @@ __device__ __forceinline__ bool gate_token(const T* __restrict__ row, const Gate
 
 constexpr int kGateWarps = 16;
 // A token per warp up to this many: one block, which then writes the counts by
-// itself (16 tokens of 64 experts: one launch instead of two).
-constexpr int kGateSmall = 32;
+// itself, in one launch instead of two.  (64 experts: 16 tokens 7.2 us with the order
+// behind it and 7.9 in two, 32 tokens 8.5 and 7.7; 384 experts 9.1 and 9.1, 11.5 and
+// 9.3.)
+constexpr int kGateSmall = 16;
 
 // SMALL: one block.  Else the counts are zero already (once the kernel before this
 // one is over) and the blocks add theirs: whole numbers, so the order does not
 // matter.
 template <int NL, bool FULL, int MODE, bool SMALL, typename T>
-__global__ void __launch_bounds__(SMALL ? 1024 : 32 * kGateWarps, SMALL ? 1 : NL > 16 ? 1 : 2)
+__global__ void __launch_bounds__(32 * (SMALL ? kGateSmall : kGateWarps), SMALL || NL > 16 ? 1 : 2)
     gate_forward_kernel(const T* __restrict__ logits, const __grid_constant__ GateArgs p) {
   __shared__ int s_count[kMaxExperts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -683,6 +686,7 @@ __global__ void __launch_bounds__(32 * kGateBackWarps)
       rest = p.scale * warp_sum(pk * dw);
       value = pk * (p.scale * dw - rest);
     }
+    __syncwarp();  // (d may be the row itself)
     if (dense && live) {
       for (int e = lane; e < p.E; e += 32) {
         const float pe = expf(to_f32(row[e]) - top) * inv;

@@ -214,8 +214,8 @@ cudaError_t launch(const Int8RowsArgs& p, bool early, cudaStream_t s) {
 
 }  // namespace
 
-// See internal.h.  Int32 sums hold K products of up to 127 x 128.
-bool int8_by_rows(int M, int K, int E) { return E == 1 && M <= 4 && K <= 131072; }
+// See internal.h.  Int32 sums hold K products of 128 x 128 below 2^17 of them.
+bool int8_by_rows(int M, int K, int E) { return E == 1 && M <= 4 && K < 131072; }
 bool int8_rows_quantize(int M, int K, int E) {
   return int8_by_rows(M, K, E) && M <= 2 && M * static_cast<int64_t>(K) <= kRowsOwn;
 }

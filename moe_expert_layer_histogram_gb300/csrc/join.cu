@@ -818,9 +818,11 @@ __global__ void __launch_bounds__(1024, 1)
     for (int64_t t = blockIdx.x; ring.ok && t < j.T; t += gridDim.x, ++n) {
       next.load(j, p.norm_rstd, p.post_rstd, t + gridDim.x, lane);
       words.leave(ring.info[n % kInfos], lane);
-      // (x' at any rate: a token has a row at least)
-      ring.put(static_cast<const X*>(p.x_out) + t * p.ld_out, H * sizeof(X), lane);
-      if (p.d_h) ring.put(static_cast<const __nv_bfloat16*>(p.d_h) + t * p.ld_dh, H * 2, lane);
+      // (of x', d h and d x' one is there: a token has a row at least)
+      if (p.d_h) {
+        ring.put(static_cast<const X*>(p.x_out) + t * p.ld_out, H * sizeof(X), lane);
+        ring.put(static_cast<const __nv_bfloat16*>(p.d_h) + t * p.ld_dh, H * 2, lane);
+      }
       if (p.d_x_out)
         ring.put(static_cast<const X*>(p.d_x_out) + t * p.ld_dxo, H * sizeof(X), lane);
       if (POST) put_rows(j, ring, t, words.row, lane, true, true);
@@ -837,9 +839,10 @@ __global__ void __launch_bounds__(1024, 1)
     int parity = 0, n = 0;
     for (int64_t t = blockIdx.x; t < j.T; t += gridDim.x, parity ^= 1, ++n) {
       const TokenInfo& info = ring.info[n % kInfos];
-      float g[kVec], a[kVec], xh[kVec];
-      ring.get<X>(H, xh);
+      float g[kVec], a[kVec];
       if (p.d_h) {
+        float xh[kVec];
+        ring.get<X>(H, xh);
         const float r = info.norm_rstd;
         float dot = 0.0f;
         load_weights<true>(j.norm_weight, j.weight_type, 0, H, a);
@@ -1114,7 +1117,7 @@ int back_blocks(int T, int H, int ring) {
 }
 
 bool back_by_ring(const JoinBackArgs& p, int size) {
-  return p.x_out && use_ring(p.j.T, p.j.H, size, true);
+  return (p.d_h || p.d_x_out) && use_ring(p.j.T, p.j.H, size, true);
 }
 
 template <typename X, bool VEC>
@@ -1218,7 +1221,8 @@ moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_ou
       return MOE_ERR_INVALID_ARG;
     JoinBackArgs p{};
     p.j = *j;
-    p.x_out = x_out, p.ld_out = ld_out, p.d_x_out = d_x_out, p.ld_dxo = ld_dxo;
+    p.x_out = d_h ? x_out : nullptr;  // (read with d_h alone)
+    p.ld_out = ld_out, p.d_x_out = d_x_out, p.ld_dxo = ld_dxo;
     p.d_h = d_h, p.ld_dh = ld_dh, p.post_rstd = post_rstd, p.norm_rstd = norm_rstd;
     p.d_x = d_x, p.ld_dx = ld_dx;
     p.d_rows = static_cast<__nv_bfloat16*>(d_rows), p.ld_drows = ld_drows;
@@ -1228,7 +1232,7 @@ moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_ou
     p.d_gate = d_gate;
     moe_join in = *j;
     in.x = nullptr;  // (not read)
-    const bool vec = join_vectors(in) && in_vectors(x_out, ld_out, xs) &&
+    const bool vec = join_vectors(in) && in_vectors(p.x_out, ld_out, xs) &&
                      in_vectors(d_x_out, ld_dxo, xs) && in_vectors(d_h, ld_dh, 2) &&
                      in_vectors(d_x, ld_dx, xs) && in_vectors(d_rows, ld_drows, 2) &&
                      in_vectors(d_shared, ld_dshared, 2);

@@ -5,6 +5,7 @@ Thin wrappers of ``moe_gate_forward``, ``moe_gate_backward`` and ``moe_order``
 (``include/moe.h`` states the formulas); work goes on torch's current stream.
 """
 import functools
+from operator import index
 
 import torch
 
@@ -39,8 +40,8 @@ def _config(score, groups, group_top, group_score, normalize, scale):
     if score not in MOE_SCORE or group_score not in MOE_GROUP:
         raise ValueError("score: one of %s, group_score: one of %s"
                          % (sorted(MOE_SCORE), sorted(MOE_GROUP)))
-    return MoEGateConfig(MOE_SCORE[score], groups, groups if group_top is None else group_top,
-                         MOE_GROUP[group_score], 1 if normalize else 0, scale)
+    return MoEGateConfig(MOE_SCORE[score], groups, group_top, MOE_GROUP[group_score], normalize,
+                         scale)
 
 
 def _logits(t, name):
@@ -70,7 +71,8 @@ def router_gate(logits, top_k, score="softmax", bias=None, groups=1, group_top=N
         check(mask, torch.bool if mask.dtype is torch.bool else torch.uint8, (T,), dev, "mask")
     fits(top_k, "top_k")
     fits(max(groups, group_top or 0), "groups")
-    config = _config(score, groups, group_top, group_score, normalize, scale)
+    config = _config(score, index(groups), index(groups if group_top is None else group_top),
+                     group_score, bool(normalize), float(scale))
     k = max(top_k, 0)
     ids = torch.empty(T, k, dtype=_I32, device=dev)
     weights = torch.empty(T, k, dtype=_F32, device=dev)

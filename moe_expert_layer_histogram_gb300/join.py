@@ -32,7 +32,7 @@ class BlockJoin:
 
 class JoinGradients:
     """Gradients of block_join's arguments, under their names; None for those
-    that it did not have."""
+    that it did not have, and for norm_weight without d_h."""
     __slots__ = ("x", "expert_rows", "weights", "shared", "gate", "post_weight", "norm_weight")
 
     def __init__(self, x, expert_rows, weights, shared, gate, post_weight, norm_weight):
@@ -84,8 +84,8 @@ def block_join(x, expert_rows=None, order=None, weights=None, shared=None, gate=
     K = ld_rows = rows = rows_ptr = slots_ptr = weights_ptr = 0
     row_of_slot = live = None
     if expert_rows is not None:
-        if order is None or weights is None or weights.dim() != 2:
-            raise ValueError("expert_rows: wanted with order and weights [T, K]")
+        if order is None or weights is None or weights.dim() != 2 or not weights.shape[1]:
+            raise ValueError("expert_rows: wanted with order and weights [T, K], K >= 1")
         K = weights.shape[1]
         row_of_slot = order
         if isinstance(order, RouterOrder):

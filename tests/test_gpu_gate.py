@@ -211,6 +211,35 @@ def test_dead_tokens_and_disabled_experts():
                 assert torch.all(d[3] == 0)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (4, 2)])
+def test_biases_as_far_apart_as_fp32_has_them(score, groups, group_top):
+    bias = torch.full((64,), 3e38, device="cuda")
+    bias[::3] = -3e38
+    bias[5::7] = 0.0
+    check(logits_of(40, 64), 8, score=score, bias=bias, groups=groups, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("E", [6, 64, 384])
+def test_gradient_in_place(score, normalize, E):
+    x = logits_of(300, E)
+    dw = torch.randn(300, 4, device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    r, want = run(x, 4, dw, score=score, normalize=normalize)
+    _, got = run(x, 4, dw, out=x, score=score, normalize=normalize)
+    assert got is x and torch.equal(got, want)
+
+
+def test_settings_go_by_their_values():
+    # (a scale in a tensor that is changed between two calls)
+    x, scale = logits_of(8, 16), torch.ones(())
+    one = run(x, 2, scale=scale)[0].weights
+    scale.fill_(3.0)
+    assert torch.equal(run(x, 2, scale=scale)[0].weights, run(x, 2, scale=3.0)[0].weights)
+    assert not torch.equal(run(x, 2, scale=scale)[0].weights, one)
+
+
 def test_infinite_biases():
     b = bias_of(64)
     b[7] = float("inf")

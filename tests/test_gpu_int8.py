@@ -177,6 +177,18 @@ def test_few_rows_of_the_largest_codes():
             close(got, want, -want, K)
 
 
+@pytest.mark.parametrize("K", [131056, 131072, 131088])
+@pytest.mark.parametrize("M", [1, 4, 5])
+def test_largest_sums(M, K):
+    # K products of -128 x -128, 2^31 of them at K = 2^17; every partial sum is a
+    # multiple of 2^14 below 2^38, so exact in fp32
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    a = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((5, K), -128, dtype=torch.int8, device="cuda")
+    got = int8_matmul(a, torch.ones(M, device="cuda"), w, torch.ones(5, device="cuda"))
+    assert torch.equal(got, torch.full((M, 5), 16384.0 * K, device="cuda").bfloat16())
+
+
 @pytest.mark.parametrize("M,N,K", [(4864, 1024, 400), (5000, 1025, 130), (9728, 500, 64),
                                    (2049, 9800, 1000), (20000, 256, 16)])
 def test_matmul_of_many_rows(M, N, K):

@@ -264,6 +264,19 @@ def test_in_place():
     assert j.x is x and torch.equal(x, want.x) and torch.equal(j.h, want.h)
 
 
+@pytest.mark.parametrize("T", [7, 2000])
+def test_without_d_h_the_new_x_is_not_read(T):
+    from moe_expert_layer_histogram_gb300 import block_join, block_join_backward
+    a, dx = make(T, 4104, 2), randn(T, 4104, seed=60)
+    j = block_join(**a)
+    want = block_join_backward(j, d_x=dx)
+    j.x, j._ld_x = torch.full((T, 4104), float("nan"), device="cuda"), 1
+    got = block_join_backward(j, d_x=dx)
+    for name in ("x", "expert_rows", "weights", "shared", "gate", "post_weight"):
+        one, two = getattr(want, name), getattr(got, name)
+        assert torch.equal(one, two) and bool(torch.isfinite(one).all()), name
+
+
 @pytest.mark.parametrize("offset,pad", [(0, 8), (1, 0), (8, 3), (16, 16)])
 def test_strided_arguments(offset, pad):
     T, H, K = 23, 160, 3
@@ -373,7 +386,7 @@ def test_refusals():
                 dict(norm_weight=None, quantize=True), dict(weights=a["weights"][:5]),
                 dict(x=a["x"][:, ::2]), dict(shared=a["shared"][:, :30]),
                 dict(expert_rows=a["expert_rows"].float()), dict(out=a["x"].bfloat16()),
-                dict(order=a["order"].rows.long())):
+                dict(order=a["order"].rows.long()), dict(weights=a["weights"][:, :0])):
         with pytest.raises((ValueError, TypeError)):
             block_join(**dict(a, **bad))
     for bad in (dict(eps=-1.0), dict(scale=float("inf"))):
