@@ -134,10 +134,11 @@ __device__ __forceinline__ void st_if_b16(bool on, void* p, uint32_t v) {
 // channel's values of both, an even lane takes the first token's pair of channels
 // from it and its neighbour, the odd one the second's.  No branches within 32
 // tokens: with them the steps of one pair waited for those of the one before, 9000
-// cycles for the 128 tokens.
+// cycles for the 128 tokens.  between: called after each 32 of them.
+template <typename F>
 __device__ __forceinline__ void store_tokens(const uint32_t (&v)[4][32], const float* scales,
                                              float s, uint16_t* out, int64_t ldo, int n, int N,
-                                             int rows, bool pairs, int lane) {
+                                             int rows, bool pairs, int lane, F&& between) {
   const bool odd = lane & 1;
   // (the last channel of an odd N has no partner; its pair's even lane stores it)
   const bool both = (n | 1) < N, one = (n & ~1) < N && !both;
@@ -177,6 +178,7 @@ __device__ __forceinline__ void store_tokens(const uint32_t (&v)[4][32], const f
       }
     }
     d += 32 * ldo;
+    between();
   }
 }
 
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const int n = it.tile * kI8Tile + half * 128 + row;
         const float s = n < p.N ? sw[n] : 0.0f;
         uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(it.row0) * p.ldo;
-        store_tokens(v, scales, s, out, p.ldo, n, p.N, it.rows, p.out_pairs, lane);
+        store_tokens(v, scales, s, out, p.ldo, n, p.N, it.rows, p.out_pairs, lane, [] {});
       }
       return true;
     };
@@ -573,15 +575,25 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 //
 // Rank 0 issues; each CTA's results are its own 128 channels (TMEM lanes) of all
 // tokens.  An item's tokens are cut in two halves of a multiple of 16, and an
-// expert's rows evenly into items, so that short and odd ones share the work.  The widening warps take every other
-// block of 128 columns: four on one, four on the next.  With SWIGLU the CTA's
-// channels are 64 gate and the 64 up channels that go with them, 16 of each to a
-// warp's 32 lanes, so that a gate and its up meet by a shuffle.
-constexpr int kP8MaxStages = 4;
+// expert's rows evenly into items, so that short and odd ones share the work.  The
+// widening warps take every other block of 128 columns: four on one, four on the
+// next.  With SWIGLU the CTA's channels are 64 gate and the 64 up channels that go
+// with them, 16 of each to a warp's 32 lanes, so that a gate and its up meet by a
+// shuffle.
+//
+// Weights and tokens have rings of their own: a stage of weights is free as soon as
+// it has been widened, long before its MMAs, and their loads have that much longer
+// (in one ring of four stages the widening waited 900 cycles a block for its
+// weights).  The stores, 4000 cycles an item, go on in four parts between the next
+// blocks' widening.  (64 experts, 24576 rows, 2048 x 1024, with the quantisation:
+// 309 us with neither, 294 with both; 8192 x 7168 -> 4096: 278 and 274.)
+constexpr int kP8WStages = 5, kP8XStages = 4;
 constexpr int kP8WBytes = 128 * 128;
 constexpr int kP8Buffers = 4;      // TMEM buffers of widened weights, 64 columns each
 constexpr uint32_t kP8Weights = 256;
 constexpr int kP8Tokens = 256;     // most tokens of an item
+constexpr int kP8XBytes = kP8Tokens / 2 * 256;
+constexpr int kP8Ahead = 3;        // blocks of the next item that come before an item's results
 
 __device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
                                                 uint32_t idesc, uint32_t accum) {
@@ -598,13 +610,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     int8_pair_kernel(const __grid_constant__ Int8Maps maps, const __grid_constant__ Int8Args p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int stage_bytes = kP8WBytes + p.a_rows / 2 * 256, stages = p.stages;
+  uint8_t* s_x = smem + kP8WStages * kP8WBytes;
   // per widening warp: the scales of its 128 tokens
-  float* s_scale = reinterpret_cast<float*>(smem + stages * stage_bytes);
+  float* s_scale = reinterpret_cast<float*>(s_x + kP8XStages * kP8XBytes);
   uint64_t* wfull = reinterpret_cast<uint64_t*>(s_scale + kI8WideWarps * 128);
-  uint64_t* xfull = wfull + kP8MaxStages;  // (rank 0's: both CTAs' tokens)
-  uint64_t* empty = xfull + kP8MaxStages;
-  uint64_t* afull = empty + kP8MaxStages;  // (rank 0's: both CTAs' weights)
+  uint64_t* wempty = wfull + kP8WStages;
+  uint64_t* xfull = wempty + kP8WStages;  // (rank 0's: both CTAs' tokens)
+  uint64_t* xempty = xfull + kP8XStages;
+  uint64_t* afull = xempty + kP8XStages;  // (rank 0's: both CTAs' weights)
   uint64_t* aempty = afull + kP8Buffers;
   uint64_t* dfull = aempty + kP8Buffers;
   uint64_t* dempty = dfull + 1;            // (rank 0's)
@@ -616,10 +629,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int rank = static_cast<int>(cluster_ctarank());
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; s < kP8WStages; ++s) {
       mbar_init(&wfull[s], 1);
+      mbar_init(&wempty[s], 4);  // the warps that widen it
+    }
+    for (int s = 0; s < kP8XStages; ++s) {
       mbar_init(&xfull[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&xempty[s], 1);
     }
     for (int b = 0; b < kP8Buffers; ++b) {
       mbar_init(&afull[b], 8);  // four warps of each CTA
@@ -665,62 +681,77 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   // rows of either CTA's part of an item (the MMA's N, both parts, is a multiple of
   // 32), and their box
   auto part_of = [](const I8Item& it) { return max((it.rows + 31) / 32 * 16, 16); };
-  auto box_of = [](int part) { return part <= 16 ? 0 : part <= 32 ? 1 : part <= 64 ? 2 : 3; };
+  auto box_of = [](int part) {
+    // (one box that holds them all: parts of 96 rows in boxes of 64 and 32 took 315 us
+    // where a box of 128 takes 294, with a quarter more bytes)
+    return part <= 16 ? 0 : part <= 32 ? 1 : part <= 64 ? 2 : 3;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
-      // -------------------------------------------------- TMA producer
+      // -------------------------------------------------- weights by TMA
+      // (they are not the kernel's before this one: no wait for it)
+      const uint64_t reused = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int item = first; ok && item < total; item += step) {
+        const I8Item it = map_item(item);
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = mbar_wait(&wempty[stage], phase ^ 1, abort_flag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&wfull[stage], kP8WBytes);
+          uint8_t* sw = smem + stage * kP8WBytes;
+          if constexpr (SWIGLU) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d_hint(sw + h * (kP8WBytes / 2), &maps.w, &wfull[stage], kb * 128,
+                               it.tile * 128 + rank * 64 + h * (p.N / 2), it.e, reused);
+          } else {
+            tma_load_3d_hint(sw, &maps.w, &wfull[stage], kb * 128, it.tile * kI8Tile + rank * 128,
+                             it.e, reused);
+          }
+          if (++stage == kP8WStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) report_status(&g_int8_status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    if (lane == 0) {
+      // -------------------------------------------------- tokens by TMA
       const uint64_t reused = l2_policy_evict_normal();
       const uint32_t xfull0 = mapa_shared(smem_u32(xfull), 0);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      auto load_w = [&](const I8Item& it, int st, int kb) {
-        mbar_arrive_expect_tx(&wfull[st], kP8WBytes);
-        if constexpr (SWIGLU) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d_hint(smem + st * stage_bytes + h * (kP8WBytes / 2), &maps.w, &wfull[st],
-                             kb * 128, it.tile * 128 + rank * 64 + h * (p.N / 2), it.e, reused);
-        } else {
-          tma_load_3d_hint(smem + st * stage_bytes, &maps.w, &wfull[st], kb * 128,
-                           it.tile * kI8Tile + rank * 128, it.e, reused);
-        }
-      };
-      int ahead = 0;  // stages of the first item whose weights are on their way
-      if (first < total) {
-        const I8Item it = map_item(first);
-        for (; ahead < min(stages, blocks); ++ahead) load_w(it, ahead, ahead);
-      }
       pdl_wait();
       fence_proxy_async_global();
       for (int item = first; ok && item < total; item += step) {
         const I8Item it = map_item(item);
         const int part = part_of(it), box = box_of(part);
         for (int kb = 0; kb < blocks; ++kb) {
-          if (ahead > 0) {
-            --ahead;
-          } else {
-            ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
-            if (!ok) break;
-            load_w(it, stage, kb);
-          }
+          ok = mbar_wait(&xempty[stage], phase ^ 1, abort_flag);
+          if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&xfull[stage], 2u * (16u << box) * 256u);
-          uint8_t* sx = smem + stage * stage_bytes + kP8WBytes;
+          uint8_t* sx = s_x + stage * kP8XBytes;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             tma_load_2d_pair(sx + h * (16 << box) * 128, &maps.x[box], xfull0 + stage * 8,
                              kb * 128 + h * 64, it.row0 + rank * part, reused);
-          if (++stage == stages) {
+          if (++stage == kP8XStages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
       // every stage's last release has arrived here before this CTA may leave
-      for (int s = 0; ok && s < stages; ++s) {
-        ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
-        if (++stage == stages) {
+      for (int s = 0; ok && s < kP8XStages; ++s) {
+        ok = mbar_wait(&xempty[stage], phase ^ 1, abort_flag);
+        if (++stage == kP8XStages) {
           stage = 0;
           phase ^= 1;
         }
@@ -745,18 +776,18 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t sx = smem_u32(smem + stage * stage_bytes + kP8WBytes);
+          const uint32_t sx = smem_u32(s_x + stage * kP8XBytes);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_f16_ts_pair(tmem, tmem + kP8Weights + buf * 64 + k * 8,
                             desc_sw128(sx + (k >> 2) * n * 128 + (k & 3) * 32), idesc,
                             kb > 0 || k > 0);
-          tc_commit_pair(&empty[stage], 3);
+          tc_commit_pair(&xempty[stage], 3);
           tc_commit_pair(&aempty[buf], 3);
           if (kb + 1 == blocks) tc_commit_pair(dfull, 3);
         }
         __syncwarp();
-        if (++stage == stages) {
+        if (++stage == kP8XStages) {
           stage = 0;
           phase ^= 1;
         }
@@ -776,19 +807,21 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     float* scales = s_scale + (warp - kI8WideWarp0) * 128;
     const uint32_t afull0 = mapa_shared(smem_u32(afull), 0);
     const uint32_t dempty0 = mapa_shared(smem_u32(dempty), 0);
-    int count = 0;  // blocks so far, of both groups
+    int next = group, limit = 0;  // this group's next block; all items' so far
     uint32_t dphase = 0;
     bool ok = true, waited = false;
 
     // Every other block: this group's turn.
     auto widen = [&](int block) {
-      const int stage = block % stages, buf = block % kP8Buffers;
-      if (!wait_warp(&wfull[stage], (block / stages) & 1, abort_flag)) return false;
-      const uint8_t* src = smem + stage * stage_bytes + row * 128;
+      const int stage = block % kP8WStages, buf = block % kP8Buffers;
+      if (!wait_warp(&wfull[stage], (block / kP8WStages) & 1, abort_flag)) return false;
+      const uint8_t* src = smem + stage * kP8WBytes + row * 128;
       uint4 v[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         v[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+      __syncwarp();
+      mbar_arrive_if(lane == 0, smem_u32(&wempty[stage]));
       if (!wait_warp(&aempty[buf], ((block / kP8Buffers) & 1) ^ 1, abort_flag)) return false;
       tc_fence_after();
 #pragma unroll
@@ -809,6 +842,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       return true;
     };
 
+    auto widen_next = [&]() {
+      if (!ok || next >= limit) return;
+      ok = widen(next);
+      next += 2;
+    };
+
+    // (the stores are as much work as a few blocks' widening and go on between those)
     auto results = [&](const I8Item& it) {
       if (!waited) {
         // (the scales are the kernel's before this one)
@@ -863,29 +903,30 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
           for (int c = 0; c < 32; c += 2) st_if_b32(c < rest && n < I, out + c * p.ldo, v[i][c]);
           out += 32 * p.ldo;
+          widen_next();
         }
       } else {
         const int n = it.tile * kI8Tile + rank * 128 + quarter * 32 + lane;
         const float s = n < p.N ? sw[n] : 0.0f;
         uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(it.row0 + c0) * p.ldo;
-        store_tokens(v, scales, s, out, p.ldo, n, p.N, left, p.out_pairs, lane);
+        store_tokens(v, scales, s, out, p.ldo, n, p.N, left, p.out_pairs, lane, widen_next);
       }
-      return true;
+      return ok;
     };
 
     I8Item before{};
     bool pending = false;
     for (int item = first; ok; item += step) {
       const bool more = item < total;
-      const int n = more ? blocks : 0, ahead = min(kP8Buffers - 1, n);
-      for (int kb = 0;; ++kb) {
-        if (pending && kb == ahead) {
+      const int ahead = limit + kP8Ahead;
+      limit += more ? blocks : 0;
+      for (;;) {
+        if (pending && next >= min(ahead, limit)) {
           ok = results(before);
           pending = false;
         }
-        if (!ok || kb == n) break;
-        if ((count & 1) == group) ok = widen(count);
-        ++count;
+        if (!ok || next >= limit) break;
+        widen_next();
       }
       if (!more) break;
       before = map_item(item);
@@ -893,9 +934,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     // the last releases of the buffers, before this CTA may leave
     for (int b = 0; ok && b < kP8Buffers; ++b)
-      if (count - 1 - b >= 0)
-        ok = wait_warp(&aempty[(count - 1 - b) % kP8Buffers],
-                       ((count - 1 - b) / kP8Buffers) & 1, abort_flag);
+      if (limit - 1 - b >= 0)
+        ok = wait_warp(&aempty[(limit - 1 - b) % kP8Buffers],
+                       ((limit - 1 - b) / kP8Buffers) & 1, abort_flag);
     if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
   }
 
@@ -950,15 +991,15 @@ cudaError_t launch_i8_pair(const Int8Maps& maps, Int8Args p, int pairs, cudaStre
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8SmemLimit);
   });
   if (ready != cudaSuccess) return ready;
-  const int stage = kP8WBytes + p.a_rows / 2 * 256;
-  const int fixed = 1024 + kI8WideWarps * 128 * 4 +
-                    (3 * kP8MaxStages + 2 * kP8Buffers + 2) * 8 + 8 + (3 * p.E + 1) * 4;
-  p.stages = std::min(kP8MaxStages, (kI8SmemLimit - fixed) / stage);
+  constexpr int fixed = 1024 + kP8WStages * kP8WBytes + kP8XStages * kP8XBytes +
+                        kI8WideWarps * 128 * 4 +
+                        (2 * kP8WStages + 2 * kP8XStages + 2 * kP8Buffers + 2) * 8 + 8;
+  static_assert(fixed + (3 * kMaxExperts + 1) * 4 <= kI8SmemLimit);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kI8Threads);
-  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.dynamicSmemBytes = fixed + (3 * p.E + 1) * 4;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
