@@ -633,9 +633,10 @@ moe_status moe_blockscale_linear(const void *x, int64_t ldx, const void *w,
  * through w2 [E, H, I]; both contiguous.  slots int32 [rows] and offsets
  * int32 [E+1] as moe_route_permute_static writes perm and offsets (that call
  * takes up to 4096 tokens of f32 logits and no mask; moe_order gives the same
- * of any ids).  H a multiple of 16 and I of 128 (else MOE_ERR_UNSUPPORTED).  workspace: device, 16-byte aligned,
- * moe_blockscale_experts_workspace(rows, H, I) bytes.  rows == 0 is a no-op.
- * The rest as moe_blockscale_swiglu and moe_blockscale_matmul.            */
+ * of any ids).  H a multiple of 16 and I of 128 (else MOE_ERR_UNSUPPORTED).
+ * workspace: device, 16-byte aligned, moe_blockscale_experts_workspace(rows, H, I)
+ * bytes.  rows == 0 is a no-op.  The rest as moe_blockscale_swiglu and
+ * moe_blockscale_matmul.                                                   */
 moe_status moe_blockscale_experts(const void *x, int64_t ldx, int T,
                                   const int32_t *slots, int top_k, int rows,
                                   const int32_t *offsets, int E,

@@ -236,6 +236,9 @@ struct Coded {
         scales(reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + code_bytes(rows, cols))) {}
 };
 
+// SwiGLU's limit: +inf for none.
+float limit_of(float clamp) { return clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY; }
+
 // The product of f16 codes x [M, K] with their scales.
 moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const float* scales,
                        bool swiglu, void* out, int64_t ldo, float clamp, cudaStream_t s) {
@@ -275,7 +278,7 @@ moe_status run_product(const Product& p, const uint16_t* x, int64_t ld, const fl
   a.ldo = ldo;
   a.out_pairs = aligned_to(out, 4) && ldo % 2 == 0;
   a.out_fours = aligned_to(out, 8) && ldo % 4 == 0;
-  a.clamp = clamp > 0.0f && std::isfinite(clamp) ? clamp : INFINITY;
+  a.clamp = limit_of(clamp);
   return take_error(launch_int8(maps, a, swiglu, *d, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -310,6 +313,22 @@ moe_status run_rows(const Product& p, const void* x, int64_t ldx, const int8_t* 
   r.M = p.M, r.N = p.N, r.K = p.K;
   r.out = static_cast<__nv_bfloat16*>(out), r.ldo = ldo;
   return take_error(launch_int8_rows(r, early, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// The products of a few rows of several experts: codes a with their scales; swiglu:
+// out is h in f32.
+moe_status run_group_rows(const Product& p, const int8_t* a, int64_t lda, const float* scales,
+                          bool swiglu, bool early, void* out, int64_t ldo, float clamp,
+                          cudaStream_t s) {
+  Int8RowsArgs r{};
+  r.w = static_cast<const int8_t*>(p.w), r.ldw = p.ldw, r.w_scales = p.w_scales;
+  r.a = a, r.lda = lda, r.a_vec = aligned_to(a, 16) && lda % 16 == 0, r.a_scales = scales;
+  r.M = p.M, r.N = p.N, r.K = p.K;
+  r.out = static_cast<__nv_bfloat16*>(out), r.h = static_cast<float*>(out), r.ldo = ldo;
+  r.offsets = p.offsets, r.E = p.E;
+  r.clamp = limit_of(clamp);
+  return take_error(launch_int8_group_rows(r, swiglu, early, s)) == cudaSuccess ? MOE_OK
+                                                                               : MOE_ERR_CUDA;
 }
 
 // Blocks of an elementwise kernel of 256 threads over n vectors.
@@ -362,6 +381,8 @@ moe_status moe_int8_matmul(const void* a, int64_t lda, const float* a_scales, co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!need)
     return run_rows(p, nullptr, 0, static_cast<const int8_t*>(a), lda, a_scales, false, out, ldo, s);
+  if (int8_by_group_rows(M, N, K, E))
+    return run_group_rows(p, static_cast<const int8_t*>(a), lda, a_scales, false, false, out, ldo, 0.0f, s);
   const Coded c(workspace, M, K);
   const int64_t vectors = static_cast<int64_t>(M) * ((K + 7) / 8);
   const cudaError_t e = launch_pdl(false, int8_widen_kernel, dim3(vector_blocks(vectors)),
@@ -442,6 +463,19 @@ moe_status moe_int8_experts(const void* x, int64_t ldx, int T, const int32_t* sl
   at += padded(static_cast<int64_t>(rows) * I * 4, 256);
   const Coded hc(at, rows, I);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (int8_by_group_rows(rows, std::max(2 * I, H), std::max(H, I), E)) {
+    // (codes of 8 bits where those of 16 would be)
+    int8_t *codes = reinterpret_cast<int8_t*>(c.codes), *h_codes = reinterpret_cast<int8_t*>(hc.codes);
+    st = run_quantize<false>(static_cast<const __nv_bfloat16*>(x), ldx, T, slots, top_k, rows, H,
+                             codes, H, c.scales, s);
+    if (st == MOE_OK)
+      st = run_group_rows(p1, codes, H, c.scales, true, true, h, I, clamp_limit, s);
+    if (st == MOE_OK)
+      st = run_quantize<false>(h, I, rows, nullptr, 1, rows, I, h_codes, I, hc.scales, s);
+    if (st == MOE_OK)
+      st = run_group_rows(p2, h_codes, I, hc.scales, false, true, out, ldo, 0.0f, s);
+    return st;
+  }
   st = run_quantize<true>(static_cast<const __nv_bfloat16*>(x), ldx, T, slots, top_k, rows, H,
                           c.codes, c.ld, c.scales, s);
   if (st == MOE_OK) st = run_product(p1, c.codes, c.ld, c.scales, true, h, I, clamp_limit, s);

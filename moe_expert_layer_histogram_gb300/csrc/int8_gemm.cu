@@ -76,23 +76,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-__device__ __forceinline__ float clamp_to(float v, float limit) {
-  // (a NaN stays one; fminf and fmaxf would drop it)
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-limit));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(limit));
-  return v;
-}
-
-__device__ __forceinline__ float swiglu(float g, float u, float clamp) {
-  g = clamp_to(g, clamp);
-  u = clamp_to(u, clamp);
-  // e^-g by the hardware's power of two, off by two ulp and |g| 2^-24 of itself,
-  // and an approximate quotient of two ulp
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  return __fdividef(g, 1.0f + e) * u;
-}
-
 struct I8Item {
   int e, tile, row0, rows;
 };

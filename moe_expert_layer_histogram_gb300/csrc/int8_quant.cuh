@@ -76,4 +76,22 @@ struct I8Coder {
   }
 };
 
+// silu(g) u, both clamped.
+__device__ __forceinline__ float clamp_to(float v, float limit) {
+  // (a NaN stays one; fminf and fmaxf would drop it)
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-limit));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(limit));
+  return v;
+}
+
+__device__ __forceinline__ float swiglu(float g, float u, float clamp) {
+  g = clamp_to(g, clamp);
+  u = clamp_to(u, clamp);
+  // e^-g by the hardware's power of two, off by two ulp and |g| 2^-24 of itself,
+  // and an approximate quotient of two ulp
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  return __fdividef(g, 1.0f + e) * u;
+}
+
 }  // namespace moe

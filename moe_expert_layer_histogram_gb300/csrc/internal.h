@@ -291,9 +291,9 @@ cudaError_t launch_int8(const Int8Maps& maps, Int8Args args, bool swiglu,
                         const BlockscaleDevice& d, cudaStream_t s);
 // Products of a few rows without the tensor cores (int8_rows.cu).
 struct Int8RowsArgs {
-  const int8_t* w;         // [N, K]
+  const int8_t* w;         // [N, K], or [E, N, K] with offsets
   int64_t ldw;
-  const float* w_scales;   // [N]
+  const float* w_scales;   // [N], [E, N]
   const __nv_bfloat16* x;  // rows that the kernel quantises itself, or null:
   int64_t ldx;
   int x_vec;               // (rows on 16 bytes)
@@ -304,13 +304,20 @@ struct Int8RowsArgs {
   int M, N, K;
   __nv_bfloat16* out;
   int64_t ldo;
-  int slices;              // set by launch_int8_rows
+  int slices;              // set by the launch
+  // of several experts
+  const int32_t* offsets;  // [E + 1]
+  int E;
+  float clamp;             // SwiGLU (+inf: none)
+  float* h;                // its result [M, ldo], in place of out
 };
 bool int8_by_rows(int M, int K, int E);
+bool int8_by_group_rows(int M, int N, int K, int E);
 bool int8_rows_quantize(int M, int K, int E);  // ... and quantises its rows
 // early: the kernel before it is the library's own, writes codes and scales, and lets
 // it start early.
 cudaError_t launch_int8_rows(Int8RowsArgs p, bool early, cudaStream_t s);
+cudaError_t launch_int8_group_rows(Int8RowsArgs p, bool swiglu, bool early, cudaStream_t s);
 
 // Whether a product runs on CTA pairs (its weights' boxes are 64 rows high with
 // swiglu), and the most rows of a chunk of its items.

@@ -262,6 +262,42 @@ def test_experts_rows(offsets, M, N, K):
     assert bool((out[~mine] == 7).all())
 
 
+FEW = [
+    (list(range(17)), 16),                            # a row each
+    ([0] * 3 + list(range(0, 25)) + [24] * 2, 24), ([0] * 12 + [24] * 13, 24),
+    ([0] * 6 + [16] * 11, 16),                        # all rows of one expert
+    ([0, 0, 1, 3, 3, 6, 6, 10] + [15] * 10, 16),      # 1, 2, 3, 4 and 5 rows, one of none
+    ([4, 4, 5] + [8] * 14, 12),                       # rows of no expert on either side
+    ([0] * 17, 1), ([0] * 16 + [1], 1), ([0] * 511 + [1, 2], 2),
+    ([5, 3, 9, 2, -1, 2 ** 31 - 1, 7, 11, 20, -2 ** 31, 14, 14, 15, 16, 90, 12, 16], 16),
+]
+
+
+@pytest.mark.parametrize("offsets,M", FEW)
+@pytest.mark.parametrize("N,K", [(1, 16), (33, 130), (256, 512), (301, 2500), (90, 7168)])
+def test_few_rows_of_experts(offsets, M, N, K):
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    E, ld = len(offsets) - 1, (K + 15) // 16 * 16
+    w = codes_of(E, N, ld, seed=8, low=-128)[:, :, :K]
+    s, ws = scales_of(M), scales_of(E, N, seed=1)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    for lead, ldo in ((0, N), (3, N + 5)):
+        a = codes_of(M, K + 7, seed=7, low=-128)[:, lead:lead + K]
+        out = torch.full((M, ldo), 7.0, dtype=torch.bfloat16, device="cuda")
+        int8_matmul(a, s, w, ws, offsets=off, out=out[:, :N])
+        want, mag = matmul_reference(a, s, w, ws, offsets)
+        mine = ~torch.isnan(want[:, 0])
+        close(out[mine][:, :N], want[mine], mag[mine], K)
+        assert bool((out[~mine] == 7).all()) and bool((out[:, N:] == 7).all())
+
+
+@pytest.mark.parametrize("T,E,k,H,I,clamp,masked", [
+    (1, 64, 8, 7168, 2048, 7.0, 0.0), (1, 2, 1, 16, 16, 0.0, 0.0), (2, 16, 8, 272, 144, 0.5, 0.0),
+    (5, 64, 3, 528, 16, 0.0, 0.4), (4, 16, 4, 2048, 1040, 7.0, 0.0), (16, 512, 1, 144, 272, 0.0, 0.0)])
+def test_experts_of_few_rows(T, E, k, H, I, clamp, masked):
+    test_experts(T, E, k, H, I, clamp, masked)
+
+
 def route(T, E, k, seed=0, masked=0.0):
     from moe_expert_layer_histogram_gb300 import router_gate, router_order
     mask = None

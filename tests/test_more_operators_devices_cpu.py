@@ -91,7 +91,7 @@ CALLS = {
        ((1, 1, 100, 64), (1, 4, 100, 131072), (8, 8, 256, 2048), (8, 700, 4096, 512),
         (8, 9000, 4096, 512))},
     **{"experts %s" % (a,): (lambda L, a=a: experts(L, *a)) for a in
-       ((8, 8, 4), (500, 500, 4), (40000, 80000, 4))},
+       ((8, 8, 4), (8, 8, 16), (500, 500, 4), (40000, 80000, 4))},
     "quantize": lambda L: L.moe_int8_quantize(P, 256, 8, None, 1, 8, 256, P, 256, P, None),
 }
 
