@@ -15,11 +15,13 @@
 //
 // So D[channel][token]: a tile is 256 channels (two halves of 128 TMEM lanes) by
 // up to 128 tokens.  Structure: one persistent CTA per SM walks the items (expert,
-// tile, chunk of at most 128 rows).  Warp 0 (one thread) fills a ring of stages by
-// TMA: 128 columns of the reduction, as 8-bit weights (32 KB) and f16 codes of the
-// chunk's rows (box height 16 / 32 / 64 / 128).  Warps 4-11 widen: warp w takes
-// the TMEM lanes 32 (w % 4).. of half (w - 4) / 4 and writes its rows' f16 into
-// one of two TMEM buffers.  Warp 1 issues the MMAs.  The widening warps also read
+// tile, chunk of at most 128 rows).  Warps 0 and 3 (a thread each) fill two rings of
+// stages by TMA, of 128 columns of the reduction: 8-bit weights (32 KB), and f16
+// codes of the chunk's rows (box height 16 / 32 / 64 / 128).  Warps 4-11 widen: warp
+// w takes the TMEM lanes 32 (w % 4).. of half (w - 4) / 4 and writes its rows' f16
+// into one of two TMEM buffers; a stage of weights is free then, before its MMAs (in
+// one ring with the tokens: 64 experts of 2048 x 1024, 6144 rows, 144 us for 130, 16
+// rows of 7168 -> 4096 11.9 for 11.0).  Warp 1 issues the MMAs.  The widening warps also read
 // the results out: after the first two blocks of the next item have been widened,
 // so the tensor cores go on as soon as the results are in registers, and the
 // scaling and the stores run beside them.
@@ -49,7 +51,7 @@ constexpr int kI8Threads = 384;
 constexpr int kI8WideWarp0 = 4;     // warps 4-11 widen the weights and read the results
 constexpr int kI8WideWarps = 8;
 constexpr int kI8Tile = 256;        // channels of an item
-constexpr int kI8MaxStages = 6;
+constexpr int kI8MaxStages = 6;   // of weights, and of tokens
 constexpr int kI8WBytes = kI8Tile * 128;
 constexpr int kI8SmemLimit = 232448;
 constexpr int kI8Buffers = 2;       // TMEM buffers of widened weights, 128 columns each
@@ -117,11 +119,10 @@ __device__ __forceinline__ void st_if_b16(bool on, void* p, uint32_t v) {
 // channel's values of both, an even lane takes the first token's pair of channels
 // from it and its neighbour, the odd one the second's.  No branches within 32
 // tokens: with them the steps of one pair waited for those of the one before, 9000
-// cycles for the 128 tokens.  between: called after each 32 of them.
-template <typename F>
+// cycles for the 128 tokens.
 __device__ __forceinline__ void store_tokens(const uint32_t (&v)[4][32], const float* scales,
                                              float s, uint16_t* out, int64_t ldo, int n, int N,
-                                             int rows, bool pairs, int lane, F&& between) {
+                                             int rows, bool pairs, int lane) {
   const bool odd = lane & 1;
   // (the last channel of an odd N has no partner; its pair's even lane stores it)
   const bool both = (n | 1) < N, one = (n & ~1) < N && !both;
@@ -161,7 +162,6 @@ __device__ __forceinline__ void store_tokens(const uint32_t (&v)[4][32], const f
       }
     }
     d += 32 * ldo;
-    between();
   }
 }
 
@@ -170,12 +170,15 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     int8_gemm_kernel(const __grid_constant__ Int8Maps maps, const __grid_constant__ Int8Args p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int x_bytes = p.a_rows * 256, stage_bytes = kI8WBytes + x_bytes, stages = p.stages;
+  const int x_bytes = p.a_rows * 256, w_stages = p.w_stages, x_stages = p.x_stages;
+  uint8_t* s_x = smem + w_stages * kI8WBytes;
   // per widening warp: the scales of a chunk's rows
-  float* s_scale = reinterpret_cast<float*>(smem + stages * stage_bytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + kI8WideWarps * 128);
-  uint64_t* empty = full + kI8MaxStages;
-  uint64_t* afull = empty + kI8MaxStages;
+  float* s_scale = reinterpret_cast<float*>(s_x + x_stages * x_bytes);
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(s_scale + kI8WideWarps * 128);
+  uint64_t* wempty = wfull + kI8MaxStages;
+  uint64_t* xfull = wempty + kI8MaxStages;
+  uint64_t* xempty = xfull + kI8MaxStages;
+  uint64_t* afull = xempty + kI8MaxStages;
   uint64_t* aempty = afull + kI8Buffers;
   uint64_t* dfull = aempty + kI8Buffers;
   uint64_t* dempty = dfull + 1;
@@ -186,9 +189,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < w_stages; ++s) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&wempty[s], kI8WideWarps);
+    }
+    for (int s = 0; s < x_stages; ++s) {
+      mbar_init(&xfull[s], 1);
+      mbar_init(&xempty[s], 1);
     }
     for (int b = 0; b < kI8Buffers; ++b) {
       mbar_init(&afull[b], kI8WideWarps);
@@ -231,46 +238,57 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      // -------------------------------------------------- TMA producer
+      // -------------------------------------------------- weights by TMA
+      // (they are not the kernel's before this one: no wait for it)
       const uint64_t once = l2_policy_evict_first(), reused = l2_policy_evict_normal();
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      auto load_w = [&](const I8Item& it, int st, int kb) {
+      for (int item = first; ok && item < total; item += step) {
+        const I8Item it = map_item(item);
         // weights of an expert with one chunk are read once
         const uint64_t policy = tab.chunk_off[it.e + 1] - tab.chunk_off[it.e] > 1 ? reused : once;
-        mbar_arrive_expect_tx(&full[st], kI8WBytes + (16u << box_of(it.rows)) * 256u);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = mbar_wait(&wempty[stage], phase ^ 1, abort_flag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&wfull[stage], kI8WBytes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n0 = SWIGLU ? it.tile * 128 + h * (p.N / 2) : it.tile * kI8Tile + h * 128;
-          tma_load_3d_hint(smem + st * stage_bytes + h * (kI8WBytes / 2), &maps.w, &full[st],
-                           kb * 128, n0, it.e, policy);
+          for (int h = 0; h < 2; ++h) {
+            const int n0 = SWIGLU ? it.tile * 128 + h * (p.N / 2) : it.tile * kI8Tile + h * 128;
+            tma_load_3d_hint(smem + stage * kI8WBytes + h * (kI8WBytes / 2), &maps.w, &wfull[stage],
+                             kb * 128, n0, it.e, policy);
+          }
+          if (++stage == w_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
-      };
-      int ahead = 0;  // stages of the first item whose weights are on their way
-      if (first < total) {
-        const I8Item it = map_item(first);
-        for (; ahead < min(stages, kb1 - kb0); ++ahead) load_w(it, ahead, kb0 + ahead);
       }
+      if (!ok) report_status(&g_int8_status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    if (lane == 0) {
+      // -------------------------------------------------- tokens by TMA
+      const uint64_t reused = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
       pdl_wait();
       fence_proxy_async_global();
       for (int item = first; ok && item < total; item += step) {
         const I8Item it = map_item(item);
         const int box = box_of(it.rows);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (ahead > 0) {
-            --ahead;
-          } else {
-            ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
-            if (!ok) break;
-            load_w(it, stage, kb);
-          }
-          uint8_t* sx = smem + stage * stage_bytes + kI8WBytes;
+          ok = mbar_wait(&xempty[stage], phase ^ 1, abort_flag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&xfull[stage], (16u << box) * 256u);
+          uint8_t* sx = s_x + stage * x_bytes;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            tma_load_2d_hint(sx + h * (16 << box) * 128, &maps.x[box], &full[stage],
+            tma_load_2d_hint(sx + h * (16 << box) * 128, &maps.x[box], &xfull[stage],
                              kb * 128 + h * 64, it.row0, reused);
-          if (++stage == stages) {
+          if (++stage == x_stages) {
             stage = 0;
             phase ^= 1;
           }
@@ -291,12 +309,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       ok = wait_warp(dempty, dphase ^ 1, abort_flag);
       dphase ^= 1;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
-        ok = wait_warp(&full[stage], phase, abort_flag) &&
+        ok = wait_warp(&xfull[stage], phase, abort_flag) &&
              wait_warp(&afull[buf], aphase, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t sx = smem_u32(smem + stage * stage_bytes + kI8WBytes);
+          const uint32_t sx = smem_u32(s_x + stage * x_bytes);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             // 16 of the 128 columns: 32 bytes further in a row of 64 f16
@@ -306,12 +324,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
               mma_f16_ts(tmem + kI8Results + h * 128, tmem + kI8Weights + buf * 128 + h * 64 + k * 8,
                          b, idesc, kb > kb0 || k > 0);
           }
-          tc_commit(&empty[stage]);
+          tc_commit(&xempty[stage]);
           tc_commit(&aempty[buf]);
           if (kb + 1 == kb1) tc_commit(dfull);
         }
         __syncwarp();
-        if (++stage == stages) {
+        if (++stage == x_stages) {
           stage = 0;
           phase ^= 1;
         }
@@ -333,12 +351,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     bool ok = true, waited = false;
 
     auto widen = [&]() {
-      if (!wait_warp(&full[stage], phase, abort_flag)) return false;
-      const uint8_t* src = smem + stage * stage_bytes + half * (kI8WBytes / 2) + row * 128;
+      if (!wait_warp(&wfull[stage], phase, abort_flag)) return false;
+      const uint8_t* src = smem + stage * kI8WBytes + half * (kI8WBytes / 2) + row * 128;
       uint4 v[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         v[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+      __syncwarp();
+      mbar_arrive_if(lane == 0, smem_u32(&wempty[stage]));
       if (!wait_warp(&aempty[buf], aphase ^ 1, abort_flag)) return false;
       tc_fence_after();
 #pragma unroll
@@ -356,7 +376,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive_if(lane == 0, smem_u32(&afull[buf]));
-      if (++stage == stages) {
+      if (++stage == w_stages) {
         stage = 0;
         phase ^= 1;
       }
@@ -388,7 +408,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       for (int i = 0; i < 4; ++i) scales[32 * i + lane] = sr[i];
       __syncwarp();
       if constexpr (SPLIT) {
-        // fp32 sums to [token][channel] in what was the ring of stages
+        // fp32 sums to [token][channel] in what were the rings of stages
         float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -454,7 +474,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const int n = it.tile * kI8Tile + half * 128 + row;
         const float s = n < p.N ? sw[n] : 0.0f;
         uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(it.row0) * p.ldo;
-        store_tokens(v, scales, s, out, p.ldo, n, p.N, it.rows, p.out_pairs, lane, [] {});
+        store_tokens(v, scales, s, out, p.ldo, n, p.N, it.rows, p.out_pairs, lane);
       }
       return true;
     };
@@ -567,9 +587,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 // Weights and tokens have rings of their own: a stage of weights is free as soon as
 // it has been widened, long before its MMAs, and their loads have that much longer
 // (in one ring of four stages the widening waited 900 cycles a block for its
-// weights).  The stores, 4000 cycles an item, go on in four parts between the next
-// blocks' widening.  (64 experts, 24576 rows, 2048 x 1024, with the quantisation:
-// 309 us with neither, 294 with both; 8192 x 7168 -> 4096: 278 and 274.)
+// weights; 64 experts, 24576 rows, 2048 x 1024, with the quantisation: 309 us for
+// 282).  The stores take 4000 cycles an item, most of them beside the MMAs of the
+// next item's first blocks, which have been widened by then (in four parts with the
+// widening of further blocks between them: 293 us).
 constexpr int kP8WStages = 5, kP8XStages = 4;
 constexpr int kP8WBytes = 128 * 128;
 constexpr int kP8Buffers = 4;      // TMEM buffers of widened weights, 64 columns each
@@ -825,13 +846,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       return true;
     };
 
-    auto widen_next = [&]() {
-      if (!ok || next >= limit) return;
-      ok = widen(next);
-      next += 2;
-    };
-
-    // (the stores are as much work as a few blocks' widening and go on between those)
     auto results = [&](const I8Item& it) {
       if (!waited) {
         // (the scales are the kernel's before this one)
@@ -886,15 +900,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
           for (int c = 0; c < 32; c += 2) st_if_b32(c < rest && n < I, out + c * p.ldo, v[i][c]);
           out += 32 * p.ldo;
-          widen_next();
         }
       } else {
         const int n = it.tile * kI8Tile + rank * 128 + quarter * 32 + lane;
         const float s = n < p.N ? sw[n] : 0.0f;
         uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(it.row0 + c0) * p.ldo;
-        store_tokens(v, scales, s, out, p.ldo, n, p.N, left, p.out_pairs, lane, widen_next);
+        store_tokens(v, scales, s, out, p.ldo, n, p.N, left, p.out_pairs, lane);
       }
-      return ok;
+      return true;
     };
 
     I8Item before{};
@@ -909,7 +922,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           pending = false;
         }
         if (!ok || next >= limit) break;
-        widen_next();
+        ok = widen(next);
+        next += 2;
       }
       if (!more) break;
       before = map_item(item);
@@ -932,7 +946,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
 // ---------------------------------------------------------------- host
 int extra_smem(int E) {
-  return kI8WideWarps * 128 * 4 + (2 * kI8MaxStages + 2 * kI8Buffers + 2) * 8 + 8 +
+  return kI8WideWarps * 128 * 4 + (4 * kI8MaxStages + 2 * kI8Buffers + 2) * 8 + 8 +
          (3 * E + 1) * 4;
 }
 
@@ -944,15 +958,16 @@ cudaError_t launch_i8(const Int8Maps& maps, Int8Args p, int grid, cudaStream_t s
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8SmemLimit);
   });
   if (ready != cudaSuccess) return ready;
-  const int stage = kI8WBytes + p.a_rows * 256, fixed = 1024 + extra_smem(p.E);
-  // (three stages of 64 KB to six of 36: one CTA to an SM, so no CTA waits for
-  // TMEM that another holds)
-  p.stages = std::min(kI8MaxStages, (kI8SmemLimit - fixed) / stage);
+  const int fixed = 1024 + extra_smem(p.E), x_bytes = p.a_rows * 256;
+  // (three to six stages of weights.  128 rows: two stages of tokens and four of weights
+  // 136 us where these take 130, for 64 experts of 2048 x 1024 and 6144 rows)
+  p.x_stages = p.a_rows <= 64 ? 4 : 3;
+  p.w_stages = std::min(kI8MaxStages, (kI8SmemLimit - fixed - p.x_stages * x_bytes) / kI8WBytes);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kI8Threads);
-  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.dynamicSmemBytes = fixed + p.w_stages * kI8WBytes + p.x_stages * x_bytes;
   cfg.stream = s;
   cfg.attrs = attr;
   attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1010,7 +1025,8 @@ int int8_chunk_rows(int M, int N, int E) {
 // See internal.h.  Chunks: of all rows where there are few, else 128; with several
 // experts of few rows each on average, twice that average at least, since a lower
 // chunk leaves room for more stages of weights (64 experts, 512 rows, 7168 x 2048:
-// chunks of 128 rows and three stages 319 + 171 us, of 32 rows and five 301 + 160),
+// chunks of 128 rows and three stages 319 + 171 us, of 32 rows and five 301 + 160, in
+// one ring),
 // and an expert with more rows reads its weights again from L2.  Fewer items than
 // half the SMs: the reduction is split over clusters of as many CTAs (up to eight)
 // as still run all at once.  Several experts only with a token's rows or two in

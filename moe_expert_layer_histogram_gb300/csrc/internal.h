@@ -283,7 +283,7 @@ struct Int8Args {
   int out_fours;           // ... on 8-byte ones
   float clamp;             // SwiGLU (+inf: none)
   // set by launch_int8
-  int a_rows, tiles, stages, split, chunk_group;
+  int a_rows, tiles, w_stages, x_stages, split, chunk_group;
 };
 // swiglu: N = 2 I, gate and up rows.  The kernel before it on the stream is the
 // library's own and lets it start early.
