@@ -348,10 +348,10 @@ cudaError_t launch(const Int8RowsArgs& p, bool early, cudaStream_t s) {
 // See internal.h.  Int32 sums hold K products of 128 x 128 below 2^17 of them.
 bool int8_by_rows(int M, int K, int E) { return E == 1 && M <= 4 && K < 131072; }
 // The experts' products on the GPU, here and on the tensor cores.  64 x (2048, 1024),
-// top-6: one token 13.0 and 27.1 us, four 43.5 and 53.3, five 55.6 and 53.8.  64 x
-// (7168, 2048), top-8: one token 70.2 and 79.8, two 127.4 and 127.2, three 179 and
-// 179, four 225 and 195.  More rows than experts: 8 x (4096, 14336), top-2: 16 rows
-// 280 and 219, where 8 rows take 178 and 176.  (Units stay in 32 bits.)
+// top-6: one token 13.0 and 27.1 us, four 43.7 and 53.3, five 55.6 and 53.8.  64 x
+// (7168, 2048), top-8: one token 65.4 and 79.8, two 116.7 and 127.2, three 166 and
+// 179, four 225 and 192.  More rows than experts: 8 x (4096, 14336), top-2: 16 rows
+// 280 and 219, where 8 rows take 176 and 176.  (Units stay in 32 bits.)
 bool int8_by_group_rows(int M, int N, int K, int E) {
   return E > 1 && M <= std::min(E, kGroupRows) && K < 131072 && M * static_cast<int64_t>(N) <= INT32_MAX;
 }
@@ -368,7 +368,10 @@ cudaError_t launch_int8_rows(Int8RowsArgs p, bool early, cudaStream_t s) {
 }
 
 cudaError_t launch_int8_group_rows(Int8RowsArgs p, bool swiglu, bool early, cudaStream_t s) {
-  p.slices = slices_of(p.K);
+  // (two warps to a reduction at most: with more the blocks wait for their slowest warp
+  // more often.  64 x (7168, 2048), top-8, two tokens: eight 127.5 us, four 123.0, two
+  // 116.7, one 115.9; 8 x (4096, 14336), top-2, four: 179, 181, 176 and 208)
+  p.slices = std::min(slices_of(p.K), 2);
   const int groups = 8 / p.slices, width = swiglu ? p.N / 2 : p.N;
   const int64_t tiles = (width - 1) / (groups * (swiglu ? 2 : kRowsChannels)) + 1;
   // (an expert has an item for each of its rows at most)
