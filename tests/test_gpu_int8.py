@@ -291,6 +291,36 @@ def test_few_rows_of_experts(offsets, M, N, K):
         assert bool((out[~mine] == 7).all()) and bool((out[:, N:] == 7).all())
 
 
+def test_experts_of_tokens_quantised_once():
+    # 8.4 M codes and more: the same bits as every expert's rows by themselves, also for
+    # slots outside the tokens (rows of zeros)
+    from moe_expert_layer_histogram_gb300 import int8_experts, int8_matmul, int8_quantize
+    T, E, k, H, I = 4200, 4, 4, 512, 144
+    x = randn(T, H)
+    w13, w2 = codes_of(E, 2 * I, H, seed=1), codes_of(E, H, I, seed=2)
+    s13, s2 = scales_of(E, 2 * I) * 0.02, scales_of(E, H, seed=1)
+    _, o = route(T, E, k, masked=0.1)
+    slots = o.slots.clone()
+    slots[3], slots[7], slots[-1] = -1, T * k, 2 ** 31 - 1
+    out = torch.full((T * k, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    int8_experts(x, slots, o.offsets, k, w13, s13, w2, s2, out=out)
+    live = int(o.offsets[-1])
+    codes, scales = int8_quantize(x, slots, k)
+    gu = int8_matmul(codes, scales, w13, s13, offsets=o.offsets)[:live]
+    assert bool((out[[3, 7]] == 0).all()) and bool((out[live:] == 7).all())
+    # h from products rounded to bf16: within 2^-8 of gate and up each, and a code's
+    # half step of the largest |h| a row
+    gate, up = gu[:, :I].double(), gu[:, I:].double()
+    h = gate * torch.sigmoid(gate) * up
+    dh = (h.abs() * (1 + gate.abs()) + 1e-30) * 3 * BF16 + h.abs().amax(1, keepdim=True) / 127
+    off = o.offsets.tolist()
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        w = w2[e].double() * s2[e].double()[:, None]
+        want, tol = h[a:b] @ w.t(), dh[a:b] @ w.abs().t()
+        assert bool(((out[a:b].double() - want).abs() <= tol + BF16 * want.abs() + 1e-30).all())
+
+
 @pytest.mark.parametrize("T,E,k,H,I,clamp,masked", [
     (1, 64, 8, 7168, 2048, 7.0, 0.0), (1, 2, 1, 16, 16, 0.0, 0.0), (2, 16, 8, 272, 144, 0.5, 0.0),
     (5, 64, 3, 528, 16, 0.0, 0.4), (4, 16, 4, 2048, 1040, 7.0, 0.0), (16, 512, 1, 144, 272, 0.0, 0.0)])
