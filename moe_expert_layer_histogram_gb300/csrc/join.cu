@@ -212,11 +212,14 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
 __device__ __forceinline__ float sigmoid(float a) {
   return expf(fminf(a, 0.0f)) / (1.0f + expf(-fabsf(a)));
 }
-__device__ __forceinline__ float gate_of(const moe_join& j, int64_t t) {
-  if (!j.gate) return 1.0f;
-  return sigmoid(j.gate_type == MOE_DTYPE_F32
-                     ? static_cast<const float*>(j.gate)[t]
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(j.gate)[t]));
+// A token's gate, 1 without one; rest: what it leaves, 1 - gate, as sigmoid(-a) (the
+// difference would have lost its digits from a = 10 on).
+__device__ __forceinline__ float gate_of(const moe_join& j, int64_t t, bool rest = false) {
+  if (!j.gate) return rest ? 0.0f : 1.0f;
+  const float a = j.gate_type == MOE_DTYPE_F32
+                      ? static_cast<const float*>(j.gate)[t]
+                      : __bfloat162float(static_cast<const __nv_bfloat16*>(j.gate)[t]);
+  return sigmoid(rest ? -a : a);
 }
 
 // The block's sum y of token t: routed rows (kAtOnce of them on their way
@@ -522,7 +525,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
           if (lane == 0) p.d_weights[t * j.K + k] = dot;
         }
       if (p.d_gate && warp == warps - 1) {
-        const float d = warp_sum(lane < warps ? dots[kMaxTopK][lane] : 0.0f) * sg * (1.0f - sg);
+        const float d =
+            warp_sum(lane < warps ? dots[kMaxTopK][lane] : 0.0f) * sg * gate_of(j, t, true);
         if (lane == 0) {
           if (j.gate_type == MOE_DTYPE_F32)
             static_cast<float*>(p.d_gate)[t] = d;
@@ -563,7 +567,7 @@ static_assert(kInfos > kMaxStages);
 struct TokenInfo {
   int row[kMaxTopK];  // -1: none
   float w[kMaxTopK];
-  float gate, norm_rstd, post_rstd, unused;
+  float gate, norm_rstd, post_rstd, gate_rest;
 };
 
 struct Ring {
@@ -705,6 +709,8 @@ struct TokenWords {
       w = norm_rstd[t];
     } else if (lane == kMaxTopK + 2 && post_rstd) {
       w = post_rstd[t];
+    } else if (lane == kMaxTopK + 3) {
+      w = gate_of(j, t, true);
     }
   }
   __device__ void leave(TokenInfo& info, int lane) const {
@@ -715,6 +721,7 @@ struct TokenWords {
     if (lane == kMaxTopK) info.gate = w;
     if (lane == kMaxTopK + 1) info.norm_rstd = w;
     if (lane == kMaxTopK + 2) info.post_rstd = w;
+    if (lane == kMaxTopK + 3) info.gate_rest = w;
     __syncwarp();
   }
 };
@@ -933,7 +940,8 @@ __global__ void __launch_bounds__(1024, 1)
             if (lane == 0) p.d_weights[t * j.K + k] = dot;
           }
         if (p.d_gate && warp == warps - 1) {
-          const float d = warp_sum(lane < warps ? dots[kMaxTopK][lane] : 0.0f) * sg * (1.0f - sg);
+          const float d =
+              warp_sum(lane < warps ? dots[kMaxTopK][lane] : 0.0f) * sg * info.gate_rest;
           if (lane == 0) {
             if (j.gate_type == MOE_DTYPE_F32)
               static_cast<float*>(p.d_gate)[t] = d;

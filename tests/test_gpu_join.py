@@ -416,3 +416,26 @@ def no_wait_gave_up():
 @pytest.mark.parametrize("x_type", [torch.float32, torch.bfloat16])
 def test_many_tokens_for_each_block(T, H, K, x_type):
     check(make(T, H, K, x_type=x_type, w_type=x_type, post=K % 2 == 0))
+
+
+@pytest.mark.parametrize("T,H", [(28, 264), (28, 2001), (4200, 1032), (420, 7168)])
+@pytest.mark.parametrize("gate_type", [torch.float32, torch.bfloat16])
+def test_gradient_of_saturated_gates(T, H, gate_type):
+    # 1 - sigmoid(a) cancels where sigmoid(a) is near 1.  Without norms d y is scale d x'
+    # to 2 u of itself (scale's rounding and the product's) and the dot product is off by
+    # 62 u of its terms' magnitudes; sigmoid(a) and sigmoid(-a) by 6 u each, their
+    # products by 2 u: no absolute term
+    from moe_expert_layer_histogram_gb300 import block_join, block_join_backward
+    a = make(T, H, 0, post=False, norm=False, gate_type=gate_type)
+    size = torch.tensor([0.5, 4.0, 8.0, 12.0, 16.0, 20.0, 40.0], device="cuda")
+    a["gate"] = torch.cat([size, -size]).repeat(T // 14).to(gate_type)
+    dx = randn(T, H, seed=70)
+    got = block_join_backward(block_join(**a), d_x=dx).gate
+    s = torch.sigmoid(d(a["gate"])) * torch.sigmoid(-d(a["gate"]))
+    parts = a["scale"] * d(dx) * d(a["shared"])
+    want = s * parts.sum(1)
+    tol = 62 * U * s * parts.abs().sum(1) + 14 * U * want.abs()
+    if gate_type is torch.bfloat16:
+        tol = tol + BF16 * (want.abs() + tol)
+    assert bool(((got.double() - want).abs() <= tol + 2.0 ** -126).all())
+    check(dict(a, norm_weight=1 + randn(H, seed=71, scale=0.3), post_weight=1 + randn(H, seed=72, scale=0.3)))
