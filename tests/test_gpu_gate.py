@@ -411,3 +411,32 @@ def test_refusals():
         router_order(r.ids.long(), 24)
     with pytest.raises(MoEError):
         router_order(r.ids, 513)
+
+
+@pytest.mark.parametrize("groups,group_top,group_score,dtype", [
+    (6, 3, "top2", torch.float32), (3, 1, "max", torch.float32), (12, 5, "max", torch.float32),
+    (6, 3, "top2", torch.bfloat16), (24, 9, "top2", torch.bfloat16)])
+def test_groups_that_are_no_power_of_two_take_the_same_way(groups, group_top, group_score, dtype):
+    # lanes without a group once sent every token through the choice in 64 bits, forty times
+    # the work of all the rest: no more than four times what 8 groups take says that few
+    # tokens go there
+    from moe_expert_layer_histogram_gb300 import router_gate
+    x = logits_of(32768, 384, dtype)
+
+    def time(groups, group_top):
+        best = float("inf")
+        for _ in range(12):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(4):
+                router_gate(x, 8, groups=groups, group_top=group_top, group_score=group_score)
+            end.record()
+            end.synchronize()
+            best = min(best, start.elapsed_time(end))
+        return best
+    time(8, 4)
+    few, many = time(groups, group_top), time(8, 4)
+    assert few <= 4.0 * many, (few / 4, many / 4)
+    y = x[:300]
+    for score in ("softmax", "sigmoid"):
+        check(y, 8, score=score, groups=groups, group_top=group_top, group_score=group_score)
