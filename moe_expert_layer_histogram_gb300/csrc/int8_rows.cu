@@ -232,7 +232,12 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsResident)
   __syncthreads();
   const int units = tab.chunk_off[p.E] * tiles;
   int unit = blockIdx.x;
-  if (unit >= units) return;
+  if (unit >= units) {
+    // (no row may have an expert, and no block a unit: this kernel is not over before the
+    // one that it overlaps, whose end the kernels after it rely on)
+    pdl_wait();
+    return;
+  }
   const int step = p.slices * 512, k_first = (slice * 32 + lane) * 16;
   uint4 w[kRowsAhead][kRowsChannels];
   int k0 = k_first;

@@ -465,3 +465,23 @@ def test_refusals():
                                      scales_of(2, 64))):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("T,k,H,I", [(1, 8, 2048, 512), (3, 8, 272, 144), (24, 1, 7168, 16)])
+def test_a_few_tokens_of_no_expert(T, k, H, I):
+    # all of a decoding step's tokens masked: no kernel has a row, none leaves before the
+    # one ahead of it is over, the result stays as it was, and so do the next calls'
+    from moe_expert_layer_histogram_gb300 import int8_experts
+    E = 64
+    x = randn(T, H)
+    w13, w2 = codes_of(E, 2 * I, H, seed=1), codes_of(E, H, I, seed=2)
+    s13, s2 = scales_of(E, 2 * I) * 0.02, scales_of(E, H, seed=1)
+    slots = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    some = torch.arange(E + 1, dtype=torch.int32, device="cuda").clamp(max=T * k)
+    want = int8_experts(x, slots, some, k, w13, s13, w2, s2)
+    for offsets in (torch.zeros_like(some), torch.full_like(some, T * k)):
+        for _ in range(20):
+            out = torch.full((T * k, H), 7.0, dtype=torch.bfloat16, device="cuda")
+            int8_experts(x, slots, offsets, k, w13, s13, w2, s2, out=out)
+            got = int8_experts(x, slots, some, k, w13, s13, w2, s2)
+            assert bool((out == 7).all()) and torch.equal(got, want)
