@@ -508,7 +508,7 @@ moe_status moe_int8_experts(const void* x, int64_t ldx, int T, const int32_t* sl
   }
   const __nv_bfloat16* tokens = static_cast<const __nv_bfloat16*>(x);
   const int64_t token_codes = padded(static_cast<int64_t>(T) * H, 256);
-  if (rows / 2 >= T && static_cast<int64_t>(rows) * H >= kOnceLeast &&
+  if (T > 0 && rows / 2 >= T && static_cast<int64_t>(rows) * H >= kOnceLeast &&
       token_codes + 4 * static_cast<int64_t>(T) <= static_cast<int64_t>(rows) * I * 4) {
     // Each token once, and its codes (where h will be) to all of its rows.
     int8_t* once = reinterpret_cast<int8_t*>(h);

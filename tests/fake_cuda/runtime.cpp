@@ -77,6 +77,7 @@ cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void
   // 48 KB in all without the attribute; a kernel's static part is not known here: 2 KB
   const auto l = limits.find({device, f});
   const size_t limit = l == limits.end() ? 46 << 10 : l->second;
+  if (!c->gridDim.x || !c->gridDim.y || !c->gridDim.z) return note(cudaErrorInvalidConfiguration);
   if (c->dynamicSmemBytes > limit) return note(cudaErrorInvalidValue);
   ++launches;
   last_grid = c->gridDim.x;

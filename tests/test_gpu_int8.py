@@ -485,3 +485,16 @@ def test_a_few_tokens_of_no_expert(T, k, H, I):
             int8_experts(x, slots, offsets, k, w13, s13, w2, s2, out=out)
             got = int8_experts(x, slots, some, k, w13, s13, w2, s2)
             assert bool((out == 7).all()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("rows", [4, 600, 40000])
+def test_experts_of_an_empty_x(rows):
+    # every slot lies outside: rows of zeros
+    from moe_expert_layer_histogram_gb300 import int8_experts
+    E, H, I = 4, 256, 128
+    w13, w2 = codes_of(E, 2 * I, H, seed=1), codes_of(E, H, I, seed=2)
+    slots = torch.arange(rows, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, rows // 4, rows // 2, rows // 2, rows], dtype=torch.int32, device="cuda")
+    out = torch.full((rows, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    int8_experts(randn(0, H), slots, off, 2, w13, scales_of(E, 2 * I), w2, scales_of(E, H), out=out)
+    assert bool((out == 0).all())

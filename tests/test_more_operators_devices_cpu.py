@@ -251,3 +251,11 @@ def test_structure_sizes():
     s = m.MoEJoin.from_buffer_copy(j._pack(*range(1, 7), 1.0, 2.0, *range(7, 19)))
     assert [getattr(s, n) for n, _ in m.MoEJoin._fields_] == [1, 2, 3, 4, 5, 6, 1.0, 2.0,
                                                               *range(7, 19)]
+
+
+@pytest.mark.parametrize("rows", [8, 500, 40000, 80000])
+def test_experts_of_no_tokens(lib, rows):
+    # slots outside an empty x: rows of zeros, whatever their number
+    before = lib.fake_launches()
+    assert experts(lib, 0, rows, 4) == OK
+    assert lib.fake_launches() > before
