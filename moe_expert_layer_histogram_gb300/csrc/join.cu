@@ -1000,6 +1000,15 @@ __global__ void __launch_bounds__(32 * kFinishRows)
     static_cast<__nv_bfloat16*>(p.out[blockIdx.y])[col] = __float2bfloat16_rn(sum);
 }
 
+// Zeros in the rows of no expert where there is no token (the passes over tokens see
+// to them themselves).
+__global__ void __launch_bounds__(256)
+    join_zero_rows_kernel(__nv_bfloat16* d_rows, int64_t ld, int rows, int H,
+                          const int32_t* live_rows) {
+  for (int64_t r = max(*live_rows, 0) + static_cast<int64_t>(blockIdx.x); r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < H; c += blockDim.x) d_rows[r * ld + c] = __float2bfloat16_rn(0.0f);
+}
+
 // ---------------------------------------------------------------- host
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t size_of(int type) { return type == MOE_DTYPE_F32 ? 4 : 2; }
@@ -1255,6 +1264,13 @@ moe_status moe_join_backward(const moe_join* j, const void* x_out, int64_t ld_ou
       e = vec ? run_backward<float, true>(p, s) : run_backward<float, false>(p, s);
     else
       e = vec ? run_backward<__nv_bfloat16, true>(p, s) : run_backward<__nv_bfloat16, false>(p, s);
+    if (take_error(e) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (j->T == 0 && d_rows && live_rows && j->rows > 0) {
+    if (!aligned_to(d_rows, 2) || !aligned_to(live_rows, 4)) return MOE_ERR_INVALID_ARG;
+    const cudaError_t e =
+        launch_pdl(false, join_zero_rows_kernel, dim3(std::min(j->rows, 8 * kSms)), dim3(256), 0, s,
+                   static_cast<__nv_bfloat16*>(d_rows), ld_drows, j->rows, j->H, live_rows);
     if (take_error(e) != cudaSuccess) return MOE_ERR_CUDA;
   }
   if (!d_post && !d_norm) return MOE_OK;

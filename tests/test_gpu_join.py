@@ -439,3 +439,31 @@ def test_gradient_of_saturated_gates(T, H, gate_type):
         tol = tol + BF16 * (want.abs() + tol)
     assert bool(((got.double() - want).abs() <= tol + 2.0 ** -126).all())
     check(dict(a, norm_weight=1 + randn(H, seed=71, scale=0.3), post_weight=1 + randn(H, seed=72, scale=0.3)))
+
+
+@pytest.mark.parametrize("H", [64, 61])
+@pytest.mark.parametrize("live", [0, 3])
+def test_no_tokens_leave_zeros_in_rows_of_no_expert(H, live):
+    from moe_expert_layer_histogram_gb300 import MoEJoin, moe_join_backward
+    rows = torch.zeros(2000, H, dtype=torch.bfloat16, device="cuda")
+    j = MoEJoin(T=0, H=H, K=2, scale=1.0, eps=1e-6, expert_rows=rows.data_ptr(), ld_rows=H, rows=2000)
+    got = torch.full((2001, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    n = torch.tensor([live], dtype=torch.int32, device="cuda")
+    moe_join_backward(j, None, H, None, None, None, H, None, H, None, H, got, H, n, None, None, H,
+                      None, None, None, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert bool((got[live:2000] == 0).all()) and bool((got[:live] == 7).all())
+    assert bool((got[2000] == 7).all())
+
+
+def test_gradients_of_a_padded_buffer_without_tokens():
+    from moe_expert_layer_histogram_gb300 import block_join, block_join_backward, router_order
+    H = 96
+    order = router_order(torch.empty(0, 2, dtype=torch.int32, device="cuda"), 4)
+    n = torch.ones(H, device="cuda")
+    j = block_join(torch.empty(0, H, device="cuda"), randn(50, H, dtype=torch.bfloat16), order,
+                   torch.empty(0, 2, device="cuda"), post_weight=n, norm_weight=n)
+    torch.full((50, H), 7.0, dtype=torch.bfloat16, device="cuda")   # (what the allocator gives next)
+    got = block_join_backward(j, d_x=torch.empty(0, H, device="cuda"),
+                              d_h=torch.empty(0, H, dtype=torch.bfloat16, device="cuda"))
+    assert got.expert_rows.shape == (50, H) and bool((got.expert_rows == 0).all())
+    assert bool((got.norm_weight == 0).all()) and bool((got.post_weight == 0).all())
