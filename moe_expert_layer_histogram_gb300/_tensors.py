@@ -9,8 +9,8 @@ _LARGEST = 2 ** 31 - 1
 
 def fits(n, name):
     """The library takes sizes as 32-bit integers (and ctypes would cut them)."""
-    if n > _LARGEST:
-        raise ValueError("%s: %d is above 2^31 - 1" % (name, n))
+    if not -_LARGEST <= n <= _LARGEST:
+        raise ValueError("%s: %d is beyond 2^31 - 1" % (name, n))
 
 
 def stream_on(device):

@@ -70,8 +70,11 @@ def router_gate(logits, top_k, score="softmax", bias=None, groups=1, group_top=N
     if mask is not None:
         check(mask, torch.bool if mask.dtype is torch.bool else torch.uint8, (T,), dev, "mask")
     fits(top_k, "top_k")
-    fits(max(groups, group_top or 0), "groups")
-    config = _config(score, index(groups), index(groups if group_top is None else group_top),
+    if group_top is None:
+        group_top = groups
+    fits(groups, "groups")
+    fits(group_top, "group_top")
+    config = _config(score, index(groups), index(group_top),
                      group_score, bool(normalize), float(scale))
     k = max(top_k, 0)
     ids = torch.empty(T, k, dtype=_I32, device=dev)

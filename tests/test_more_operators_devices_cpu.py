@@ -259,3 +259,31 @@ def test_experts_of_no_tokens(lib, rows):
     before = lib.fake_launches()
     assert experts(lib, 0, rows, 4) == OK
     assert lib.fake_launches() > before
+
+
+LOW = -(2 ** 32) + 4                                  # 4, if cut to 32 bits
+
+
+def test_numbers_below_32_bits_are_refused(monkeypatch):
+    from moe_expert_layer_histogram_gb300 import _tensors, balance, blockscale, int8
+    from moe_expert_layer_histogram_gb300 import gate as g
+    for n in (LOW, -(2 ** 31) - 1):
+        with pytest.raises(ValueError):
+            _tensors.fits(n, "top_k")
+    assert _tensors.fits(-1, "top_k") is None          # (the library's own refusal)
+    for module in (g, balance, blockscale, int8):
+        monkeypatch.setattr(module, "stream_on", lambda device: 0)
+    ids = Fake(torch.int32, (16,))
+    ids.numel = lambda: 16
+    x = Fake(torch.float32, (4, 8))
+    with pytest.raises(ValueError):
+        g.router_order(ids, LOW)
+    for bad in (dict(top_k=LOW), dict(top_k=2, groups=LOW), dict(top_k=2, groups=4, group_top=LOW)):
+        with pytest.raises(ValueError):
+            g.router_gate(x, **bad)
+    with pytest.raises(ValueError):
+        balance.router_balance(x, LOW)
+    rows = Fake(torch.bfloat16, (4, 16))
+    for quantize in (blockscale.blockscale_quantize, int8.int8_quantize):
+        with pytest.raises(ValueError):
+            quantize(rows, ids, LOW)
