@@ -1050,16 +1050,14 @@ bool join_vectors(const moe_join& j) {
          in_vectors(j.norm_weight, 0, 1);
 }
 
-// Vectors per thread: one up to 1024 threads, else as few as 512 threads allow.
+// Vectors per thread: one up to 1024 threads, else four of 512 threads at most.
 // (More threads with little to keep beat fewer with more: 4096 x 7168 in two vectors
 // of 448 threads took 150 us forward and 470 backward.)
 struct Shape {
   int nv, threads;
 };
 Shape shape_of(int H) {
-  const int vectors = (H + kVec - 1) / kVec;
-  int nv = 1;
-  while ((vectors + nv - 1) / nv > (nv == 1 ? 1024 : 512)) nv *= 2;
+  const int vectors = (H + kVec - 1) / kVec, nv = vectors <= 1024 ? 1 : 4;
   return {nv, ((vectors + nv - 1) / nv + 31) / 32 * 32};
 }
 
@@ -1119,9 +1117,7 @@ cudaError_t run_forward(const JoinArgs& p, cudaStream_t s) {
     }
   const Shape q = shape_of(p.j.H);
   auto go = [&](auto k) { return launch_pdl(false, k, dim3(T), dim3(q.threads), 0, s, p); };
-  if (q.nv == 1) return go(join_forward_kernel<X, 1, VEC>);
-  if (q.nv == 2) return go(join_forward_kernel<X, 2, VEC>);
-  return go(join_forward_kernel<X, 4, VEC>);
+  return q.nv == 1 ? go(join_forward_kernel<X, 1, VEC>) : go(join_forward_kernel<X, 4, VEC>);
 }
 
 // Blocks of the backward pass: as many as run at a time (ring: 0, or the size of x's
@@ -1151,9 +1147,7 @@ cudaError_t run_backward(const JoinBackArgs& p, cudaStream_t s) {
   auto go = [&](auto k) {
     return launch_pdl(false, k, dim3(back_blocks(p.j.T, p.j.H, 0)), dim3(q.threads), 0, s, p);
   };
-  if (q.nv == 1) return go(join_backward_kernel<X, 1, VEC>);
-  if (q.nv == 2) return go(join_backward_kernel<X, 2, VEC>);
-  return go(join_backward_kernel<X, 4, VEC>);
+  return q.nv == 1 ? go(join_backward_kernel<X, 1, VEC>) : go(join_backward_kernel<X, 4, VEC>);
 }
 
 }  // namespace
