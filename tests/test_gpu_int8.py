@@ -498,3 +498,61 @@ def test_experts_of_an_empty_x(rows):
     out = torch.full((rows, H), 7.0, dtype=torch.bfloat16, device="cuda")
     int8_experts(randn(0, H), slots, off, 2, w13, scales_of(E, 2 * I), w2, scales_of(E, H), out=out)
     assert bool((out == 0).all())
+
+
+def test_gathered_rows_have_the_bits_of_smaller_calls():
+    # 8.6 M codes of tokens quantised once, and the same rows quantised for themselves in a
+    # call for each expert: 512 products of codes stay below 2^24, so all sums are exact
+    # and every kernel gives the same bits
+    from moe_expert_layer_histogram_gb300 import int8_experts
+    T, E, k, H, I = 4200, 4, 4, 512, 144
+    x = randn(T, H)
+    w13, w2 = codes_of(E, 2 * I, H, seed=1), codes_of(E, H, I, seed=2)
+    s13, s2 = scales_of(E, 2 * I) * 0.02, scales_of(E, H, seed=1)
+    _, o = route(T, E, k, masked=0.1)
+    slots = o.slots.clone()
+    slots[3], slots[7], slots[-1] = -1, T * k, 2 ** 31 - 1
+    out = int8_experts(x, slots, o.offsets, k, w13, s13, w2, s2)
+    off = o.offsets.tolist()
+    for e in range(E):
+        for a in range(off[e], off[e + 1], 1000):
+            part = slots[a:min(a + 1000, off[e + 1])]
+            own = torch.full((E + 1,), len(part), dtype=torch.int32, device="cuda")
+            own[:e + 1] = 0
+            got = int8_experts(x, part, own, k, w13, s13, w2, s2)
+            assert torch.equal(got, out[a:a + len(part)])
+
+
+@pytest.mark.parametrize("T,E,k", [(2, 16, 8), (20, 1, 1), (100, 4, 2), (9800, 1, 1), (5000, 4, 4)])
+def test_codes_of_h(T, E, k):
+    # With the unit matrix for w2 an output is a code of h times its row's scale; in bf16
+    # it is off by at most 127 2^-8 < 1/2 of that scale, so the code can be told.  Sums of
+    # 1024 products of codes are exact.  Gate and up are off by 2 u of themselves (their
+    # scales), the power by (4 + |g|) u, the quotient by 4 u, the product by u: h by
+    # (13 + 3 |g|) u, at most 34 u with |g| <= 7, its scale by 2 u more.  So a quotient is
+    # off by 127 * 70 u, and codes are those of 64 bits unless it lies as near to a half.
+    from moe_expert_layer_histogram_gb300 import int8_experts
+    H, I, clamp = 1024, 256, 7.0
+    x = randn(T, H)
+    w13 = codes_of(E, 2 * I, H, seed=1)
+    s13 = scales_of(E, 2 * I) * 0.2
+    w2 = torch.zeros(E, H, I, dtype=torch.int8, device="cuda")
+    w2[:, torch.arange(I), torch.arange(I)] = 1
+    _, o = route(T, E, k)
+    out = int8_experts(x, o.slots, o.offsets, k, w13, s13, w2, torch.ones(E, H, device="cuda"),
+                       clamp=clamp)
+    assert bool((out[:, I:] == 0).all())
+    q, s = quantized(x)
+    off, rows = o.offsets.tolist(), o.slots.long() // k
+    for e in range(E):
+        r = rows[off[e]:off[e + 1]]
+        gu, _ = matmul_reference(q[r], s[r], w13[e], s13[e])
+        gate, up = gu[:, :I].clamp(-clamp, clamp), gu[:, I:].clamp(-clamp, clamp)
+        h = gate * torch.sigmoid(gate) * up
+        sh = h.abs().amax(1, keepdim=True) / 127
+        quot = h / sh
+        got = torch.round(out[off[e]:off[e + 1], :I].double() / sh)
+        near = ((quot - torch.floor(quot)) - 0.5).abs() <= 127 * 70 * U
+        assert bool((near | (got == torch.round(quot))).all())
+        assert bool(((got - quot).abs() <= 0.5 + 127 * 70 * U).all())
+        assert not near.numel() or float(near.double().mean()) < 0.01
