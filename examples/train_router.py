@@ -17,8 +17,8 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from moe_expert_layer_histogram_gb300 import (blockscale_experts,  # noqa: E402
-                                              router_balance, router_balance_backward)
+from moe_expert_layer_histogram_gb300 import (blockscale_experts, router_balance,  # noqa: E402
+                                              router_balance_backward, router_order)
 
 
 def quantize_weight(w):
@@ -33,12 +33,9 @@ def quantize_weight(w):
 def expert_order(routing):
     """The routed slots t * K + k in expert order, as blockscale_experts takes
     them: slots int32 [T * K], offsets int32 [E + 1].  Slots of tokens that are
-    not live (id -1) come first and belong to no expert."""
-    ids = routing.ids.flatten()
-    slots = torch.sort(ids, stable=True).indices.to(torch.int32)
-    offsets = torch.zeros(routing.counts.numel() + 1, dtype=torch.int32, device=ids.device)
-    torch.cumsum(routing.counts, 0, dtype=torch.int32, out=offsets[1:])
-    return slots, offsets + (ids.numel() - offsets[-1])
+    not live (id -1) come last and belong to no expert."""
+    order = router_order(routing.ids, routing.counts.numel())
+    return order.slots, order.offsets
 
 
 class FrozenExperts:
