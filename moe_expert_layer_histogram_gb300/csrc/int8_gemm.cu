@@ -78,6 +78,15 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// No copy of this thread is in flight when it leaves, also after a wait that gave up:
+// `loads` so far, the latest in the stages before the next one's.
+__device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int loads) {
+  for (int back = 1; back <= stages && back <= loads; ++back) {
+    const int load = loads - back;
+    mbar_wait(&full[load % stages], static_cast<uint32_t>((load / stages) & 1), nullptr);
+  }
+}
+
 struct I8Item {
   int e, tile, row0, rows;
 };
@@ -182,7 +191,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   uint64_t* aempty = afull + kI8Buffers;
   uint64_t* dfull = aempty + kI8Buffers;
   uint64_t* dempty = dfull + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dempty + 1);
+  uint64_t* drained = dempty + 1;  // all MMAs are over
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_tab = reinterpret_cast<int*>(tmem_holder + 2);
   const ExpertTable tab{s_tab, s_tab + p.E + 1, s_tab + 2 * p.E + 1};
@@ -203,6 +213,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     mbar_init(dfull, 1);
     mbar_init(dempty, kI8WideWarps);
+    mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       // -------------------------------------------------- weights by TMA
       // (they are not the kernel's before this one: no wait for it)
       const uint64_t once = l2_policy_evict_first(), reused = l2_policy_evict_normal();
-      int stage = 0;
+      int stage = 0, loads = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int item = first; ok && item < total; item += step) {
@@ -258,12 +269,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             tma_load_3d_hint(smem + stage * kI8WBytes + h * (kI8WBytes / 2), &maps.w, &wfull[stage],
                              kb * 128, n0, it.e, policy);
           }
+          ++loads;
           if (++stage == w_stages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
+      drain_loads(wfull, w_stages, loads);
       if (!ok) report_status(&g_int8_status, kStatusTimeout);
     }
     __syncwarp();
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     if (lane == 0) {
       // -------------------------------------------------- tokens by TMA
       const uint64_t reused = l2_policy_evict_normal();
-      int stage = 0;
+      int stage = 0, loads = 0;
       uint32_t phase = 0;
       bool ok = true;
       pdl_wait();
@@ -288,12 +301,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           for (int h = 0; h < 2; ++h)
             tma_load_2d_hint(sx + h * (16 << box) * 128, &maps.x[box], &xfull[stage],
                              kb * 128 + h * 64, it.row0, reused);
+          ++loads;
           if (++stage == x_stages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
+      drain_loads(xfull, x_stages, loads);
       if (!ok) report_status(&g_int8_status, kStatusTimeout);
     }
     __syncwarp();
@@ -339,6 +354,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         }
       }
     }
+    // (the same lane is elected every time: its commit covers all that it issued)
+    if (elect_one()) tc_commit(drained);
+    __syncwarp();
+    if (lane == 0) mbar_wait(drained, 0, nullptr);
+    __syncwarp();
     if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
   } else if (warp >= kI8WideWarp0) {
     // ---------------------------------------------------- widen, and results
@@ -625,7 +645,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   uint64_t* aempty = afull + kP8Buffers;
   uint64_t* dfull = aempty + kP8Buffers;
   uint64_t* dempty = dfull + 1;            // (rank 0's)
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dempty + 1);
+  uint64_t* drained = dempty + 1;          // all MMAs are over
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_tab = reinterpret_cast<int*>(tmem_holder + 2);
   const ExpertTable tab{s_tab, s_tab + p.E + 1, s_tab + 2 * p.E + 1};
@@ -647,6 +668,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     mbar_init(dfull, 1);
     mbar_init(dempty, 2 * kI8WideWarps);
+    mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -696,7 +718,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       // -------------------------------------------------- weights by TMA
       // (they are not the kernel's before this one: no wait for it)
       const uint64_t reused = l2_policy_evict_normal();
-      int stage = 0;
+      int stage = 0, loads = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int item = first; ok && item < total; item += step) {
@@ -715,12 +737,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             tma_load_3d_hint(sw, &maps.w, &wfull[stage], kb * 128, it.tile * kI8Tile + rank * 128,
                              it.e, reused);
           }
+          ++loads;
           if (++stage == kP8WStages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
+      drain_loads(wfull, kP8WStages, loads);
       if (!ok) report_status(&g_int8_status, kStatusTimeout);
     }
     __syncwarp();
@@ -729,7 +753,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       // -------------------------------------------------- tokens by TMA
       const uint64_t reused = l2_policy_evict_normal();
       const uint32_t xfull0 = mapa_shared(smem_u32(xfull), 0);
-      int stage = 0;
+      int stage = 0, loads = 0;
       uint32_t phase = 0;
       bool ok = true;
       pdl_wait();
@@ -746,12 +770,15 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           for (int h = 0; h < 2; ++h)
             tma_load_2d_pair(sx + h * (16 << box) * 128, &maps.x[box], xfull0 + stage * 8,
                              kb * 128 + h * 64, it.row0 + rank * part, reused);
+          ++loads;
           if (++stage == kP8XStages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
+      // (rank 0's barriers count both CTAs' copies, and neither leaves before the other)
+      if (rank == 0) drain_loads(xfull, kP8XStages, loads);
       // every stage's last release has arrived here before this CTA may leave
       for (int s = 0; ok && s < kP8XStages; ++s) {
         ok = mbar_wait(&xempty[stage], phase ^ 1, abort_flag);
@@ -801,6 +828,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         }
       }
     }
+    // (the same lane is elected every time: its commit covers all that it issued)
+    if (elect_one()) tc_commit_pair(drained, 3);
+    __syncwarp();
     if (!ok && lane == 0) report_status(&g_int8_status, kStatusTimeout);
   } else if (warp >= kI8WideWarp0) {
     // ---------------------------------------------------- widen, and results
@@ -939,6 +969,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // every MMA of the pair is over
+  if (warp == 1 && lane == 0) mbar_wait(drained, 0, nullptr);
+  __syncthreads();
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
@@ -946,7 +979,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
 // ---------------------------------------------------------------- host
 int extra_smem(int E) {
-  return kI8WideWarps * 128 * 4 + (4 * kI8MaxStages + 2 * kI8Buffers + 2) * 8 + 8 +
+  return kI8WideWarps * 128 * 4 + (4 * kI8MaxStages + 2 * kI8Buffers + 3) * 8 + 8 +
          (3 * E + 1) * 4;
 }
 
@@ -991,7 +1024,7 @@ cudaError_t launch_i8_pair(const Int8Maps& maps, Int8Args p, int pairs, cudaStre
   if (ready != cudaSuccess) return ready;
   constexpr int fixed = 1024 + kP8WStages * kP8WBytes + kP8XStages * kP8XBytes +
                         kI8WideWarps * 128 * 4 +
-                        (2 * kP8WStages + 2 * kP8XStages + 2 * kP8Buffers + 2) * 8 + 8;
+                        (2 * kP8WStages + 2 * kP8XStages + 2 * kP8Buffers + 3) * 8 + 8;
   static_assert(fixed + (3 * kMaxExperts + 1) * 4 <= kI8SmemLimit);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
