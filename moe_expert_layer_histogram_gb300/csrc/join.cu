@@ -581,7 +581,7 @@ struct Ring {
   uint64_t *full, *empty;
   volatile int* abort;
   int stages, bytes;
-  int stage = 0;
+  int stage = 0, loads = 0;
   uint32_t phase = 0;
   bool ok = true;
 
@@ -615,7 +615,16 @@ struct Ring {
       mbar_arrive_expect_tx(&full[stage], n);
       bulk_load(data + stage * bytes, row, n, &full[stage]);
     }
+    ++loads;
     next();
+  }
+  // ... which leaves when no copy is in flight, also after a wait that gave up.
+  __device__ void drain(int lane) {
+    for (int back = 1; lane == 0 && back <= stages && back <= loads; ++back) {
+      const int load = loads - back;
+      mbar_wait(&full[load % stages], static_cast<uint32_t>((load / stages) & 1), nullptr);
+    }
+    __syncwarp();
   }
   // A consumer's vector of the next row.
   template <typename T>
@@ -763,6 +772,7 @@ __global__ void __launch_bounds__(1024, 1)
       put_rows(j, ring, t, words.row, lane, true, true);
       words = next;
     }
+    ring.drain(lane);
     if (!ring.ok && lane == 0) report_status(&g_join_status, kStatusTimeout);
     return;
   }
@@ -851,6 +861,7 @@ __global__ void __launch_bounds__(1024, 1)
       if (block) put_rows(j, ring, t, words.row, lane, p.d_weights != nullptr, p.d_gate != nullptr);
       words = next;
     }
+    ring.drain(lane);
     if (!ring.ok && lane == 0) report_status(&g_join_status, kStatusTimeout);
   } else {
     float acc_norm[kVec], acc_post[POST ? kVec : 1];
