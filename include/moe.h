@@ -468,7 +468,9 @@ moe_status moe_order(const int32_t *ids, int n, int E, int32_t *slots,
  * x' is stored in x's type and h is the norm of what was stored.  A row_of_slot
  * outside [0, rows) is no term of its sum (whatever its weight).  With K = 0 and
  * shared alone this is the end of a dense block (shared: its output); with
- * neither there is nothing to join and h is the norm of x.                 */
+ * neither there is nothing to join and h is the norm of x.  (shared alone behind a
+ * gate and a norm: the norm undoes the gate but for eps, and so the gate's gradient
+ * is rounding.)                                                            */
 typedef struct {
     int T, H, K;               /* tokens, width (1..16384), slots per token
                                   (0..16)                                   */
@@ -679,7 +681,8 @@ size_t moe_int8_experts_workspace(int rows, int H, int I);
 
 /* out[m, n] = a_scales[m] w_scales[e, n] sum_k a[m, k] w_e[n, k] for the rows m of
  * each expert e, one rounding to bf16; products are exact, sums in fp32 (exact
- * up to 2^24).  a: int8 [M, K], row stride lda, any alignment; offsets: device
+ * up to 2^24; of a few rows in int32), and the two scales' product is an fp32
+ * number.  a: int8 [M, K], row stride lda, any alignment; offsets: device
  * int32 [E + 1], rows offsets[e] .. offsets[e+1] - 1 belong to expert e, or NULL
  * for one expert of all M rows (E = 1).  w: 16-byte aligned, ldw >= K a
  * multiple of 16.  out: bf16 [M, N], row stride ldo.  Rows of no expert are not

@@ -7,10 +7,10 @@
 // cores' staging.  A warp takes four channels and a slice of the reduction, 16 codes
 // a lane and channel at a time; it has its first loads under way before anything
 // else: one or two rows are quantised by every block for itself meanwhile (QUANT),
-// more by a kernel that this one overlaps.  On the GPU, 7168 -> 4096: one row 7.1
-// us, three 9.3, four 10.0, eight 18.6 (the dot products take the time by then);
-// through the tensor cores nine rows 12.4.  4096 -> 14592 (60 MB, 8.8 us of HBM): one
-// row 8.7, four 14.0, nine 15.9.
+// more by a kernel that this one overlaps.  On the GPU, 7168 -> 4096: one row 7.0
+// us, two 9.7, three 9.3, four 9.9; five, through the tensor cores, 10.7.  4096 ->
+// 14592 (60 MB, 8.8 us of HBM): one row 8.7, two 10.9, three 12.5, four 13.9 (the dot
+// products take the time by then); five 13.5.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -28,10 +28,11 @@
 // ahead of the others and fills a ring of stages in shared memory, one row each, so
 // that a token's dozen rows, which depend on its indices and on one another's sums,
 // are all on their way at once and the next token's behind them (4096 x 7168, top-8:
-// 127 us forward and 203 backward, 6.4 TB/s; with rows loaded by the threads that use
+// 127 us forward and 205 backward, 6.1 TB/s; with rows loaded by the threads that use
 // them 143 and 318).  With few tokens to a block there is little to run ahead of, and
-// narrow rows have more blocks to an SM; those, and rows that do not start on 16
-// bytes, are loaded by their threads (use_ring).
+// narrow rows have more blocks to an SM; those, rows that do not start on 16 bytes, and
+// rows of more than 7936 columns, whose vectors and filling warp are more than a block's
+// threads, are loaded by their threads (use_ring).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1091,7 +1092,7 @@ Shape shape_of(int H) {
 struct RingShape {
   int threads, blocks, stages, smem;
 };
-constexpr int kRingMost = 1024 - 32;  // consumers
+constexpr int kRingMost = 1024 - 32;  // consumers, of a vector each
 constexpr int kSmSmem = 233472;       // of which each block has 1 KB more than it asks for
 constexpr int kRingStatic = 5120;     // static shared memory, at most
 constexpr int kRingDynamic = 232448 - kRingStatic;
@@ -1114,7 +1115,8 @@ RingShape ring_shape(int H, int size) {
 // against 15 of loads, 1024 38 and 42, 2048 70 and 75; 2048 columns: 4096 tokens 41
 // and 38.  Backward pass, 7168: 304 tokens 23 and 27, 512 42 and 58, 2048 112 and
 // 176; 2048 with a norm after the block: 1024 tokens 33 and 29, 4096 97 and 97; 512:
-// 8192 tokens 40 and 53.
+// 8192 tokens 40 and 53.  (4096 tokens, top-8, forward and backward: 7936 columns by
+// the ring 134 and 228, 8192 by loads 157 and 352, 16384 466 and 955.)
 bool use_ring(int T, int H, int size, bool backward) {
   if (!ring_fits(H)) return false;
   const bool wide = H > 4096;

@@ -72,8 +72,8 @@ def block_join(x, expert_rows=None, order=None, weights=None, shared=None, gate=
     """x [T, H] f32 or bf16; expert_rows bf16 [R, H] with order (router_order's
     RouterOrder, or int32 rows [T * K]: the row of each slot, anything outside
     [0, R) for none) and weights f32 [T, K]; shared bf16 [T, H] with gate [T]
-    (logits, f32 or bf16) or without; post_weight and norm_weight [H], f32 or
-    bf16 -> BlockJoin.  h comes in 8 bits if `quantize`; out: where the new x
+    (logits, f32 or bf16) or without; post_weight and norm_weight [H], both f32 or
+    both bf16 -> BlockJoin.  h comes in 8 bits if `quantize`; out: where the new x
     goes (x itself, say)."""
     x_type = _type(x, "x")
     dtype = x.dtype
@@ -167,7 +167,8 @@ def block_join_backward(fwd, d_x=None, d_h=None):
     block_join's result, whose x, and the arguments it was given, are as they
     were.  The gradient of expert_rows is zero for rows of no expert, where fwd
     was given a RouterOrder; with plain rows it has whatever was in memory in
-    rows that no slot names."""
+    rows that no slot names, and a row may be named by one slot at most (the
+    gradients of several are not added up)."""
     x = fwd.x
     expert_rows, _, weights, shared, gate, post_weight, norm_weight = fwd._inputs
     live = fwd._live
