@@ -556,3 +556,40 @@ def test_codes_of_h(T, E, k):
         assert bool((near | (got == torch.round(quot))).all())
         assert bool(((got - quot).abs() <= 0.5 + 127 * 70 * U).all())
         assert not near.numel() or float(near.double().mean()) < 0.01
+
+
+@pytest.mark.parametrize("M,N,K", [(128, 2048, 8192), (100, 4096, 4096), (300, 4096, 7168), (69, 1995, 5756),
+                                   (131, 2146, 4540), (1296, 23, 5388), (5236, 16, 1824), (64, 640, 8192),
+                                   (33, 4096, 8192), (16, 4096, 7168), (2000, 2000, 5000), (6000, 3000, 2500)])
+def test_many_blocks_of_reduction_give_the_same_bits_every_time(M, N, K):
+    # codes of +-31: at most 8192 * 31^2 < 2^23, so every partial sum is exact in fp32.  The
+    # rings go round several times in each CTA; a stage filled again too early shows as
+    # wrong channels in some of the calls
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    g = torch.Generator(device="cuda").manual_seed(K)
+    ld = (K + 15) // 16 * 16
+    a = torch.randint(-31, 32, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-31, 32, (N, ld), generator=g, device="cuda", dtype=torch.int8)[:, :K]
+    s, ws = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    want = (a.double() @ w.double().t()).float().bfloat16()
+    bad = sum(not torch.equal(int8_matmul(a, s, w, ws), want) for _ in range(60))
+    assert bad == 0
+
+
+@pytest.mark.parametrize("T,H,I", [(128, 4096, 1024), (100, 4096, 528), (70, 2048, 1024)])
+def test_one_expert_of_long_rows_has_the_bits_of_smaller_calls(T, H, I):
+    # tokens' codes of +-127 and weights of +-31: 4096 * 127 * 31 < 2^24, exact sums
+    from moe_expert_layer_histogram_gb300 import int8_experts
+    g = torch.Generator(device="cuda").manual_seed(H)
+    x = randn(T, H)
+    w13 = torch.randint(-31, 32, (1, 2 * I, H), generator=g, device="cuda", dtype=torch.int8)
+    w2 = torch.randint(-31, 32, (1, H, I), generator=g, device="cuda", dtype=torch.int8)
+    s13, s2 = scales_of(1, 2 * I) * 0.02, scales_of(1, H, seed=1)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+
+    def run(a, b):
+        off = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        return int8_experts(x, slots[a:b].contiguous(), off, 1, w13, s13, w2, s2)
+    want = torch.cat([run(a, min(a + 16, T)) for a in range(0, T, 16)])
+    for _ in range(60):
+        assert torch.equal(run(0, T), want)
