@@ -1,11 +1,11 @@
 """Products of 8-bit integers with a scale per token and a scale per output
 channel, on torch tensors.
 
-Weights are int8 codes [N, K] (or [E, N, K]) with fp32 scales [N] ([E, N]);
-activations come in bf16 and are quantised per token on the way in, or as int8
-codes with one fp32 scale per row (int8_quantize, or block_join's).  Thin wrappers
-of the ``moe_int8_*`` calls (``include/moe.h`` states the formulas); work goes on
-torch's current stream, and the workspaces live in torch's allocator for the
+Weights are int8 codes [N, K] (or [E, N, K]), each row on 16 bytes, with fp32 scales
+[N] ([E, N]); activations come in bf16 and are quantised per token on the way in, or
+as int8 codes with one fp32 scale per row (int8_quantize, or block_join's).  Thin
+wrappers of the ``moe_int8_*`` calls (``include/moe.h`` states the formulas); work
+goes on torch's current stream, and the workspaces live in torch's allocator for the
 length of the call.
 """
 import torch
@@ -37,8 +37,8 @@ def _weights(w, w_scales):
     if one != 1 and K > 1:
         raise ValueError("w: contiguous rows")
     fits(max(E, N, K), "w")
-    if N == 1 and ldw < K:  # (one expert)
-        ldw = K
+    if E == 1 and N == 1:  # (nor does that of the only one)
+        ldw = (K + 15) // 16 * 16
     check(w_scales, _F32, scales, w.device, "w_scales")
     return E, N, K, ldw
 

@@ -593,3 +593,15 @@ def test_one_expert_of_long_rows_has_the_bits_of_smaller_calls(T, H, I):
     want = torch.cat([run(a, min(a + 16, T)) for a in range(0, T, 16)])
     for _ in range(60):
         assert torch.equal(run(0, T), want)
+
+
+@pytest.mark.parametrize("M", [1, 3, 40])
+@pytest.mark.parametrize("K", [1, 33, 250])
+def test_one_channel_of_any_width(M, K):
+    from moe_expert_layer_histogram_gb300 import int8_linear, int8_matmul, int8_quantize
+    flat = torch.cat([codes_of(K, seed=2), torch.full((64,), 127, dtype=torch.int8, device="cuda")])
+    w, ws = flat[:K].view(1, K), scales_of(1)
+    a, s = codes_of(M, K, seed=1), scales_of(M)
+    close(int8_matmul(a, s, w, ws), *matmul_reference(a, s, w, ws), K)
+    x = randn(M, K)
+    assert torch.equal(int8_linear(x, w, ws), int8_matmul(*int8_quantize(x), w, ws))

@@ -287,3 +287,11 @@ def test_numbers_below_32_bits_are_refused(monkeypatch):
     for quantize in (blockscale.blockscale_quantize, int8.int8_quantize):
         with pytest.raises(ValueError):
             quantize(rows, ids, LOW)
+
+
+@pytest.mark.parametrize("strides", [(33, 1), (0, 1), (100, 1)])
+def test_the_stride_of_a_single_row_says_nothing(strides):
+    # (the library wants strides of 16 bytes; there is no second row to be reached by one)
+    from moe_expert_layer_histogram_gb300 import int8
+    assert int8._weights(*weights((1, 33), strides)) == (1, 1, 33, 48)
+    assert int8._weights(*weights((1, 1, 33), (33,) + strides)) == (1, 1, 33, 48)
