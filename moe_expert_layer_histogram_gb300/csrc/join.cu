@@ -653,6 +653,7 @@ struct Ring {
         }
       }
     }
+    fence_proxy_async_shared();  // (the next copy into the stage comes after these reads)
     __syncwarp();
     mbar_arrive_if((threadIdx.x & 31) == 0, smem_u32(&empty[stage]));
     next();

@@ -467,3 +467,28 @@ def test_gradients_of_a_padded_buffer_without_tokens():
                               d_h=torch.empty(0, H, dtype=torch.bfloat16, device="cuda"))
     assert got.expert_rows.shape == (50, H) and bool((got.expert_rows == 0).all())
     assert bool((got.norm_weight == 0).all()) and bool((got.post_weight == 0).all())
+
+
+@pytest.mark.parametrize("T,H,K,x_type", [(2000, 7168, 8, torch.bfloat16), (1600, 4104, 3, torch.float32),
+                                          (1000, 7936, 5, torch.bfloat16), (6000, 2048, 6, torch.bfloat16)])
+def test_a_ring_gives_the_bits_of_small_calls_every_time(T, H, K, x_type):
+    # many tokens to a block, whose rows come through a ring of stages, against calls of
+    # few tokens, whose rows do not: x' is summed in the same order
+    from moe_expert_layer_histogram_gb300 import block_join, block_join_backward
+    a = make(T, H, K, x_type=x_type, w_type=x_type, post=False)
+    want = []
+    for t in range(0, T, 100):
+        few = slice(t, min(t + 100, T))
+        b = dict(a, order=a["order"].rows.view(T, K)[few].contiguous(),
+                 **{n: a[n][few].contiguous() for n in ("x", "weights", "shared", "gate")})
+        want.append(block_join(**b).x)
+    want = torch.cat(want)
+    dx, dh = randn(T, H, seed=80, dtype=x_type), randn(T, H, seed=81, dtype=torch.bfloat16)
+    first = None
+    for _ in range(30):
+        j = block_join(**a)
+        g = block_join_backward(j, dx, dh)
+        assert torch.equal(j.x, want)
+        now = [j.h, g.x, g.expert_rows, g.weights, g.shared, g.gate, g.norm_weight]
+        first = first or now
+        assert all(torch.equal(p, q) for p, q in zip(now, first))
