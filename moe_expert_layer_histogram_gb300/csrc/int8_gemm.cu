@@ -617,6 +617,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 // next item's first blocks, which have been widened by then (in four parts with the
 // widening of further blocks between them: 293 us).
 constexpr int kP8WStages = 5, kP8XStages = 4;
+// Barriers of filled weights, two to a stage by turns: the stages' number is odd, so a
+// stage's uses go to the two halves of the widening warps by turns, and a barrier's
+// phase tells only neighbouring uses apart.  (One to a stage: where a load came after
+// those of the two blocks behind it, the half that had skipped a use took the stage for
+// its own next one, with what was there.)
+constexpr int kP8WFull = 2 * kP8WStages;
 constexpr int kP8WBytes = 128 * 128;
 constexpr int kP8Buffers = 4;      // TMEM buffers of widened weights, 64 columns each
 constexpr uint32_t kP8Weights = 256;
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   // per widening warp: the scales of its 128 tokens
   float* s_scale = reinterpret_cast<float*>(s_x + kP8XStages * kP8XBytes);
   uint64_t* wfull = reinterpret_cast<uint64_t*>(s_scale + kI8WideWarps * 128);
-  uint64_t* wempty = wfull + kP8WStages;
+  uint64_t* wempty = wfull + kP8WFull;
   uint64_t* xfull = wempty + kP8WStages;  // (rank 0's: both CTAs' tokens)
   uint64_t* xempty = xfull + kP8XStages;
   uint64_t* afull = xempty + kP8XStages;  // (rank 0's: both CTAs' weights)
@@ -659,10 +665,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int rank = static_cast<int>(cluster_ctarank());
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kP8WStages; ++s) {
-      mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], 4);  // the warps that widen it
-    }
+    for (int s = 0; s < kP8WFull; ++s) mbar_init(&wfull[s], 1);
+    for (int s = 0; s < kP8WStages; ++s) mbar_init(&wempty[s], 4);  // the warps that widen it
     for (int s = 0; s < kP8XStages; ++s) {
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
@@ -731,16 +735,17 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         for (int kb = 0; kb < blocks; ++kb) {
           ok = mbar_wait(&wempty[stage], phase ^ 1, abort_flag);
           if (!ok) break;
-          mbar_arrive_expect_tx(&wfull[stage], kP8WBytes);
+          uint64_t* full = &wfull[loads % kP8WFull];
+          mbar_arrive_expect_tx(full, kP8WBytes);
           uint8_t* sw = smem + stage * kP8WBytes;
           if constexpr (SWIGLU) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              tma_load_3d_hint(sw + h * (kP8WBytes / 2), &maps.w, &wfull[stage], kb * 128,
+              tma_load_3d_hint(sw + h * (kP8WBytes / 2), &maps.w, full, kb * 128,
                                it.tile * 128 + rank * 64 + h * (p.N / 2), it.e, reused);
           } else {
-            tma_load_3d_hint(sw, &maps.w, &wfull[stage], kb * 128, it.tile * kI8Tile + rank * 128,
-                             it.e, reused);
+            tma_load_3d_hint(sw, &maps.w, full, kb * 128, it.tile * kI8Tile + rank * 128, it.e,
+                             reused);
           }
           ++loads;
           if (++stage == kP8WStages) {
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           }
         }
       }
-      drain_loads(wfull, kP8WStages, loads);
+      drain_loads(wfull, kP8WFull, loads);
       if (!ok) report_status(&g_int8_status, kStatusTimeout);
     }
     __syncwarp();
@@ -853,7 +858,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     // Every other block: this group's turn.
     auto widen = [&](int block) {
       const int stage = block % kP8WStages, buf = block % kP8Buffers;
-      if (!wait_warp(&wfull[stage], (block / kP8WStages) & 1, abort_flag)) return false;
+      if (!wait_warp(&wfull[block % kP8WFull], (block / kP8WFull) & 1, abort_flag)) return false;
       const uint8_t* src = smem + stage * kP8WBytes + row * 128;
       uint4 v[8];
 #pragma unroll
@@ -1030,7 +1035,7 @@ cudaError_t launch_i8_pair(const Int8Maps& maps, Int8Args p, int pairs, cudaStre
   if (ready != cudaSuccess) return ready;
   constexpr int fixed = 1024 + kP8WStages * kP8WBytes + kP8XStages * kP8XBytes +
                         kI8WideWarps * 128 * 4 +
-                        (2 * kP8WStages + 2 * kP8XStages + 2 * kP8Buffers + 3) * 8 + 8;
+                        (kP8WFull + kP8WStages + 2 * kP8XStages + 2 * kP8Buffers + 3) * 8 + 8;
   static_assert(fixed + (3 * kMaxExperts + 1) * 4 <= kI8SmemLimit);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};

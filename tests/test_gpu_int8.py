@@ -605,3 +605,26 @@ def test_one_channel_of_any_width(M, K):
     close(int8_matmul(a, s, w, ws), *matmul_reference(a, s, w, ws), K)
     x = randn(M, K)
     assert torch.equal(int8_linear(x, w, ws), int8_matmul(*int8_quantize(x), w, ws))
+
+
+@pytest.mark.parametrize("E,M,N,K,rows", [(16, 5552, 4269, 9304, 1), (8, 3500, 2100, 9000, 1),
+                                          (8, 3500, 2100, 9000, 40), (4, 2900, 4100, 5000, 130)])
+def test_pairs_of_few_rows_wait_for_their_weights(E, M, N, K, rows):
+    # experts of few rows in a call of many: weights come out of HBM more slowly than they
+    # are used, and not in order.  Codes of +-31: exact sums (9304 * 31^2 < 2^24)
+    from moe_expert_layer_histogram_gb300 import int8_matmul
+    g = torch.Generator(device="cuda").manual_seed(K)
+    ld = (K + 15) // 16 * 16
+    a = torch.randint(-31, 32, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-31, 32, (E, N, ld), generator=g, device="cuda", dtype=torch.int8)[:, :, :K]
+    s, ws = torch.ones(M, device="cuda"), torch.ones(E, N, device="cuda")
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * rows
+    want = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    for e in range(E):
+        part = a[e * rows:(e + 1) * rows].double() @ w[e].double().t()
+        want[e * rows:(e + 1) * rows] = part.float().bfloat16()
+    out = torch.full_like(want, 7.0)
+    for _ in range(60):
+        int8_matmul(a, s, w, ws, offsets=off, out=out)
+        assert torch.equal(out, want)
+        out[:E * rows] = 0
