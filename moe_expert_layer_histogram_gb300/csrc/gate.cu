@@ -479,7 +479,7 @@ __device__ __forceinline__ bool gate_token(const T* __restrict__ row, const Gate
       // (Lanes past the last group hold no words: no part in the votes below.  Their empty
       // words are a NaN's as logits, and sent every token of 3, 5, 6, .. groups to the
       // choice in 64 bits: 32768 x 384 f32, softmax without a bias, 3 of 6 groups by "top2"
-      // 2680 us where it takes 76 to 88, and 4 of 8 groups 58 to 73.)
+      // 2680 us where it takes 75 to 88, and 4 of 8 groups 58 to 73.)
       if (!FULL && !sh.in) {
         v = -INFINITY;
         d = 0.0f;

@@ -8,9 +8,9 @@
 // a lane and channel at a time; it has its first loads under way before anything
 // else: one or two rows are quantised by every block for itself meanwhile (QUANT),
 // more by a kernel that this one overlaps.  On the GPU, 7168 -> 4096: one row 7.0
-// us, two 9.7, three 9.3, four 9.9; five, through the tensor cores, 10.7.  4096 ->
-// 14592 (60 MB, 8.8 us of HBM): one row 8.7, two 10.9, three 12.5, four 13.9 (the dot
-// products take the time by then); five 13.5.
+// us, two 9.7, three 9.4, four 10.0; five, through the tensor cores, 11.1.  4096 ->
+// 14592 (60 MB, 8.8 us of HBM): one row 8.7, two 10.9, three 12.6, four 13.5 (the dot
+// products take the time by then); five 14.3.
 #include <cuda_bf16.h>
 
 #include <algorithm>

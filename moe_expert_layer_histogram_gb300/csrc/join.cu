@@ -28,7 +28,7 @@
 // ahead of the others and fills a ring of stages in shared memory, one row each, so
 // that a token's dozen rows, which depend on its indices and on one another's sums,
 // are all on their way at once and the next token's behind them (4096 x 7168, top-8:
-// 127 us forward and 205 backward, 6.1 TB/s; with rows loaded by the threads that use
+// 128 us forward and 208 backward, 6.0 TB/s; with rows loaded by the threads that use
 // them 143 and 318).  With few tokens to a block there is little to run ahead of, and
 // narrow rows have more blocks to an SM; those, rows that do not start on 16 bytes, and
 // rows of more than 7936 columns, whose vectors and filling warp are more than a block's
@@ -707,8 +707,8 @@ __device__ __forceinline__ void put_rows(const moe_join& j, Ring& ring, int64_t 
 
 // What a token's threads want to know of it, a lane a word: loaded a token ahead, and
 // left in the ring.  The gate's sigmoids wait until then, so that the filling warp does
-// not wait for their logit (at once: 4096 x 7168, top-8, 134 us forward and 218 backward
-// where these take 128 and 211).
+// not wait for their logit (at once: 4096 x 7168, top-8, six microseconds more forward
+// and seven backward).
 struct TokenWords {
   int row = -1;
   float w = 0.0f;
@@ -1117,7 +1117,7 @@ RingShape ring_shape(int H, int size) {
 // and 38.  Backward pass, 7168: 304 tokens 23 and 27, 512 42 and 58, 2048 112 and
 // 176; 2048 with a norm after the block: 1024 tokens 33 and 29, 4096 97 and 97; 512:
 // 8192 tokens 40 and 53.  (4096 tokens, top-8, forward and backward: 7936 columns by
-// the ring 134 and 228, 8192 by loads 157 and 352, 16384 466 and 955.)
+// the ring 136 and 228, 8192 by loads 157 and 352, 16384 467 and 957.)
 bool use_ring(int T, int H, int size, bool backward) {
   if (!ring_fits(H)) return false;
   const bool wide = H > 4096;
