@@ -20,8 +20,8 @@
 // codes of the chunk's rows (box height 16 / 32 / 64 / 128).  Warps 4-11 widen: warp
 // w takes the TMEM lanes 32 (w % 4).. of half (w - 4) / 4 and writes its rows' f16
 // into one of two TMEM buffers; a stage of weights is free then, before its MMAs (in
-// one ring with the tokens: 64 experts of 2048 x 1024, 6144 rows, 144 us for 130, 16
-// rows of 7168 -> 4096 11.9 for 11.0).  Warp 1 issues the MMAs.  The widening warps also read
+// one ring with the tokens: 64 experts of 2048 x 1024, 6144 rows, 144 us for 130).  Warp
+// 1 issues the MMAs.  The widening warps also read
 // the results out: after the first two blocks of the next item have been widened,
 // so the tensor cores go on as soon as the results are in registers, and the
 // scaling and the stores run beside them.
