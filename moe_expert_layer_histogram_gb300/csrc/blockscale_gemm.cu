@@ -68,7 +68,7 @@
 #include "blockscale_quant.cuh"
 #include "expert_table.cuh"
 #include "internal.h"
-#include "ptx.cuh"
+#include "ptx_pipeline.cuh"
 
 namespace moe {
 

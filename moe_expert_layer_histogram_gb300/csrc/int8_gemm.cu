@@ -41,7 +41,7 @@
 #include "expert_table.cuh"
 #include "int8_quant.cuh"
 #include "internal.h"
-#include "ptx.cuh"
+#include "ptx_pipeline.cuh"
 
 namespace moe {
 

@@ -42,7 +42,7 @@
 #include "int8_quant.cuh"
 #include "internal.h"
 #include "moe.h"
-#include "ptx.cuh"
+#include "ptx_pipeline.cuh"
 
 namespace moe {
 
